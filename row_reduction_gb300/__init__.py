@@ -1,5 +1,7 @@
 """GB300 (sm_103a) per-row FP32 reductions: RMSNorm, LayerNorm, residual
-LayerNorm, softmax, row sum and cross-entropy.
+LayerNorm, softmax, row sum and cross-entropy; and the row operators between
+a decoder's matrix products: rotary positions, the quantised cache and the
+processing of logits (``include/mt_decoder.h``).
 
 The computation is the CUDA library ``_lib/libmt_rowreduce.so`` (C ABI in
 ``include/mt_rowreduce.h``), built by :func:`row_reduction_gb300.build.build`.
@@ -37,6 +39,16 @@ from ._binding import (  # noqa: F401
     mt_rmsnorm_f32_with_plan, mt_row_sum_f32, mt_row_sum_f32_with_plan,
     mt_softmax_f32, mt_softmax_f32_with_plan, mt_status_string,
     status_string)
+from ._decoder import (  # noqa: F401
+    DECODER_EXPORTS, MT_CACHE_E4M3, MT_CACHE_INT8, MT_LOGITS,
+    MT_LOGITS_LOG_SOFTMAX, MT_LOGITS_SOFTMAX, MT_ROTARY_BANDS,
+    MT_ROTARY_LINEAR, MT_ROTARY_NTK, MT_ROTARY_PLAIN, MT_ROTARY_YARN,
+    MtCacheCall, MtCacheRows, MtLogitsCall, MtRotaryCall, MtRotaryHeads,
+    MtRotaryScaling, RotaryFrequencies, cache_alloc, cache_read, cache_slots,
+    cache_write, mt_cache_read, mt_cache_slots, mt_cache_write,
+    mt_process_logits, mt_rotary, mt_rotary_backward,
+    mt_rotary_backward_workspace, mt_rotary_frequencies, mt_rotary_turns,
+    process_logits, rotary, rotary_backward, rotary_frequencies)
 
 
 def _shape(x):

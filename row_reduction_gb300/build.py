@@ -19,14 +19,18 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT, "libmt_rowreduce.so")
-HEADER = os.path.join(ROOT, "include", "mt_rowreduce.h")
+HEADERS = [os.path.join(ROOT, "include", name)
+           for name in ("mt_rowreduce.h", "mt_decoder.h")]
 
 OPS = ("rmsnorm", "layernorm", "residual_layernorm", "softmax", "row_sum",
        "cross_entropy", "residual_rmsnorm", "log_softmax")
 DTYPES = ("f32", "f16", "bf16")
-SOURCES = (["api.cpp", "planner.cpp", "mean.cu", "probe.cu"] +
+SOURCES = (["api.cpp", "planner.cpp", "mean.cu", "probe.cu", "decoder.cpp",
+            "cache.cu", "logits.cu"] +
+           [f"rotary_{dt}.cu" for dt in DTYPES] +
            [f"ops_{op}_{dt}.cu" for op in OPS for dt in DTYPES])
-DEPENDS = ["mt_internal.h", "mt_kernels.cuh", "mt_stage.cuh", "plan_table.inc"]
+DEPENDS = ["mt_internal.h", "mt_kernels.cuh", "mt_stage.cuh", "plan_table.inc",
+           "mt_decoder_internal.h", "mt_decoder.cuh", "rotary.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler",
@@ -46,8 +50,9 @@ def _stamp(nvcc: str) -> str:
     for name in SOURCES + DEPENDS:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
-    with open(HEADER, "rb") as f:
-        h.update(f.read())
+    for path in HEADERS:
+        with open(path, "rb") as f:
+            h.update(f.read())
     h.update(" ".join([nvcc] + ARCH + CFLAGS).encode())
     h.update(os.uname().machine.encode())
     return h.hexdigest()
