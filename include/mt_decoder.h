@@ -209,7 +209,7 @@ MT_API mt_status mt_cache_slots(const int32_t *table, int64_t table_stride,
  *                                z -= frequency * c + presence
  *   each of the row's biases:    z += value
  *   z /= temperature             (a temperature that is not > 0 counts as 1,
- *                                one below 2^-126 as 2^-126)
+ *                                one beyond 2^-126 .. 2^126 as the bound)
  *   bit of the mask is 0:        z = -infinity, whatever stood there
  * and y = z, softmax(z) or log_softmax(z).  A row of which nothing is left
  * (every z is -infinity) gives probabilities 0 and log-probabilities
@@ -224,7 +224,7 @@ typedef struct mt_logits_call {
     const void *x;             /* rows x vocab, row stride x_stride */
     void *y;                   /* same type, row stride y_stride >= vocab */
     int64_t rows, x_stride, y_stride;
-    int32_t vocab;             /* 1..786432 */
+    int32_t vocab;             /* 1..524280 */
     int32_t mode;              /* mt_logits_mode */
     const int32_t *tokens;     /* rows x history token ids, row stride
                                   tokens_stride; ids outside [0, vocab) are
@@ -236,7 +236,8 @@ typedef struct mt_logits_call {
                                   values are clamped to 0..history) */
     const int32_t *prompt_lengths; /* rows: how many of them, from the start,
                                   are the prompt (NULL: none) */
-    const float *repetition, *frequency, *presence; /* rows each */
+    const float *repetition, *frequency, *presence; /* rows each; repetition
+                                  at least 2^-126 */
     const int32_t *bias_ids;   /* rows x biases, contiguous; ids outside
                                   [0, vocab) are passed over; the same id may
                                   come several times: its biases add up in

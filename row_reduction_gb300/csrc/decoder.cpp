@@ -268,7 +268,7 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     // the rows.
     *vec = c->group % 8 == 0 && (code_bits & 7) == 0 &&
            (bits & (uint64_t)(16 / es - 1)) == 0 &&
-           (!write || c->group <= 256);
+           (!write || c->group <= 512);
     a->slot = c->slot;
     a->tokens = c->tokens;
     a->slots = c->slots;

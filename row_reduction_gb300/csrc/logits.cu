@@ -1,13 +1,23 @@
 // logits.cu -- a row of logits: penalties for tokens of its history, biases,
 // temperature, grammar mask, and the row's softmax or log-softmax.
 //
-// A row is cut into slices, one CTA each.  A CTA counts, for its own slice
-// only, the tokens of the row's history in shared memory (integer atomics:
-// their order changes nothing), then passes over the slice's logits once.
-// Every CTA of a row reads the whole history, from L2 after the first.  For
-// the softmax modes the CTAs of a row are a cluster: z stays in shared
-// memory as FP32 in the place of the counters, and one exchange of (max,
-// sum) through distributed shared memory joins the slices.
+// A row is shared out between C CTAs (a power of two) so that a CTA's logits
+// stay in registers: K packs of V values per thread, asked for before anything
+// else.  While they arrive, the CTA counts, for its own logits only, the
+// tokens of the row's history in shared memory; integer atomics, whose order
+// changes nothing.  A bit per logit says whether its counter is in use, so
+// the pass over the logits reads one byte per pack and the counters of
+// touched tokens only.  Every CTA of a row reads the whole history, from L2
+// after the first.
+//
+// Ownership.  Chunks of 32 packs (one access of a warp) go round robin to the
+// CTAs: frequent tokens have low ids in most vocabularies, and contiguous
+// slices would give one CTA most of a row's history.
+//
+// Softmax.  A thread takes its exponentials about its own largest value; the
+// (max, sum) pairs of all warps of a row's CTAs, a cluster, are exchanged
+// through distributed shared memory behind one cluster barrier, and each
+// thread scales its exponentials once.
 //
 // Alignment.  Packs of V values start at 16-byte boundaries of x: pack p of
 // a row holds columns p V - shift + e, shift being the row's address modulo
@@ -18,262 +28,539 @@ namespace mt {
 namespace {
 
 // Counter of a token: bit 31 "in the prompt", bits 20..30 the number of its
-// first bias + 1, bits 0..19 how often it comes after the prompt.
+// bias + 1 (kSeveral: more than one), bits 0..19 how often it comes after
+// the prompt.
 constexpr unsigned kPrompt = 1u << 31;
 constexpr int kBiasShift = 20;
 constexpr unsigned kCountMask = (1u << kBiasShift) - 1;
+constexpr unsigned kSeveral = 0x7ffu;
 constexpr int kMaxThreads = 512;
+
+// Reads a pair at the same shared-memory offset in the CTA of cluster rank
+// `rank`.
+__device__ __forceinline__ float2 ld_cluster2(const float2 *p, unsigned rank) {
+    const unsigned local =
+        static_cast<unsigned>(__cvta_generic_to_shared(p));
+    unsigned remote;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(remote)
+                 : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(remote)
+                 : "memory");
+    return v;
+}
 
 struct Params {
     mt_logits_call_t c;
-    int32_t slices;  // CTAs per row
-    int32_t packs;   // packs per slice
+    int32_t log2C;   // CTAs per row
+    int32_t packs;   // packs per CTA, a multiple of 32
+    int32_t wide_tokens;  // every row of tokens starts at a 16-byte boundary
 };
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kMaxThreads)
+// Which tokens are a CTA's own, and where it keeps their counters.
+template <int V>
+struct Place {
+    static constexpr int kLog2Chunk = V == 8 ? 8 : 7;  // 32 V columns
+    int shift, log2C, rank, vocab;
+    __device__ __forceinline__ int mine(int id) const {
+        return ((unsigned)id < (unsigned)vocab) &
+               ((((id + shift) ^ (rank << kLog2Chunk)) &
+                 (((1 << log2C) - 1) << kLog2Chunk)) == 0);
+    }
+    __device__ __forceinline__ int element(int id) const {
+        const int at = id + shift;
+        return (at >> (kLog2Chunk + log2C) << kLog2Chunk) |
+               (at & (32 * V - 1));
+    }
+};
+
+// Tokens of this CTA that a lane has found and not counted yet.  Few of a
+// history's tokens are a CTA's own, so the pass over the history only looks
+// and puts them by, each lane in a column of shared memory of its own; they
+// are counted when a lane may run out of room, most lanes at work.
+constexpr int kRoom = 16;   // entries per lane
+constexpr int kLooks = 8;   // ids that a lane looks at between two checks
+template <int V>
+struct Found {
+    unsigned column;  // shared address; entry j is at column + 128 j
+    unsigned *count, *used;
+    Place<V> place;
+    int n;
+
+    // Four ids; `left` of them are there, `prompt` of them the prompt's.  No
+    // branches: a history is mostly others' tokens, and a warp's time is the
+    // length of this chain.
+    __device__ __forceinline__ void look(const int4 &v, int left, int prompt) {
+        const int id[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int mine = (j < left) & place.mine(id[j]);
+            const unsigned entry =
+                (unsigned)id[j] | (j < prompt ? kPrompt : 0u);
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+                "@p st.shared.u32 [%0], %1;\n\t}" ::"r"(column + 128 * n),
+                "r"(entry), "r"(mine)
+                : "memory");
+            n += mine;
+        }
+    }
+    // Counts what the lanes of a warp hold.  A counter that is not zero has
+    // its bit set already and a prompt token that was seen needs nothing:
+    // frequent tokens cost a read instead of atomics on one address.
+    __device__ __forceinline__ void drain() {
+#pragma unroll 1
+        for (int j = 0; __any_sync(kFull, j < n); ++j) {
+            if (j >= n) continue;
+            unsigned entry;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(entry)
+                         : "r"(column + 128 * j)
+                         : "memory");
+            const int i = place.element((int)(entry & ~kPrompt));
+            const unsigned before =
+                *static_cast<volatile unsigned *>(count + i);
+            if (before == 0) atomicOr(used + (i >> 5), 1u << (i & 31));
+            if (!(entry & kPrompt))
+                atomicAdd(count + i, 1u);
+            else if (!(before & kPrompt))
+                atomicOr(count + i, kPrompt);
+        }
+        n = 0;
+    }
+    // Called by whole warps after at most kLooks ids.
+    __device__ __forceinline__ void keep_room() {
+        if (__any_sync(kFull, n > kRoom - kLooks)) drain();
+    }
+};
+
+// Sum of a token's biases, in the order given (several for one token: rare).
+__device__ __noinline__ float several(const float *bias, const int32_t *ids,
+                                      int biases, int column) {
+    float s = 0.f;
+    for (int j = 0; j < biases; ++j)
+        if (ids[j] == column) s += bias[j];
+    return s;
+}
+
+// A touched logit: penalties, then biases.
+__device__ __forceinline__ float touched(float z, unsigned m, float rep,
+                                         float inv_rep, float freq,
+                                         float pres) {
+    const unsigned often = m & kCountMask;
+    const float f = z > 0.f ? inv_rep : rep;
+    z *= (m & (kCountMask | kPrompt)) ? f : 1.f;
+    return often ? z - (freq * (float)often + pres) : z;
+}
+
+// 2^t: one MUFU operation (2^-inf = 0, NaN stays NaN, results below 2^-126
+// flush to zero).
+__device__ __forceinline__ float pow2(float t) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+__device__ __forceinline__ float nanmax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Up to 32 values per thread leave registers for two CTAs per SM.
+template <typename T, int MODE, int K>
+__global__ void __launch_bounds__(kMaxThreads,
+                                  K * 16 / (int)sizeof(T) <= 32 ? 2 : 1)
     logits_kernel(const Params p) {
     constexpr int V = 16 / (int)sizeof(T);
     extern __shared__ __align__(16) unsigned count[];
-    __shared__ RedScratch red;
+    // (max, sum of exponentials about it) of each warp
+    __shared__ float2 pairs[kMaxThreads / 32], joined;
     grid_launch_dependents();
     grid_wait_prerequisites();
     const mt_logits_call_t &c = p.c;
-    const int rank = (int)(blockIdx.x % (unsigned)p.slices);
-    const int64_t row = blockIdx.x / (unsigned)p.slices;
+    const int C = 1 << p.log2C;
+    const int64_t row = blockIdx.x >> p.log2C;
+    const int rank = (int)(blockIdx.x & (unsigned)(C - 1));
     const T *x = static_cast<const T *>(c.x) + row * c.x_stride;
     T *y = static_cast<T *>(c.y) + row * c.y_stride;
     const int shift =
         (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (V - 1));
     const int yshift =
         (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) & (V - 1));
-    const int all = (c.vocab + shift + V - 1) / V;  // packs of the row
-    const int first = rank * p.packs;
-    const int n = max(0, min(p.packs, all - first));  // packs of the slice
-    const int base = first * V - shift;  // column of the slice's element 0
     const int T_ = (int)blockDim.x, tid = (int)threadIdx.x;
-    float *zs = reinterpret_cast<float *>(count);
-    float *bias_sum = zs + p.packs * V;
-    int *bias_id = reinterpret_cast<int *>(bias_sum + c.biases);
+    // Local pack tid + k T_ holds the columns from first + k next on.
+    const int first =
+        ((((tid >> 5) << p.log2C) + rank) * 32 + (tid & 31)) * V - shift;
+    const int next = (T_ << p.log2C) * V;
 
-    const bool history = c.tokens != nullptr && c.history > 0;
-    const bool marks = history || c.biases > 0;
-    if (marks) {
-        for (int i = tid; i < n; i += T_) {
+    // The CTA's logits; packs that are cut by an end of the row are read
+    // value by value.
+    Raw<T, V> raw[K];
 #pragma unroll
-            for (int w = 0; w < V; w += 4)
-                *reinterpret_cast<uint4 *>(count + i * V + w) =
-                    make_uint4(0, 0, 0, 0);
-        }
-        for (int i = tid; i < c.biases; i += T_)
-            bias_id[i] = c.bias_ids[row * c.biases + i];
-        __syncthreads();
-        const unsigned width = (unsigned)(n * V);
-        if (history) {
-            int len = c.history;
-            if (c.lengths) len = min(len, max(0, c.lengths[row]));
-            const int prompt = c.prompt_lengths ? c.prompt_lengths[row] : 0;
-            const int32_t *ids = c.tokens + row * c.tokens_stride;
-            for (int i = tid; i < len; i += T_) {
-                const int id = ids[i];
-                const unsigned at = (unsigned)id - (unsigned)base;
-                if (id >= 0 && id < c.vocab && at < width) {
-                    if (i < prompt)
-                        atomicOr(count + at, kPrompt);
-                    else
-                        atomicAdd(count + at, 1u);
+    for (int k = 0; k < K; ++k) {
+        const int col = first + k * next;
+        raw[k].zero();
+        if (col >= 0 && col + V <= c.vocab) {
+            raw[k].load(x + col);
+        } else if (col + V > 0 && col < c.vocab) {
+            for (int e = 0; e < V; ++e)
+                if (col + e >= 0 && col + e < c.vocab) {
+                    Raw<T, 1> one;
+                    one.load(x + col + e);
+                    raw[k].w[e * (int)sizeof(T) / 4] |=
+                        one.w[0] << (e * (int)sizeof(T) % 4 * 8);
                 }
-            }
         }
-        // The first bias of a token adds up all of its biases in order.
-        for (int i = tid; i < c.biases; i += T_) {
-            const int id = bias_id[i];
-            const unsigned at = (unsigned)id - (unsigned)base;
-            if (id < 0 || id >= c.vocab || at >= width) continue;
-            bool mine = true;
-            for (int j = 0; j < i && mine; ++j) mine = bias_id[j] != id;
-            if (!mine) continue;
-            float b = 0.f;
-            for (int j = i; j < c.biases; ++j)
-                if (bias_id[j] == id) b += c.bias[row * c.biases + j];
-            bias_sum[i] = b;
-            atomicOr(count + at, (unsigned)(i + 1) << kBiasShift);
-        }
-        __syncthreads();
     }
+    // Everything that the row needs is asked for before any of it is waited
+    // for: the logits above, the row's parameters, the mask, the first
+    // tokens.  What is computed from them stands behind the counting.
     const float rep = c.repetition ? c.repetition[row] : 1.f;
     const float freq = c.frequency ? c.frequency[row] : 0.f;
     const float pres = c.presence ? c.presence[row] : 0.f;
     const float temp = c.temperature ? c.temperature[row] : 1.f;
-    const float inv_temp =
-        temp > 0.f ? 1.f / fmaxf(temp, 1.17549435e-38f) : 1.f;
-    const uint32_t *mask = c.mask ? c.mask + row * c.mask_stride : nullptr;
-
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += T_) {
-        const int col = base + i * V;
-        const bool whole = col >= 0 && col + V <= c.vocab;
-        float z[V];
-        if (whole) {
-            ld_vec<T, V>(x + col, z);
-        } else {
+    const int length = c.lengths ? c.lengths[row] : c.history;
+    const int prompt = c.prompt_lengths ? c.prompt_lengths[row] : 0;
+    // The one or two mask bytes of a pack's columns (one where packs start
+    // at a multiple of their width).
+    const uint8_t *mask =
+        c.mask ? reinterpret_cast<const uint8_t *>(c.mask +
+                                                   row * c.mask_stride)
+               : nullptr;
+    unsigned bits0[K], bits1[K];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                z[e] = col + e >= 0 && col + e < c.vocab ? to_f(x[col + e])
-                                                         : -INFINITY;
+    for (int k = 0; k < K; ++k) {
+        const int col = first + k * next;
+        const int from = max(col, 0), last = min(col + V, c.vocab) - 1;
+        bits0[k] = bits1[k] = ~0u;
+        if (mask != nullptr && from <= last) {
+            bits0[k] = __ldg(mask + (from >> 3));
+            if (shift != 0 && last >> 3 > from >> 3)
+                bits1[k] = __ldg(mask + (last >> 3));
         }
-        if (marks) {
+    }
+    const bool marks = c.tokens != nullptr || c.biases > 0;
+    unsigned *used = count + p.packs * V;
+    float *bias = reinterpret_cast<float *>(used + p.packs * V / 32);
+    int32_t *bias_ids = reinterpret_cast<int32_t *>(bias + c.biases);
+    unsigned *found_at = reinterpret_cast<unsigned *>(bias_ids + c.biases);
+    if (marks) {
+        const int32_t *ids = c.tokens + row * c.tokens_stride;
+        const int quads = p.wide_tokens ? c.history >> 2 : 0;
+        // 16-byte loads of tokens, four in flight per thread
+        const auto quad = [ids, quads](int q) {
+            return q < quads ? reinterpret_cast<const int4 *>(ids)[q]
+                             : make_int4(-1, -1, -1, -1);
+        };
+        int4 v0 = quad(tid), v1 = quad(tid + T_);
+        int4 w0 = quad(tid + 2 * T_), w1 = quad(tid + 3 * T_);
+        for (int i = tid; i < p.packs * V / 4; i += T_)
+            reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < p.packs * V / 32; i += T_) used[i] = 0;
+        for (int i = tid; i < c.biases; i += T_) {
+            bias_ids[i] = c.bias_ids[row * c.biases + i];
+            bias[i] = c.bias[row * c.biases + i];
+        }
+        const int len = min(max(length, 0), c.history);
+        __syncthreads();
+        const Place<V> place = {shift, p.log2C, rank, c.vocab};
+        // Whole warps go through the history together.
+        const int lane = tid & 31;
+        Found<V> found = {
+            (unsigned)__cvta_generic_to_shared(found_at +
+                                               (tid >> 5) * 32 * kRoom + lane),
+            count, used, place, 0};
+#pragma unroll 1
+        for (int q0 = tid - lane; q0 < quads && q0 * 4 < len; q0 += 2 * T_) {
+            const int at = (q0 + lane) * 4;
+            const int4 a0 = v0, a1 = v1;
+            v0 = w0;
+            v1 = w1;
+            w0 = quad(q0 + lane + 4 * T_);
+            w1 = quad(q0 + lane + 5 * T_);
+            found.look(a0, len - at, prompt - at);
+            found.look(a1, len - at - 4 * T_, prompt - at - 4 * T_);
+            found.keep_room();
+        }
+#pragma unroll 1
+        for (int i0 = quads * 4 + tid - lane; i0 < len; i0 += T_) {
+            const int at = i0 + lane;
+            found.look(make_int4(at < len ? ids[at] : -1, -1, -1, -1), 1,
+                       at < prompt);
+            found.keep_room();
+        }
+        found.drain();
+        // A bias leaves its number in its token's counter; where another one
+        // was there before (in any order), the field becomes kSeveral and
+        // the pass below adds them up in the order given.
+        for (int i = tid; i < c.biases; i += T_) {
+            if (place.mine(bias_ids[i])) {
+                const int j = place.element(bias_ids[i]);
+                atomicOr(used + (j >> 5), 1u << (j & 31));
+                const unsigned before =
+                    atomicOr(count + j, (unsigned)(i + 1) << kBiasShift);
+                if ((before >> kBiasShift) & kSeveral)
+                    atomicOr(count + j, kSeveral << kBiasShift);
+            }
+        }
+        __syncthreads();
+    }
+
+    const float inv_rep = 1.f / rep;
+    // 2^-126 .. 2^126: -infinity keeps its sign and is never multiplied by 0
+    const float inv_temp =
+        temp > 0.f
+            ? 1.f / fminf(fmaxf(temp, 1.17549435e-38f), 8.5070592e+37f)
+            : 1.f;
+    // Bits of the values that lie in the row and that the mask leaves.
+    constexpr unsigned kAll = (1u << V) - 1u;
+    unsigned keep[K];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const unsigned m = count[i * V + e];
-                if (m != 0) {
-                    const unsigned often = m & kCountMask;
-                    const unsigned b = (m >> kBiasShift) & 0x7ffu;
-                    if (often != 0 || (m & kPrompt))
-                        z[e] = z[e] > 0.f ? z[e] / rep : z[e] * rep;
-                    if (often != 0) z[e] -= freq * (float)often + pres;
-                    if (b != 0) z[e] += bias_sum[b - 1];
+    for (int k = 0; k < K; ++k) {
+        const int col = first + k * next;
+        const int from = max(col, 0), to = min(col + V, c.vocab);
+        keep[k] = ((bits0[k] & 0xffu) | bits1[k] << 8) >> (from & 7) & kAll;
+        if (to - from < V)
+            keep[k] = from < to
+                          ? (keep[k] & ((1u << (to - from)) - 1u))
+                                << (from - col)
+                          : 0u;
+    }
+    // Touched logits of the thread's own packs: their new values, FP32, take
+    // the place of their counters.  A compact loop: few of them, and code that
+    // runs once per CTA costs its fetch.
+    if (marks) {
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+            const int i = (tid + k * T_) * V;
+            if (i >= p.packs * V) break;
+            unsigned hit = used[i >> 5] >> (i & 31) & kAll;
+#pragma unroll 1
+            while (hit) {
+                const int e = __ffs(hit) - 1, col = first + k * next + e;
+                hit &= hit - 1;
+                const unsigned m = count[i + e];
+                float v = touched(to_f(x[col]), m, rep, inv_rep, freq, pres);
+                const unsigned b = m >> kBiasShift & kSeveral;
+                if (b == kSeveral)
+                    v += several(bias, bias_ids, c.biases, col);
+                else if (b != 0)
+                    v += bias[b - 1];
+                count[i + e] = __float_as_uint(v);
+            }
+        }
+    }
+    // Values before temperature, -infinity where the mask (or the row's end)
+    // leaves nothing; packs of which nothing is left are not looked at.
+    float2 z[K][V / 2];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (keep[k] == 0) continue;
+        float *v = &z[k][0].x;
+        raw[k].widen(v);
+        if (marks) {
+            const int i = (tid + k * T_) * V;
+            const unsigned hit = used[i >> 5] >> (i & 31) & kAll;
+            if (hit) {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const float4 n =
+                        *reinterpret_cast<const float4 *>(count + i + e);
+                    v[e] = hit >> e & 1u ? n.x : v[e];
+                    v[e + 1] = hit >> (e + 1) & 1u ? n.y : v[e + 1];
+                    v[e + 2] = hit >> (e + 2) & 1u ? n.z : v[e + 2];
+                    v[e + 3] = hit >> (e + 3) & 1u ? n.w : v[e + 3];
                 }
             }
         }
-        unsigned bits = ~0u;
-        if (mask) {
-            // Bits of columns col .. col+V-1 (of a partial pack, those that
-            // exist; the row's first columns when col < 0).
-            const int from = max(col, 0);
-            const int word = from >> 5, last = min(col + V, c.vocab) - 1;
-            const unsigned lo = __ldg(mask + word);
-            const unsigned hi = last >> 5 > word ? __ldg(mask + word + 1) : 0u;
-            bits = __funnelshift_r(lo, hi, from & 31) << (from - col);
+        if (keep[k] != kAll) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = keep[k] >> e & 1u ? v[e] : -INFINITY;
         }
+        if (MODE != MT_LOGITS) {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            z[e] = (bits >> e) & 1u ? z[e] * inv_temp : -INFINITY;
-        if (MODE == MT_LOGITS) {
-            if (whole && yshift == shift) {
-                st_vec<T, V>(y + col, z);
-            } else {
+            for (int h = 0; h < V / 2; ++h)
+                top = nanmax3(top, z[k][h].x, z[k][h].y);
+        }
+    }
+    float mul = inv_temp, sub = 0.f, log_total = 0.f;
+    if (MODE != MT_LOGITS) {
+        // e^((v - w) / temperature) as 2^((v - w) a): the difference is
+        // formed first (exact near w), so its error is 4 roundings of the
+        // exponent.  The thread's exponentials are taken about its own
+        // largest value (about 0 where it has none: all of them are 0).
+        const float a = inv_temp * 1.4426950408889634f;
+        const float ref = top == -INFINITY ? 0.f : top;
+        float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (col + e >= 0 && col + e < c.vocab)
-                        y[col + e] = from_f<T>(z[e]);
+        for (int k = 0; k < K; ++k) {
+            if (keep[k] == 0) continue;
+#pragma unroll
+            for (int h = 0; h < V / 2; ++h) {
+                const float2 t = mul2(add2(z[k][h], both(-ref)), both(a));
+                const float2 ex = make_float2(pow2(t.x), pow2(t.y));
+                sums = add2(sums, ex);
+                if (MODE == MT_LOGITS_SOFTMAX) z[k][h] = ex;
             }
+        }
+        const float sum = sums.x + sums.y;
+        // The warp's pair.
+        const int lane = tid & 31, warps = T_ >> 5;
+        const float wtop = warp_nanmax(top);
+        float wsum = top == -INFINITY ? 0.f : sum * pow2((top - wtop) * a);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            wsum += __shfl_xor_sync(kFull, wsum, o);
+        if (lane == 0) pairs[tid >> 5] = make_float2(wtop, wsum);
+        __syncthreads();
+        // The CTA's pair, by every warp in the same order, and then the
+        // row's.
+        float M, total;
+        const auto join = [a, &M, &total](float2 v) {
+            M = warp_nanmax(v.x);
+            total = v.x == -INFINITY ? 0.f : v.y * pow2((v.x - M) * a);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                total += __shfl_xor_sync(kFull, total, o);
+        };
+        const float2 none = make_float2(-INFINITY, 0.f);
+        join((lane & 15) < warps ? pairs[lane & 15] : none);
+        if (C > 1) {
+            if (tid == 0) joined = make_float2(M, total);
+            cluster_sync();
+            join((lane & 15) < C ? ld_cluster2(&joined, (unsigned)lane & 15u)
+                                 : none);
+        }
+        // No CTA may end before all have read its pairs: arrive (with release
+        // order behind the reads) here, wait at the end.
+        if (C > 1)
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::
+                             : "memory");
+        // Softmax: e^(v - top) e^(top - M) / total; a row with nothing left
+        // has total 0 and gives 0.  Log-softmax: (v - M) / temperature -
+        // log(total); such a row keeps its -infinities.
+        if (MODE == MT_LOGITS_SOFTMAX)
+            mul = total == 0.f || top == -INFINITY
+                      ? 0.f : pow2((top - M) * a) / total;
+        if (MODE == MT_LOGITS_LOG_SOFTMAX && total != 0.f) {
+            sub = M;
+            log_total = logf(total);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = first + k * next;
+        if (col + V <= 0 || col >= c.vocab) continue;
+        float *v = &z[k][0].x;
+        if (keep[k] == 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = MODE == MT_LOGITS_SOFTMAX ? 0.f : -INFINITY;
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (!whole && (col + e < 0 || col + e >= c.vocab))
-                    z[e] = -INFINITY;
-                top = nanmax(top, z[e]);
-                zs[i * V + e] = z[e];
+            for (int h = 0; h < V / 2; ++h) {
+                if (MODE == MT_LOGITS_LOG_SOFTMAX)
+                    z[k][h] = add2(z[k][h], both(-sub));
+                z[k][h] = mul2(z[k][h], both(mul));
+                if (MODE == MT_LOGITS_LOG_SOFTMAX)
+                    z[k][h] = add2(z[k][h], both(-log_total));
             }
         }
-    }
-    if (MODE == MT_LOGITS) return;
-
-    int parity = 0;
-    top = row_allreduce<MaxOp>(top, T_, red, parity);
-    // A slice of which nothing is left: every e^z is 0.
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int i = tid; i < n; i += T_) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float ex = exp_shifted(zs[i * V + e] - ref);
-            sum += ex;
-            if (MODE == MT_LOGITS_SOFTMAX) zs[i * V + e] = ex;
-        }
-    }
-    sum = row_allreduce<SumOp>(sum, T_, red, parity);
-    float M = top, total = sum;
-    if (p.slices > 1) {
-        if (tid == 0) {
-            red.cl[0][0] = top;
-            red.cl[0][1] = sum;
-        }
-        cluster_sync();
-        M = -INFINITY;
-        for (int r = 0; r < p.slices; ++r)
-            M = nanmax(M, ld_cluster(&red.cl[0][0], (unsigned)r));
-        total = 0.f;
-        for (int r = 0; r < p.slices; ++r) {
-            const float m = ld_cluster(&red.cl[0][0], (unsigned)r);
-            const float s = ld_cluster(&red.cl[0][1], (unsigned)r);
-            total += m == -INFINITY ? 0.f : s * exp_shifted(m - M);
-        }
-        // No CTA ends while another may still read its sums.
-        cluster_sync();
-    }
-    // Softmax: e^(z - top) e^(top - M) / total; a row with nothing left has
-    // total 0 and gives 0.  Log-softmax: (z - M) - log(total); such a row
-    // keeps its -infinities.
-    float mul = 0.f, sub = 0.f, log_total = 0.f;
-    if (total != 0.f) {
-        mul = (top == M ? 1.f : exp_shifted(top - M)) / total;
-        sub = M;
-        log_total = logf(total);
-    }
-    for (int i = tid; i < n; i += T_) {
-        const int col = base + i * V;
-        float z[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float v = zs[i * V + e];
-            z[e] = MODE == MT_LOGITS_SOFTMAX ? v * mul
-                                             : (v - sub) - log_total;
-        }
         if (col >= 0 && col + V <= c.vocab && yshift == shift) {
-            st_vec<T, V>(y + col, z);
+            st_vec<T, V>(y + col, v);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (col + e >= 0 && col + e < c.vocab)
-                    y[col + e] = from_f<T>(z[e]);
+                    y[col + e] = from_f<T>(v[e]);
         }
     }
+    if (MODE != MT_LOGITS && C > 1)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <typename T, int MODE>
-cudaError_t launch_as(const mt_logits_call_t &c, cudaStream_t s) {
+template <typename T, int MODE, int K>
+cudaError_t launch_packs(const Params &p, int threads, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
-    int sms = 0;
-    cudaError_t e = current_sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    const int all = (c.vocab + 2 * V - 2) / V;  // with the largest shift
-    // Slices: at most 16384 values each (64 KiB of counters, three CTAs per
-    // SM), up to 16 CTAs, the largest cluster; more of them while the rows
-    // leave SMs idle and a slice keeps 2048 values.
-    int slices = 1;
-    while (slices < 16 && (all + slices - 1) / slices * V > 16384) slices *= 2;
-    while (slices < 16 && c.rows * slices < 2 * sms &&
-           (all + slices - 1) / slices * V > 4096)
-        slices *= 2;
-    Params p = {c, slices, (all + slices - 1) / slices};
-    int threads = 64;
-    while (threads < kMaxThreads && threads < p.packs) threads *= 2;
-    const bool marks = (c.tokens && c.history > 0) || c.biases > 0;
-    size_t smem = 0;
-    if (MODE != MT_LOGITS || marks)
-        smem = (size_t)p.packs * V * 4 + (size_t)c.biases * 8;
-    const void *k = reinterpret_cast<const void *>(logits_kernel<T, MODE>);
-    if (smem > 48 * 1024)
-        if ((e = allow_max_smem(k)) != cudaSuccess) return e;
-    if (slices > 8 && MODE != MT_LOGITS)
-        if ((e = allow_nonportable_cluster(k)) != cudaSuccess) return e;
+    const mt_logits_call_t &c = p.c;
+    const void *k = reinterpret_cast<const void *>(logits_kernel<T, MODE, K>);
+    size_t smem = 0;  // a counter and a bit per logit of the slice, biases
+    if (c.tokens != nullptr || c.biases > 0)
+        smem = (size_t)p.packs * V * 4 + (size_t)p.packs * V / 8 +
+               (size_t)c.biases * 8 + (size_t)threads * kRoom * 4;
+    cudaError_t e = cudaSuccess;
+    if (smem > 40 * 1024 && (e = allow_max_smem(k)) != cudaSuccess) return e;
+    const bool cluster = MODE != MT_LOGITS && p.log2C > 0;
+    if (cluster && p.log2C > 3 &&
+        (e = allow_nonportable_cluster(k)) != cudaSuccess)
+        return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)slices;
+    attr[1].val.clusterDim.x = 1u << p.log2C;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(c.rows * slices));
+    cfg.gridDim = dim3((unsigned)(c.rows << p.log2C));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = MODE != MT_LOGITS && slices > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, logits_kernel<T, MODE>, p);
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, logits_kernel<T, MODE, K>, p);
+}
+
+// Slices, packs per thread and threads.
+template <typename T, int MODE>
+cudaError_t launch_as(const mt_logits_call_t &c, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int kMost = 64 / V;  // packs per thread: at most 64 values
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    // The largest shift that a row of this call can have.
+    const bool whole =
+        (reinterpret_cast<uintptr_t>(c.x) & 15) == 0 &&
+        (c.rows == 1 || c.x_stride * (int64_t)sizeof(T) % 16 == 0);
+    const int all = (c.vocab + (whole ? 0 : V - 1) + V - 1) / V;
+    const int chunks = (all + 31) / 32;
+    const auto packs = [&](int l) {
+        return (chunks + (1 << l) - 1) / (1 << l) * 32;
+    };
+    // Enough CTAs that 512 threads hold their part with 32 values each, and
+    // more while the rows leave SMs idle and a CTA keeps 128 threads busy.
+    // Softmax: clusters of up to 8; 16 only for rows that 8 CTAs cannot hold
+    // with 64 values per thread (BF16 softmax 256x131072: 43 us on 8 CTAs per
+    // row, 116 us on 16, of which the device places few at a time).
+    const int most = MODE == MT_LOGITS ? 6 : 3;
+    int l = 0;
+    while (l < most && packs(l) * V > 32 * kMaxThreads) ++l;
+    while (packs(l) * V > 64 * kMaxThreads) ++l;
+    while (l < most && c.rows << l < 2 * sms && packs(l) > 256) ++l;
+    Params p = {c, l, packs(l), 0};
+    if (p.c.history == 0) p.c.tokens = nullptr;
+    p.wide_tokens = (reinterpret_cast<uintptr_t>(c.tokens) & 15) == 0 &&
+                    (c.rows == 1 || c.tokens_stride % 4 == 0);
+    // Fewest packs per thread that 512 threads can do with; one pack per
+    // thread needs the fewest threads of a small slice.
+    int K = 1;
+    while (K < kMost && (int64_t)K * kMaxThreads < p.packs) K *= 2;
+    int threads = 64;
+    while (threads < kMaxThreads && threads * K < p.packs) threads *= 2;
+    switch (K) {
+        case 1: return launch_packs<T, MODE, 1>(p, threads, s);
+        case 2: return launch_packs<T, MODE, 2>(p, threads, s);
+        case 4: return launch_packs<T, MODE, 4>(p, threads, s);
+        case 8: return launch_packs<T, MODE, 8>(p, threads, s);
+    }
+    if constexpr (kMost >= 16) return launch_packs<T, MODE, 16>(p, threads, s);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>

@@ -27,4 +27,73 @@ cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int threads,
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// ---- pairs of FP32 values ---------------------------------------------------
+// Two FP32 operations per instruction (sm_100 family), each rounded as the
+// single ones are.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// V values of T as they lie in memory (aligned to V*sizeof(T) bytes): loads
+// can be issued long before their values are widened.
+template <typename T, int V>
+struct Raw {
+    static constexpr int kBytes = V * (int)sizeof(T);
+    static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+    unsigned w[kWords];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (kWords == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else if constexpr (kWords == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x; w[1] = u.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const unsigned *>(p);
+        } else {
+            w[0] = *reinterpret_cast<const unsigned short *>(p);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void widen(float *d) const {
+        if constexpr (kBytes >= 4) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                Pack<T>::unpack(w[i], d + i * Pack<T>::kPerWord);
+        } else {
+            const unsigned short h = (unsigned short)w[0];
+            d[0] = to_f(*reinterpret_cast<const T *>(&h));
+        }
+    }
+};
+
 }  // namespace mt

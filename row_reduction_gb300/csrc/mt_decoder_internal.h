@@ -89,7 +89,8 @@ cudaError_t launch_cache_slots(const int32_t *table, int64_t stride,
                                cudaStream_t s);
 
 // ---- logits ----------------------------------------------------------------
-constexpr int kLogitsMaxVocab = 786432;
+// 16 CTAs of 512 threads with 64 values each, less a pack's shift.
+constexpr int kLogitsMaxVocab = 524280;
 constexpr int kLogitsMaxBias = 1024;
 cudaError_t launch_logits(int dtype, const mt_logits_call_t &c,
                           cudaStream_t s);

@@ -189,7 +189,7 @@ def logits_ref(x, tokens=None, lengths=None, prompt_lengths=None,
                     mag[r, t] += abs(b) * bias_ids.shape[1] / 4 + abs(b)
         if temperature is not None:
             t = float(temperature[r])
-            t = max(t, 2.0 ** -126) if t > 0 else 1.0
+            t = min(max(t, 2.0 ** -126), 2.0 ** 126) if t > 0 else 1.0
             z[r] /= t
             mag[r] /= t
     if mask is not None:

@@ -660,13 +660,13 @@ def test_process_logits_temperatures():
     assert torch.equal(y[:3], x[:3])
     check_logits(x[4:5], dict(temperature=t[4:5]), "logits", y[4:5])
     check_logits(x[6:], dict(temperature=t[6:]), "logits", y[6:])
-    assert bool((y[5] == 0).all())
+    assert torch.equal(y[5], x[5] * 2.0 ** -126)
     assert torch.equal(y[3], torch.sign(x[3]) * torch.where(
         x[3].abs() >= 4, math.inf, (x[3].abs() * 2.0 ** 126)))
 
 
 def test_process_logits_largest_vocabulary():
-    x, kw = logits_inputs(37, 2, 786432, 100, 5, True, torch.bfloat16)
+    x, kw = logits_inputs(37, 2, 524280, 100, 5, True, torch.bfloat16)
     for mode in ("logits", "softmax"):
         y = mt.process_logits(x, mode=mode, **kw)
         check_logits(x, kw, mode, y)
@@ -704,7 +704,7 @@ def test_process_logits_refuses_on_the_device():
     with pytest.raises(mt.MTError):
         mt.process_logits(x, out=x[:1].expand(2, -1))
     with pytest.raises(mt.MTError):
-        mt.process_logits(torch.zeros(1, 786433, device="cuda"))
+        mt.process_logits(torch.zeros(1, 524281, device="cuda"))
 
 
 # ---- streams, graphs, together -----------------------------------------------

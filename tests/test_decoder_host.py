@@ -352,7 +352,7 @@ def logits(**kw):
 @pytest.mark.parametrize("c,want", [
     (logits(rows=-1), INV), (logits(vocab=0), INV), (logits(mode=3), INV),
     (logits(mode=-1), INV), (logits(history=-1), INV),
-    (logits(biases=-1), INV), (logits(vocab=786433, y_stride=786433), UNS),
+    (logits(biases=-1), INV), (logits(vocab=524281, y_stride=524281), UNS),
     (logits(history=1 << 20, tokens=A), UNS), (logits(biases=1025), UNS),
     (logits(x=None), INV), (logits(y=None), INV), (logits(x=A + 1), INV),
     (logits(y=A + 1), INV), (logits(history=4), INV),
