@@ -11,9 +11,11 @@ synchronises, and every call can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import struct
 from collections import namedtuple
 
-from ._binding import DTYPE_IDS, _check, lib as _base_lib
+from ._binding import (DTYPE_IDS, LIB_PATH, MT_OK, MTError,
+                       lib as _base_lib, _check)
 
 MT_ROTARY_PLAIN, MT_ROTARY_LINEAR, MT_ROTARY_NTK = 0, 1, 2
 MT_ROTARY_YARN, MT_ROTARY_BANDS = 3, 4
@@ -167,35 +169,74 @@ def mt_process_logits(dtype, call, stream):
 
 
 # ---- tensors -----------------------------------------------------------------
-_DTYPES = None
+# A call's time on the host is most of a small call's, so the functions below
+# look at a tensor once (type, device, shape, strides, address), and pack the
+# C structure in one step; only where something is wrong do they go through
+# the checks one by one for what to say.
+_torch = None
+_DTYPES = {}
+_calls = {}
+# The C structures in one go (mt_rotary_call_t, mt_cache_call_t,
+# mt_logits_call_t), native alignment.
+_ROTARY = struct.Struct("@" + 2 * "5P6q2i" + "2Pq5i2fi")
+_CACHE = struct.Struct("@" + 2 * "3P2q" + "Pqq4i")
+_LOGITS = struct.Struct("@2P3q2iPq2i8PqP")
 
 
-def _dtype_id(t, name):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: DTYPE_IDS["f32"],
-                   torch.float16: DTYPE_IDS["f16"],
-                   torch.bfloat16: DTYPE_IDS["bf16"]}
-    got = _DTYPES.get(t.dtype)
-    if got is None:
+def _setup():
+    """Torch and the library, once."""
+    global _torch
+    import torch
+    _decoder_lib()
+    _DTYPES.update({torch.float32: DTYPE_IDS["f32"],
+                    torch.float16: DTYPE_IDS["f16"],
+                    torch.bfloat16: DTYPE_IDS["bf16"]})
+    L = ctypes.CDLL(LIB_PATH)  # the same library; packed structures as bytes
+    text = ctypes.c_char_p
+    for name, args in {
+            "mt_rotary": [_I32, text, _P],
+            "mt_rotary_backward": [_I32, text, _P, ctypes.c_size_t, _P],
+            "mt_cache_write": [_I32, text, _P],
+            "mt_cache_read": [_I32, text, _P],
+            "mt_process_logits": [_I32, text, _P]}.items():
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
+        _calls[name] = fn
+    _torch = torch
+
+
+def _call(name, *args):
+    st = _calls[name](*args)
+    if st != MT_OK:
+        raise MTError(st, name)
+
+
+def _first(t, name):
+    """(mt_dtype, device index) of a call's first tensor."""
+    if _torch is None:
+        _setup()
+    try:
+        dt, index = _DTYPES.get(t.dtype), t.get_device()
+    except AttributeError:
+        dt, index = None, -1
+    if dt is None or index < 0:
+        _tensor(t, name)
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got "
                         f"{t.dtype}")
-    return got
+    return dt, index
 
 
-def _tensor(t, name, dtype=None, shape=None, like=None):
-    """Checks one tensor: CUDA, its type, its shape (None entries are free)
-    and the device of `like`."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _tensor(t, name, dtype=None, shape=None, index=None):
+    """Checks one tensor: CUDA, its type, its device, its shape (None entries
+    are free)."""
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name}: expected a CUDA tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if shape is not None:
         if t.dim() != len(shape) or any(
                 w is not None and g != w for g, w in zip(t.shape, shape)):
@@ -204,56 +245,84 @@ def _tensor(t, name, dtype=None, shape=None, like=None):
     return t
 
 
-def _dense(t, name, dtype, shape, like):
-    _tensor(t, name, dtype, shape, like)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _dense(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of this type, shape and device."""
+    try:
+        if (t.dtype is dtype and t.get_device() == index and
+                t.shape == shape and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _tensor(t, name, dtype, shape, index)
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _heads_view(t, name, dtype=None, shape=None, like=None):
-    """A [tokens, heads, dim] tensor whose last dimension is dense."""
-    _tensor(t, name, dtype, shape, like)
+def _opt(t, name, dtype, shape, index):
+    return 0 if t is None else _dense(t, name, dtype, shape, index)
+
+
+def _heads(t, name, dtype, shape, index):
+    """(address, token stride, head stride) of a [tokens, heads, dim] tensor
+    whose last dimension is dense."""
+    try:
+        st = t.stride()
+        if (t.dtype is dtype and t.get_device() == index and
+                t.shape == shape and (st[2] == 1 or shape[2] <= 1)):
+            return t.data_ptr(), st[0], st[1]
+    except (AttributeError, IndexError):
+        pass
+    _tensor(t, name, dtype, None, index)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}: the last dimension must be dense")
-    return t
+    _tensor(t, name, dtype, shape, index)
+    raise ValueError(f"{name}: the last dimension must be dense")
+
+
+def _rows(t, name, dtype, rows, index):
+    """(address, row stride, width) of a [rows, width] tensor with dense
+    rows."""
+    try:
+        st, sh = t.stride(), t.shape
+        if (t.dtype is dtype and t.get_device() == index and len(sh) == 2 and
+                sh[0] == rows and (st[1] == 1 or sh[1] <= 1)):
+            return t.data_ptr(), st[0], sh[1]
+    except (AttributeError, IndexError):
+        pass
+    _tensor(t, name, dtype, (rows, None), index)
+    raise ValueError(f"{name}: rows must be dense")
 
 
 class _On:
-    """Runs a call on a tensor's device and on `stream`: allocations inside
-    belong to that stream, `handle` is its raw handle."""
+    """A call's device and stream as a context: allocations inside belong to
+    that stream, `handle` is its raw handle."""
 
-    def __init__(self, device, stream):
-        import torch
+    def __init__(self, index, stream):
         if stream is None:
-            self.stream = None
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        elif isinstance(stream, int):
-            self.stream = torch.cuda.ExternalStream(stream, device=device)
-            self.handle = stream
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors "
-                                 f"are on {device}")
-            self.stream, self.handle = stream, stream.cuda_stream
-        if self.stream is not None:
-            self.context = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != device.index:
-            self.context = torch.cuda.device(device)
-        else:
-            self.context = None
+            self.context = _torch.cuda.device(index)
+            self.handle = _torch.cuda.current_stream(index).cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = _torch.cuda.ExternalStream(stream, device=index)
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors are "
+                             f"on cuda:{index}")
+        self.context = _torch.cuda.stream(stream)
+        self.handle = stream.cuda_stream
 
     def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
+        self.context.__enter__()
         return self.handle
 
     def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
-        return False
+        return self.context.__exit__(*exc)
+
+
+def _here(index, stream):
+    """The raw handle of the current stream where the call needs no other
+    device or stream than the current ones, else None."""
+    if stream is None and _torch._C._cuda_getDevice() == index:
+        return _torch._C._cuda_getCurrentRawStream(index)
+    return None
 
 
 # ---- rotary positions -------------------------------------------------------
@@ -312,44 +381,46 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, freqs=None,
         factor if scale is None else float(scale), rotary_dim)
 
 
-def _rotary_call(q, k, positions, freqs, interleaved, eps):
-    """The parts that forward and backward share; q and k are the tensors
-    whose heads are turned."""
-    import torch
-    dt = _dtype_id(_heads_view(q, "q"), "q")
-    tokens, _, dim = q.shape
-    if k is not None:
-        _heads_view(k, "k", q.dtype, (tokens, None, dim), q)
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"positions must be int32 or int64, got "
-                        f"{positions.dtype}")
-    c = MtRotaryCall()
-    c.positions = _dense(positions, "positions", positions.dtype, (tokens,),
-                         q)
-    c.turns = _dense(freqs.turns, "freqs", torch.int64,
-                     (freqs.rotary_dim // 2,), q)
-    c.tokens, c.dim, c.rotary_dim = tokens, dim, freqs.rotary_dim
-    c.position_bytes = 8 if positions.dtype == torch.int64 else 4
-    c.interleaved, c.scale = bool(interleaved), freqs.scale
-    c.norm, c.eps = eps is not None, 0.0 if eps is None else eps
-    return dt, c
+_ABSENT = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
 
 
-def _out_pair(out, q, k):
+def _tail(positions, freqs, tokens, dim, interleaved, eps, index):
+    """The fields of mt_rotary_call_t behind the heads."""
+    pt = getattr(positions, "dtype", None)
+    if pt is _torch.int64:
+        size = 8
+    elif pt is _torch.int32:
+        size = 4
+    else:
+        raise TypeError(f"positions must be int32 or int64, got {pt}")
+    turns, scale, rotary_dim = freqs
+    return (_dense(positions, "positions", pt, (tokens,), index),
+            _dense(turns, "freqs", _torch.int64, (rotary_dim >> 1,), index),
+            tokens, size, dim, rotary_dim, 1 if interleaved else 0,
+            0 if eps is None else 1, 0.0 if eps is None else eps, scale, 0)
+
+
+def _three(t, name):
+    sh = t.shape
+    if len(sh) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim]")
+    return sh
+
+
+def _out_pair(out, alone):
     if out is None:
         return None, None
-    if k is None and not isinstance(out, (tuple, list)):
+    if alone and not isinstance(out, (tuple, list)):
         return out, None
-    yq, yk = out
-    return yq, yk
+    return out
 
 
-def _weight(w, name, q, eps):
+def _weight(w, name, dtype, dim, eps, index):
     if w is None:
-        return None
+        return 0
     if eps is None:
         raise ValueError(f"{name} belongs to the norm: give eps")
-    return _dense(w, name, q.dtype, (q.shape[2],), q)
+    return _dense(w, name, dtype, (dim,), index)
 
 
 def rotary(q, k, positions, freqs, interleaved=False, q_weight=None,
@@ -361,30 +432,43 @@ def rotary(q, k, positions, freqs, interleaved=False, q_weight=None,
     multiplied by q_weight or k_weight (None: ones).  out: (q, k) to write to;
     the inputs themselves turn them in place.  Returns (q, k), or q alone
     where k is None."""
-    import torch
-    dt, c = _rotary_call(q, k, positions, freqs, interleaved, eps)
-    if k is None and k_weight is not None:
+    dt, index = _first(q, "q")
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return _rotary(dt, index, handle, q, k, positions, freqs,
+                           interleaved, q_weight, k_weight, eps, out)
+    return _rotary(dt, index, handle, q, k, positions, freqs, interleaved,
+                   q_weight, k_weight, eps, out)
+
+
+def _rotary(dt, index, handle, q, k, positions, freqs, interleaved, q_weight,
+            k_weight, eps, out):
+    dtype, shape = q.dtype, _three(q, "q")
+    tokens, q_heads, dim = shape
+    tail = _tail(positions, freqs, tokens, dim, interleaved, eps, index)
+    x, xt, xh = _heads(q, "q", dtype, shape, index)
+    w = _weight(q_weight, "q_weight", dtype, dim, eps, index)
+    yq, yk = _out_pair(out, k is None)
+    if k is not None:
+        k_shape = (tokens, _three(k, "k")[1], dim)
+        kx, kxt, kxh = _heads(k, "k", dtype, k_shape, index)
+        kw = _weight(k_weight, "k_weight", dtype, dim, eps, index)
+    elif k_weight is not None:
         raise ValueError("k_weight without k")
-    yq, yk = _out_pair(out, q, k)
-    with _On(q.device, stream) as handle:
-        for t, y, w, h, name in ((q, yq, q_weight, c.q, "q"),
-                                 (k, yk, k_weight, c.k, "k")):
-            if t is None:
-                continue
-            if y is None:
-                y = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                if name == "q":
-                    yq = y
-                else:
-                    yk = y
-            else:
-                _heads_view(y, f"out ({name})", t.dtype, t.shape, q)
-            h.x, h.y = t.data_ptr(), y.data_ptr()
-            h.weight = _weight(w, f"{name}_weight", q, eps)
-            h.x_token, h.x_head = t.stride(0), t.stride(1)
-            h.y_token, h.y_head = y.stride(0), y.stride(1)
-            h.heads = t.shape[1]
-        mt_rotary(dt, c, handle)
+    if yq is None:
+        yq = _torch.empty(shape, dtype=dtype, device=q.device)
+    y, yt, yh = _heads(yq, "out (q)", dtype, shape, index)
+    if k is None:
+        keys = _ABSENT
+    else:
+        if yk is None:
+            yk = _torch.empty(k_shape, dtype=dtype, device=q.device)
+        ky, kyt, kyh = _heads(yk, "out (k)", dtype, k_shape, index)
+        keys = (kx, 0, ky, kw, 0, kxt, kxh, 0, 0, kyt, kyh, k_shape[1], 0)
+    _call("mt_rotary", dt,
+          _ROTARY.pack(x, 0, y, w, 0, xt, xh, 0, 0, yt, yh, q_heads, 0,
+                       *keys, *tail), handle)
     return yq if k is None else (yq, yk)
 
 
@@ -396,50 +480,61 @@ def rotary_backward(dq, dk, positions, freqs, interleaved=False, q=None,
     Returns (dq, dk) of the inputs, with eps (dq, dk, dq_weight, dk_weight),
     the weights' in FP32 (None where there is no weight).  out: (dq, dk) to
     write to; they may be dq and dk themselves."""
-    import torch
-    dt, c = _rotary_call(dq, dk, positions, freqs, interleaved, eps)
-    norm = eps is not None
-    if not norm and (q is not None or k is not None):
+    dt, index = _first(dq, "dq")
+    if eps is None and (q is not None or k is not None):
         raise ValueError("q and k belong to the norm: give eps")
     if dk is None and (k is not None or k_weight is not None):
         raise ValueError("k without dk")
-    gq, gk = _out_pair(out, dq, dk)
-    dws = [None, None]
-    with _On(dq.device, stream) as handle:
-        for i, (g, x, y, w, h, name) in enumerate(
-                ((dq, q, gq, q_weight, c.q, "q"),
-                 (dk, k, gk, k_weight, c.k, "k"))):
-            if g is None:
-                continue
-            if y is None:
-                y = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-                if i == 0:
-                    gq = y
-                else:
-                    gk = y
-            else:
-                _heads_view(y, f"out ({name})", g.dtype, g.shape, dq)
-            if norm:
-                if x is None:
-                    raise ValueError(f"the norm's backward pass needs {name}")
-                _heads_view(x, name, g.dtype, g.shape, dq)
-                h.x, h.x_token, h.x_head = (x.data_ptr(), x.stride(0),
-                                            x.stride(1))
-            h.weight = _weight(w, f"{name}_weight", dq, eps)
-            if w is not None:
-                dws[i] = torch.empty(g.shape[2], dtype=torch.float32,
-                                     device=g.device)
-                h.dweight = dws[i].data_ptr()
-            h.dy, h.y = g.data_ptr(), y.data_ptr()
-            h.dy_token, h.dy_head = g.stride(0), g.stride(1)
-            h.y_token, h.y_head = y.stride(0), y.stride(1)
-            h.heads = g.shape[1]
-        n = mt_rotary_backward_workspace(c)
-        ws = torch.empty(n, dtype=torch.uint8, device=dq.device) if n else None
-        mt_rotary_backward(dt, c, ws.data_ptr() if n else None, n, handle)
-    if norm:
-        return gq, gk, dws[0], dws[1]
-    return gq, gk
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return _rotary_backward(dt, index, handle, dq, dk, positions,
+                                    freqs, interleaved, q, k, q_weight,
+                                    k_weight, eps, out)
+    return _rotary_backward(dt, index, handle, dq, dk, positions, freqs,
+                            interleaved, q, k, q_weight, k_weight, eps, out)
+
+
+def _gradients(name, g, x, y, w, tokens, dim, dtype, eps, index):
+    """One tensor of a backward call: its fields, its gradient and its
+    weight's."""
+    shape = (tokens, _three(g, "d" + name)[1], dim)
+    d, dt_, dh = _heads(g, "d" + name, dtype, shape, index)
+    px = xt = xh = 0
+    if eps is not None:
+        if x is None:
+            raise ValueError(f"the norm's backward pass needs {name}")
+        px, xt, xh = _heads(x, name, dtype, shape, index)
+    pw, dw, pdw = _weight(w, name + "_weight", dtype, dim, eps, index), None, 0
+    if y is None:
+        y = _torch.empty(shape, dtype=dtype, device=g.device)
+    py, yt, yh = _heads(y, f"out ({name})", dtype, shape, index)
+    if w is not None:
+        dw = _torch.empty(dim, dtype=_torch.float32, device=g.device)
+        pdw = dw.data_ptr()
+    return (px, d, py, pw, pdw, xt, xh, dt_, dh, yt, yh, shape[1], 0), y, dw
+
+
+def _rotary_backward(dt, index, handle, dq, dk, positions, freqs, interleaved,
+                     q, k, q_weight, k_weight, eps, out):
+    dtype = dq.dtype
+    tokens, _, dim = _three(dq, "dq")
+    tail = _tail(positions, freqs, tokens, dim, interleaved, eps, index)
+    gq, gk = _out_pair(out, dk is None)
+    queries, gq, wq = _gradients("q", dq, q, gq, q_weight, tokens, dim, dtype,
+                                 eps, index)
+    keys, wk = _ABSENT, None
+    if dk is not None:
+        keys, gk, wk = _gradients("k", dk, k, gk, k_weight, tokens, dim,
+                                  dtype, eps, index)
+    call = _ROTARY.pack(*queries, *keys, *tail)
+    n, address = 0, None
+    if wq is not None or wk is not None:
+        n = mt_rotary_backward_workspace(MtRotaryCall.from_buffer_copy(call))
+        workspace = _torch.empty(n, dtype=_torch.uint8, device=dq.device)
+        address = workspace.data_ptr()
+    _call("mt_rotary_backward", dt, call, address, n, handle)
+    return (gq, gk) if eps is None else (gq, gk, wq, wk)
 
 
 # ---- quantised cache --------------------------------------------------------
@@ -460,35 +555,40 @@ def cache_alloc(slots, heads, dim, group=None, format="e4m3", device="cuda"):
                               dtype=torch.float32, device=device)
 
 
-def _cache_call(k_cache, v_cache, slots, dt_like):
-    import torch
-    codes, scales = k_cache
-    _tensor(codes, "k_cache codes", like=dt_like)
-    formats = {torch.float8_e4m3fn: MT_CACHE_E4M3, torch.int8: MT_CACHE_INT8}
-    if codes.dtype not in formats:
+_FORMATS = {}
+
+
+def _cache(cache, name, like, index):
+    """(codes' address, scales' address, their shapes) of one cache tensor;
+    `like`: the shapes that it has to have, or None."""
+    if not _FORMATS:
+        _FORMATS.update({_torch.float8_e4m3fn: MT_CACHE_E4M3,
+                         _torch.int8: MT_CACHE_INT8})
+    codes, scales = cache
+    if like is not None:
+        return (_dense(codes, name + " codes", like[0], like[1], index),
+                _dense(scales, name + " scales", _torch.float32, like[2],
+                       index), like)
+    _tensor(codes, name + " codes")
+    if codes.dtype not in _FORMATS:
         raise TypeError(f"cache codes must be float8_e4m3fn or int8, got "
                         f"{codes.dtype}")
-    if codes.dim() != 3 or scales.dim() != 3:
+    cs, ss = codes.shape, getattr(scales, "shape", ())
+    if len(cs) != 3 or len(ss) != 3:
         raise ValueError("a cache is (codes [slots, heads, dim], scales "
                          "[slots, heads, dim/group])")
-    n, heads, dim = codes.shape
-    groups = scales.shape[2]
-    if groups < 1 or dim % groups:
-        raise ValueError(f"{groups} scales per head do not divide dim {dim}")
-    c = MtCacheCall()
-    c.format = formats[codes.dtype]
-    c.slots, c.heads, c.dim, c.group = n, heads, dim, dim // groups
-    c.tokens = slots.shape[0] if slots.dim() == 1 else 0
-    c.slot = _dense(slots, "slots", torch.int64, (c.tokens,), codes)
-    for name, cache, rows in (("k_cache", k_cache, c.k),
-                              ("v_cache", v_cache, c.v)):
-        if cache is None:
-            continue
-        rows.codes = _dense(cache[0], f"{name} codes", codes.dtype,
-                            (n, heads, dim), codes)
-        rows.scales = _dense(cache[1], f"{name} scales", torch.float32,
-                             (n, heads, groups), codes)
-    return c
+    if ss[2] < 1 or cs[2] % ss[2]:
+        raise ValueError(f"{ss[2]} scales per head do not divide dim {cs[2]}")
+    return _cache(cache, name, (codes.dtype, cs, (cs[0], cs[1], ss[2])),
+                  codes.get_device() if index is None else index)
+
+
+def _cache_pack(kc, ks, kr, vc, vs, vr, slots, like, tokens, index):
+    (n, heads, dim), groups = like[1], like[2][2]
+    return _CACHE.pack(
+        kc, ks, *kr, vc, vs, *vr,
+        _dense(slots, "slots", _torch.int64, (tokens,), index), tokens, n,
+        heads, dim, dim // groups, _FORMATS[like[0]])
 
 
 def cache_write(k, v, k_cache, v_cache, slots, stream=None):
@@ -497,19 +597,24 @@ def cache_write(k, v, k_cache, v_cache, slots, stream=None):
     slots[token] (int64) of k_cache and v_cache, each (codes, scales) as from
     :func:`cache_alloc`.  A token whose slot is outside the cache (-1: padding)
     stores nothing; the slots inside must differ from one another."""
-    dt = _dtype_id(_heads_view(k, "k"), "k")
+    dt, index = _first(k, "k")
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache come together")
-    c = _cache_call(k_cache, v_cache, slots, k)
-    shape = (c.tokens, c.heads, c.dim)
-    for name, t, rows in (("k", k, c.k), ("v", v, c.v)):
-        if t is None:
-            continue
-        _heads_view(t, name, k.dtype, shape, k)
-        rows.rows = t.data_ptr()
-        rows.token_stride, rows.head_stride = t.stride(0), t.stride(1)
-    with _On(k.device, stream) as handle:
-        mt_cache_write(dt, c, handle)
+    kc, ks, like = _cache(k_cache, "k_cache", None, index)
+    tokens = _three(k, "k")[0]
+    shape = (tokens, like[1][1], like[1][2])
+    kr = _heads(k, "k", k.dtype, shape, index)
+    vc = vs = 0
+    vr = (0, 0, 0)
+    if v is not None:
+        vc, vs, _ = _cache(v_cache, "v_cache", like, index)
+        vr = _heads(v, "v", k.dtype, shape, index)
+    call = _cache_pack(kc, ks, kr, vc, vs, vr, slots, like, tokens, index)
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return _call("mt_cache_write", dt, call, handle)
+    _call("mt_cache_write", dt, call, handle)
 
 
 def cache_read(k_cache, v_cache, slots, dtype=None, out=None, stream=None):
@@ -517,24 +622,47 @@ def cache_read(k_cache, v_cache, slots, dtype=None, out=None, stream=None):
     torch.bfloat16), or k alone where v_cache is None.  out: (k, v) to write
     to, strided views included; the row of a token whose slot is outside the
     cache is left as it was (in a new output: zero)."""
-    import torch
-    c = _cache_call(k_cache, v_cache, slots, k_cache[0])
-    k, v = _out_pair(out, k_cache, v_cache)
-    dtype = dtype or (torch.bfloat16 if k is None else k.dtype)
-    shape, device = (c.tokens, c.heads, c.dim), k_cache[0].device
-    with _On(device, stream) as handle:
-        if k is None:
-            k = torch.zeros(shape, dtype=dtype, device=device)
-        if v_cache is not None and v is None:
-            v = torch.zeros(shape, dtype=dtype, device=device)
-        dt = _dtype_id(k, "out")
-        for name, t, rows in (("out (k)", k, c.k), ("out (v)", v, c.v)):
-            if t is None:
-                continue
-            _heads_view(t, name, dtype, shape, k_cache[0])
-            rows.rows = t.data_ptr()
-            rows.token_stride, rows.head_stride = t.stride(0), t.stride(1)
-        mt_cache_read(dt, c, handle)
+    if _torch is None:
+        _setup()
+    kc, ks, like = _cache(k_cache, "k_cache", None, None)
+    index = k_cache[0].get_device()
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return _cache_read(kc, ks, like, index, handle, k_cache, v_cache,
+                               slots, dtype, out)
+    return _cache_read(kc, ks, like, index, handle, k_cache, v_cache, slots,
+                       dtype, out)
+
+
+def _cache_read(kc, ks, like, index, handle, k_cache, v_cache, slots, dtype,
+                out):
+    k, v = _out_pair(out, v_cache is None)
+    if k is not None:
+        dt, _ = _first(k, "out (k)")
+        dtype = k.dtype if dtype is None else dtype
+    else:
+        dtype = _torch.bfloat16 if dtype is None else dtype
+        dt = _DTYPES.get(dtype)
+        if dt is None:
+            raise TypeError(f"dtype must be float32, float16 or bfloat16, got "
+                            f"{dtype}")
+    _tensor(slots, "slots", _torch.int64, (None,), index)
+    tokens = slots.shape[0]
+    shape = (tokens, like[1][1], like[1][2])
+    if k is None:
+        k = _torch.zeros(shape, dtype=dtype, device=k_cache[0].device)
+    kr = _heads(k, "out (k)", dtype, shape, index)
+    vc = vs = 0
+    vr = (0, 0, 0)
+    if v_cache is not None:
+        vc, vs, _ = _cache(v_cache, "v_cache", like, index)
+        if v is None:
+            v = _torch.zeros(shape, dtype=dtype, device=k_cache[0].device)
+        vr = _heads(v, "out (v)", dtype, shape, index)
+    _call("mt_cache_read", dt,
+          _cache_pack(kc, ks, kr, vc, vs, vr, slots, like, tokens, index),
+          handle)
     return k if v_cache is None else (k, v)
 
 
@@ -546,20 +674,28 @@ def cache_slots(table, offsets, starts, page_size, rows, out=None,
     batch, and positions without a page (a negative entry, past the table),
     get -1.  table [sequences, pages], offsets [sequences+1] and starts
     [sequences] are int32."""
-    import torch
-    _tensor(table, "table", torch.int32)
+    if _torch is None:
+        _setup()
+    i32, i64 = _torch.int32, _torch.int64
+    _tensor(table, "table", i32)
     if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be [sequences, pages] with dense rows")
-    n, pages = table.shape
-    with _On(table.device, stream) as handle:
+    (n, pages), index = table.shape, table.get_device()
+    starts_at = _dense(starts, "starts", i32, (n,), index)
+    offsets_at = _dense(offsets, "offsets", i32, (n + 1,), index)
+
+    def run(handle, out):
         if out is None:
-            out = torch.empty(rows, dtype=torch.int64, device=table.device)
-        mt_cache_slots(
-            table.data_ptr(), table.stride(0), pages,
-            _dense(offsets, "offsets", torch.int32, (n + 1,), table),
-            _dense(starts, "starts", torch.int32, (n,), table), n, page_size,
-            rows, _dense(out, "out", torch.int64, (rows,), table), handle)
-    return out
+            out = _torch.empty(rows, dtype=i64, device=table.device)
+        mt_cache_slots(table.data_ptr(), table.stride(0), pages, offsets_at,
+                       starts_at, n, page_size, rows,
+                       _dense(out, "out", i64, (rows,), index), handle)
+        return out
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return run(handle, out)
+    return run(handle, out)
 
 
 # ---- logits -----------------------------------------------------------------
@@ -586,72 +722,65 @@ def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None,
     mode: "logits", "softmax" or "log_softmax"; a row of which the mask leaves
     nothing has probabilities 0 and log-probabilities -inf.  out may be
     logits."""
-    import torch
+    dt, index = _first(logits, "logits")
+    dtype = logits.dtype
     _tensor(logits, "logits", shape=(None, None))
-    dt = _dtype_id(logits, "logits")
-    rows, vocab = logits.shape
-    if vocab > 1 and logits.stride(1) != 1:
-        raise ValueError("logits: rows must be dense")
-    if mode not in _MODES:
+    x, x_stride, vocab = _rows(logits, "logits", dtype, logits.shape[0], index)
+    rows = logits.shape[0]
+    kind = _MODES.get(mode)
+    if kind is None:
         raise ValueError(f"mode must be one of {sorted(_MODES)}, got {mode!r}")
-    f32, i32 = torch.float32, torch.int32
-    c = MtLogitsCall()
-    c.rows, c.vocab, c.mode = rows, vocab, _MODES[mode]
-    c.x, c.x_stride = logits.data_ptr(), logits.stride(0)
+    f32, i32 = _torch.float32, _torch.int32
+    each = (rows,)
+    ids = ids_stride = history = count = 0
+    lens = prompts = rep = freq = pres = 0
     if tokens is not None:
-        _tensor(tokens, "tokens", i32, (rows, None), logits)
-        if tokens.shape[1] > 1 and tokens.stride(1) != 1:
-            raise ValueError("tokens: rows must be dense")
-        if tokens.shape[1] > 0:
-            c.tokens, c.history = tokens.data_ptr(), tokens.shape[1]
-            c.tokens_stride = tokens.stride(0)
-            if lengths is not None:
-                c.lengths = _dense(lengths, "lengths", i32, (rows,), logits)
-            if prompt_lengths is not None:
-                c.prompt_lengths = _dense(prompt_lengths, "prompt_lengths",
-                                          i32, (rows,), logits)
-            if repetition is not None:
-                c.repetition = _dense(repetition, "repetition", f32, (rows,),
-                                      logits)
-            if frequency is not None:
-                c.frequency = _dense(frequency, "frequency", f32, (rows,),
-                                     logits)
-            if presence is not None:
-                c.presence = _dense(presence, "presence", f32, (rows,),
-                                    logits)
+        ids, ids_stride, history = _rows(tokens, "tokens", i32, rows, index)
+        lens = _opt(lengths, "lengths", i32, each, index)
+        prompts = _opt(prompt_lengths, "prompt_lengths", i32, each, index)
+        rep = _opt(repetition, "repetition", f32, each, index)
+        freq = _opt(frequency, "frequency", f32, each, index)
+        pres = _opt(presence, "presence", f32, each, index)
+        if history == 0:
+            ids = lens = prompts = rep = freq = pres = 0
     elif not (lengths is prompt_lengths is repetition is frequency is
               presence is None):
         raise ValueError("lengths and penalties need tokens")
-    if (bias is None) != (bias_ids is None):
-        raise ValueError("bias and bias_ids come together")
-    if bias is not None:
-        c.bias_ids = _dense(bias_ids, "bias_ids", i32, (rows, None), logits)
-        c.biases = bias_ids.shape[1]
-        c.bias = _dense(bias, "bias", f32, (rows, c.biases), logits)
+    b_ids = b = 0
+    if bias is not None or bias_ids is not None:
+        if bias is None or bias_ids is None:
+            raise ValueError("bias and bias_ids come together")
+        _tensor(bias_ids, "bias_ids", i32, (rows, None), index)
+        count = bias_ids.shape[1]
+        b_ids = _dense(bias_ids, "bias_ids", i32, (rows, count), index)
+        b = _dense(bias, "bias", f32, (rows, count), index)
+    m = m_stride = 0
     if mask is not None:
-        _tensor(mask, "mask", i32, None, logits)
-        if mask.dim() not in (1, 2) or (mask.dim() == 2 and
-                                        mask.shape[0] != rows):
-            raise ValueError(f"mask must be [{rows}, words] or [words], got "
-                             f"{tuple(mask.shape)}")
-        if mask.shape[-1] < (vocab + 31) // 32:
-            raise ValueError(f"mask needs {(vocab + 31) // 32} words per row, "
-                             f"got {mask.shape[-1]}")
-        if mask.shape[-1] > 1 and mask.stride(-1) != 1:
-            raise ValueError("mask: rows must be dense")
-        c.mask = mask.data_ptr()
-        c.mask_stride = mask.stride(0) if mask.dim() == 2 and rows > 1 else 0
-    if temperature is not None:
-        c.temperature = _dense(temperature, "temperature", f32, (rows,),
-                               logits)
-    with _On(logits.device, stream) as handle:
+        if mask.dim() == 1:
+            mask = mask[None].expand(rows, -1)
+        m, m_stride, words = _rows(mask, "mask", i32, rows, index)
+        if words < (vocab + 31) >> 5:
+            raise ValueError(f"mask needs {(vocab + 31) >> 5} words per row, "
+                             f"got {words}")
+        if rows == 1:
+            m_stride = 0
+    temp = _opt(temperature, "temperature", f32, each, index)
+
+    def run(handle, out):
         if out is None:
-            out = torch.empty(logits.shape, dtype=logits.dtype,
-                              device=logits.device)
-        else:
-            _tensor(out, "out", logits.dtype, logits.shape, logits)
-            if vocab > 1 and out.stride(1) != 1:
-                raise ValueError("out: rows must be dense")
-        c.y, c.y_stride = out.data_ptr(), out.stride(0)
-        mt_process_logits(dt, c, handle)
-    return out
+            out = _torch.empty(logits.shape, dtype=dtype,
+                               device=logits.device)
+        y, y_stride, width = _rows(out, "out", dtype, rows, index)
+        if width != vocab:
+            raise ValueError(f"out must have shape {tuple(logits.shape)}, got "
+                             f"{tuple(out.shape)}")
+        _call("mt_process_logits", dt,
+              _LOGITS.pack(x, y, rows, x_stride, y_stride, vocab, kind, ids,
+                           ids_stride, history, count, lens, prompts, rep,
+                           freq, pres, b_ids, b, m, m_stride, temp), handle)
+        return out
+    handle = _here(index, stream)
+    if handle is None:
+        with _On(index, stream) as handle:
+            return run(handle, out)
+    return run(handle, out)

@@ -60,6 +60,68 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// N values at a time, in pairs where there are pairs: o = a b + c, o = a b.
+template <int N>
+__device__ __forceinline__ void fma_n(float *o, const float *a,
+                                      const float *b, const float *c) {
+    if constexpr (N == 1) {
+        o[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 v = fma2(make_float2(a[i], a[i + 1]),
+                                  make_float2(b[i], b[i + 1]),
+                                  make_float2(c[i], c[i + 1]));
+            o[i] = v.x;
+            o[i + 1] = v.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void mul_n(float *o, const float *a,
+                                      const float *b) {
+    if constexpr (N == 1) {
+        o[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 v = mul2(make_float2(a[i], a[i + 1]),
+                                  make_float2(b[i], b[i + 1]));
+            o[i] = v.x;
+            o[i + 1] = v.y;
+        }
+    }
+}
+// o = s a and o = s a + c for one factor s.
+template <int N>
+__device__ __forceinline__ void scale_n(float *o, const float *a, float s) {
+    if constexpr (N == 1) {
+        o[0] = a[0] * s;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 v = mul2(make_float2(a[i], a[i + 1]), both(s));
+            o[i] = v.x;
+            o[i + 1] = v.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void scale_add_n(float *o, const float *a, float s,
+                                            const float *c) {
+    if constexpr (N == 1) {
+        o[0] = fmaf(a[0], s, c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 v = fma2(make_float2(a[i], a[i + 1]), both(s),
+                                  make_float2(c[i], c[i + 1]));
+            o[i] = v.x;
+            o[i + 1] = v.y;
+        }
+    }
+}
+
 // V values of T as they lie in memory (aligned to V*sizeof(T) bytes): loads
 // can be issued long before their values are widened.
 template <typename T, int V>
@@ -78,6 +140,17 @@ struct Raw {
             w[0] = *reinterpret_cast<const unsigned *>(p);
         } else {
             w[0] = *reinterpret_cast<const unsigned short *>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (kWords == 4) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if constexpr (kWords == 2) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (kBytes == 4) {
+            *reinterpret_cast<unsigned *>(p) = w[0];
+        } else {
+            *reinterpret_cast<unsigned short *>(p) = (unsigned short)w[0];
         }
     }
     __device__ __forceinline__ void zero() {

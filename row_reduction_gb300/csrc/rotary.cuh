@@ -22,65 +22,91 @@
 // of 2^-65 turns grows to 2^-34 turns at position 2^31).  Its top 32 bits,
 // taken as signed, give the angle in [-pi, pi) to 2^-33 turns, and their
 // conversion to FP32 rounds at 2^-25 of half a turn: 1e-7 radians, whatever
-// the position.
+// the position.  FP32 storage then takes sincospif (2 ulp).  For 16-bit
+// storage __sinf and __cosf are enough: on [-pi, pi] they are off by at most
+// 2^-21.4 and 2^-21.2, with the angle's three roundings 1e-6 in all, where the
+// output's own rounding is up to 2^-12 (FP16) or 2^-9 (BF16); sincospif there
+// costs as much as the rest of a token.
 #pragma once
 
 #include "mt_decoder.cuh"
 
 namespace mt {
 
-template <typename T, int V, int K, bool ILV>
-struct RotSlots {
-    // Offsets of the two packs of slot j.
-    static __device__ __forceinline__ void offsets(const RotArgs &a, int j,
-                                                   int &lo, int &hi) {
-        if (ILV || j >= a.rot_slots) {
-            lo = 2 * j * V;
-            hi = lo + V;
+// A lane's slot: where its two packs are, and its values as V first and V
+// second members of pairs (a, b).
+template <typename T, int V, bool ILV>
+struct RotSlot {
+    int lo, hi;    // offsets of the packs
+    bool in;       // the head has such a slot
+    bool rot;      // ... and its pairs are turned
+    bool second;   // the second pack exists (not in an odd head's last slot)
+
+    __device__ __forceinline__ RotSlot(const RotArgs &a, int j) {
+        in = j < a.slots;
+        rot = j < a.rot_slots;
+        lo = ILV || !rot ? 2 * j * V : j * V;
+        hi = ILV || !rot ? lo + V : a.pairs + j * V;
+        second = V > 1 || hi < a.dim;
+    }
+    struct Packs {
+        Raw<T, V> lo, hi;
+    };
+    __device__ __forceinline__ void load(const T *p, bool there,
+                                         Packs &r) const {
+        r.lo.zero();
+        r.hi.zero();
+        if (there && in) {
+            r.lo.load(p + lo);
+            if (second) r.hi.load(p + hi);
+        }
+    }
+    static __device__ __forceinline__ void split(const Packs &r, float *a,
+                                                 float *b) {
+        if (!ILV) {
+            r.lo.widen(a);
+            r.hi.widen(b);
         } else {
-            lo = j * V;
-            hi = a.pairs + j * V;
-        }
-    }
-    static __device__ __forceinline__ void load(const RotArgs &a, const T *p,
-                                                int j, float *z) {
-        int lo, hi;
-        offsets(a, j, lo, hi);
-        ld_vec<T, V>(p + lo, z);
-        if (V > 1 || hi < a.dim)
-            ld_vec<T, V>(p + hi, z + V);
-        else
-            z[V] = 0.f;  // an odd head's last value has no partner
-    }
-    static __device__ __forceinline__ void store(const RotArgs &a, T *p,
-                                                 int j, const float *z) {
-        int lo, hi;
-        offsets(a, j, lo, hi);
-        st_vec<T, V>(p + lo, z);
-        if (V > 1 || hi < a.dim) st_vec<T, V>(p + hi, z + V);
-    }
-    static __device__ __forceinline__ void weights(const RotArgs &a,
-                                                   const T *w, int j,
-                                                   float *z) {
-        if (w == nullptr) {
+            float z[2 * V];
+            r.lo.widen(z);
+            r.hi.widen(z + V);
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) z[e] = 1.f;
-            return;
+            for (int e = 0; e < V; ++e) {
+                a[e] = z[2 * e];
+                b[e] = z[2 * e + 1];
+            }
         }
-        int lo, hi;
-        offsets(a, j, lo, hi);
-        ld_vec<T, V, true>(w + lo, z);
-        if (V > 1 || hi < a.dim)
-            ld_vec<T, V, true>(w + hi, z + V);
-        else
-            z[V] = 0.f;
     }
-    // s cos and s sin of the slot's pairs at position p (1 and 0 for a slot
-    // that is not rotated).
-    static __device__ __forceinline__ void angles(const RotArgs &a,
-                                                  int64_t pos, int j,
-                                                  float *c, float *s) {
-        const bool rot = j < a.rot_slots;
+    __device__ __forceinline__ void store(T *p, const float *a,
+                                          const float *b) const {
+        if (!ILV) {
+            st_vec<T, V>(p + lo, a);
+            if (second) st_vec<T, V>(p + hi, b);
+        } else {
+            float z[2 * V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                z[2 * e] = a[e];
+                z[2 * e + 1] = b[e];
+            }
+            st_vec<T, V>(p + lo, z);
+            if (second) st_vec<T, V>(p + hi, z + V);
+        }
+    }
+    __device__ __forceinline__ void weights(const T *w, float *a,
+                                            float *b) const {
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[e] = b[e] = 1.f;
+        if (w != nullptr && in) {
+            Packs r;
+            load(w, true, r);
+            split(r, a, b);
+        }
+    }
+    // s cos and s sin of the slot's pairs at position p; 1 and 0 for a slot
+    // that is not turned.
+    __device__ __forceinline__ void angles(const RotArgs &a, int64_t pos,
+                                           int j, float *c, float *s) const {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             c[e] = 1.f;
@@ -91,23 +117,20 @@ struct RotSlots {
                     __ldg(reinterpret_cast<const unsigned long long *>(
                               a.turns) +
                           j * V + e);
-                const float half_turns =
-                    (float)(int32_t)(t >> 32) * 4.6566128730773926e-10f;
+                const float turned = (float)(int32_t)(t >> 32);
                 float sn, cs;
-                sincospif(half_turns, &sn, &cs);
+                if (sizeof(T) == 4) {
+                    // half turns, in [-1, 1)
+                    sincospif(turned * 4.6566128730773926e-10f, &sn, &cs);
+                } else {
+                    // radians, in [-pi, pi)
+                    const float x = turned * 1.4629180792671596e-09f;
+                    sn = __sinf(x);
+                    cs = __cosf(x);
+                }
                 c[e] = cs * a.scale;
                 s[e] = sn * a.scale * a.sign;
             }
-        }
-    }
-    static __device__ __forceinline__ void turn(float *z, const float *c,
-                                                const float *s) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int ia = ILV ? 2 * e : e, ib = ILV ? 2 * e + 1 : V + e;
-            const float x = z[ia], y = z[ib];
-            z[ia] = x * c[e] - y * s[e];
-            z[ib] = x * s[e] + y * c[e];
         }
     }
 };
@@ -124,11 +147,16 @@ __device__ __forceinline__ float head_sum(float v, int log2L) {
     return v;
 }
 
+// Forward (and, with the sines' sign turned, backward without norm).  The
+// loads of U groups of heads are issued before the angles are computed and
+// before any of them is used.  With the norm, weights and rotation become
+// four coefficients per pair, once per token and tensor:
+//     y_a = r (a k1 + b k2),  y_b = r (a k3 + b k4).
 template <typename T, int V, int K, bool ILV, bool NORM>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, 2)
     rotary_kernel(const RotArgs a) {
-    using S = RotSlots<T, V, K, ILV>;
-    constexpr int U = K == 1 ? 2 : 1;  // groups of heads in flight
+    using S = RotSlot<T, V, ILV>;
+    constexpr int U = K == 1 ? 4 : (K == 2 ? 2 : 1);
     grid_launch_dependents();
     grid_wait_prerequisites();
     const int lane = threadIdx.x & 31;
@@ -139,68 +167,113 @@ __global__ void __launch_bounds__(kRotThreads)
                          (threadIdx.x >> 5);
     const int64_t t = unit >> a.log2S;
     if (t >= a.tokens) return;  // whole warps
-    const int S_ = 1 << a.log2S;
-    const int first = (int)(unit & (S_ - 1));
+    const int split = 1 << a.log2S;
+    const int first = (int)(unit & (split - 1));
     const int64_t pos = rot_position(a, t);
+    typename S::Packs raw[U][K];
+    // The warps of a token take its groups of heads in turn; the key heads'
+    // groups follow the query heads'.
+    const int first_k = (first - a.t[0].groups) & (split - 1);
+    bool loaded = false;
+    {
+        const RotHeads &h = a.t[0];
+        const T *x = static_cast<const T *>(h.x) + t * h.xt;
+        if (first < h.groups) {
+            loaded = true;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int head = (first + u * split) * heads_per_warp + sub;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    S(a, l + k * L).load(x + head * h.xh, head < h.heads,
+                                         raw[u][k]);
+            }
+        }
+    }
     float c[K][V], s[K][V];
 #pragma unroll
-    for (int k = 0; k < K; ++k) S::angles(a, pos, l + k * L, c[k], s[k]);
+    for (int k = 0; k < K; ++k)
+        S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const RotHeads &h = a.t[i];
-        if (h.heads == 0) continue;
+        const int g0 = i == 0 ? first : first_k;
+        if (g0 >= h.groups) continue;
         const T *x = static_cast<const T *>(h.x) + t * h.xt;
         T *y = static_cast<T *>(h.y) + t * h.yt;
-        float w[NORM ? K : 1][2 * V];
-        if (NORM) {
+        float k1[K][V], k2[K][V], k3[K][V], k4[K][V];
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (l + k * L < a.slots)
-                    S::weights(a, static_cast<const T *>(h.w), l + k * L,
-                               w[k]);
+        for (int k = 0; k < K; ++k) {
+            float wa[V], wb[V];
+            if (NORM)
+                S(a, l + k * L).weights(static_cast<const T *>(h.w), wa, wb);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                k1[k][e] = NORM ? wa[e] * c[k][e] : c[k][e];
+                k2[k][e] = NORM ? -wb[e] * s[k][e] : -s[k][e];
+                k3[k][e] = NORM ? wa[e] * s[k][e] : s[k][e];
+                k4[k][e] = NORM ? wb[e] * c[k][e] : c[k][e];
+            }
         }
-        // The warps of a token take its groups of heads in turn; the key
-        // heads' groups follow the query heads'.
-        const int g0 = i == 0 ? first : (first - a.t[0].groups) & (S_ - 1);
-        for (int g = g0; g < h.groups; g += U * S_) {
-            float z[U][K][2 * V];
-            bool in[U][K];
+#pragma unroll 1
+        for (int g = g0; g < h.groups; g += U * split) {
+            if (!(loaded && i == 0 && g == g0)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int head = (g + u * S_) * heads_per_warp + sub;
+                for (int u = 0; u < U; ++u) {
+                    const int head = (g + u * split) * heads_per_warp + sub;
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    in[u][k] = head < h.heads && l + k * L < a.slots;
-                    if (in[u][k])
-                        S::load(a, x + head * h.xh, l + k * L, z[u][k]);
+                    for (int k = 0; k < K; ++k)
+                        S(a, l + k * L).load(x + head * h.xh, head < h.heads,
+                                             raw[u][k]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int head = (g + u * S_) * heads_per_warp + sub;
+                if (g + u * split >= h.groups) break;  // whole warps
+                const int head = (g + u * split) * heads_per_warp + sub;
+                float va[K][V], vb[K][V];
+                float r = 1.f;
                 if (NORM) {
+                    float sq[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sq[e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        S::split(raw[u][k], va[k], vb[k]);
+                        fma_n<V>(sq, va[k], va[k], sq);
+                        fma_n<V>(sq, vb[k], vb[k], sq);
+                    }
                     float ss = 0.f;
 #pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (in[u][k]) {
-#pragma unroll
-                            for (int e = 0; e < 2 * V; ++e)
-                                ss += z[u][k][e] * z[u][k][e];
-                        }
-                    const float r =
-                        rsqrtf(head_sum(ss, a.log2L) * a.inv_dim + a.eps);
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-#pragma unroll
-                        for (int e = 0; e < 2 * V; ++e)
-                            z[u][k][e] *= r * w[k][e];
+                    for (int e = 0; e < V; ++e) ss += sq[e];
+                    r = rsqrtf(head_sum(ss, a.log2L) * a.inv_dim + a.eps);
                 }
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (in[u][k]) {
-                        S::turn(z[u][k], c[k], s[k]);
-                        S::store(a, y + head * h.yh, l + k * L, z[u][k]);
+                for (int k = 0; k < K; ++k) {
+                    const S slot(a, l + k * L);
+                    if (!slot.in || head >= h.heads) continue;
+                    T *out = y + head * h.yh;
+                    if (!NORM) {
+                        if (!slot.rot) {  // copied bit for bit
+                            raw[u][k].lo.store(out + slot.lo);
+                            if (slot.second) raw[u][k].hi.store(out + slot.hi);
+                            continue;
+                        }
+                        S::split(raw[u][k], va[k], vb[k]);
                     }
+                    float oa[V], ob[V];
+                    mul_n<V>(oa, va[k], k1[k]);
+                    mul_n<V>(ob, vb[k], k4[k]);
+                    if (slot.rot) {  // 0 times a neighbour may be NaN
+                        fma_n<V>(oa, vb[k], k2[k], oa);
+                        fma_n<V>(ob, va[k], k3[k], ob);
+                    }
+                    if (NORM) {
+                        scale_n<V>(oa, oa, r);
+                        scale_n<V>(ob, ob, r);
+                    }
+                    slot.store(out, oa, ob);
+                }
             }
         }
     }
@@ -211,10 +284,11 @@ __global__ void __launch_bounds__(kRotThreads)
 // the lanes and warps that own the same slot are added in a fixed order and
 // the CTA writes one row of partial sums, which rotary_dweight_kernel adds.
 template <typename T, int V, int K, bool ILV>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, 2)
     rotary_backward_kernel(const RotArgs a) {
-    using S = RotSlots<T, V, K, ILV>;
+    using S = RotSlot<T, V, ILV>;
     constexpr int kWarps = kRotThreads / 32;
+    constexpr int U = K == 1 ? 2 : 1;
     __shared__ float sums[kWarps][kRotMaxDim];
     grid_launch_dependents();
     grid_wait_prerequisites();
@@ -225,16 +299,16 @@ __global__ void __launch_bounds__(kRotThreads)
     const int i = (int)blockIdx.x < a.blocks[0] ? 0 : 1;
     const int block = (int)blockIdx.x - (i ? a.blocks[0] : 0);
     const RotHeads &h = a.t[i];
-    const int S_ = 1 << a.log2S;
-    float w[K][2 * V], dw[K][2 * V];
+    const int split = 1 << a.log2S;
+    float wa[K][V], wb[K][V], da[K][V], db[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+        S(a, l + k * L).weights(static_cast<const T *>(h.w), wa[k], wb[k]);
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) w[k][e] = dw[k][e] = 0.f;
-        if (l + k * L < a.slots)
-            S::weights(a, static_cast<const T *>(h.w), l + k * L, w[k]);
+        for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.f;
     }
     const int64_t units = a.tokens << a.log2S;
+#pragma unroll 1
     for (int64_t unit = (int64_t)block * kWarps + warp; unit < units;
          unit += (int64_t)a.blocks[i] * kWarps) {
         const int64_t t = unit >> a.log2S;
@@ -242,68 +316,114 @@ __global__ void __launch_bounds__(kRotThreads)
         const T *x = static_cast<const T *>(h.x) + t * h.xt;
         const T *dy = static_cast<const T *>(h.dy) + t * h.dt;
         T *y = static_cast<T *>(h.y) + t * h.yt;
+        const int g0 = (int)(unit & (split - 1));
+        typename S::Packs rx[U][K], rd[U][K];
+        const auto load = [&](int g) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int head = (g + u * split) * heads_per_warp + sub;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const S slot(a, l + k * L);
+                    slot.load(x + head * h.xh, head < h.heads, rx[u][k]);
+                    slot.load(dy + head * h.dh, head < h.heads, rd[u][k]);
+                }
+            }
+        };
+        load(g0);
         float c[K][V], s[K][V];
 #pragma unroll
-        for (int k = 0; k < K; ++k) S::angles(a, pos, l + k * L, c[k], s[k]);
-        for (int g = (int)(unit & (S_ - 1)); g < h.groups; g += S_) {
-            const int head = g * heads_per_warp + sub;
-            float z[K][2 * V], d[K][2 * V];
-            float xx = 0.f, gx = 0.f;
+        for (int k = 0; k < K; ++k)
+            S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
+#pragma unroll 1
+        for (int g = g0; g < h.groups; g += U * split) {
+            if (g != g0) load(g);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (head < h.heads && l + k * L < a.slots) {
-                    S::load(a, x + head * h.xh, l + k * L, z[k]);
-                    S::load(a, dy + head * h.dh, l + k * L, d[k]);
-                } else {
+            for (int u = 0; u < U; ++u) {
+                if (g + u * split >= h.groups) break;  // whole warps
+                const int head = (g + u * split) * heads_per_warp + sub;
+                float xa[K][V], xb[K][V], ga[K][V], gb[K][V];
+                float sq[V], dot[V];
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) z[k][e] = d[k][e] = 0.f;
+                for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const S slot(a, l + k * L);
+                    S::split(rx[u][k], xa[k], xb[k]);
+                    S::split(rd[u][k], ga[k], gb[k]);
+                    if (slot.rot) {
+                        // g = R^T dy: a.sign has turned the sines, so that
+                        // g_a = a c - b s, g_b = a s + b c
+                        float ta[V], tb[V], m[V];
+                        mul_n<V>(ta, ga[k], c[k]);
+                        mul_n<V>(tb, gb[k], c[k]);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) m[e] = -gb[k][e];
+                        fma_n<V>(tb, ga[k], s[k], tb);
+                        fma_n<V>(ga[k], m, s[k], ta);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) gb[k][e] = tb[e];
+                    }
+                    float ta[V], tb[V];
+                    fma_n<V>(sq, xa[k], xa[k], sq);
+                    fma_n<V>(sq, xb[k], xb[k], sq);
+                    mul_n<V>(ta, ga[k], wa[k]);
+                    mul_n<V>(tb, gb[k], wb[k]);
+                    fma_n<V>(dot, ta, xa[k], dot);
+                    fma_n<V>(dot, tb, xb[k], dot);
                 }
-            }
+                float xx = 0.f, gx = 0.f;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                S::turn(d[k], c[k], s[k]);
-#pragma unroll
-                for (int e = 0; e < 2 * V; ++e) {
-                    xx += z[k][e] * z[k][e];
-                    gx += d[k][e] * w[k][e] * z[k][e];
+                for (int e = 0; e < V; ++e) {
+                    xx += sq[e];
+                    gx += dot[e];
                 }
-            }
-            xx = head_sum(xx, a.log2L);
-            gx = head_sum(gx, a.log2L);
-            // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
-            const float r = head < h.heads
-                                ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
-            const float m = gx * a.inv_dim * r * r;
+                xx = head_sum(xx, a.log2L);
+                gx = head_sum(gx, a.log2L);
+                // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
+                const float r = head < h.heads
+                                    ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
+                const float m = -gx * a.inv_dim * r * r;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-#pragma unroll
-                for (int e = 0; e < 2 * V; ++e) {
-                    dw[k][e] += d[k][e] * (z[k][e] * r);
-                    d[k][e] = r * (d[k][e] * w[k][e] - z[k][e] * m);
+                for (int k = 0; k < K; ++k) {
+                    const S slot(a, l + k * L);
+                    // g r: dw += (g r) x, dx = (g r) w - x (m r)
+                    scale_n<V>(ga[k], ga[k], r);
+                    scale_n<V>(gb[k], gb[k], r);
+                    fma_n<V>(da[k], ga[k], xa[k], da[k]);
+                    fma_n<V>(db[k], gb[k], xb[k], db[k]);
+                    if (head < h.heads && slot.in) {
+                        float oa[V], ob[V];
+                        mul_n<V>(oa, ga[k], wa[k]);
+                        mul_n<V>(ob, gb[k], wb[k]);
+                        scale_add_n<V>(oa, xa[k], m * r, oa);
+                        scale_add_n<V>(ob, xb[k], m * r, ob);
+                        slot.store(y + head * h.yh, oa, ob);
+                    }
                 }
-                if (head < h.heads && l + k * L < a.slots)
-                    S::store(a, y + head * h.yh, l + k * L, d[k]);
             }
         }
     }
     if (a.partial == nullptr) return;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+        const S slot(a, l + k * L);
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e)
-            for (int off = L; off < 32; off <<= 1)
-                dw[k][e] += __shfl_xor_sync(kFull, dw[k][e], off);
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (sub == 0 && l + k * L < a.slots) {
-            int lo, hi;
-            S::offsets(a, l + k * L, lo, hi);
+        for (int e = 0; e < V; ++e)
+            for (int off = L; off < 32; off <<= 1) {
+                da[k][e] += __shfl_xor_sync(kFull, da[k][e], off);
+                db[k][e] += __shfl_xor_sync(kFull, db[k][e], off);
+            }
+        if (sub == 0 && slot.in) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                sums[warp][lo + e] = dw[k][e];
-                if (hi + e < a.dim) sums[warp][hi + e] = dw[k][V + e];
+                const int ia = ILV ? slot.lo + 2 * e : slot.lo + e;
+                const int ib = ILV ? slot.lo + 2 * e + 1 : slot.hi + e;
+                sums[warp][ia] = da[k][e];
+                if (ib < a.dim) sums[warp][ib] = db[k][e];
             }
         }
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < a.dim; d += kRotThreads) {
         float v = 0.f;

@@ -72,7 +72,13 @@ def pair_sum(x, rotary_dim, interleaved, scale):
 # Cosine and sine of an angle in turns: the angle is rounded at 2^-25 of half
 # a turn (9.4e-8 radians), sincospif is off by at most 2 ulp of 1 (1.2e-7),
 # and the factor and the two products and the sum round once each.
-ANGLE = 9.4e-8 + 1.2e-7 + 4 * U
+#
+# 16-bit storage takes __sinf and __cosf, off by at most 2^-21.19 on
+# [-pi, pi], of an angle in radians that rounds three times at pi 2^-24.
+def angle_error(dtype):
+    if dtype == torch.float32:
+        return 9.4e-8 + 1.2e-7 + 4 * U
+    return 2.0 ** -21.19 + 3 * math.pi * U + 4 * U
 
 
 def norm64(x, weight, eps):
@@ -91,14 +97,14 @@ NORM = 12 * U + 4 * U + 2 * U
 def rotary_ref(x, positions, freqs, scale, rotary_dim, interleaved, weight,
                eps):
     """(value, FP32 error bound) of the forward pass."""
-    rel = 0.0
+    rel, angle = 0.0, angle_error(x.dtype)
     x = x.double()
     if eps is not None:
         x, _ = norm64(x, weight, eps)
         rel = NORM
     y = rotate(x, positions, freqs, scale, rotary_dim, interleaved)
     mag = pair_sum(x, rotary_dim, interleaved, scale)
-    err = mag * (ANGLE + rel)
+    err = mag * (angle + rel)
     if eps is None:  # values that pass are copied
         err[..., rotary_dim:] = 0.0
     return y, err
@@ -107,10 +113,11 @@ def rotary_ref(x, positions, freqs, scale, rotary_dim, interleaved, weight,
 def rotary_backward_ref(dy, x, positions, freqs, scale, rotary_dim,
                         interleaved, weight, eps):
     """(dx, its bound, dweight, its bound); the last two None without norm."""
+    angle = angle_error(dy.dtype)
     g = rotate(dy, positions, freqs, scale, rotary_dim, interleaved, -1.0)
     mag = pair_sum(dy, rotary_dim, interleaved, scale)
     if eps is None:
-        err = mag * ANGLE
+        err = mag * angle
         err[..., rotary_dim:] = 0.0
         return g, err, None, None
     x = x.double()
@@ -120,15 +127,15 @@ def rotary_backward_ref(dy, x, positions, freqs, scale, rotary_dim,
     m = (g * w * x).mean(-1, keepdim=True) * r * r
     dx = r * (g * w - x * m)
     big = (mag * abs(w) * x.abs()).mean(-1, keepdim=True) * r * r
-    # g: ANGLE; r three times over in the second term; the mean 24 roundings;
+    # g: the angle; r three times over in the second term; the mean 24 roundings;
     # a handful of products.
-    err = r * (mag * abs(w) * (ANGLE + NORM + 4 * U) +
-               x.abs() * big * (ANGLE + 3 * NORM + 30 * U))
+    err = r * (mag * abs(w) * (angle + NORM + 4 * U) +
+               x.abs() * big * (angle + 3 * NORM + 30 * U))
     terms = g * x * r
     count = terms.shape[0] * terms.shape[1]
     # however the rows are added up, at most `count` roundings touch a term
     werr = ((mag * x.abs() * r).sum((0, 1)) *
-            (ANGLE + NORM + 3 * U + count * U))
+            (angle + NORM + 3 * U + count * U))
     return dx, err, terms.sum((0, 1)), werr
 
 

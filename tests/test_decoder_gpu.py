@@ -188,6 +188,26 @@ def test_rotary_non_finite_rows_stay_in_their_heads():
     assert bool((mt.rotary(z, None, pos[:2], tab, eps=1e-6) == 0).all())
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rotary", [(64, 32), (80, 40), (18, 6)])
+def test_rotary_values_that_pass_keep_infinities_and_nan(dim, rotary,
+                                                         interleaved):
+    """A value that is not turned is nobody's partner: infinities and NaN stay
+    in their places there, forward and backward."""
+    q, _, pos, _, _ = rot_inputs(16, 5, 2, 1, dim, torch.bfloat16)
+    q = q.clone()
+    q[1, 0, rotary] = math.inf
+    q[2, 1, dim - 1] = -math.inf
+    q[3, 0, rotary + 1] = math.nan
+    _, _, tab = table(rotary)
+    for y in (mt.rotary(q, None, pos, tab, interleaved=interleaved),
+              mt.rotary_backward(q, None, pos, tab,
+                                 interleaved=interleaved)[0]):
+        assert torch.equal(y[..., rotary:].view(torch.int16),
+                           q[..., rotary:].contiguous().view(torch.int16))
+        assert bool(torch.isfinite(y[..., :rotary]).all())
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("norm", [False, True])
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -259,7 +279,7 @@ def test_rotary_backward_forms():
 
 def test_rotary_backward_matches_differences_of_the_kernel():
     """<dy, f(x + h v) - f(x - h v)> / 2h of the FP32 forward kernel against
-    <dx, v>.  The forward's error is ANGLE + NORM of sqrt(2) times a value of
+    <dx, v>.  The forward's error is that of angle and norm, of sqrt(2) times a value of
     about 1, at most 2e-6 each, summed with random signs over n values of dy
     ~ 1: below 2e-6 sqrt(n) * 4 / h; the third derivative adds h^2 sqrt(n)."""
     n, h = 40 * 4 * 64, 1e-2

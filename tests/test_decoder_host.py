@@ -400,3 +400,31 @@ def test_tensor_functions_refuse_cpu_tensors():
         mt.cache_alloc(4, 3, 16, group=5, device="cpu")
     with pytest.raises(ValueError, match="format"):
         mt.cache_alloc(4, 3, 16, format="int4", device="cpu")
+
+
+def test_packed_structures_match_the_header():
+    for packed, cls in ((dec._ROTARY, dec.MtRotaryCall),
+                        (dec._CACHE, dec.MtCacheCall),
+                        (dec._LOGITS, dec.MtLogitsCall)):
+        assert packed.size == ctypes.sizeof(cls)
+
+        def leaves(c):
+            out = []
+            for name, kind in c._fields_:
+                if issubclass(kind, ctypes.Structure):
+                    out += leaves(kind)
+                else:
+                    out.append(kind)
+            return out
+        kinds = leaves(cls)
+        values = [float(i) if k is ctypes.c_float else i + 1
+                  for i, k in enumerate(kinds)]
+        got = cls.from_buffer_copy(packed.pack(*values))
+
+        def read(c):
+            out = []
+            for name, kind in c._fields_:
+                v = getattr(c, name)
+                out += read(v) if isinstance(v, ctypes.Structure) else [v]
+            return out
+        assert read(got) == values
