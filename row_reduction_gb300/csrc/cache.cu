@@ -98,34 +98,91 @@ struct Map {
     int32_t log2L;    // write: lanes of a group
 };
 
-// Writing: groups of up to 512 values, 8 values (one 16-byte access; two for
-// FP32) P times per lane, L lanes per group: lane l owns the packs l and
-// (P = 2) l + L, so that every access of a warp is contiguous.  N tokens of
-// a lane are in flight.
-constexpr int kV = 8;
-
-template <typename T>
-struct Values8 {
-    static constexpr int kLoads = sizeof(T) == 4 ? 2 : 1;
-    Raw<T, kV / kLoads> raw[kLoads];
+// V values of a row as they lie in memory: 16 (32-byte accesses; one for
+// 16-bit types, two for FP32) or 8 (16-byte ones).
+template <typename T, int V>
+struct Values {
+    static constexpr int kWords = V * (int)sizeof(T) / 4;
+    unsigned w[kWords];
     __device__ __forceinline__ void load(const T *p) {
+        const unsigned *q = reinterpret_cast<const unsigned *>(p);
+        if constexpr (V == 16) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) raw[i].load(p + i * (kV / kLoads));
+            for (int i = 0; i < kWords; i += 8)
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, "
+                             "%7}, [%8];"
+                             : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]),
+                               "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                               "=r"(w[i + 6]), "=r"(w[i + 7])
+                             : "l"(q + i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(q + i);
+                w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+            }
+        }
     }
-    __device__ __forceinline__ void widen(float2 *z) const {
+    // Four values from 4 i on.
+    __device__ __forceinline__ void four(int i, float2 &a, float2 &b) const {
+        float z[4];
+        if constexpr (sizeof(T) == 2) {
+            Pack<T>::unpack(w[2 * i], z);
+            Pack<T>::unpack(w[2 * i + 1], z + 2);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            raw[i].widen(&z[0].x + i * (kV / kLoads));
+            for (int e = 0; e < 4; ++e) z[e] = __uint_as_float(w[4 * i + e]);
+        }
+        a = make_float2(z[0], z[1]);
+        b = make_float2(z[2], z[3]);
+    }
+    // Largest magnitude, as the bits of its type: for floats of one sign the
+    // order of the bits is the order of the values, NaN above infinity.
+    __device__ __forceinline__ unsigned largest() const {
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            m = sizeof(T) == 2 ? __vmaxu2(m, w[i] & 0x7fff7fffu)
+                               : max(m, w[i] & 0x7fffffffu);
+        return sizeof(T) == 2 ? max(m & 0xffffu, m >> 16) : m;
     }
 };
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float2 *z) {
-    st_vec<T, 16 / sizeof(T)>(p, &z[0].x);
-    if (sizeof(T) == 4) st_vec<T, 16 / sizeof(T)>(p + 4, &z[0].x + 4);
+__device__ __forceinline__ float magnitude(unsigned bits) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+    const unsigned short h = (unsigned short)bits;
+    return to_f(*reinterpret_cast<const T *>(&h));
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_values(T *p, const float2 *z) {
+    constexpr int kWords = V * (int)sizeof(T) / 4;
+    constexpr int kPer = Pack<T>::kPerWord;
+    unsigned w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = Pack<T>::pack(&z[0].x + i * kPer);
+    unsigned *q = reinterpret_cast<unsigned *>(p);
+    if constexpr (V == 16) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
+                         "%8};" ::"l"(q + i),
+                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]),
+                         "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
+                         "r"(w[i + 6]), "r"(w[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            *reinterpret_cast<uint4 *>(q + i) =
+                make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
 }
 
-template <typename T, bool INT8, int P, int N>
-__global__ void __launch_bounds__(kMaxThreads)
+// Writing: groups of up to 32 V values, V per lane and L lanes per group.
+// The next token's values are on their way while a token's are reduced and
+// stored.
+template <typename T, bool INT8, int V>
+__global__ void __launch_bounds__(kMaxThreads, 2)
     write_wide_kernel(const CacheArgs a, const Map m) {
     grid_launch_dependents();
     grid_wait_prerequisites();
@@ -139,68 +196,57 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int i = gt >= per_tensor ? 1 : 0;
     const unsigned g = gt - (i ? per_tensor : 0);
     const unsigned head = g / groups;
-    const int l = (int)(u & (unsigned)(L - 1));
-    const bool mine = row < m.rows && gt < per_tensor * (unsigned)a.tensors;
-    const int at0 = l * kV;
-    const T *x = static_cast<const T *>(a.rows[i]) + (int64_t)head * a.hs[i] +
-                 (int64_t)(g - head * groups) * a.group;
+    const int at = (int)(u & (unsigned)(L - 1)) * V;
+    const bool mine = row < m.rows && at < a.group &&
+                      gt < per_tensor * (unsigned)a.tensors;
     const int64_t ts = a.ts[i];
-    // Tokens of this lane: first, first + step, ...; the loop's length is
-    // the same for all lanes of a CTA (the exchanges need whole warps).
     const int64_t step = (int64_t)gridDim.x * m.rows;
-    for (int64_t base = (int64_t)blockIdx.x * m.rows; base < a.tokens;
-         base += step * N) {
-        Values8<T> raw[N][P];
-        int64_t slot[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int64_t t = base + n * step + row;
-            slot[n] = -1;
-            if (mine && t < a.tokens) {
-                slot[n] = a.slot[t];
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    if (at0 + p * L * kV < a.group)
-                        raw[n][p].load(x + t * ts + at0 + p * L * kV);
-            }
+    int64_t base = (int64_t)blockIdx.x * m.rows;  // the CTA's, of each round
+    const T *x = static_cast<const T *>(a.rows[i]) + (int64_t)head * a.hs[i] +
+                 (int64_t)(g - head * groups) * a.group + at +
+                 (base + row) * ts;
+    uint8_t *codes = a.codes[i] + (int64_t)g * a.group + at;
+    float *scales = a.scales[i] + g;
+    Values<T, V> next;
+    int64_t next_slot = -1;
+    bool in = mine && base + row < a.tokens;
+    if (in) {
+        next.load(x);
+        next_slot = a.slot[base + row];
+    }
+    // The loop's length is the same for all lanes of a CTA (the exchanges
+    // need whole warps).
+    for (; base < a.tokens; base += step) {
+        const Values<T, V> v = next;
+        const int64_t slot = in ? next_slot : -1;
+        const bool there = in;
+        x += step * ts;
+        in = mine && base + step + row < a.tokens;
+        if (in) {
+            next.load(x);
+            next_slot = a.slot[base + step + row];
         }
+        unsigned bits = there ? v.largest() : 0u;
+        for (int off = L >> 1; off > 0; off >>= 1)
+            bits = max(bits, __shfl_xor_sync(kFull, bits, off));
+        if (slot < 0 || slot >= a.slots) continue;
+        float inv;
+        bool bad;
+        const float s = group_scale<INT8>(magnitude<T>(bits), inv, bad);
+        unsigned w[V / 4];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            if (base + n * step >= a.tokens) break;  // whole CTAs
-            const bool in = mine && base + n * step + row < a.tokens;
-            float2 z[P][kV / 2];
-            float amax = 0.f;
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                if (in && at0 + p * L * kV < a.group) {
-                    raw[n][p].widen(z[p]);
-#pragma unroll
-                    for (int e = 0; e < kV / 2; ++e)
-                        amax = nanmax(amax, nanmax(fabsf(z[p][e].x),
-                                                   fabsf(z[p][e].y)));
-                }
-            for (int off = L >> 1; off > 0; off >>= 1)
-                amax = nanmax(amax, __shfl_xor_sync(kFull, amax, off));
-            if (!in || slot[n] < 0 || slot[n] >= a.slots) continue;
-            float inv;
-            bool bad;
-            const float s = group_scale<INT8>(amax, inv, bad);
-            const int64_t group = slot[n] * per_tensor + g;
-            uint8_t *c = a.codes[i] + group * a.group + at0;
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                if (at0 + p * L * kV < a.group) {
-                    unsigned w[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        w[h] = bad ? 0u
-                                   : encode4<INT8>(z[p][2 * h],
-                                                   z[p][2 * h + 1], inv);
-                    *reinterpret_cast<uint2 *>(c + p * L * kV) =
-                        make_uint2(w[0], w[1]);
-                }
-            if (l == 0) a.scales[i][group] = s;
+        for (int h = 0; h < V / 4; ++h) {
+            float2 p, q;
+            v.four(h, p, q);
+            w[h] = bad ? 0u : encode4<INT8>(p, q, inv);
         }
+        uint8_t *c = codes + slot * per_tensor * a.group;
+        if constexpr (V == 16)
+            *reinterpret_cast<uint4 *>(c) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(c) = make_uint2(w[0], w[1]);
+        if (at == 0) scales[slot * per_tensor] = s;
     }
 }
 
@@ -238,11 +284,12 @@ __global__ void __launch_bounds__(kThreads)
     if (lane == 0) a.scales[i][group] = s;
 }
 
-// Reading back.  A row's codes are contiguous (heads x dim bytes): 8 of them
-// per lane, the lane's place in the row the same for all its tokens, N tokens
-// in flight.
-template <typename T, bool INT8, int N>
-__global__ void __launch_bounds__(kMaxThreads)
+// Reading back.  A row's codes are contiguous (heads x dim bytes): V of them
+// per lane, the lane's place in the row the same for all its tokens.  N
+// tokens' codes are on their way while N tokens are stored, and the slots of
+// the N after them.
+template <typename T, bool INT8, int V, int N>
+__global__ void __launch_bounds__(kMaxThreads, 2)
     read_wide_kernel(const CacheArgs a, const Map m) {
     grid_launch_dependents();
     grid_wait_prerequisites();
@@ -250,45 +297,68 @@ __global__ void __launch_bounds__(kMaxThreads)
     const unsigned row = unit / m.per;
     const unsigned u = unit - row * m.per;
     const unsigned width = (unsigned)(a.heads * a.dim);
-    const unsigned packs = width / kV;
+    const unsigned packs = width / V;
     const int i = u >= packs ? 1 : 0;
     if (row >= m.rows || u >= packs * (unsigned)a.tensors) return;
-    const unsigned v = (u - (i ? packs : 0)) * kV;
+    const unsigned v = (u - (i ? packs : 0)) * V;
     const unsigned head = v / (unsigned)a.dim;
     const uint8_t *codes = a.codes[i] + v;
     const float *scales = a.scales[i] + v / (unsigned)a.group;
     const unsigned groups = width / (unsigned)a.group;
+    const int64_t ts = a.ts[i];
     T *y = static_cast<T *>(a.rows[i]) + (int64_t)head * a.hs[i] +
            (v - head * (unsigned)a.dim);
-    const int64_t ts = a.ts[i];
     const int64_t step = (int64_t)gridDim.x * m.rows;
-    for (int64_t t0 = (int64_t)blockIdx.x * m.rows + row; t0 < a.tokens;
-         t0 += step * N) {
+    int64_t t = (int64_t)blockIdx.x * m.rows + row;
+    struct Stage {
         int64_t slot[N];
+        unsigned c[N][V / 4];
+        float s[N];
+    };
+    const auto look = [&](int64_t from, int64_t *slot) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int64_t t = t0 + n * step;
-            slot[n] = t < a.tokens ? a.slot[t] : -1;
-            if (slot[n] >= a.slots) slot[n] = -1;
+            const int64_t at = from + n * step;
+            slot[n] = at < a.tokens ? a.slot[at] : -1;
         }
-        uint2 c[N];
-        float s[N];
+    };
+    const auto load = [&](const int64_t *slot, Stage &st) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            if (slot[n] >= 0) {
-                c[n] = *reinterpret_cast<const uint2 *>(codes +
-                                                        slot[n] * width);
-                s[n] = scales[slot[n] * groups];
+        for (int n = 0; n < N; ++n) {
+            st.slot[n] = slot[n] < a.slots ? slot[n] : -1;
+            if (st.slot[n] < 0) continue;
+            const uint8_t *c = codes + st.slot[n] * width;
+            if constexpr (V == 16) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(c);
+                st.c[n][0] = q.x; st.c[n][1] = q.y;
+                st.c[n][2] = q.z; st.c[n][3] = q.w;
+            } else {
+                const uint2 q = *reinterpret_cast<const uint2 *>(c);
+                st.c[n][0] = q.x; st.c[n][1] = q.y;
             }
+            st.s[n] = scales[st.slot[n] * groups];
+        }
+    };
+    Stage next;
+    int64_t slot[N];
+    look(t, slot);
+    load(slot, next);
+    look(t + N * step, slot);
+    for (; t < a.tokens; t += N * step) {
+        const Stage now = next;
+        load(slot, next);
+        look(t + 2 * N * step, slot);
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            if (slot[n] >= 0) {
-                float2 z[kV / 2];
-                decode4<INT8>(c[n].x, z[0], z[1]);
-                decode4<INT8>(c[n].y, z[2], z[3]);
+            if (now.slot[n] >= 0) {
+                float2 z[V / 2];
 #pragma unroll
-                for (int e = 0; e < kV / 2; ++e) z[e] = mul2(z[e], both(s[n]));
-                store8<T>(y + (t0 + n * step) * ts, z);
+                for (int h = 0; h < V / 4; ++h)
+                    decode4<INT8>(now.c[n][h], z[2 * h], z[2 * h + 1]);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e)
+                    z[e] = mul2(z[e], both(now.s[n]));
+                store_values<T, V>(y + (t + n * step) * ts, z);
             }
     }
 }
@@ -341,15 +411,14 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Threads, tokens per CTA and grid for `per` lanes per token: as many tokens
-// as fit 256 threads, a CTA of at most 512; at most four waves of CTAs, which
-// then loop over tokens.
+// as fit 256 threads, a CTA of at most 512; CTAs enough to fill the device
+// once (two of 512 threads per SM), each of which loops over its tokens.
 struct Shape {
     Map map;
     dim3 grid;
     int threads;
 };
-cudaError_t shape_for(int64_t tokens, unsigned per, int log2L, int flight,
-                      Shape *out) {
+cudaError_t shape_for(int64_t tokens, unsigned per, int log2L, Shape *out) {
     int sms = 0;
     cudaError_t e = current_sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -359,12 +428,12 @@ cudaError_t shape_for(int64_t tokens, unsigned per, int log2L, int flight,
     const unsigned parts = (lanes + kMaxThreads - 1) / kMaxThreads;
     const unsigned threads = ((lanes + parts - 1) / parts + 31) / 32 * 32;
     const int64_t need = (tokens + rows - 1) / rows;
-    const int64_t full = (int64_t)sms * (2048 / threads) / parts;
-    // few tokens: one round of one token each; many: `flight` per round
-    int64_t x = need;
-    if (x > 4 * full) x = 4 * full;
-    (void)flight;
+    int64_t x = (int64_t)sms * (1024 / threads) / parts;
     if (x < 1) x = 1;
+    // rounds of equal length
+    if (x > need) x = need;
+    const int64_t rounds = (need + x - 1) / x;
+    x = (need + rounds - 1) / rounds;
     out->map = {per, rows, log2L};
     out->grid = dim3((unsigned)x, parts);
     out->threads = (int)threads;
@@ -387,22 +456,20 @@ cudaError_t launch_shape(K kernel, const Shape &s, const CacheArgs &a,
 }
 
 template <typename T, bool INT8>
-cudaError_t write_as(const CacheArgs &a, bool vec, cudaStream_t s) {
+cudaError_t write_as(const CacheArgs &a, int vec, cudaStream_t s) {
     const unsigned per_row = (unsigned)(a.heads * (a.dim / a.group));
     const int64_t groups = a.tokens * a.tensors * (int64_t)per_row;
     if (vec) {
-        // two packs per lane where the group has them
-        const int P = a.group > kV ? 2 : 1;
         int log2L = 0;
-        while ((kV * P << log2L) < a.group) ++log2L;
+        while ((vec << log2L) < a.group) ++log2L;
         Shape shape;
         cudaError_t e = shape_for(
-            a.tokens, (unsigned)(a.tensors * per_row) << log2L, log2L, 2,
+            a.tokens, (unsigned)(a.tensors * per_row) << log2L, log2L,
             &shape);
         if (e != cudaSuccess) return e;
-        return P == 2
-                   ? launch_shape(write_wide_kernel<T, INT8, 2, 2>, shape, a, s)
-                   : launch_shape(write_wide_kernel<T, INT8, 1, 2>, shape, a, s);
+        return vec == 16
+                   ? launch_shape(write_wide_kernel<T, INT8, 16>, shape, a, s)
+                   : launch_shape(write_wide_kernel<T, INT8, 8>, shape, a, s);
     }
     const int64_t per = kThreads / 32;
     return launch_dependent(write_any_kernel<T, INT8>,
@@ -411,15 +478,17 @@ cudaError_t write_as(const CacheArgs &a, bool vec, cudaStream_t s) {
 }
 
 template <typename T, bool INT8>
-cudaError_t read_as(const CacheArgs &a, bool vec, cudaStream_t s) {
+cudaError_t read_as(const CacheArgs &a, int vec, cudaStream_t s) {
     const unsigned width = (unsigned)(a.heads * a.dim);
     if (vec) {
         Shape shape;
-        cudaError_t e = shape_for(a.tokens,
-                                  (unsigned)a.tensors * (width / kV), 0, 4,
-                                  &shape);
+        cudaError_t e = shape_for(
+            a.tokens, (unsigned)a.tensors * (width / (unsigned)vec), 0,
+            &shape);
         if (e != cudaSuccess) return e;
-        return launch_shape(read_wide_kernel<T, INT8, 4>, shape, a, s);
+        return vec == 16
+                   ? launch_shape(read_wide_kernel<T, INT8, 16, 2>, shape, a, s)
+                   : launch_shape(read_wide_kernel<T, INT8, 8, 2>, shape, a, s);
     }
     const int64_t n = a.tokens * a.tensors * (int64_t)width;
     return launch_dependent(read_any_kernel<T, INT8>,
@@ -442,11 +511,11 @@ cudaError_t read_as(const CacheArgs &a, bool vec, cudaStream_t s) {
                           : f<__nv_bfloat16, false>(a, vec, s);              \
     }
 
-cudaError_t launch_cache_write(int dtype, const CacheArgs &a, bool vec,
+cudaError_t launch_cache_write(int dtype, const CacheArgs &a, int vec,
                                cudaStream_t s) {
     MT_CACHE_TYPES(write_as)
 }
-cudaError_t launch_cache_read(int dtype, const CacheArgs &a, bool vec,
+cudaError_t launch_cache_read(int dtype, const CacheArgs &a, int vec,
                               cudaStream_t s) {
     MT_CACHE_TYPES(read_as)
 }

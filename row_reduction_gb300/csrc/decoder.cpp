@@ -225,7 +225,7 @@ size_t backward_workspace(const mt_rotary_call_t *c) {
 
 // ---- cache -----------------------------------------------------------------
 mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
-                      CacheArgs *a, bool *vec, bool *empty) {
+                      CacheArgs *a, int *vec, bool *empty) {
     if (c == nullptr || !known_dtype(dtype)) return MT_ERR_INVALID_ARGUMENT;
     if (c->tokens < 0 || c->slots < 0 || c->heads < 1 || c->dim < 1 ||
         c->group < 1 || c->group > c->dim || c->dim % c->group != 0 ||
@@ -237,8 +237,7 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     const int es = dtype_size(dtype);
     const bool both = c->v.codes || c->v.scales || c->v.rows;
     *empty = c->tokens == 0;
-    uint64_t bits = (uint64_t)c->group;
-    uint64_t code_bits = 0;
+    uint64_t bits = 0, code_bits = 0;
     const mt_cache_rows_t *rs[2] = {&c->k, &c->v};
     for (int i = 0; i < (both ? 2 : 1); ++i) {
         const mt_cache_rows_t &r = *rs[i];
@@ -264,11 +263,16 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     if (*empty) return MT_OK;
     if (c->slot == nullptr || misaligned(c->slot, 8))
         return MT_ERR_INVALID_ARGUMENT;
-    // 8 values per lane: 8 bytes of codes, one or two 16-byte accesses of
-    // the rows.
-    *vec = c->group % 8 == 0 && (code_bits & 7) == 0 &&
-           (bits & (uint64_t)(16 / es - 1)) == 0 &&
-           (!write || c->group <= 512);
+    // Values per lane: 16 where groups hold whole sixteens and the rows'
+    // addresses and strides allow 32-byte accesses (64 bytes are two of them
+    // for FP32) and the codes 16-byte ones; else 8 with accesses half as
+    // wide; else one value at a time.  A warp holds a group when writing.
+    *vec = 0;
+    for (int v = 16; v >= 8 && *vec == 0; v /= 2)
+        if (c->group % v == 0 && (code_bits & (uint64_t)(v - 1)) == 0 &&
+            (bits & (uint64_t)(2 * v / es - 1)) == 0 &&
+            (!write || c->group <= 32 * v))
+            *vec = v;
     a->slot = c->slot;
     a->tokens = c->tokens;
     a->slots = c->slots;
@@ -431,10 +435,10 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
     }
     // The CTAs are shared out between queries and keys by their heads' groups.
     const int g0 = a.t[0].groups, g1 = a.t[1].groups;
-    a.log2S = split_log2(a.tokens, g0 > g1 ? g0 : g1, kRotWarps);
-    const int64_t units = a.tokens << a.log2S;
-    const int64_t need = (units + kRotThreads / 32 - 1) / (kRotThreads / 32);
     for (int i = 0; i < 2; ++i) {
+        const int64_t items = a.tokens * a.t[i].groups;
+        const int64_t need =
+            (items + kRotThreads / 32 - 1) / (kRotThreads / 32);
         int64_t share = (int64_t)kRotBackBlocks * a.t[i].groups / (g0 + g1);
         if (share < 1) share = 1;
         if (share > need) share = need;
@@ -466,7 +470,8 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
 mt_status mt_cache_write(int dtype, const mt_cache_call_t *call,
                          mt_stream_t stream) {
     CacheArgs a = {};
-    bool vec = false, empty = false;
+    int vec = 0;
+    bool empty = false;
     if (mt_status st = cache_setup(dtype, call, true, &a, &vec, &empty))
         return st;
     if (empty || a.slots == 0) return MT_OK;
@@ -477,7 +482,8 @@ mt_status mt_cache_write(int dtype, const mt_cache_call_t *call,
 mt_status mt_cache_read(int dtype, const mt_cache_call_t *call,
                         mt_stream_t stream) {
     CacheArgs a = {};
-    bool vec = false, empty = false;
+    int vec = 0;
+    bool empty = false;
     if (mt_status st = cache_setup(dtype, call, false, &a, &vec, &empty))
         return st;
     if (empty || a.slots == 0) return MT_OK;

@@ -47,8 +47,9 @@ struct RotArgs {
 };
 constexpr int kRotThreads = 256;
 constexpr int kRotMaxDim = 512;
-// Most CTAs of the backward pass with norm (rows of partial sums).
-constexpr int kRotBackBlocks = 608;
+// Most CTAs of the backward pass with norm (rows of partial sums): two for
+// each of 152 SMs, as many as are resident at once.
+constexpr int kRotBackBlocks = 304;
 
 #define MT_DECLARE_ROTARY(dt)                                                \
     cudaError_t launch_rotary_##dt(const RotArgs &a, int V, int K,           \
@@ -78,9 +79,10 @@ struct CacheArgs {
     int32_t heads, dim, group;
     int32_t int8;
 };
-cudaError_t launch_cache_write(int dtype, const CacheArgs &a, bool vec,
+// vec: values per lane, 16 or 8; 0: any sizes and addresses.
+cudaError_t launch_cache_write(int dtype, const CacheArgs &a, int vec,
                                cudaStream_t s);
-cudaError_t launch_cache_read(int dtype, const CacheArgs &a, bool vec,
+cudaError_t launch_cache_read(int dtype, const CacheArgs &a, int vec,
                               cudaStream_t s);
 cudaError_t launch_cache_slots(const int32_t *table, int64_t stride,
                                int32_t width, const int32_t *offsets,

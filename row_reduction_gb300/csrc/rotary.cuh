@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     const int i = (int)blockIdx.x < a.blocks[0] ? 0 : 1;
     const int block = (int)blockIdx.x - (i ? a.blocks[0] : 0);
     const RotHeads &h = a.t[i];
-    const int split = 1 << a.log2S;
     float wa[K][V], wb[K][V], da[K][V], db[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -307,21 +306,28 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 #pragma unroll
         for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.f;
     }
-    const int64_t units = a.tokens << a.log2S;
+    // A warp takes an equal share of the tensor's (token, group) items, in
+    // order, so that no warp has more than one more than another.
+    const int64_t items = a.tokens * h.groups;
+    const int64_t warps = (int64_t)a.blocks[i] * kWarps;
+    const int64_t w_ = (int64_t)block * kWarps + warp;
+    int64_t item = items / warps * w_ + min(items % warps, w_);
+    const int64_t end = item + items / warps + (w_ < items % warps ? 1 : 0);
+    int64_t t = item / h.groups;
+    int g0 = (int)(item - t * h.groups);
 #pragma unroll 1
-    for (int64_t unit = (int64_t)block * kWarps + warp; unit < units;
-         unit += (int64_t)a.blocks[i] * kWarps) {
-        const int64_t t = unit >> a.log2S;
+    for (; item < end; ++t, g0 = 0) {
+        const int g1 = (int)min((int64_t)h.groups, g0 + (end - item));
+        item += g1 - g0;
         const int64_t pos = rot_position(a, t);
         const T *x = static_cast<const T *>(h.x) + t * h.xt;
         const T *dy = static_cast<const T *>(h.dy) + t * h.dt;
         T *y = static_cast<T *>(h.y) + t * h.yt;
-        const int g0 = (int)(unit & (split - 1));
         typename S::Packs rx[U][K], rd[U][K];
         const auto load = [&](int g) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int head = (g + u * split) * heads_per_warp + sub;
+                const int head = (g + u) * heads_per_warp + sub;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const S slot(a, l + k * L);
@@ -336,12 +342,12 @@ __global__ void __launch_bounds__(kRotThreads, 2)
         for (int k = 0; k < K; ++k)
             S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
 #pragma unroll 1
-        for (int g = g0; g < h.groups; g += U * split) {
+        for (int g = g0; g < g1; g += U) {
             if (g != g0) load(g);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (g + u * split >= h.groups) break;  // whole warps
-                const int head = (g + u * split) * heads_per_warp + sub;
+                if (g + u >= g1) break;  // whole warps
+                const int head = (g + u) * heads_per_warp + sub;
                 float xa[K][V], xb[K][V], ga[K][V], gb[K][V];
                 float sq[V], dot[V];
 #pragma unroll

@@ -9,7 +9,7 @@ namespace mt {
 // dweight[d] = sum over a tensor's rows of partial sums.  A CTA adds 32
 // columns: 32 threads wide, kRows rows deep, then the rows in order.
 namespace {
-constexpr int kRows = 8;
+constexpr int kRows = 32;
 __global__ void __launch_bounds__(32 * kRows)
     rotary_dweight_kernel(const float *partial, int dim, int blocks0,
                           int blocks1, float *dw0, float *dw1) {

@@ -270,7 +270,7 @@ def test_rotary_backward_workspace():
         call(norm=1, q=heads(dy=A))) == 0
     n = mt.mt_rotary_backward_workspace(
         call(norm=1, q=heads(dy=A, dweight=A)))
-    assert n == 608 * 16 * 4
+    assert n == 304 * 16 * 4
     with pytest.raises(mt.MTError):
         mt.mt_rotary_backward_workspace(call(dim=513))
 
