@@ -200,12 +200,11 @@ mt_status rotary_setup(int dtype, const mt_rotary_call_t *c, RotKind kind,
 
 // Warps per token (a power of two): one while the tokens fill the device,
 // more where there are few, up to one group of heads each.
-int split_log2(int64_t tokens, int groups, int64_t want) {
+int split_log2(int64_t tokens, int groups) {
     int l = 0;
-    while ((1 << l) < groups && (tokens << l) < want) ++l;
+    while ((1 << l) < groups && (tokens << l) < 152 * 16) ++l;
     return l;
 }
-constexpr int64_t kRotWarps = 152 * 16;
 
 cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
                           bool norm, cudaStream_t s) {
@@ -377,7 +376,7 @@ mt_status mt_rotary(int dtype, const mt_rotary_call_t *call,
         return st;
     if (empty) return MT_OK;
     if (too_many_tokens(a.tokens)) return MT_ERR_UNSUPPORTED;
-    a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups, kRotWarps);
+    a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
     return status_from_cuda(rotary_launch(dtype, a, V, K,
                                           call->interleaved != 0,
                                           call->norm != 0,
@@ -427,8 +426,7 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
             a.t[i].xt = a.t[i].dt;
             a.t[i].xh = a.t[i].dh;
         }
-        a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups,
-                             kRotWarps);
+        a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
         return status_from_cuda(rotary_launch(dtype, a, V, K,
                                               call->interleaved != 0, false,
                                               s));

@@ -37,7 +37,7 @@ struct RotArgs {
     int32_t rot_slots;  // slots that are rotated
     int32_t slots;      // all slots of a head
     int32_t log2L;
-    int32_t log2S;      // warps that share one token
+    int32_t log2S;      // forward: warps that share one token
     float eps, inv_dim, scale;
     float sign;         // +1 forward, -1 backward (transposed rotation)
     // backward with norm: one row of dim partial sums per CTA, the first

@@ -51,11 +51,16 @@ struct RotSlot {
     }
     struct Packs {
         Raw<T, V> lo, hi;
+        __device__ __forceinline__ void zero() {
+            lo.zero();
+            hi.zero();
+        }
     };
+    // Leaves r as it was where there is no such slot: zeroed once, it adds
+    // nothing to its head's sums.  (A head that is not there may leave the
+    // values of another, of which nothing is stored.)
     __device__ __forceinline__ void load(const T *p, bool there,
                                          Packs &r) const {
-        r.lo.zero();
-        r.hi.zero();
         if (there && in) {
             r.lo.load(p + lo);
             if (second) r.hi.load(p + hi);
@@ -99,6 +104,7 @@ struct RotSlot {
         for (int e = 0; e < V; ++e) a[e] = b[e] = 1.f;
         if (w != nullptr && in) {
             Packs r;
+            r.zero();
             load(w, true, r);
             split(r, a, b);
         }
@@ -142,10 +148,36 @@ __device__ __forceinline__ int64_t rot_position(const RotArgs &a, int64_t t) {
 
 // Sum over the L lanes of a head (xor butterfly; every lane gets it).
 __device__ __forceinline__ float head_sum(float v, int log2L) {
-    for (int off = (1 << log2L) >> 1; off > 0; off >>= 1)
-        v += __shfl_xor_sync(kFull, v, off);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        if (i < log2L) v += __shfl_xor_sync(kFull, v, 1 << i);
     return v;
 }
+
+// The (token, group of heads) items of a warp: an equal share, in order, so
+// that no warp has more than one more than another and the angles of a token
+// are computed by few warps.
+struct RotItems {
+    int64_t left;  // items to come, this one included
+    int64_t t;
+    int g;
+    __device__ __forceinline__ RotItems(int64_t tokens, int groups,
+                                        int64_t warps, int64_t warp) {
+        const int64_t items = tokens * groups;
+        const int64_t each = items / warps, more = items - each * warps;
+        const int64_t first = each * warp + min(more, warp);
+        left = each + (warp < more ? 1 : 0);
+        t = first / groups;
+        g = (int)(first - t * groups);
+    }
+    __device__ __forceinline__ void next(int groups) {
+        --left;
+        if (++g == groups) {
+            g = 0;
+            ++t;
+        }
+    }
+};
 
 // Forward (and, with the sines' sign turned, backward without norm).  The
 // loads of U groups of heads are issued before the angles are computed and
@@ -170,26 +202,27 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     const int split = 1 << a.log2S;
     const int first = (int)(unit & (split - 1));
     const int64_t pos = rot_position(a, t);
-    typename S::Packs raw[U][K];
     // The warps of a token take its groups of heads in turn; the key heads'
     // groups follow the query heads'.
     const int first_k = (first - a.t[0].groups) & (split - 1);
-    bool loaded = false;
-    {
-        const RotHeads &h = a.t[0];
-        const T *x = static_cast<const T *>(h.x) + t * h.xt;
-        if (first < h.groups) {
-            loaded = true;
+    const int stride = split * heads_per_warp;  // heads between two groups
+    const bool all_rot = a.rot_slots == a.slots;
+    typename S::Packs raw[U][K];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int head = (first + u * split) * heads_per_warp + sub;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    S(a, l + k * L).load(x + head * h.xh, head < h.heads,
-                                         raw[u][k]);
-            }
-        }
-    }
+        for (int k = 0; k < K; ++k) raw[u][k].zero();
+    const auto load = [&](const T *x, int64_t step, int head, int heads) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                S(a, l + k * L).load(x + u * step, head + u * stride < heads,
+                                     raw[u][k]);
+    };
+    const int q0 = first * heads_per_warp + sub;
+    load(static_cast<const T *>(a.t[0].x) + t * a.t[0].xt + q0 * a.t[0].xh,
+         stride * a.t[0].xh, q0, a.t[0].heads);
     float c[K][V], s[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -199,8 +232,11 @@ __global__ void __launch_bounds__(kRotThreads, 2)
         const RotHeads &h = a.t[i];
         const int g0 = i == 0 ? first : first_k;
         if (g0 >= h.groups) continue;
-        const T *x = static_cast<const T *>(h.x) + t * h.xt;
-        T *y = static_cast<T *>(h.y) + t * h.yt;
+        int head = g0 * heads_per_warp + sub;
+        const int heads = h.heads;
+        const int64_t xs = stride * h.xh, ys = stride * h.yh;
+        const T *x = static_cast<const T *>(h.x) + t * h.xt + head * h.xh;
+        T *y = static_cast<T *>(h.y) + t * h.yt + head * h.yh;
         float k1[K][V], k2[K][V], k3[K][V], k4[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -217,44 +253,36 @@ __global__ void __launch_bounds__(kRotThreads, 2)
         }
 #pragma unroll 1
         for (int g = g0; g < h.groups; g += U * split) {
-            if (!(loaded && i == 0 && g == g0)) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int head = (g + u * split) * heads_per_warp + sub;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        S(a, l + k * L).load(x + head * h.xh, head < h.heads,
-                                             raw[u][k]);
-                }
-            }
+            if (i != 0 || g != g0) load(x, xs, head, heads);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (g + u * split >= h.groups) break;  // whole warps
-                const int head = (g + u * split) * heads_per_warp + sub;
                 float va[K][V], vb[K][V];
                 float r = 1.f;
                 if (NORM) {
                     float sq[V];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) sq[e] = 0.f;
-#pragma unroll
                     for (int k = 0; k < K; ++k) {
                         S::split(raw[u][k], va[k], vb[k]);
-                        fma_n<V>(sq, va[k], va[k], sq);
+                        if (k == 0)
+                            mul_n<V>(sq, va[k], va[k]);
+                        else
+                            fma_n<V>(sq, va[k], va[k], sq);
                         fma_n<V>(sq, vb[k], vb[k], sq);
                     }
-                    float ss = 0.f;
+                    float ss = sq[0];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) ss += sq[e];
+                    for (int e = 1; e < V; ++e) ss += sq[e];
                     r = rsqrtf(head_sum(ss, a.log2L) * a.inv_dim + a.eps);
                 }
+                T *out = y + u * ys;
+                const bool there = head + u * stride < heads;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const S slot(a, l + k * L);
-                    if (!slot.in || head >= h.heads) continue;
-                    T *out = y + head * h.yh;
+                    if (!slot.in || !there) continue;
                     if (!NORM) {
-                        if (!slot.rot) {  // copied bit for bit
+                        if (!all_rot && !slot.rot) {  // copied bit for bit
                             raw[u][k].lo.store(out + slot.lo);
                             if (slot.second) raw[u][k].hi.store(out + slot.hi);
                             continue;
@@ -264,7 +292,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
                     float oa[V], ob[V];
                     mul_n<V>(oa, va[k], k1[k]);
                     mul_n<V>(ob, vb[k], k4[k]);
-                    if (slot.rot) {  // 0 times a neighbour may be NaN
+                    if (all_rot || slot.rot) {  // 0 * a neighbour may be NaN
                         fma_n<V>(oa, vb[k], k2[k], oa);
                         fma_n<V>(ob, va[k], k3[k], ob);
                     }
@@ -275,6 +303,9 @@ __global__ void __launch_bounds__(kRotThreads, 2)
                     slot.store(out, oa, ob);
                 }
             }
+            x += U * xs;
+            y += U * ys;
+            head += U * stride;
         }
     }
 }
@@ -288,7 +319,6 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     rotary_backward_kernel(const RotArgs a) {
     using S = RotSlot<T, V, ILV>;
     constexpr int kWarps = kRotThreads / 32;
-    constexpr int U = K == 1 ? 2 : 1;
     __shared__ float sums[kWarps][kRotMaxDim];
     grid_launch_dependents();
     grid_wait_prerequisites();
@@ -306,107 +336,107 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 #pragma unroll
         for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.f;
     }
-    // A warp takes an equal share of the tensor's (token, group) items, in
-    // order, so that no warp has more than one more than another.
-    const int64_t items = a.tokens * h.groups;
-    const int64_t warps = (int64_t)a.blocks[i] * kWarps;
-    const int64_t w_ = (int64_t)block * kWarps + warp;
-    int64_t item = items / warps * w_ + min(items % warps, w_);
-    const int64_t end = item + items / warps + (w_ < items % warps ? 1 : 0);
-    int64_t t = item / h.groups;
-    int g0 = (int)(item - t * h.groups);
+    RotItems now(a.tokens, h.groups, (int64_t)a.blocks[i] * kWarps,
+                 (int64_t)block * kWarps + warp);
+    const auto load = [&](const RotItems &item, typename S::Packs *rx,
+                          typename S::Packs *rd) {
+        const int head = item.g * heads_per_warp + sub;
+        const bool there = item.left > 0 && head < h.heads;
+        const T *x = static_cast<const T *>(h.x) + item.t * h.xt +
+                     head * h.xh;
+        const T *dy = static_cast<const T *>(h.dy) + item.t * h.dt +
+                      head * h.dh;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const S slot(a, l + k * L);
+            slot.load(x, there, rx[k]);
+            slot.load(dy, there, rd[k]);
+        }
+    };
+    int64_t pos = now.left > 0 ? rot_position(a, now.t) : 0;
+    typename S::Packs nx[K], nd[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        nx[k].zero();
+        nd[k].zero();
+    }
+    load(now, nx, nd);
+    float c[K][V], s[K][V];
+    bool turned = true;
 #pragma unroll 1
-    for (; item < end; ++t, g0 = 0) {
-        const int g1 = (int)min((int64_t)h.groups, g0 + (end - item));
-        item += g1 - g0;
-        const int64_t pos = rot_position(a, t);
-        const T *x = static_cast<const T *>(h.x) + t * h.xt;
-        const T *dy = static_cast<const T *>(h.dy) + t * h.dt;
-        T *y = static_cast<T *>(h.y) + t * h.yt;
-        typename S::Packs rx[U][K], rd[U][K];
-        const auto load = [&](int g) {
+    for (; now.left > 0;) {
+        float xa[K][V], xb[K][V], ga[K][V], gb[K][V];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int head = (g + u) * heads_per_warp + sub;
+        for (int k = 0; k < K; ++k) {
+            S::split(nx[k], xa[k], xb[k]);
+            S::split(nd[k], ga[k], gb[k]);
+        }
+        const int head = now.g * heads_per_warp + sub;
+        T *out = static_cast<T *>(h.y) + now.t * h.yt + head * h.yh;
+        if (turned) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const S slot(a, l + k * L);
-                    slot.load(x + head * h.xh, head < h.heads, rx[u][k]);
-                    slot.load(dy + head * h.dh, head < h.heads, rd[u][k]);
-                }
+            for (int k = 0; k < K; ++k)
+                S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
+        }
+        // The next item is on its way while this one is worked on.
+        now.next(h.groups);
+        load(now, nx, nd);
+        turned = now.g == 0;
+        if (turned && now.left > 0) pos = rot_position(a, now.t);
+
+        float sq[V], dot[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const S slot(a, l + k * L);
+            if (slot.rot) {
+                // g = R^T dy: a.sign has turned the sines, so that
+                // g_a = a c - b s, g_b = a s + b c
+                float ta[V], tb[V], m[V];
+                mul_n<V>(ta, ga[k], c[k]);
+                mul_n<V>(tb, gb[k], c[k]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) m[e] = -gb[k][e];
+                fma_n<V>(tb, ga[k], s[k], tb);
+                fma_n<V>(ga[k], m, s[k], ta);
+#pragma unroll
+                for (int e = 0; e < V; ++e) gb[k][e] = tb[e];
             }
-        };
-        load(g0);
-        float c[K][V], s[K][V];
+            float ta[V], tb[V];
+            fma_n<V>(sq, xa[k], xa[k], sq);
+            fma_n<V>(sq, xb[k], xb[k], sq);
+            mul_n<V>(ta, ga[k], wa[k]);
+            mul_n<V>(tb, gb[k], wb[k]);
+            fma_n<V>(dot, ta, xa[k], dot);
+            fma_n<V>(dot, tb, xb[k], dot);
+        }
+        float xx = 0.f, gx = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
-#pragma unroll 1
-        for (int g = g0; g < g1; g += U) {
-            if (g != g0) load(g);
+        for (int e = 0; e < V; ++e) {
+            xx += sq[e];
+            gx += dot[e];
+        }
+        xx = head_sum(xx, a.log2L);
+        gx = head_sum(gx, a.log2L);
+        // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
+        const float r = head < h.heads ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
+        const float m = -gx * a.inv_dim * r * r;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (g + u >= g1) break;  // whole warps
-                const int head = (g + u) * heads_per_warp + sub;
-                float xa[K][V], xb[K][V], ga[K][V], gb[K][V];
-                float sq[V], dot[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const S slot(a, l + k * L);
-                    S::split(rx[u][k], xa[k], xb[k]);
-                    S::split(rd[u][k], ga[k], gb[k]);
-                    if (slot.rot) {
-                        // g = R^T dy: a.sign has turned the sines, so that
-                        // g_a = a c - b s, g_b = a s + b c
-                        float ta[V], tb[V], m[V];
-                        mul_n<V>(ta, ga[k], c[k]);
-                        mul_n<V>(tb, gb[k], c[k]);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) m[e] = -gb[k][e];
-                        fma_n<V>(tb, ga[k], s[k], tb);
-                        fma_n<V>(ga[k], m, s[k], ta);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) gb[k][e] = tb[e];
-                    }
-                    float ta[V], tb[V];
-                    fma_n<V>(sq, xa[k], xa[k], sq);
-                    fma_n<V>(sq, xb[k], xb[k], sq);
-                    mul_n<V>(ta, ga[k], wa[k]);
-                    mul_n<V>(tb, gb[k], wb[k]);
-                    fma_n<V>(dot, ta, xa[k], dot);
-                    fma_n<V>(dot, tb, xb[k], dot);
-                }
-                float xx = 0.f, gx = 0.f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    xx += sq[e];
-                    gx += dot[e];
-                }
-                xx = head_sum(xx, a.log2L);
-                gx = head_sum(gx, a.log2L);
-                // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
-                const float r = head < h.heads
-                                    ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
-                const float m = -gx * a.inv_dim * r * r;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const S slot(a, l + k * L);
-                    // g r: dw += (g r) x, dx = (g r) w - x (m r)
-                    scale_n<V>(ga[k], ga[k], r);
-                    scale_n<V>(gb[k], gb[k], r);
-                    fma_n<V>(da[k], ga[k], xa[k], da[k]);
-                    fma_n<V>(db[k], gb[k], xb[k], db[k]);
-                    if (head < h.heads && slot.in) {
-                        float oa[V], ob[V];
-                        mul_n<V>(oa, ga[k], wa[k]);
-                        mul_n<V>(ob, gb[k], wb[k]);
-                        scale_add_n<V>(oa, xa[k], m * r, oa);
-                        scale_add_n<V>(ob, xb[k], m * r, ob);
-                        slot.store(y + head * h.yh, oa, ob);
-                    }
-                }
+        for (int k = 0; k < K; ++k) {
+            const S slot(a, l + k * L);
+            // g r: dw += (g r) x, dx = (g r) w - x (m r)
+            scale_n<V>(ga[k], ga[k], r);
+            scale_n<V>(gb[k], gb[k], r);
+            fma_n<V>(da[k], ga[k], xa[k], da[k]);
+            fma_n<V>(db[k], gb[k], xb[k], db[k]);
+            if (head < h.heads && slot.in) {
+                float oa[V], ob[V];
+                mul_n<V>(oa, ga[k], wa[k]);
+                mul_n<V>(ob, gb[k], wb[k]);
+                scale_add_n<V>(oa, xa[k], m * r, oa);
+                scale_add_n<V>(ob, xb[k], m * r, ob);
+                slot.store(out, oa, ob);
             }
         }
     }
