@@ -154,31 +154,6 @@ __device__ __forceinline__ float head_sum(float v, int log2L) {
     return v;
 }
 
-// The (token, group of heads) items of a warp: an equal share, in order, so
-// that no warp has more than one more than another and the angles of a token
-// are computed by few warps.
-struct RotItems {
-    int64_t left;  // items to come, this one included
-    int64_t t;
-    int g;
-    __device__ __forceinline__ RotItems(int64_t tokens, int groups,
-                                        int64_t warps, int64_t warp) {
-        const int64_t items = tokens * groups;
-        const int64_t each = items / warps, more = items - each * warps;
-        const int64_t first = each * warp + min(more, warp);
-        left = each + (warp < more ? 1 : 0);
-        t = first / groups;
-        g = (int)(first - t * groups);
-    }
-    __device__ __forceinline__ void next(int groups) {
-        --left;
-        if (++g == groups) {
-            g = 0;
-            ++t;
-        }
-    }
-};
-
 // Forward (and, with the sines' sign turned, backward without norm).  The
 // loads of U groups of heads are issued before the angles are computed and
 // before any of them is used.  With the norm, weights and rotation become
@@ -336,61 +311,83 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 #pragma unroll
         for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.f;
     }
-    RotItems now(a.tokens, h.groups, (int64_t)a.blocks[i] * kWarps,
-                 (int64_t)block * kWarps + warp);
-    const auto load = [&](const RotItems &item, typename S::Packs *rx,
-                          typename S::Packs *rd) {
-        const int head = item.g * heads_per_warp + sub;
-        const bool there = item.left > 0 && head < h.heads;
-        const T *x = static_cast<const T *>(h.x) + item.t * h.xt +
-                     head * h.xh;
-        const T *dy = static_cast<const T *>(h.dy) + item.t * h.dt +
-                      head * h.dh;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const S slot(a, l + k * L);
-            slot.load(x, there, rx[k]);
-            slot.load(dy, there, rd[k]);
-        }
-    };
-    int64_t pos = now.left > 0 ? rot_position(a, now.t) : 0;
+    // A warp takes an equal share of the tensor's (token, group) items, in
+    // order, so that no warp has more than one more than another and the
+    // angles of a token are computed by few warps.
+    int64_t left, t;
+    int head;  // the lane's
+    {
+        const int64_t items = a.tokens * h.groups;
+        const int64_t warps = (int64_t)a.blocks[i] * kWarps;
+        const int64_t me = (int64_t)block * kWarps + warp;
+        const int64_t each = items / warps, more = items - each * warps;
+        const int64_t first = each * me + min(more, me);
+        left = each + (me < more ? 1 : 0);
+        t = first / h.groups;
+        head = (int)(first - t * h.groups) * heads_per_warp + sub;
+    }
+    const int heads = h.heads;
+    const int64_t xs = heads_per_warp * h.xh, ds = heads_per_warp * h.dh,
+                  ys = heads_per_warp * h.yh;
+    const T *x = static_cast<const T *>(h.x) + t * h.xt + head * h.xh;
+    const T *dy = static_cast<const T *>(h.dy) + t * h.dt + head * h.dh;
+    T *y = static_cast<T *>(h.y) + t * h.yt + head * h.yh;
     typename S::Packs nx[K], nd[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         nx[k].zero();
         nd[k].zero();
     }
-    load(now, nx, nd);
+    const auto load = [&]() {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const S slot(a, l + k * L);
+            slot.load(x, left > 0 && head < heads, nx[k]);
+            slot.load(dy, left > 0 && head < heads, nd[k]);
+        }
+    };
+    int64_t pos = left > 0 ? rot_position(a, t) : 0;
+    load();
     float c[K][V], s[K][V];
+    const bool all_rot = a.rot_slots == a.slots;
     bool turned = true;
 #pragma unroll 1
-    for (; now.left > 0;) {
+    while (left > 0) {
         float xa[K][V], xb[K][V], ga[K][V], gb[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             S::split(nx[k], xa[k], xb[k]);
             S::split(nd[k], ga[k], gb[k]);
         }
-        const int head = now.g * heads_per_warp + sub;
-        T *out = static_cast<T *>(h.y) + now.t * h.yt + head * h.yh;
+        T *out = y;
+        const bool there = head < heads;
         if (turned) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
         }
         // The next item is on its way while this one is worked on.
-        now.next(h.groups);
-        load(now, nx, nd);
-        turned = now.g == 0;
-        if (turned && now.left > 0) pos = rot_position(a, now.t);
+        --left;
+        head += heads_per_warp;
+        x += xs;
+        dy += ds;
+        y += ys;
+        turned = head - sub >= heads;  // whole warps
+        if (turned) {
+            head = sub;
+            ++t;
+            x = static_cast<const T *>(h.x) + t * h.xt + head * h.xh;
+            dy = static_cast<const T *>(h.dy) + t * h.dt + head * h.dh;
+            y = static_cast<T *>(h.y) + t * h.yt + head * h.yh;
+            if (left > 0) pos = rot_position(a, t);
+        }
+        load();
 
         float sq[V], dot[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) sq[e] = dot[e] = 0.f;
-#pragma unroll
         for (int k = 0; k < K; ++k) {
             const S slot(a, l + k * L);
-            if (slot.rot) {
+            if (all_rot || slot.rot) {
                 // g = R^T dy: a.sign has turned the sines, so that
                 // g_a = a c - b s, g_b = a s + b c
                 float ta[V], tb[V], m[V];
@@ -404,11 +401,16 @@ __global__ void __launch_bounds__(kRotThreads, 2)
                 for (int e = 0; e < V; ++e) gb[k][e] = tb[e];
             }
             float ta[V], tb[V];
-            fma_n<V>(sq, xa[k], xa[k], sq);
-            fma_n<V>(sq, xb[k], xb[k], sq);
             mul_n<V>(ta, ga[k], wa[k]);
             mul_n<V>(tb, gb[k], wb[k]);
-            fma_n<V>(dot, ta, xa[k], dot);
+            if (k == 0) {
+                mul_n<V>(sq, xa[k], xa[k]);
+                mul_n<V>(dot, ta, xa[k]);
+            } else {
+                fma_n<V>(sq, xa[k], xa[k], sq);
+                fma_n<V>(dot, ta, xa[k], dot);
+            }
+            fma_n<V>(sq, xb[k], xb[k], sq);
             fma_n<V>(dot, tb, xb[k], dot);
         }
         float xx = 0.f, gx = 0.f;
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
         xx = head_sum(xx, a.log2L);
         gx = head_sum(gx, a.log2L);
         // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
-        const float r = head < h.heads ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
+        const float r = there ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
         const float m = -gx * a.inv_dim * r * r;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
             scale_n<V>(gb[k], gb[k], r);
             fma_n<V>(da[k], ga[k], xa[k], da[k]);
             fma_n<V>(db[k], gb[k], xb[k], db[k]);
-            if (head < h.heads && slot.in) {
+            if (there && slot.in) {
                 float oa[V], ob[V];
                 mul_n<V>(oa, ga[k], wa[k]);
                 mul_n<V>(ob, gb[k], wb[k]);
