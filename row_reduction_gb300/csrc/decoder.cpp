@@ -558,7 +558,10 @@ mt_status mt_process_logits(int dtype, const mt_logits_call_t *call,
     if (c.mask && !add_extent(c.mask_stride, c.rows, &extent))
         return MT_ERR_INVALID_ARGUMENT;
     if (c.rows > (1LL << 24)) return MT_ERR_UNSUPPORTED;
-    return status_from_cuda(launch_logits(dtype, c, (cudaStream_t)stream));
+    cudaStream_t s = (cudaStream_t)stream;
+    return status_from_cuda(dtype == DT_F32   ? launch_logits_f32(c, s)
+                            : dtype == DT_F16 ? launch_logits_f16(c, s)
+                                              : launch_logits_bf16(c, s));
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
-// logits.cu -- a row of logits: penalties for tokens of its history, biases,
-// temperature, grammar mask, and the row's softmax or log-softmax.
+// logits.cuh -- a row of logits: penalties for tokens of its history, biases,
+// temperature, grammar mask, and the row's softmax or log-softmax (one
+// translation unit per storage type).
 //
 // A row is shared out between C CTAs (a power of two) so that a CTA's logits
 // stay in registers: K packs of V values per thread, asked for before anything
@@ -22,6 +23,8 @@
 // Alignment.  Packs of V values start at 16-byte boundaries of x: pack p of
 // a row holds columns p V - shift + e, shift being the row's address modulo
 // 16 in elements, so only a row's first and last pack can be partial.
+#pragma once
+
 #include "mt_decoder.cuh"
 
 namespace mt {
@@ -64,11 +67,16 @@ struct Params {
 template <int V>
 struct Place {
     static constexpr int kLog2Chunk = V == 8 ? 8 : 7;  // 32 V columns
-    int shift, log2C, rank, vocab;
-    __device__ __forceinline__ int mine(int id) const {
-        return ((unsigned)id < (unsigned)vocab) &
-               ((((id + shift) ^ (rank << kLog2Chunk)) &
-                 (((1 << log2C) - 1) << kLog2Chunk)) == 0);
+    int shift, log2C, vocab;
+    unsigned mine, mask;  // (id + shift) & mask == mine: a CTA's chunk
+    __device__ __forceinline__ Place(int shift_, int log2C_, int rank,
+                                     int vocab_)
+        : shift(shift_), log2C(log2C_), vocab(vocab_),
+          mine((unsigned)rank << kLog2Chunk),
+          mask(((1u << log2C_) - 1u) << kLog2Chunk) {}
+    __device__ __forceinline__ bool has(int id) const {
+        return (unsigned)id < (unsigned)vocab &&
+               ((unsigned)(id + shift) & mask) == mine;
     }
     __device__ __forceinline__ int element(int id) const {
         const int at = id + shift;
@@ -84,42 +92,54 @@ struct Place {
 constexpr int kRoom = 16;   // entries per lane
 constexpr int kLooks = 8;   // ids that a lane looks at between two checks
 template <int V>
+__device__ __forceinline__ unsigned in_use(const unsigned *used, int pack) {
+    const unsigned byte = reinterpret_cast<const uint8_t *>(used)[
+        V == 8 ? pack : pack >> 1];
+    return V == 8 ? byte : byte >> (pack & 1) * 4 & 15u;
+}
+
+template <int V>
 struct Found {
-    unsigned column;  // shared address; entry j is at column + 128 j
+    unsigned column, top;  // shared addresses: entry j at column + 128 j
     unsigned *count, *used;
     Place<V> place;
-    int n;
 
     // Four ids; `left` of them are there, `prompt` of them the prompt's.  No
     // branches: a history is mostly others' tokens, and a warp's time is the
     // length of this chain.
-    __device__ __forceinline__ void look(const int4 &v, int left, int prompt) {
-        const int id[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int mine = (j < left) & place.mine(id[j]);
-            const unsigned entry =
-                (unsigned)id[j] | (j < prompt ? kPrompt : 0u);
-            asm volatile(
-                "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t"
-                "@p st.shared.u32 [%0], %1;\n\t}" ::"r"(column + 128 * n),
-                "r"(entry), "r"(mine)
-                : "memory");
-            n += mine;
+    __device__ __forceinline__ void look(int4 v, int left, int prompt) {
+        if (left < 4) {
+            v.w = -1;
+            if (left < 3) v.z = -1;
+            if (left < 2) v.y = -1;
+            if (left < 1) v.x = -1;
         }
+        put(v.x, prompt > 0);
+        put(v.y, prompt > 1);
+        put(v.z, prompt > 2);
+        put(v.w, prompt > 3);
+    }
+    __device__ __forceinline__ void put(int id, bool prompt) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b32 t;\n\t"
+            "add.s32 t, %1, %2;\n\tand.b32 t, t, %3;\n\t"
+            "setp.eq.u32 p, t, %4;\n\tsetp.lt.and.u32 p, %1, %5, p;\n\t"
+            "@p st.shared.u32 [%0], %6;\n\t@p add.u32 %0, %0, 128;\n\t}"
+            : "+r"(top)
+            : "r"(id), "r"(place.shift), "r"(place.mask), "r"(place.mine),
+              "r"(place.vocab), "r"((unsigned)id | (prompt ? kPrompt : 0u))
+            : "memory");
     }
     // Counts what the lanes of a warp hold.  A counter that is not zero has
     // its bit set already and a prompt token that was seen needs nothing:
     // frequent tokens cost a read instead of atomics on one address.
     __device__ __forceinline__ void drain() {
 #pragma unroll 1
-        for (int j = 0; __any_sync(kFull, j < n); ++j) {
-            if (j >= n) continue;
+        for (unsigned at = column; __any_sync(kFull, at < top); at += 128) {
+            if (at >= top) continue;
             unsigned entry;
             asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(entry)
-                         : "r"(column + 128 * j)
-                         : "memory");
+                         : "=r"(entry) : "r"(at) : "memory");
             const int i = place.element((int)(entry & ~kPrompt));
             const unsigned before =
                 *static_cast<volatile unsigned *>(count + i);
@@ -129,11 +149,11 @@ struct Found {
             else if (!(before & kPrompt))
                 atomicOr(count + i, kPrompt);
         }
-        n = 0;
+        top = column;
     }
     // Called by whole warps after at most kLooks ids.
     __device__ __forceinline__ void keep_room() {
-        if (__any_sync(kFull, n > kRoom - kLooks)) drain();
+        if (__any_sync(kFull, top > column + 128 * (kRoom - kLooks))) drain();
     }
 };
 
@@ -169,8 +189,9 @@ __device__ __forceinline__ float nanmax3(float a, float b, float c) {
     return r;
 }
 
+// AL: every row of x and y starts at a 16-byte boundary and has whole packs.
 // Up to 32 values per thread leave registers for two CTAs per SM.
-template <typename T, int MODE, int K>
+template <typename T, int MODE, int K, bool AL>
 __global__ void __launch_bounds__(kMaxThreads,
                                   K * 16 / (int)sizeof(T) <= 32 ? 2 : 1)
     logits_kernel(const Params p) {
@@ -187,9 +208,9 @@ __global__ void __launch_bounds__(kMaxThreads,
     const T *x = static_cast<const T *>(c.x) + row * c.x_stride;
     T *y = static_cast<T *>(c.y) + row * c.y_stride;
     const int shift =
-        (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (V - 1));
+        AL ? 0 : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (V - 1));
     const int yshift =
-        (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) & (V - 1));
+        AL ? 0 : (int)((reinterpret_cast<uintptr_t>(y) / sizeof(T)) & (V - 1));
     const int T_ = (int)blockDim.x, tid = (int)threadIdx.x;
     // Local pack tid + k T_ holds the columns from first + k next on.
     const int first =
@@ -202,6 +223,10 @@ __global__ void __launch_bounds__(kMaxThreads,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int col = first + k * next;
+        if (AL) {
+            if (col < c.vocab) raw[k].load(x + col);
+            continue;
+        }
         raw[k].zero();
         if (col >= 0 && col + V <= c.vocab) {
             raw[k].load(x + col);
@@ -236,6 +261,11 @@ __global__ void __launch_bounds__(kMaxThreads,
         const int col = first + k * next;
         const int from = max(col, 0), last = min(col + V, c.vocab) - 1;
         bits0[k] = bits1[k] = ~0u;
+        if (AL) {
+            if (mask != nullptr && col < c.vocab)
+                bits0[k] = __ldg(mask + (col >> 3));
+            continue;
+        }
         if (mask != nullptr && from <= last) {
             bits0[k] = __ldg(mask + (from >> 3));
             if (shift != 0 && last >> 3 > from >> 3)
@@ -265,39 +295,44 @@ __global__ void __launch_bounds__(kMaxThreads,
             bias[i] = c.bias[row * c.biases + i];
         }
         const int len = min(max(length, 0), c.history);
-        __syncthreads();
-        const Place<V> place = {shift, p.log2C, rank, c.vocab};
-        // Whole warps go through the history together.
+        // Whole warps go through the history together; what the first ids
+        // give is put by before the counters are known to be zero.
         const int lane = tid & 31;
-        Found<V> found = {
-            (unsigned)__cvta_generic_to_shared(found_at +
-                                               (tid >> 5) * 32 * kRoom + lane),
-            count, used, place, 0};
-#pragma unroll 1
-        for (int q0 = tid - lane; q0 < quads && q0 * 4 < len; q0 += 2 * T_) {
+        const Place<V> place(shift, p.log2C, rank, c.vocab);
+        const unsigned column = (unsigned)__cvta_generic_to_shared(
+            found_at + (tid >> 5) * 32 * kRoom + lane);
+        Found<V> found = {column, column, count, used, place};
+        int q0 = tid - lane;
+        if (q0 < quads && q0 * 4 < len) {
             const int at = (q0 + lane) * 4;
-            const int4 a0 = v0, a1 = v1;
+            found.look(v0, len - at, prompt - at);
+            if (q0 + T_ < quads)
+                found.look(v1, len - at - 4 * T_, prompt - at - 4 * T_);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (q0 += 2 * T_; q0 < quads && q0 * 4 < len; q0 += 2 * T_) {
+            found.keep_room();
+            const int at = (q0 + lane) * 4;
             v0 = w0;
             v1 = w1;
-            w0 = quad(q0 + lane + 4 * T_);
-            w1 = quad(q0 + lane + 5 * T_);
-            found.look(a0, len - at, prompt - at);
-            found.look(a1, len - at - 4 * T_, prompt - at - 4 * T_);
-            found.keep_room();
+            w0 = quad(q0 + lane + 2 * T_);
+            w1 = quad(q0 + lane + 3 * T_);
+            found.look(v0, len - at, prompt - at);
+            found.look(v1, len - at - 4 * T_, prompt - at - 4 * T_);
         }
 #pragma unroll 1
         for (int i0 = quads * 4 + tid - lane; i0 < len; i0 += T_) {
-            const int at = i0 + lane;
-            found.look(make_int4(at < len ? ids[at] : -1, -1, -1, -1), 1,
-                       at < prompt);
             found.keep_room();
+            const int at = i0 + lane;
+            found.put(at < len ? ids[at] : -1, at < prompt);
         }
         found.drain();
         // A bias leaves its number in its token's counter; where another one
         // was there before (in any order), the field becomes kSeveral and
         // the pass below adds them up in the order given.
         for (int i = tid; i < c.biases; i += T_) {
-            if (place.mine(bias_ids[i])) {
+            if (place.has(bias_ids[i])) {
                 const int j = place.element(bias_ids[i]);
                 atomicOr(used + (j >> 5), 1u << (j & 31));
                 const unsigned before =
@@ -321,6 +356,10 @@ __global__ void __launch_bounds__(kMaxThreads,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int col = first + k * next;
+        if (AL) {
+            keep[k] = col < c.vocab ? bits0[k] >> (col & 7) & kAll : 0u;
+            continue;
+        }
         const int from = max(col, 0), to = min(col + V, c.vocab);
         keep[k] = ((bits0[k] & 0xffu) | bits1[k] << 8) >> (from & 7) & kAll;
         if (to - from < V)
@@ -337,7 +376,7 @@ __global__ void __launch_bounds__(kMaxThreads,
         for (int k = 0; k < K; ++k) {
             const int i = (tid + k * T_) * V;
             if (i >= p.packs * V) break;
-            unsigned hit = used[i >> 5] >> (i & 31) & kAll;
+            unsigned hit = in_use<V>(used, tid + k * T_);
 #pragma unroll 1
             while (hit) {
                 const int e = __ffs(hit) - 1, col = first + k * next + e;
@@ -364,7 +403,7 @@ __global__ void __launch_bounds__(kMaxThreads,
         raw[k].widen(v);
         if (marks) {
             const int i = (tid + k * T_) * V;
-            const unsigned hit = used[i >> 5] >> (i & 31) & kAll;
+            const unsigned hit = in_use<V>(used, tid + k * T_);
             if (hit) {
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
@@ -455,7 +494,7 @@ __global__ void __launch_bounds__(kMaxThreads,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int col = first + k * next;
-        if (col + V <= 0 || col >= c.vocab) continue;
+        if ((!AL && col + V <= 0) || col >= c.vocab) continue;
         float *v = &z[k][0].x;
         if (keep[k] == 0) {
 #pragma unroll
@@ -471,7 +510,7 @@ __global__ void __launch_bounds__(kMaxThreads,
                     z[k][h] = add2(z[k][h], both(-log_total));
             }
         }
-        if (col >= 0 && col + V <= c.vocab && yshift == shift) {
+        if (AL || (col >= 0 && col + V <= c.vocab && yshift == shift)) {
             st_vec<T, V>(y + col, v);
         } else {
 #pragma unroll
@@ -484,11 +523,11 @@ __global__ void __launch_bounds__(kMaxThreads,
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <typename T, int MODE, int K>
+template <typename T, int MODE, int K, bool AL>
 cudaError_t launch_packs(const Params &p, int threads, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     const mt_logits_call_t &c = p.c;
-    const void *k = reinterpret_cast<const void *>(logits_kernel<T, MODE, K>);
+    const void *k = reinterpret_cast<const void *>(logits_kernel<T, MODE, K, AL>);
     size_t smem = 0;  // a counter and a bit per logit of the slice, biases
     if (c.tokens != nullptr || c.biases > 0)
         smem = (size_t)p.packs * V * 4 + (size_t)p.packs * V / 8 +
@@ -513,7 +552,7 @@ cudaError_t launch_packs(const Params &p, int threads, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, logits_kernel<T, MODE, K>, p);
+    return cudaLaunchKernelEx(&cfg, logits_kernel<T, MODE, K, AL>, p);
 }
 
 // Slices, packs per thread and threads.
@@ -553,13 +592,22 @@ cudaError_t launch_as(const mt_logits_call_t &c, cudaStream_t s) {
     while (K < kMost && (int64_t)K * kMaxThreads < p.packs) K *= 2;
     int threads = 64;
     while (threads < kMaxThreads && threads * K < p.packs) threads *= 2;
-    switch (K) {
-        case 1: return launch_packs<T, MODE, 1>(p, threads, s);
-        case 2: return launch_packs<T, MODE, 2>(p, threads, s);
-        case 4: return launch_packs<T, MODE, 4>(p, threads, s);
-        case 8: return launch_packs<T, MODE, 8>(p, threads, s);
+    const bool aligned =
+        whole && c.vocab % V == 0 &&
+        (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 &&
+        (c.rows == 1 || c.y_stride * (int64_t)sizeof(T) % 16 == 0);
+#define MT_LOGITS_CASE(k)                                                    \
+    if (K == k)                                                              \
+        return aligned ? launch_packs<T, MODE, k, true>(p, threads, s)       \
+                       : launch_packs<T, MODE, k, false>(p, threads, s);
+    MT_LOGITS_CASE(1)
+    MT_LOGITS_CASE(2)
+    MT_LOGITS_CASE(4)
+    MT_LOGITS_CASE(8)
+    if constexpr (kMost >= 16) {
+        MT_LOGITS_CASE(16)
     }
-    if constexpr (kMost >= 16) return launch_packs<T, MODE, 16>(p, threads, s);
+#undef MT_LOGITS_CASE
     return cudaErrorInvalidValue;
 }
 
@@ -574,13 +622,10 @@ cudaError_t launch_mode(const mt_logits_call_t &c, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_logits(int dtype, const mt_logits_call_t &c,
-                          cudaStream_t s) {
-    switch (dtype) {
-        case DT_F32: return launch_mode<float>(c, s);
-        case DT_F16: return launch_mode<__half>(c, s);
-        default: return launch_mode<__nv_bfloat16>(c, s);
+#define MT_DEFINE_LOGITS(T, dt)                                              \
+    cudaError_t launch_logits_##dt(const mt_logits_call_t &c,                \
+                                   cudaStream_t s) {                         \
+        return launch_mode<T>(c, s);                                         \
     }
-}
 
 }  // namespace mt

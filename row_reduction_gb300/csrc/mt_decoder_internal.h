@@ -94,7 +94,8 @@ cudaError_t launch_cache_slots(const int32_t *table, int64_t stride,
 // 16 CTAs of 512 threads with 64 values each, less a pack's shift.
 constexpr int kLogitsMaxVocab = 524280;
 constexpr int kLogitsMaxBias = 1024;
-cudaError_t launch_logits(int dtype, const mt_logits_call_t &c,
-                          cudaStream_t s);
+cudaError_t launch_logits_f32(const mt_logits_call_t &c, cudaStream_t s);
+cudaError_t launch_logits_f16(const mt_logits_call_t &c, cudaStream_t s);
+cudaError_t launch_logits_bf16(const mt_logits_call_t &c, cudaStream_t s);
 
 }  // namespace mt
