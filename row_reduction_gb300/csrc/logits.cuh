@@ -98,10 +98,23 @@ __device__ __forceinline__ unsigned in_use(const unsigned *used, int pack) {
     return V == 8 ? byte : byte >> (pack & 1) * 4 & 15u;
 }
 
+// Adds (or ORs) to a word of shared memory where `on`.
+template <bool OR>
+__device__ __forceinline__ void red_shared(bool on, unsigned at, unsigned v) {
+    if (OR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+                     "@p red.shared.or.b32 [%1], %2;\n\t}" ::"r"((unsigned)on),
+                     "r"(at), "r"(v) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+                     "@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"((unsigned)on),
+                     "r"(at), "r"(v) : "memory");
+}
+
 template <int V>
 struct Found {
     unsigned column, top;  // shared addresses: entry j at column + 128 j
-    unsigned *count, *used;
+    unsigned count, used;  // shared addresses
     Place<V> place;
 
     // Four ids; `left` of them are there, `prompt` of them the prompt's.  No
@@ -135,19 +148,37 @@ struct Found {
     // frequent tokens cost a read instead of atomics on one address.
     __device__ __forceinline__ void drain() {
 #pragma unroll 1
-        for (unsigned at = column; __any_sync(kFull, at < top); at += 128) {
-            if (at >= top) continue;
-            unsigned entry;
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(entry) : "r"(at) : "memory");
-            const int i = place.element((int)(entry & ~kPrompt));
-            const unsigned before =
-                *static_cast<volatile unsigned *>(count + i);
-            if (before == 0) atomicOr(used + (i >> 5), 1u << (i & 31));
-            if (!(entry & kPrompt))
-                atomicAdd(count + i, 1u);
-            else if (!(before & kPrompt))
-                atomicOr(count + i, kPrompt);
+        for (unsigned at = column; __any_sync(kFull, at < top); at += 256) {
+            // two entries of the lane at a time
+            unsigned entry[2], i[2], before[2];
+            bool there[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                there[j] = at + 128 * j < top;
+                entry[j] = 0;
+                if (there[j])
+                    asm volatile("ld.shared.u32 %0, [%1];"
+                                 : "=r"(entry[j]) : "r"(at + 128 * j)
+                                 : "memory");
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                i[j] = (unsigned)place.element((int)(entry[j] & ~kPrompt));
+                before[j] = 0;
+                if (there[j])
+                    asm volatile("ld.volatile.shared.u32 %0, [%1];"
+                                 : "=r"(before[j]) : "r"(count + 4 * i[j])
+                                 : "memory");
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool prompt = entry[j] & kPrompt;
+                red_shared<true>(there[j] && before[j] == 0,
+                                 used + (i[j] >> 5) * 4, 1u << (i[j] & 31));
+                red_shared<true>(there[j] && prompt && !(before[j] & kPrompt),
+                                 count + 4 * i[j], kPrompt);
+                red_shared<false>(there[j] && !prompt, count + 4 * i[j], 1u);
+            }
         }
         top = column;
     }
@@ -217,6 +248,30 @@ __global__ void __launch_bounds__(kMaxThreads,
         ((((tid >> 5) << p.log2C) + rank) * 32 + (tid & 31)) * V - shift;
     const int next = (T_ << p.log2C) * V;
 
+    // Everything that the row needs is asked for before any of it is waited
+    // for, what is needed first before the rest: the row's parameters and
+    // first tokens, the logits, the mask.  What is computed from them stands
+    // behind the counting.
+    const float rep = c.repetition ? c.repetition[row] : 1.f;
+    const float freq = c.frequency ? c.frequency[row] : 0.f;
+    const float pres = c.presence ? c.presence[row] : 0.f;
+    const float temp = c.temperature ? c.temperature[row] : 1.f;
+    const int length = c.lengths ? c.lengths[row] : c.history;
+    const int prompt = c.prompt_lengths ? c.prompt_lengths[row] : 0;
+    const bool marks = c.tokens != nullptr || c.biases > 0;
+    const int32_t *ids = c.tokens + row * c.tokens_stride;
+    const int quads = c.tokens && p.wide_tokens ? c.history >> 2 : 0;
+    // 16-byte loads of tokens, four in flight per thread
+    const auto quad = [ids, quads](int q) {
+        return q < quads ? reinterpret_cast<const int4 *>(ids)[q]
+                         : make_int4(-1, -1, -1, -1);
+    };
+    int4 v0 = quad(tid), v1 = quad(tid + T_);
+    int4 w0 = quad(tid + 2 * T_), w1 = quad(tid + 3 * T_);
+    const int32_t *row_bias_ids = c.bias_ids + row * c.biases;
+    const float *row_bias = c.bias + row * c.biases;
+    const int my_bias_id = tid < c.biases ? row_bias_ids[tid] : -1;
+    const float my_bias = tid < c.biases ? row_bias[tid] : 0.f;
     // The CTA's logits; packs that are cut by an end of the row are read
     // value by value.
     Raw<T, V> raw[K];
@@ -240,15 +295,6 @@ __global__ void __launch_bounds__(kMaxThreads,
                 }
         }
     }
-    // Everything that the row needs is asked for before any of it is waited
-    // for: the logits above, the row's parameters, the mask, the first
-    // tokens.  What is computed from them stands behind the counting.
-    const float rep = c.repetition ? c.repetition[row] : 1.f;
-    const float freq = c.frequency ? c.frequency[row] : 0.f;
-    const float pres = c.presence ? c.presence[row] : 0.f;
-    const float temp = c.temperature ? c.temperature[row] : 1.f;
-    const int length = c.lengths ? c.lengths[row] : c.history;
-    const int prompt = c.prompt_lengths ? c.prompt_lengths[row] : 0;
     // The one or two mask bytes of a pack's columns (one where packs start
     // at a multiple of their width).
     const uint8_t *mask =
@@ -272,27 +318,21 @@ __global__ void __launch_bounds__(kMaxThreads,
                 bits1[k] = __ldg(mask + (last >> 3));
         }
     }
-    const bool marks = c.tokens != nullptr || c.biases > 0;
     unsigned *used = count + p.packs * V;
-    float *bias = reinterpret_cast<float *>(used + p.packs * V / 32);
+    unsigned *found_at = used + p.packs * V / 32;
+    float *bias = reinterpret_cast<float *>(found_at + T_ * kRoom);
     int32_t *bias_ids = reinterpret_cast<int32_t *>(bias + c.biases);
-    unsigned *found_at = reinterpret_cast<unsigned *>(bias_ids + c.biases);
     if (marks) {
-        const int32_t *ids = c.tokens + row * c.tokens_stride;
-        const int quads = p.wide_tokens ? c.history >> 2 : 0;
-        // 16-byte loads of tokens, four in flight per thread
-        const auto quad = [ids, quads](int q) {
-            return q < quads ? reinterpret_cast<const int4 *>(ids)[q]
-                             : make_int4(-1, -1, -1, -1);
-        };
-        int4 v0 = quad(tid), v1 = quad(tid + T_);
-        int4 w0 = quad(tid + 2 * T_), w1 = quad(tid + 3 * T_);
         for (int i = tid; i < p.packs * V / 4; i += T_)
             reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
         for (int i = tid; i < p.packs * V / 32; i += T_) used[i] = 0;
-        for (int i = tid; i < c.biases; i += T_) {
-            bias_ids[i] = c.bias_ids[row * c.biases + i];
-            bias[i] = c.bias[row * c.biases + i];
+        if (tid < c.biases) {
+            bias_ids[tid] = my_bias_id;
+            bias[tid] = my_bias;
+        }
+        for (int i = tid + T_; i < c.biases; i += T_) {
+            bias_ids[i] = row_bias_ids[i];
+            bias[i] = row_bias[i];
         }
         const int len = min(max(length, 0), c.history);
         // Whole warps go through the history together; what the first ids
@@ -301,7 +341,9 @@ __global__ void __launch_bounds__(kMaxThreads,
         const Place<V> place(shift, p.log2C, rank, c.vocab);
         const unsigned column = (unsigned)__cvta_generic_to_shared(
             found_at + (tid >> 5) * 32 * kRoom + lane);
-        Found<V> found = {column, column, count, used, place};
+        Found<V> found = {column, column,
+                          (unsigned)__cvta_generic_to_shared(count),
+                          (unsigned)__cvta_generic_to_shared(used), place};
         int q0 = tid - lane;
         if (q0 < quads && q0 * 4 < len) {
             const int at = (q0 + lane) * 4;
@@ -370,8 +412,17 @@ __global__ void __launch_bounds__(kMaxThreads,
     }
     // Touched logits of the thread's own packs: their new values, FP32, take
     // the place of their counters.  A compact loop: few of them, and code that
-    // runs once per CTA costs its fetch.
+    // runs once per CTA costs its fetch.  It picks a pack's value by index
+    // from shared memory, where the thread's entries of the history were.
     if (marks) {
+        T *own = reinterpret_cast<T *>(found_at) + tid * V;
+        constexpr bool kOwn = K * V * (int)sizeof(T) <= 4 * kRoom;
+        if (kOwn) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (tid + k * T_ < p.packs && in_use<V>(used, tid + k * T_))
+                    raw[k].store(own + k * T_ * V);
+        }
 #pragma unroll 1
         for (int k = 0; k < K; ++k) {
             const int i = (tid + k * T_) * V;
@@ -382,7 +433,8 @@ __global__ void __launch_bounds__(kMaxThreads,
                 const int e = __ffs(hit) - 1, col = first + k * next + e;
                 hit &= hit - 1;
                 const unsigned m = count[i + e];
-                float v = touched(to_f(x[col]), m, rep, inv_rep, freq, pres);
+                float v = touched(to_f(kOwn ? own[k * T_ * V + e] : x[col]),
+                                  m, rep, inv_rep, freq, pres);
                 const unsigned b = m >> kBiasShift & kSeveral;
                 if (b == kSeveral)
                     v += several(bias, bias_ids, c.biases, col);
