@@ -638,12 +638,15 @@ cudaError_t launch_as(const mt_logits_call_t &c, cudaStream_t s) {
     if (p.c.history == 0) p.c.tokens = nullptr;
     p.wide_tokens = (reinterpret_cast<uintptr_t>(c.tokens) & 15) == 0 &&
                     (c.rows == 1 || c.tokens_stride % 4 == 0);
-    // Fewest packs per thread that 512 threads can do with; one pack per
-    // thread needs the fewest threads of a small slice.
+    // Fewest packs per thread that 512 threads can do with, fewest threads
+    // that do with that; more for a long history, which a CTA goes through
+    // alone.
     int K = 1;
     while (K < kMost && (int64_t)K * kMaxThreads < p.packs) K *= 2;
     int threads = 64;
-    while (threads < kMaxThreads && threads * K < p.packs) threads *= 2;
+    while (threads < kMaxThreads &&
+           (threads * K < p.packs || (p.c.tokens && threads * 8 < c.history)))
+        threads *= 2;
     const bool aligned =
         whole && c.vocab % V == 0 &&
         (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 &&
