@@ -33,6 +33,10 @@
 
 namespace mt {
 
+// Groups of heads whose loads a warp has in flight, for K slots per lane.
+template <int K>
+constexpr int kRotFlight = K == 1 ? 4 : (K == 2 ? 2 : 1);
+
 // A lane's slot: where its two packs are, and its values as V first and V
 // second members of pairs (a, b).
 template <typename T, int V, bool ILV>
@@ -154,16 +158,83 @@ __device__ __forceinline__ float head_sum(float v, int log2L) {
     return v;
 }
 
+// What the forward pass multiplies a pair with, once per token and tensor:
+//     y_a = r (a k1 + b k2),  y_b = r (a k3 + b k4).
+template <int V>
+struct RotFactors {
+    float k1[V], k2[V], k3[V], k4[V];
+};
+
+// Works on and stores U groups of heads of one tensor (the first `here` of
+// them exist, for whole warps): x's packs in raw, the lane's head of the
+// first group in `head`, `stride` heads and `ys` values of y between groups.
+template <typename T, int V, int K, bool ILV, bool NORM, int U>
+__device__ __forceinline__ void rot_groups(
+    const RotArgs &a, int l, int L, const typename RotSlot<T, V, ILV>::Packs
+    (*raw)[K], const RotFactors<V> *f, T *y, int64_t ys, int head, int stride,
+    int heads, int here, bool all_rot) {
+    using S = RotSlot<T, V, ILV>;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u >= here) break;
+        float va[K][V], vb[K][V];
+        float r = 1.f;
+        if (NORM) {
+            float sq[V];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                S::split(raw[u][k], va[k], vb[k]);
+                if (k == 0)
+                    mul_n<V>(sq, va[k], va[k]);
+                else
+                    fma_n<V>(sq, va[k], va[k], sq);
+                fma_n<V>(sq, vb[k], vb[k], sq);
+            }
+            float ss = sq[0];
+#pragma unroll
+            for (int e = 1; e < V; ++e) ss += sq[e];
+            r = rsqrtf(head_sum(ss, a.log2L) * a.inv_dim + a.eps);
+        }
+        T *out = y + u * ys;
+        const bool there = head + u * stride < heads;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const S slot(a, l + k * L);
+            if (!slot.in || !there) continue;
+            if (!NORM) {
+                if (!all_rot && !slot.rot) {  // copied bit for bit
+                    raw[u][k].lo.store(out + slot.lo);
+                    if (slot.second) raw[u][k].hi.store(out + slot.hi);
+                    continue;
+                }
+                S::split(raw[u][k], va[k], vb[k]);
+            }
+            float oa[V], ob[V];
+            mul_n<V>(oa, va[k], f[k].k1);
+            mul_n<V>(ob, vb[k], f[k].k4);
+            if (all_rot || slot.rot) {  // 0 times a neighbour may be NaN
+                fma_n<V>(oa, vb[k], f[k].k2, oa);
+                fma_n<V>(ob, va[k], f[k].k3, ob);
+            }
+            if (NORM) {
+                scale_n<V>(oa, oa, r);
+                scale_n<V>(ob, ob, r);
+            }
+            slot.store(out, oa, ob);
+        }
+    }
+}
+
 // Forward (and, with the sines' sign turned, backward without norm).  The
 // loads of U groups of heads are issued before the angles are computed and
-// before any of them is used.  With the norm, weights and rotation become
-// four coefficients per pair, once per token and tensor:
-//     y_a = r (a k1 + b k2),  y_b = r (a k3 + b k4).
-template <typename T, int V, int K, bool ILV, bool NORM>
+// before any of them is used.  FEW: a warp has at most U/2 groups of queries
+// and U/2 of keys, all of them asked for at once.
+template <typename T, int V, int K, bool ILV, bool NORM, bool FEW>
 __global__ void __launch_bounds__(kRotThreads, 2)
     rotary_kernel(const RotArgs a) {
     using S = RotSlot<T, V, ILV>;
-    constexpr int U = K == 1 ? 4 : (K == 2 ? 2 : 1);
+    constexpr int U = kRotFlight<K>;
+    constexpr int H = FEW ? U / 2 : U;  // groups of one tensor at a time
     grid_launch_dependents();
     grid_wait_prerequisites();
     const int lane = threadIdx.x & 31;
@@ -187,100 +258,80 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < K; ++k) raw[u][k].zero();
-    const auto load = [&](const T *x, int64_t step, int head, int heads) {
+    const auto load = [&](const T *x, int64_t step, int head, int heads,
+                          int at) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < H; ++u)
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 S(a, l + k * L).load(x + u * step, head + u * stride < heads,
-                                     raw[u][k]);
+                                     raw[FEW ? at + u : u][k]);
     };
     const int q0 = first * heads_per_warp + sub;
     load(static_cast<const T *>(a.t[0].x) + t * a.t[0].xt + q0 * a.t[0].xh,
-         stride * a.t[0].xh, q0, a.t[0].heads);
+         stride * a.t[0].xh, q0, a.t[0].heads, 0);
+    if (FEW) {
+        const int k0 = first_k * heads_per_warp + sub;
+        load(static_cast<const T *>(a.t[1].x) + t * a.t[1].xt +
+                 k0 * a.t[1].xh,
+             stride * a.t[1].xh, k0, a.t[1].heads, H);
+    }
     float c[K][V], s[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
         S(a, l + k * L).angles(a, pos, l + k * L, c[k], s[k]);
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        const RotHeads &h = a.t[i];
-        const int g0 = i == 0 ? first : first_k;
-        if (g0 >= h.groups) continue;
-        int head = g0 * heads_per_warp + sub;
-        const int heads = h.heads;
-        const int64_t xs = stride * h.xh, ys = stride * h.yh;
-        const T *x = static_cast<const T *>(h.x) + t * h.xt + head * h.xh;
-        T *y = static_cast<T *>(h.y) + t * h.yt + head * h.yh;
-        float k1[K][V], k2[K][V], k3[K][V], k4[K][V];
+    const auto factors = [&](const T *weight, RotFactors<V> *f) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float wa[V], wb[V];
-            if (NORM)
-                S(a, l + k * L).weights(static_cast<const T *>(h.w), wa, wb);
+            if (NORM) S(a, l + k * L).weights(weight, wa, wb);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                k1[k][e] = NORM ? wa[e] * c[k][e] : c[k][e];
-                k2[k][e] = NORM ? -wb[e] * s[k][e] : -s[k][e];
-                k3[k][e] = NORM ? wa[e] * s[k][e] : s[k][e];
-                k4[k][e] = NORM ? wb[e] * c[k][e] : c[k][e];
+                f[k].k1[e] = NORM ? wa[e] * c[k][e] : c[k][e];
+                f[k].k2[e] = NORM ? -wb[e] * s[k][e] : -s[k][e];
+                f[k].k3[e] = NORM ? wa[e] * s[k][e] : s[k][e];
+                f[k].k4[e] = NORM ? wb[e] * c[k][e] : c[k][e];
             }
         }
+    };
+    if constexpr (FEW) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const RotHeads &h = a.t[i];
+            const int g0 = i == 0 ? first : first_k;
+            if (g0 >= h.groups) continue;
+            const int head = g0 * heads_per_warp + sub;
+            RotFactors<V> f[K];
+            factors(static_cast<const T *>(h.w), f);
+            rot_groups<T, V, K, ILV, NORM, H>(
+                a, l, L, raw + i * H, f,
+                static_cast<T *>(h.y) + t * h.yt + head * h.yh,
+                stride * h.yh, head, stride, h.heads,
+                (h.groups - g0 + split - 1) >> a.log2S, all_rot);
+        }
+    } else {
 #pragma unroll 1
-        for (int g = g0; g < h.groups; g += U * split) {
-            if (i != 0 || g != g0) load(x, xs, head, heads);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (g + u * split >= h.groups) break;  // whole warps
-                float va[K][V], vb[K][V];
-                float r = 1.f;
-                if (NORM) {
-                    float sq[V];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        S::split(raw[u][k], va[k], vb[k]);
-                        if (k == 0)
-                            mul_n<V>(sq, va[k], va[k]);
-                        else
-                            fma_n<V>(sq, va[k], va[k], sq);
-                        fma_n<V>(sq, vb[k], vb[k], sq);
-                    }
-                    float ss = sq[0];
-#pragma unroll
-                    for (int e = 1; e < V; ++e) ss += sq[e];
-                    r = rsqrtf(head_sum(ss, a.log2L) * a.inv_dim + a.eps);
-                }
-                T *out = y + u * ys;
-                const bool there = head + u * stride < heads;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const S slot(a, l + k * L);
-                    if (!slot.in || !there) continue;
-                    if (!NORM) {
-                        if (!all_rot && !slot.rot) {  // copied bit for bit
-                            raw[u][k].lo.store(out + slot.lo);
-                            if (slot.second) raw[u][k].hi.store(out + slot.hi);
-                            continue;
-                        }
-                        S::split(raw[u][k], va[k], vb[k]);
-                    }
-                    float oa[V], ob[V];
-                    mul_n<V>(oa, va[k], k1[k]);
-                    mul_n<V>(ob, vb[k], k4[k]);
-                    if (all_rot || slot.rot) {  // 0 * a neighbour may be NaN
-                        fma_n<V>(oa, vb[k], k2[k], oa);
-                        fma_n<V>(ob, va[k], k3[k], ob);
-                    }
-                    if (NORM) {
-                        scale_n<V>(oa, oa, r);
-                        scale_n<V>(ob, ob, r);
-                    }
-                    slot.store(out, oa, ob);
-                }
+        for (int i = 0; i < 2; ++i) {
+            const RotHeads &h = a.t[i];
+            const int g0 = i == 0 ? first : first_k;
+            if (g0 >= h.groups) continue;
+            int head = g0 * heads_per_warp + sub;
+            const int heads = h.heads;
+            const int64_t xs = stride * h.xh, ys = stride * h.yh;
+            const T *x = static_cast<const T *>(h.x) + t * h.xt + head * h.xh;
+            T *y = static_cast<T *>(h.y) + t * h.yt + head * h.yh;
+            RotFactors<V> f[K];
+            factors(static_cast<const T *>(h.w), f);
+#pragma unroll 1
+            for (int g = g0; g < h.groups; g += U * split) {
+                if (i != 0 || g != g0) load(x, xs, head, heads, 0);
+                rot_groups<T, V, K, ILV, NORM, U>(
+                    a, l, L, raw, f, y, ys, head, stride, heads,
+                    (h.groups - g + split - 1) >> a.log2S, all_rot);
+                x += U * xs;
+                y += U * ys;
+                head += U * stride;
             }
-            x += U * xs;
-            y += U * ys;
-            head += U * stride;
         }
     }
 }
@@ -492,16 +543,25 @@ cudaError_t rot_dispatch(int V, int K, F f) {
     return cudaErrorInvalidValue;
 }
 
+// FEW where the groups of each tensor fit half of a warp's loads in flight
+// (BF16, 57359 tokens of 15 + 3 heads of 64, norm: 93 us without it).
 template <typename T, bool ILV, bool NORM>
 cudaError_t launch_rotary_as(const RotArgs &a, int V, int K, cudaStream_t s) {
     const int64_t units = a.tokens << a.log2S;
     const int64_t grid =
         (units + kRotThreads / 32 - 1) / (kRotThreads / 32);
+    const int most = a.t[0].groups > a.t[1].groups ? a.t[0].groups
+                                                   : a.t[1].groups;
     return rot_dispatch<T, ILV>(V, K, [&](auto v, auto k) {
-        return launch_dependent(
-            rotary_kernel<T, decltype(v)::value, decltype(k)::value, ILV,
-                          NORM>,
-            grid, kRotThreads, 0, s, a);
+        constexpr int VV = decltype(v)::value, KK = decltype(k)::value;
+        if constexpr (kRotFlight<KK> > 1) {
+            if (most <= kRotFlight<KK> / 2 << a.log2S)
+                return launch_dependent(
+                    rotary_kernel<T, VV, KK, ILV, NORM, true>, grid,
+                    kRotThreads, 0, s, a);
+        }
+        return launch_dependent(rotary_kernel<T, VV, KK, ILV, NORM, false>,
+                                grid, kRotThreads, 0, s, a);
     });
 }
 
