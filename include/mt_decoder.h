@@ -26,8 +26,9 @@
  *            rule gives MT_ERR_INVALID_ARGUMENT, a size beyond a stated limit
  *            MT_ERR_UNSUPPORTED, a workspace that is too small
  *            MT_ERR_OUT_OF_RESOURCES.  Calls with nothing to do (no tokens,
- *            no rows) return MT_OK without a launch and outputs untouched,
- *            except weight gradients, which are set to zero.
+ *            no rows, a cache without slots) return MT_OK without a launch
+ *            and outputs untouched, except weight gradients, which are set to
+ *            zero.
  * Numerics   FP32 arithmetic with one rounding at each output store (half
  *            step, to nearest even); sums run in a fixed order, so the same
  *            call gives the same bits.  No float atomics.

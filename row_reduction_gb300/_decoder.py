@@ -301,7 +301,9 @@ class _On:
             self.context = _torch.cuda.device(index)
             self.handle = _torch.cuda.current_stream(index).cuda_stream
             return
-        if isinstance(stream, int):
+        if stream == 0:
+            stream = _torch.cuda.default_stream(index)
+        elif isinstance(stream, int):
             stream = _torch.cuda.ExternalStream(stream, device=index)
         if stream.device.index != index:
             raise ValueError(f"stream is on {stream.device}, the tensors are "

@@ -235,7 +235,7 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     if (c->slots > kMaxOffset / width) return MT_ERR_INVALID_ARGUMENT;
     const int es = dtype_size(dtype);
     const bool both = c->v.codes || c->v.scales || c->v.rows;
-    *empty = c->tokens == 0;
+    *empty = c->tokens == 0 || c->slots == 0;
     uint64_t bits = 0, code_bits = 0;
     const mt_cache_rows_t *rs[2] = {&c->k, &c->v};
     for (int i = 0; i < (both ? 2 : 1); ++i) {
@@ -280,8 +280,10 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     a->dim = c->dim;
     a->group = c->group;
     a->int8 = c->format == MT_CACHE_INT8;
-    // threads of a call (a warp per group at most) must fit a grid
-    if (c->tokens > (1LL << 36) / width) return MT_ERR_UNSUPPORTED;
+    // The kernels for any sizes take a warp per group (or a thread per
+    // value), which must fit a grid; the wide ones loop.
+    if (c->tokens > (1LL << (*vec ? 40 : 32)) / width)
+        return MT_ERR_UNSUPPORTED;
     return MT_OK;
 }
 
@@ -472,7 +474,7 @@ mt_status mt_cache_write(int dtype, const mt_cache_call_t *call,
     bool empty = false;
     if (mt_status st = cache_setup(dtype, call, true, &a, &vec, &empty))
         return st;
-    if (empty || a.slots == 0) return MT_OK;
+    if (empty) return MT_OK;
     return status_from_cuda(
         launch_cache_write(dtype, a, vec, (cudaStream_t)stream));
 }
@@ -484,7 +486,7 @@ mt_status mt_cache_read(int dtype, const mt_cache_call_t *call,
     bool empty = false;
     if (mt_status st = cache_setup(dtype, call, false, &a, &vec, &empty))
         return st;
-    if (empty || a.slots == 0) return MT_OK;
+    if (empty) return MT_OK;
     return status_from_cuda(
         launch_cache_read(dtype, a, vec, (cudaStream_t)stream));
 }
@@ -559,9 +561,13 @@ mt_status mt_process_logits(int dtype, const mt_logits_call_t *call,
         return MT_ERR_INVALID_ARGUMENT;
     if (c.rows > (1LL << 24)) return MT_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
-    return status_from_cuda(dtype == DT_F32   ? launch_logits_f32(c, s)
-                            : dtype == DT_F16 ? launch_logits_f16(c, s)
-                                              : launch_logits_bf16(c, s));
+    try {
+        return status_from_cuda(dtype == DT_F32   ? launch_logits_f32(c, s)
+                                : dtype == DT_F16 ? launch_logits_f16(c, s)
+                                                  : launch_logits_bf16(c, s));
+    } catch (...) {  // no memory for a table of what kernels were set up
+        return MT_ERR_OUT_OF_RESOURCES;
+    }
 }
 
 }  // extern "C"

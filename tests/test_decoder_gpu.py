@@ -727,6 +727,99 @@ def test_process_logits_refuses_on_the_device():
         mt.process_logits(torch.zeros(1, 524281, device="cuda"))
 
 
+def test_calls_with_nothing_to_do():
+    """Empty batches: outputs of the right shapes, nothing written."""
+    _, _, tab = table(16)
+    q = torch.empty(0, 2, 16, dtype=torch.bfloat16, device="cuda")
+    pos = torch.empty(0, dtype=torch.int64, device="cuda")
+    y, z = mt.rotary(q, q[:, :1], pos, tab, eps=1e-6)
+    assert y.shape == (0, 2, 16) and z.shape == (0, 1, 16)
+    c = mt.cache_alloc(4, 2, 16)
+    s = torch.empty(0, dtype=torch.int64, device="cuda")
+    mt.cache_write(q, q, c, mt.cache_alloc(4, 2, 16), s)
+    assert mt.cache_read(c, None, s).shape == (0, 2, 16)
+    none = mt.cache_alloc(0, 2, 16)         # a cache without slots
+    x = torch.ones(3, 2, 16, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, -1], device="cuda")
+    mt.cache_write(x, None, none, None, at)
+    assert bool((mt.cache_read(none, None, at) == 0).all())
+    e = torch.empty(0, 50, device="cuda")
+    for mode in ("logits", "softmax"):
+        assert mt.process_logits(e, mode=mode, tokens=torch.empty(
+            0, 4, dtype=torch.int32, device="cuda")).shape == (0, 50)
+    t = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    o = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert mt.cache_slots(t, o, o[:0], 16, 2).tolist() == [-1, -1]
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotary_keys_alone_and_more_keys_than_queries(norm):
+    q, k, pos, wq, wk = rot_inputs(17, 30, 1, 9, 32, torch.bfloat16)
+    freqs, scale, tab = table(32)
+    kw = dict(eps=1e-6) if norm else {}
+    eps = 1e-6 if norm else None
+    for a in (q, q[:, :0]):  # one query head, none
+        y, z = mt.rotary(a, k, pos, tab, **(
+            dict(kw, q_weight=wq, k_weight=wk) if norm else {}))
+        ref, err = rotary_ref(k, pos, freqs, scale, 32, False,
+                              wk if norm else None, eps)
+        check(z, ref, err + half_step(ref, torch.bfloat16))
+        assert y.shape == a.shape
+        g = mt.rotary_backward(a, k, pos, tab, **(
+            dict(kw, q=a, k=k, q_weight=wq, k_weight=wk) if norm else {}))
+        dx, err, dw, werr = rotary_backward_ref(
+            k, k, pos, freqs, scale, 32, False, wk, eps)
+        check(g[1], dx, err + half_step(dx, torch.bfloat16))
+        if norm:
+            check(g[3], dw, werr)
+            if a.shape[1] == 0:
+                assert bool((g[2] == 0).all())
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotary_backward_with_a_scale(norm):
+    """The factor of a scaled rotation, part of a head, float32."""
+    f, s = mt.mt_rotary_frequencies(24, 10000.0, mt.MtRotaryScaling(
+        type=mt.MT_ROTARY_YARN, factor=4.0, original_length=64.0, low=1.0,
+        high=32.0))
+    tab = mt.rotary_frequencies(24, scaling=dict(
+        type="yarn", factor=4.0, original_length=64))
+    q, _, pos, wq, _ = rot_inputs(18, 13, 2, 1, 40, torch.float32)
+    dq, _, _, _, _ = rot_inputs(19, 13, 2, 1, 40, torch.float32)
+    kw = dict(q=q, q_weight=wq, eps=1e-6) if norm else {}
+    g = mt.rotary_backward(dq, None, pos, tab, interleaved=True, **kw)
+    dx, err, dw, werr = rotary_backward_ref(
+        dq, q, pos, f, s, 24, True, wq, 1e-6 if norm else None)
+    check(g[0], dx, err + half_step(dx, torch.float32))
+    if norm:
+        check(g[2], dw, werr)
+
+
+def test_rotary_rows_of_zeros_without_eps():
+    """eps = 0: a zero row is 0/0, and no head that is not there adds a NaN to
+    the weight's gradient."""
+    q, _, pos, wq, _ = rot_inputs(20, 9, 3, 1, 32, torch.float32)
+    freqs, scale, tab = table(32)
+    g = mt.rotary_backward(q, None, pos, tab, q=q, q_weight=wq, eps=0.0)
+    dx, err, dw, werr = rotary_backward_ref(q, q, pos, freqs, scale, 32,
+                                            False, wq, 0.0)
+    check(g[0], dx, err + half_step(dx, torch.float32))
+    check(g[2], dw, werr)
+
+
+@pytest.mark.parametrize("rows,vocab,history", [
+    (3, 200, 30000), (1, 64, 5000), (40, 1000, 2047), (2, 9000, 33333)])
+def test_process_logits_long_histories_of_small_vocabularies(rows, vocab,
+                                                            history):
+    """Every CTA's queue fills and drains many times; counts stay exact (a
+    frequency of 2^-12 makes the sums exact in FP32)."""
+    x, kw = logits_inputs(rows + history, rows, vocab, history, 40, True)
+    kw["frequency"] = torch.full((rows,), 2.0 ** -12, device="cuda")
+    for mode in ("logits", "softmax"):
+        y = mt.process_logits(x, mode=mode, **kw)
+        check_logits(x, kw, mode, y)
+
+
 # ---- streams, graphs, together -----------------------------------------------
 def test_other_stream_and_large_offsets():
     """Work on a stream of its own; more than 2^31 values of rows."""
@@ -745,7 +838,10 @@ def test_other_stream_and_large_offsets():
                           128, False, None, None)
     check(x[[0, 300_000, tokens - 1]], ref,
           err + half_step(ref, torch.bfloat16))
-    # the stream as a raw handle
+    # the stream as a raw handle, 0 for the default stream
+    z = mt.process_logits(torch.ones(2, 10, device="cuda"), stream=0)
+    torch.cuda.synchronize()
+    assert bool((z == 1).all())
     y = mt.process_logits(torch.ones(2, 10, device="cuda"), mode="softmax",
                           stream=s.cuda_stream)
     s.synchronize()

@@ -307,7 +307,7 @@ def cache(k=None, v=None, **kw):
     (cache(heads=1 << 20, dim=16), UNS),
     (cache(slots=2 ** 60), INV),
     (cache(k=rows(token_stride=2 ** 62)), INV),
-    (cache(tokens=2 ** 36), UNS),
+    (cache(tokens=2 ** 36), UNS), (cache(tokens=2 ** 28, group=4), UNS),
 ])
 def test_cache_refuses(c, want, write):
     with pytest.raises(mt.MTError) as e:
