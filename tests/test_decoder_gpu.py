@@ -705,6 +705,47 @@ def test_process_logits_more_than_2_31_values():
                  x[[0, 9000, rows - 1]])
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", ["logits", "softmax", "log_softmax"])
+@pytest.mark.parametrize("rows,vocab,history,biases,mask", [
+    (1300, 32000, 300, 20, True), (700, 33008, 0, 0, False),
+    (400, 131072, 2500, 3, True), (5000, 4008, 40, 0, False)])
+def test_process_logits_many_rows(dt, mode, rows, vocab, history, biases,
+                                  mask):
+    """More rows than the device holds at once: some against the 64-bit form
+    (rows masked out as a whole among them), others against a call on few
+    rows, which shares a row out between more CTAs; then in place."""
+    x, kw = logits_inputs(rows, rows, vocab, history, biases, mask,
+                          DTYPES[dt])
+    if mask:
+        kw["mask"][5] = 0
+        kw["mask"][rows - 2] = 0
+    y = mt.process_logits(x, mode=mode, **kw)
+    for r in (0, 5, rows // 2, rows - 2, rows - 1):
+        one = {n: t[r:r + 1].contiguous() for n, t in kw.items()}
+        check_logits(x[r:r + 1], one, mode, y[r:r + 1], f"row {r}")
+    for lo in range(0, rows, 97):
+        some = {n: t[lo:lo + 3].contiguous() for n, t in kw.items()}
+        z = mt.process_logits(x[lo:lo + 3], mode=mode, **some)
+        if mode == "logits":  # the same FP32 steps
+            assert torch.equal(y[lo:lo + 3], z)
+            continue
+        # Each is within |d| 2^-22 (the exponent's roundings) + 200 U (the
+        # sum's) of the exact value, relative for a softmax and absolute for
+        # its logarithm, d the distance to the row's maximum: |d| <= |ln p|,
+        # since the sum is at least 1.  Twice that, and a step of storage.
+        z = z.double()
+        log = z if mode == "log_softmax" else torch.log(z)
+        off = 2 * (torch.nan_to_num(log, neginf=0.0).abs() * 2.0 ** -22 +
+                   200 * 2.0 ** -24)
+        size = torch.nan_to_num(z, neginf=0.0).abs()
+        check(y[lo:lo + 3], z, (off if mode == "log_softmax" else off * size) +
+              torch.finfo(x.dtype).eps * size + 1e-37, f"rows from {lo}")
+    w = x.clone()
+    mt.process_logits(w, mode=mode, out=w, **kw)
+    assert torch.equal(w, y)
+
+
 def test_process_logits_refuses_on_the_device():
     x = torch.zeros(2, 100, device="cuda")
     ids = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
