@@ -383,6 +383,14 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, freqs=None,
         factor if scale is None else float(scale), rotary_dim)
 
 
+def _new_like(t, shape, st0, st1):
+    """A new dense tensor of t's shape: empty_like, the quicker call, unless
+    rows repeat (its strides may then be in any order)."""
+    if st0 and st1:
+        return _torch.empty_like(t)
+    return _torch.empty(shape, dtype=t.dtype, device=t.device)
+
+
 _ABSENT = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
 
 
@@ -459,13 +467,13 @@ def _rotary(dt, index, handle, q, k, positions, freqs, interleaved, q_weight,
     elif k_weight is not None:
         raise ValueError("k_weight without k")
     if yq is None:
-        yq = _torch.empty(shape, dtype=dtype, device=q.device)
+        yq = _new_like(q, shape, xt, xh)
     y, yt, yh = _heads(yq, "out (q)", dtype, shape, index)
     if k is None:
         keys = _ABSENT
     else:
         if yk is None:
-            yk = _torch.empty(k_shape, dtype=dtype, device=q.device)
+            yk = _new_like(k, k_shape, kxt, kxh)
         ky, kyt, kyh = _heads(yk, "out (k)", dtype, k_shape, index)
         keys = (kx, 0, ky, kw, 0, kxt, kxh, 0, 0, kyt, kyh, k_shape[1], 0)
     _call("mt_rotary", dt,
@@ -497,9 +505,8 @@ def rotary_backward(dq, dk, positions, freqs, interleaved=False, q=None,
                             interleaved, q, k, q_weight, k_weight, eps, out)
 
 
-def _gradients(name, g, x, y, w, tokens, dim, dtype, eps, index):
-    """One tensor of a backward call: its fields, its gradient and its
-    weight's."""
+def _gradients(name, g, x, y, w, dw, tokens, dim, dtype, eps, index):
+    """One tensor of a backward call: its fields and its gradient."""
     shape = (tokens, _three(g, "d" + name)[1], dim)
     d, dt_, dh = _heads(g, "d" + name, dtype, shape, index)
     px = xt = xh = 0
@@ -507,14 +514,12 @@ def _gradients(name, g, x, y, w, tokens, dim, dtype, eps, index):
         if x is None:
             raise ValueError(f"the norm's backward pass needs {name}")
         px, xt, xh = _heads(x, name, dtype, shape, index)
-    pw, dw, pdw = _weight(w, name + "_weight", dtype, dim, eps, index), None, 0
+    pw = _weight(w, name + "_weight", dtype, dim, eps, index)
     if y is None:
-        y = _torch.empty(shape, dtype=dtype, device=g.device)
+        y = _new_like(g, shape, dt_, dh)
     py, yt, yh = _heads(y, f"out ({name})", dtype, shape, index)
-    if w is not None:
-        dw = _torch.empty(dim, dtype=_torch.float32, device=g.device)
-        pdw = dw.data_ptr()
-    return (px, d, py, pw, pdw, xt, xh, dt_, dh, yt, yh, shape[1], 0), y, dw
+    pdw = 0 if dw is None else dw.data_ptr()
+    return (px, d, py, pw, pdw, xt, xh, dt_, dh, yt, yh, shape[1], 0), y
 
 
 def _rotary_backward(dt, index, handle, dq, dk, positions, freqs, interleaved,
@@ -523,12 +528,19 @@ def _rotary_backward(dt, index, handle, dq, dk, positions, freqs, interleaved,
     tokens, _, dim = _three(dq, "dq")
     tail = _tail(positions, freqs, tokens, dim, interleaved, eps, index)
     gq, gk = _out_pair(out, dk is None)
-    queries, gq, wq = _gradients("q", dq, q, gq, q_weight, tokens, dim, dtype,
-                                 eps, index)
-    keys, wk = _ABSENT, None
+    wq = wk = None
+    if eps is not None:
+        f32 = _torch.float32
+        if q_weight is not None:
+            wq = _torch.empty_like(q_weight, dtype=f32)
+        if k_weight is not None:
+            wk = _torch.empty_like(k_weight, dtype=f32)
+    queries, gq = _gradients("q", dq, q, gq, q_weight, wq, tokens, dim, dtype,
+                             eps, index)
+    keys = _ABSENT
     if dk is not None:
-        keys, gk, wk = _gradients("k", dk, k, gk, k_weight, tokens, dim,
-                                  dtype, eps, index)
+        keys, gk = _gradients("k", dk, k, gk, k_weight, wk, tokens, dim,
+                              dtype, eps, index)
     call = _ROTARY.pack(*queries, *keys, *tail)
     n, address = 0, None
     if wq is not None or wk is not None:
@@ -770,8 +782,7 @@ def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None,
 
     def run(handle, out):
         if out is None:
-            out = _torch.empty(logits.shape, dtype=dtype,
-                               device=logits.device)
+            out = _new_like(logits, logits.shape, x_stride, 1)
         y, y_stride, width = _rows(out, "out", dtype, rows, index)
         if width != vocab:
             raise ValueError(f"out must have shape {tuple(logits.shape)}, got "
