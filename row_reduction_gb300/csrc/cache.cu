@@ -180,7 +180,9 @@ __device__ __forceinline__ void store_values(T *p, const float2 *z) {
 
 // Writing: groups of up to 32 V values, V per lane and L lanes per group.
 // The next token's values are on their way while a token's are reduced and
-// stored.
+// stored.  Bound by the loads in flight: BF16, 16384 rows of 2 x 8 heads of
+// 128 to int8 by 64 20 us, 5.2 TB/s (36 us before rows overlapped, with
+// 16-byte accesses).
 template <typename T, bool INT8, int V>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     write_wide_kernel(const CacheArgs a, const Map m) {
@@ -287,7 +289,9 @@ __global__ void __launch_bounds__(kThreads)
 // Reading back.  A row's codes are contiguous (heads x dim bytes): V of them
 // per lane, the lane's place in the row the same for all its tokens.  N
 // tokens' codes are on their way while N tokens are stored, and the slots of
-// the N after them.
+// the N after them.  Bound by the loads in flight: 100003 rows of 2 x 8 heads
+// of 128 from e4m3 to BF16 106 us, 5.9 TB/s, 87% of the measured copy
+// bandwidth (117 us with 8 values per lane and no overlap of rows).
 template <typename T, bool INT8, int V, int N>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     read_wide_kernel(const CacheArgs a, const Map m) {

@@ -20,6 +20,12 @@
 // through distributed shared memory behind one cluster barrier, and each
 // thread scales its exponentials once.
 //
+// Bound.  Without history 5.3 us for 64 x 131072 BF16 (its bytes' time) and
+// 41 us for the softmax of 256 x 131072 (half the copy bandwidth).  With
+// history a CTA is a chain of short phases (count, touch, join, write), of
+// which the two CTAs that 64 registers allow per SM do not hide all: 19 us
+// with 8192 tokens and 300 biases per row, 65 us with 1024 tokens and a mask.
+//
 // Alignment.  Packs of V values start at 16-byte boundaries of x: pack p of
 // a row holds columns p V - shift + e, shift being the row's address modulo
 // 16 in elements, so only a row's first and last pack can be partial.

