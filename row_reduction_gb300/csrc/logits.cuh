@@ -15,9 +15,9 @@
 // CTAs: frequent tokens have low ids in most vocabularies, and contiguous
 // slices would give one CTA most of a row's history.
 //
-// Softmax.  A thread takes its exponentials about its own largest value; the
-// (max, sum) pairs of all warps of a row's CTAs, a cluster, are exchanged
-// through distributed shared memory behind one cluster barrier, and each
+// Softmax.  A thread takes its exponentials about its own largest value;
+// warps, then CTAs, join their (max, sum) pairs, the CTAs of a row, a cluster,
+// through distributed shared memory behind one cluster barrier; and each
 // thread scales its exponentials once.
 //
 // Bound.  Without history 5.3 us for 64 x 131072 BF16 (its bytes' time) and
@@ -91,12 +91,7 @@ struct Place {
     }
 };
 
-// Tokens of this CTA that a lane has found and not counted yet.  Few of a
-// history's tokens are a CTA's own, so the pass over the history only looks
-// and puts them by, each lane in a column of shared memory of its own; they
-// are counted when a lane may run out of room, most lanes at work.
-constexpr int kRoom = 16;   // entries per lane
-constexpr int kLooks = 8;   // ids that a lane looks at between two checks
+// The bits of a pack's counters that are in use.
 template <int V>
 __device__ __forceinline__ unsigned in_use(const unsigned *used, int pack) {
     const unsigned byte = reinterpret_cast<const uint8_t *>(used)[
@@ -117,6 +112,12 @@ __device__ __forceinline__ void red_shared(bool on, unsigned at, unsigned v) {
                      "r"(at), "r"(v) : "memory");
 }
 
+// Tokens of this CTA that a lane has found and not counted yet.  Few of a
+// history's tokens are a CTA's own, so the pass over the history only looks
+// and puts them by, each lane in a column of shared memory of its own; they
+// are counted when a lane may run out of room, most lanes at work.
+constexpr int kRoom = 16;   // entries per lane
+constexpr int kLooks = 8;   // ids that a lane looks at between two checks
 template <int V>
 struct Found {
     unsigned column, top;  // shared addresses: entry j at column + 128 j
@@ -486,6 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads,
         }
     }
     float mul = inv_temp, sub = 0.f, log_total = 0.f;
+    float nothing = -INFINITY;  // what a masked value gives
     if (MODE != MT_LOGITS) {
         // e^((v - w) / temperature) as 2^((v - w) a): the difference is
         // formed first (exact near w), so its error is 4 roundings of the
@@ -540,10 +542,15 @@ __global__ void __launch_bounds__(kMaxThreads,
                              : "memory");
         // Softmax: e^(v - top) e^(top - M) / total; a row with nothing left
         // has total 0 and gives 0.  Log-softmax: (v - M) / temperature -
-        // log(total); such a row keeps its -infinities.
-        if (MODE == MT_LOGITS_SOFTMAX)
-            mul = total == 0.f || top == -INFINITY
-                      ? 0.f : pow2((top - M) * a) / total;
+        // log(total); such a row keeps its -infinities.  A total that is NaN
+        // makes the whole row NaN, masked values too.
+        if (MODE == MT_LOGITS_SOFTMAX) {
+            mul = 0.f;
+            if (total != 0.f)
+                mul = (top == -INFINITY ? 0.f : pow2((top - M) * a)) / total;
+            nothing = 0.f * mul;
+        }
+        if (total != total) nothing = total;
         if (MODE == MT_LOGITS_LOG_SOFTMAX && total != 0.f) {
             sub = M;
             log_total = logf(total);
@@ -556,8 +563,7 @@ __global__ void __launch_bounds__(kMaxThreads,
         float *v = &z[k][0].x;
         if (keep[k] == 0) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                v[e] = MODE == MT_LOGITS_SOFTMAX ? 0.f : -INFINITY;
+            for (int e = 0; e < V; ++e) v[e] = nothing;
         } else {
 #pragma unroll
             for (int h = 0; h < V / 2; ++h) {

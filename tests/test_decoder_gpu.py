@@ -627,6 +627,24 @@ def test_process_logits_nan_and_infinity_where_allowed():
     assert torch.equal(torch.nan_to_num(z), torch.nan_to_num(x))
 
 
+@pytest.mark.parametrize("mode", ["softmax", "log_softmax"])
+@pytest.mark.parametrize("vocab", [100, 5003, 131072])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_process_logits_nan_rows_are_nan_as_a_whole(mode, vocab, value):
+    """One NaN (or +infinity, whose softmax is NaN) that the mask leaves, most
+    of the row masked out: every value of that row is NaN, no other row's."""
+    x, _ = logits_inputs(39, 3, vocab)
+    x[1, vocab - 2] = value
+    mask = torch.zeros(3, (vocab + 31) // 32, dtype=torch.int32,
+                       device="cuda")
+    mask[:, 0] = 0b110
+    at = vocab - 2
+    mask[:, at // 32] |= 1 << (at % 32) if at % 32 < 31 else -2 ** 31
+    y = mt.process_logits(x, mask=mask, mode=mode)
+    assert bool(torch.isnan(y[1]).all())
+    check_logits(x[::2], dict(mask=mask[::2].contiguous()), mode, y[::2])
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16"])
 @pytest.mark.parametrize("mode", ["logits", "softmax"])
 def test_process_logits_strided_rows(dt, mode):
