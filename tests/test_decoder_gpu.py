@@ -63,7 +63,8 @@ def table(rotary, **kw):
     (1, 1, 1, 2, 2), (1, 32, 8, 128, 128), (3, 2, 1, 64, 32), (7, 5, 3, 80, 40),
     (5, 3, 1, 96, 24), (2, 4, 4, 256, 256), (2, 3, 1, 512, 512),
     (4, 1, 1, 130, 66), (3, 2, 2, 17, 6), (2, 2, 1, 77, 70), (33, 9, 1, 20, 20),
-    (2, 1, 1, 511, 510), (300, 4, 2, 64, 64),
+    (2, 1, 1, 511, 510), (300, 4, 2, 64, 64), (3, 2, 1, 264, 264),
+    (3, 3, 1, 132, 132), (2600, 3, 1, 64, 32), (2500, 41, 9, 64, 64),
 ])
 def test_rotary(dt, norm, interleaved, tokens, hq, hk, dim, rotary):
     dtype = DTYPES[dt]
@@ -215,7 +216,8 @@ def test_rotary_values_that_pass_keep_infinities_and_nan(dim, rotary,
     (1, 1, 1, 2, 2), (1, 8, 2, 128, 128), (3, 2, 1, 64, 32), (7, 5, 3, 80, 40),
     (2, 3, 1, 512, 512), (4, 1, 1, 130, 66), (3, 2, 2, 17, 6),
     (2, 2, 1, 77, 70), (33, 9, 1, 20, 20), (5, 3, 0, 64, 64),
-    (200, 2, 1, 64, 64),
+    (200, 2, 1, 64, 64), (3, 2, 1, 264, 264), (3, 3, 1, 132, 132),
+    (2, 1, 1, 511, 510), (700, 33, 5, 64, 64),
 ])
 def test_rotary_backward(dt, norm, interleaved, tokens, hq, hk, dim, rotary):
     dtype = DTYPES[dt]
@@ -342,6 +344,7 @@ def snapshot(cache):
     (1, 1, 1, 1), (1, 8, 128, 128), (5, 3, 80, 80), (64, 2, 64, 32),
     (7, 1, 96, 24), (3, 2, 256, 256), (9, 4, 128, 16), (2, 1, 576, 576),
     (4, 3, 20, 5), (3, 5, 33, 11), (130, 1, 8, 8), (3, 2, 1024, 512),
+    (9001, 4, 64, 64), (3000, 1, 40, 8), (2, 700, 16, 16),
 ])
 def test_cache_write_and_read(dt, fmt, tokens, heads, dim, group):
     dtype = DTYPES[dt]
