@@ -230,14 +230,14 @@ __device__ __forceinline__ void rot_groups(
 // four groups): BF16, 16384 tokens of 32 + 8 heads of 128 with norm 60 us,
 // 5.6 TB/s, 82% of the measured copy bandwidth.  The
 // loads of U groups of heads are issued before the angles are computed and
-// before any of them is used.  FEW: a warp has at most U/2 groups of queries
-// and U/2 of keys, all of them asked for at once.
-template <typename T, int V, int K, bool ILV, bool NORM, bool FEW>
+// before any of them is used.  HQ < U: a warp has at most HQ groups of
+// queries and U - HQ of keys, all of them asked for at once.
+template <typename T, int V, int K, bool ILV, bool NORM, int HQ>
 __global__ void __launch_bounds__(kRotThreads, 2)
     rotary_kernel(const RotArgs a) {
     using S = RotSlot<T, V, ILV>;
     constexpr int U = kRotFlight<K>;
-    constexpr int H = FEW ? U / 2 : U;  // groups of one tensor at a time
+    constexpr bool kFew = HQ < U;
     grid_launch_dependents();
     grid_wait_prerequisites();
     const int lane = threadIdx.x & 31;
@@ -262,22 +262,26 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 #pragma unroll
         for (int k = 0; k < K; ++k) raw[u][k].zero();
     const auto load = [&](const T *x, int64_t step, int head, int heads,
-                          int at) {
+                          auto from, auto to) {
+        constexpr int at = decltype(from)::value, end = decltype(to)::value;
 #pragma unroll
-        for (int u = 0; u < H; ++u)
+        for (int u = 0; u < end - at; ++u)
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 S(a, l + k * L).load(x + u * step, head + u * stride < heads,
-                                     raw[FEW ? at + u : u][k]);
+                                     raw[at + u][k]);
     };
+    const std::integral_constant<int, 0> none{};
+    const std::integral_constant<int, HQ> keys{};
+    const std::integral_constant<int, U> all{};
     const int q0 = first * heads_per_warp + sub;
     load(static_cast<const T *>(a.t[0].x) + t * a.t[0].xt + q0 * a.t[0].xh,
-         stride * a.t[0].xh, q0, a.t[0].heads, 0);
-    if (FEW) {
+         stride * a.t[0].xh, q0, a.t[0].heads, none, keys);
+    if (kFew) {
         const int k0 = first_k * heads_per_warp + sub;
         load(static_cast<const T *>(a.t[1].x) + t * a.t[1].xt +
                  k0 * a.t[1].xh,
-             stride * a.t[1].xh, k0, a.t[1].heads, H);
+             stride * a.t[1].xh, k0, a.t[1].heads, keys, all);
     }
     float c[K][V], s[K][V];
 #pragma unroll
@@ -297,21 +301,23 @@ __global__ void __launch_bounds__(kRotThreads, 2)
             }
         }
     };
-    if constexpr (FEW) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+    if constexpr (kFew) {
+        const auto groups = [&](int i, auto from, auto to) {
+            constexpr int at = decltype(from)::value;
             const RotHeads &h = a.t[i];
             const int g0 = i == 0 ? first : first_k;
-            if (g0 >= h.groups) continue;
+            if (g0 >= h.groups) return;
             const int head = g0 * heads_per_warp + sub;
             RotFactors<V> f[K];
             factors(static_cast<const T *>(h.w), f);
-            rot_groups<T, V, K, ILV, NORM, H>(
-                a, l, L, raw + i * H, f,
+            rot_groups<T, V, K, ILV, NORM, decltype(to)::value - at>(
+                a, l, L, raw + at, f,
                 static_cast<T *>(h.y) + t * h.yt + head * h.yh,
                 stride * h.yh, head, stride, h.heads,
                 (h.groups - g0 + split - 1) >> a.log2S, all_rot);
-        }
+        };
+        groups(0, none, keys);
+        groups(1, keys, all);
     } else {
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
             factors(static_cast<const T *>(h.w), f);
 #pragma unroll 1
             for (int g = g0; g < h.groups; g += U * split) {
-                if (i != 0 || g != g0) load(x, xs, head, heads, 0);
+                if (i != 0 || g != g0) load(x, xs, head, heads, none, all);
                 rot_groups<T, V, K, ILV, NORM, U>(
                     a, l, L, raw, f, y, ys, head, stride, heads,
                     (h.groups - g + split - 1) >> a.log2S, all_rot);
@@ -548,25 +554,34 @@ cudaError_t rot_dispatch(int V, int K, F f) {
     return cudaErrorInvalidValue;
 }
 
-// FEW where the groups of each tensor fit half of a warp's loads in flight
-// (BF16, 57359 tokens of 15 + 3 heads of 64, norm: 93 us without it).
+// All groups at once where a warp's loads in flight hold them: as many of
+// queries as of keys (BF16, 57359 tokens of 15 + 3 heads of 64, norm: 70 us,
+// and 93 us without it), or one group of keys and the rest of queries (FP32,
+// 44536 tokens of 6 + 2 heads of 96: 41 us, and 64 us without it).
 template <typename T, bool ILV, bool NORM>
 cudaError_t launch_rotary_as(const RotArgs &a, int V, int K, cudaStream_t s) {
     const int64_t units = a.tokens << a.log2S;
     const int64_t grid =
         (units + kRotThreads / 32 - 1) / (kRotThreads / 32);
-    const int most = a.t[0].groups > a.t[1].groups ? a.t[0].groups
-                                                   : a.t[1].groups;
+    const auto fits = [&](int queries, int keys) {  // per warp
+        return a.t[0].groups <= queries << a.log2S &&
+               a.t[1].groups <= keys << a.log2S;
+    };
     return rot_dispatch<T, ILV>(V, K, [&](auto v, auto k) {
         constexpr int VV = decltype(v)::value, KK = decltype(k)::value;
-        if constexpr (kRotFlight<KK> > 1) {
-            if (most <= kRotFlight<KK> / 2 << a.log2S)
-                return launch_dependent(
-                    rotary_kernel<T, VV, KK, ILV, NORM, true>, grid,
-                    kRotThreads, 0, s, a);
-        }
-        return launch_dependent(rotary_kernel<T, VV, KK, ILV, NORM, false>,
-                                grid, kRotThreads, 0, s, a);
+        constexpr int U = kRotFlight<KK>;
+        const auto run = [&](auto queries) {
+            return launch_dependent(
+                rotary_kernel<T, VV, KK, ILV, NORM, decltype(queries)::value>,
+                grid, kRotThreads, 0, s, a);
+        };
+        if constexpr (U > 1)
+            if (fits(U / 2, U / 2))
+                return run(std::integral_constant<int, U / 2>{});
+        if constexpr (U > 2)
+            if (fits(U - 1, 1))
+                return run(std::integral_constant<int, U - 1>{});
+        return run(std::integral_constant<int, U>{});
     });
 }
 
