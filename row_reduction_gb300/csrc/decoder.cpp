@@ -102,6 +102,22 @@ int widest(uint64_t bits, int full) {
 // ---- rotary ----------------------------------------------------------------
 enum RotKind { ROT_FORWARD, ROT_BACKWARD };
 
+// Slots and groups of heads at V values per pack; K is returned: one slot per
+// lane, or (heads wider than a warp's slots) as many as the widest head needs
+// at this V.
+int rotary_layout(RotArgs *a, int V) {
+    const int rest = a->dim - 2 * a->pairs;
+    a->rot_slots = a->pairs / V;
+    a->slots = a->rot_slots + (rest + 2 * V - 1) / (2 * V);
+    a->log2L = 0;
+    while (a->log2L < 5 && (1 << a->log2L) < a->slots) ++a->log2L;
+    for (int i = 0; i < 2; ++i)
+        a->t[i].groups =
+            (int32_t)(((int64_t)a->t[i].heads + (32 >> a->log2L) - 1) >>
+                      (5 - a->log2L));
+    return a->slots <= 32 ? 1 : kRotMaxDim / (64 * V);
+}
+
 // Common checks; fills `a`, V and K.  With nothing to do, *empty.
 mt_status rotary_setup(int dtype, const mt_rotary_call_t *c, RotKind kind,
                        RotArgs *a, int *V, int *K, bool *empty) {
@@ -180,17 +196,7 @@ mt_status rotary_setup(int dtype, const mt_rotary_call_t *c, RotKind kind,
     a->tokens = c->tokens;
     a->dim = c->dim;
     a->pairs = c->rotary_dim / 2;
-    a->rot_slots = a->pairs / *V;
-    a->slots = a->rot_slots + (rest + 2 * *V - 1) / (2 * *V);
-    a->log2L = 0;
-    while (a->log2L < 5 && (1 << a->log2L) < a->slots) ++a->log2L;
-    // One slot per lane, or (heads wider than a warp's slots) as many as the
-    // widest head needs at this V.
-    *K = a->slots <= 32 ? 1 : kRotMaxDim / (64 * *V);
-    for (int i = 0; i < 2; ++i)
-        a->t[i].groups =
-            (int32_t)(((int64_t)a->t[i].heads + (32 >> a->log2L) - 1) >>
-                      (5 - a->log2L));
+    *K = rotary_layout(a, *V);
     a->eps = c->eps;
     a->inv_dim = 1.f / (float)c->dim;
     a->scale = c->scale;
@@ -213,6 +219,30 @@ cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
         case DT_F16: return launch_rotary_f16(a, V, K, ilv, norm, s);
         default: return launch_rotary_bf16(a, V, K, ilv, norm, s);
     }
+}
+
+// 16-bit values go in packs of 16 bytes, of which each lane's eight angles
+// and coefficients serve many heads, or of 8 bytes: twice the groups, but
+// half the angles and 80 registers for 122.  The latter where a warp then
+// still asks for all its groups at once (BF16 with norm: 57359 tokens of 4 + 1
+// heads of 64 32 us for 54, 40000 of 3 + 1 of 128 27 for 42, 8 of 32 + 8 of
+// 128 1.6 for 2.0), or where there is neither the norm's sum to add over
+// twice the lanes (40000 of 16 + 4 of 128: 95 us for 86) nor, interleaved, a
+// neighbouring pack in the same sector (without norm: 76 us for 68); with
+// neither, 64 us for 69, and 16384 of 32 + 8 of 128 51 us either way.
+cudaError_t rotary_forward(int dtype, RotArgs a, int V, int K, bool ilv,
+                           bool norm, cudaStream_t s) {
+    a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
+    if (V == 8) {
+        RotArgs b = a;
+        if (rotary_layout(&b, 4) == 1) {
+            b.log2S = split_log2(b.tokens, b.t[0].groups + b.t[1].groups);
+            if (rotary_fits(b, 2, 2) || rotary_fits(b, 3, 1) ||
+                (!norm && !ilv))
+                return rotary_launch(dtype, b, 4, 1, ilv, norm, s);
+        }
+    }
+    return rotary_launch(dtype, a, V, K, ilv, norm, s);
 }
 
 // A launch's grid (warps of kRotThreads/32 per CTA) must fit 2^31 - 1.
@@ -378,11 +408,10 @@ mt_status mt_rotary(int dtype, const mt_rotary_call_t *call,
         return st;
     if (empty) return MT_OK;
     if (too_many_tokens(a.tokens)) return MT_ERR_UNSUPPORTED;
-    a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
-    return status_from_cuda(rotary_launch(dtype, a, V, K,
-                                          call->interleaved != 0,
-                                          call->norm != 0,
-                                          (cudaStream_t)stream));
+    return status_from_cuda(rotary_forward(dtype, a, V, K,
+                                           call->interleaved != 0,
+                                           call->norm != 0,
+                                           (cudaStream_t)stream));
 }
 
 mt_status mt_rotary_backward_workspace(const mt_rotary_call_t *call,
@@ -428,10 +457,9 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
             a.t[i].xt = a.t[i].dt;
             a.t[i].xh = a.t[i].dh;
         }
-        a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
-        return status_from_cuda(rotary_launch(dtype, a, V, K,
-                                              call->interleaved != 0, false,
-                                              s));
+        return status_from_cuda(rotary_forward(dtype, a, V, K,
+                                               call->interleaved != 0, false,
+                                               s));
     }
     // The CTAs are shared out between queries and keys by their heads' groups.
     const int g0 = a.t[0].groups, g1 = a.t[1].groups;

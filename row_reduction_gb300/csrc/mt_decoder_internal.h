@@ -51,6 +51,12 @@ constexpr int kRotMaxDim = 512;
 // each of 152 SMs, as many as are resident at once.
 constexpr int kRotBackBlocks = 304;
 
+// Whether each warp of a token has at most so many groups of heads.
+inline bool rotary_fits(const RotArgs &a, int queries, int keys) {
+    return a.t[0].groups <= queries << a.log2S &&
+           a.t[1].groups <= keys << a.log2S;
+}
+
 #define MT_DECLARE_ROTARY(dt)                                                \
     cudaError_t launch_rotary_##dt(const RotArgs &a, int V, int K,           \
                                    bool interleaved, bool norm,              \

@@ -563,9 +563,8 @@ cudaError_t launch_rotary_as(const RotArgs &a, int V, int K, cudaStream_t s) {
     const int64_t units = a.tokens << a.log2S;
     const int64_t grid =
         (units + kRotThreads / 32 - 1) / (kRotThreads / 32);
-    const auto fits = [&](int queries, int keys) {  // per warp
-        return a.t[0].groups <= queries << a.log2S &&
-               a.t[1].groups <= keys << a.log2S;
+    const auto fits = [&](int queries, int keys) {
+        return rotary_fits(a, queries, keys);
     };
     return rot_dispatch<T, ILV>(V, K, [&](auto v, auto k) {
         constexpr int VV = decltype(v)::value, KK = decltype(k)::value;
