@@ -212,6 +212,28 @@ int split_log2(int64_t tokens, int groups) {
     return l;
 }
 
+// Whether a warp of the forward rotation, with one slot per lane, asks for all
+// its groups at once.
+bool rotary_at_once(const RotArgs &a) {
+    return rotary_fits(a, 2, 2) || rotary_fits(a, 3, 1);
+}
+
+// Twice the warps where each then asks for all its groups at once: without
+// norm they only turn the angles twice (BF16, 57359 tokens of 15 + 3 heads of
+// 64: 47 us for 52; FP32, 16049 of 10 + 2 of 96: 26 for 32, 700 of 32 + 8 of
+// 128: 4.2 for 5.1); with it, where they still fit the device at once
+// (1237 of 15 + 5 of 80: 4.5 for 5.9; many tokens 69 for 62).  Not with eight
+// angles to a lane (30000 of 5 + 5 of 160, interleaved: 51 for 46).
+void rotary_split(RotArgs *a, int V, int K, bool norm) {
+    a->log2S = split_log2(a->tokens, a->t[0].groups + a->t[1].groups);
+    if (K != 1 || V == 8 || rotary_at_once(*a) ||
+        a->tokens << a->log2S >= (norm ? 152 * 24 : 1 << 30))
+        return;
+    RotArgs b = *a;
+    ++b.log2S;
+    if (rotary_at_once(b)) *a = b;
+}
+
 cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
                           bool norm, cudaStream_t s) {
     switch (dtype) {
@@ -232,13 +254,12 @@ cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
 // neither, 64 us for 69, and 16384 of 32 + 8 of 128 51 us either way.
 cudaError_t rotary_forward(int dtype, RotArgs a, int V, int K, bool ilv,
                            bool norm, cudaStream_t s) {
-    a.log2S = split_log2(a.tokens, a.t[0].groups + a.t[1].groups);
+    rotary_split(&a, V, K, norm);
     if (V == 8) {
         RotArgs b = a;
         if (rotary_layout(&b, 4) == 1) {
-            b.log2S = split_log2(b.tokens, b.t[0].groups + b.t[1].groups);
-            if (rotary_fits(b, 2, 2) || rotary_fits(b, 3, 1) ||
-                (!norm && !ilv))
+            rotary_split(&b, 4, 1, norm);
+            if (rotary_at_once(b) || (!norm && !ilv))
                 return rotary_launch(dtype, b, 4, 1, ilv, norm, s);
         }
     }

@@ -65,7 +65,8 @@ def table(rotary, **kw):
     (4, 1, 1, 130, 66), (3, 2, 2, 17, 6), (2, 2, 1, 77, 70), (33, 9, 1, 20, 20),
     (2, 1, 1, 511, 510), (300, 4, 2, 64, 64), (3, 2, 1, 264, 264),
     (3, 3, 1, 132, 132), (2600, 3, 1, 64, 32), (2500, 41, 9, 64, 64),
-    (2700, 6, 2, 96, 96), (2600, 9, 3, 128, 128),
+    (2700, 6, 2, 96, 96), (2600, 9, 3, 128, 128), (1250, 15, 5, 80, 40),
+    (2500, 15, 3, 64, 16), (2450, 8, 1, 128, 128),
 ])
 def test_rotary(dt, norm, interleaved, tokens, hq, hk, dim, rotary):
     dtype = DTYPES[dt]
