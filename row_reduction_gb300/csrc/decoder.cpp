@@ -483,11 +483,18 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
                                                s));
     }
     // The CTAs are shared out between queries and keys by their heads' groups.
+    // FP32 takes the larger CTAs where every warp has work: few items are
+    // done sooner by warps with all their registers (333 tokens of 12 + 4
+    // heads of 64: 5.8 us for 6.9).
     const int g0 = a.t[0].groups, g1 = a.t[1].groups;
+    a.threads = dtype == DT_F32 && K == 1 &&
+                        a.tokens * (g0 + g1) >
+                            (int64_t)kRotBackBlocks * (kRotBackThreads / 32)
+                    ? kRotBackThreads : kRotThreads;
+    const int warps = a.threads / 32;
     for (int i = 0; i < 2; ++i) {
         const int64_t items = a.tokens * a.t[i].groups;
-        const int64_t need =
-            (items + kRotThreads / 32 - 1) / (kRotThreads / 32);
+        const int64_t need = (items + warps - 1) / warps;
         int64_t share = (int64_t)kRotBackBlocks * a.t[i].groups / (g0 + g1);
         if (share < 1) share = 1;
         if (share > need) share = need;

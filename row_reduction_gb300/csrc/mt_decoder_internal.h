@@ -44,8 +44,10 @@ struct RotArgs {
     // blocks[0] CTAs serving t[0], the others t[1]
     float *partial;
     int32_t blocks[2];
+    int32_t threads;    // per CTA: kRotThreads, or for FP32 kRotBackThreads
 };
 constexpr int kRotThreads = 256;
+constexpr int kRotBackThreads = 384;
 constexpr int kRotMaxDim = 512;
 // Most CTAs of the backward pass with norm (rows of partial sums): two for
 // each of 152 SMs, as many as are resident at once.

@@ -350,12 +350,14 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 // the lanes and warps that own the same slot are added in a fixed order and
 // the CTA writes one row of partial sums, which rotary_dweight_kernel adds.
 // Bound by dependent arithmetic at 16 warps per SM, with one item's loads on
-// their way: BF16, 8192 tokens of 32 + 8 heads of 128 54 us, 4.6 TB/s.
-template <typename T, int V, int K, bool ILV>
-__global__ void __launch_bounds__(kRotThreads, 2)
+// their way: BF16, 8192 tokens of 32 + 8 heads of 128 54 us, 4.6 TB/s.  FP32
+// packs hold half the values; at 80 registers (of 110) 24 warps fit: 86 us for
+// 94 there.  (BF16 with half as many per lane: 56 us at 24 warps.)
+template <typename T, int V, int K, bool ILV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2)
     rotary_backward_kernel(const RotArgs a) {
     using S = RotSlot<T, V, ILV>;
-    constexpr int kWarps = kRotThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     __shared__ float sums[kWarps][kRotMaxDim];
     grid_launch_dependents();
     grid_wait_prerequisites();
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
         }
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < a.dim; d += kRotThreads) {
+    for (int d = threadIdx.x; d < a.dim; d += THREADS) {
         float v = 0.f;
 #pragma unroll
         for (int j = 0; j < kWarps; ++j) v += sums[j][d];
@@ -598,10 +600,17 @@ template <typename T, bool ILV>
 cudaError_t launch_rotary_backward_as(const RotArgs &a, int V, int K,
                                       cudaStream_t s) {
     return rot_dispatch<T, ILV>(V, K, [&](auto v, auto k) {
+        constexpr int VV = decltype(v)::value, KK = decltype(k)::value;
+        const int grid = a.blocks[0] + a.blocks[1];
+        if constexpr (sizeof(T) == 4 && KK == 1) {
+            if (a.threads == kRotBackThreads)
+                return launch_dependent(
+                    rotary_backward_kernel<T, VV, KK, ILV, kRotBackThreads>,
+                    grid, kRotBackThreads, 0, s, a);
+        }
         return launch_dependent(
-            rotary_backward_kernel<T, decltype(v)::value, decltype(k)::value,
-                                   ILV>,
-            a.blocks[0] + a.blocks[1], kRotThreads, 0, s, a);
+            rotary_backward_kernel<T, VV, KK, ILV, kRotThreads>, grid,
+            kRotThreads, 0, s, a);
     });
 }
 
