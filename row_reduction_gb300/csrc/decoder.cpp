@@ -248,10 +248,9 @@ cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
 // half the angles and 80 registers for 122.  The latter where a warp then
 // still asks for all its groups at once (BF16 with norm: 57359 tokens of 4 + 1
 // heads of 64 32 us for 54, 40000 of 3 + 1 of 128 27 for 42, 8 of 32 + 8 of
-// 128 1.6 for 2.0), or where there is neither the norm's sum to add over
-// twice the lanes (40000 of 16 + 4 of 128: 95 us for 86) nor, interleaved, a
-// neighbouring pack in the same sector (without norm: 76 us for 68); with
-// neither, 64 us for 69, and 16384 of 32 + 8 of 128 51 us either way.
+// 128 1.6 for 2.0), or where there is no norm's sum to add over twice the
+// lanes (40000 of 16 + 4 of 128: 95 us for 86 with it, 64 for 69 without, and
+// 16384 of 32 + 8 of 128 51 us either way).
 cudaError_t rotary_forward(int dtype, RotArgs a, int V, int K, bool ilv,
                            bool norm, cudaStream_t s) {
     rotary_split(&a, V, K, norm);
@@ -259,7 +258,7 @@ cudaError_t rotary_forward(int dtype, RotArgs a, int V, int K, bool ilv,
         RotArgs b = a;
         if (rotary_layout(&b, 4) == 1) {
             rotary_split(&b, 4, 1, norm);
-            if (rotary_at_once(b) || (!norm && !ilv))
+            if (rotary_at_once(b) || !norm)
                 return rotary_launch(dtype, b, 4, 1, ilv, norm, s);
         }
     }

@@ -227,13 +227,14 @@ __device__ __forceinline__ void rot_groups(
 
 // Forward (and, with the sines' sign turned, backward without norm).  Bound by
 // latency at 16 warps per SM (128 registers: coefficients, and the loads of
-// four groups): BF16, 16384 tokens of 32 + 8 heads of 128 with norm 60 us,
+// four groups; 24 warps with 8-byte packs and no norm): BF16, 16384 tokens of 32 + 8 heads of 128 with norm 60 us,
 // 5.6 TB/s, 82% of the measured copy bandwidth.  The
 // loads of U groups of heads are issued before the angles are computed and
 // before any of them is used.  HQ < U: a warp has at most HQ groups of
 // queries and U - HQ of keys, all of them asked for at once.
 template <typename T, int V, int K, bool ILV, bool NORM, int HQ>
-__global__ void __launch_bounds__(kRotThreads, 2)
+__global__ void __launch_bounds__(
+    kRotThreads, sizeof(T) == 2 && V * K <= 4 && !NORM ? 3 : 2)
     rotary_kernel(const RotArgs a) {
     using S = RotSlot<T, V, ILV>;
     constexpr int U = kRotFlight<K>;
