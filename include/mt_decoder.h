@@ -236,7 +236,8 @@ typedef struct mt_logits_call {
     const int32_t *lengths;    /* rows: ids of the row that count (NULL: all;
                                   values are clamped to 0..history) */
     const int32_t *prompt_lengths; /* rows: how many of them, from the start,
-                                  are the prompt (NULL: none) */
+                                  are the prompt (NULL: none; values are
+                                  clamped to 0..history) */
     const float *repetition, *frequency, *presence; /* rows each; repetition
                                   at least 2^-126 */
     const int32_t *bias_ids;   /* rows x biases, contiguous; ids outside

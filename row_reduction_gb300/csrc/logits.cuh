@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kMaxThreads,
     const float pres = c.presence ? c.presence[row] : 0.f;
     const float temp = c.temperature ? c.temperature[row] : 1.f;
     const int length = c.lengths ? c.lengths[row] : c.history;
-    const int prompt = c.prompt_lengths ? c.prompt_lengths[row] : 0;
+    const int given = c.prompt_lengths ? c.prompt_lengths[row] : 0;
     const bool marks = c.tokens != nullptr || c.biases > 0;
     const int32_t *ids = c.tokens + row * c.tokens_stride;
     const int quads = c.tokens && p.wide_tokens ? c.history >> 2 : 0;
@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(kMaxThreads,
             bias_ids[i] = row_bias_ids[i];
             bias[i] = row_bias[i];
         }
+        // Clamped, so that the differences below stay in range.
         const int len = min(max(length, 0), c.history);
+        const int prompt = min(max(given, 0), c.history);
         // Whole warps go through the history together; what the first ids
         // give is put by before the counters are known to be zero.
         const int lane = tid & 31;
