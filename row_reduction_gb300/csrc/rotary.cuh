@@ -486,8 +486,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         xx = head_sum(xx, a.log2L);
         gx = head_sum(gx, a.log2L);
-        // no head: r = 0, so that eps = 0 adds no 0 * inf to dw
-        const float r = there ? rsqrtf(xx * a.inv_dim + a.eps) : 0.f;
+        const float r = rsqrtf(xx * a.inv_dim + a.eps);
         const float m = -gx * a.inv_dim * r * r;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -495,9 +494,11 @@ __global__ void __launch_bounds__(THREADS, 2)
             // g r: dw += (g r) x, dx = (g r) w - x (m r)
             scale_n<V>(ga[k], ga[k], r);
             scale_n<V>(gb[k], gb[k], r);
-            fma_n<V>(da[k], ga[k], xa[k], da[k]);
-            fma_n<V>(db[k], gb[k], xb[k], db[k]);
+            // A lane without a head holds another's values: it adds nothing
+            // (0 times an infinity would be NaN).
             if (there && slot.in) {
+                fma_n<V>(da[k], ga[k], xa[k], da[k]);
+                fma_n<V>(db[k], gb[k], xb[k], db[k]);
                 float oa[V], ob[V];
                 mul_n<V>(oa, ga[k], wa[k]);
                 mul_n<V>(ob, gb[k], wb[k]);
