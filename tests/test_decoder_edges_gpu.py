@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import row_reduction_gb300 as mt
-from decoder_util import DTYPES, U, check, half_step, logits_ref
+from decoder_util import (DTYPES, NORM, U, angle_error, check, half_step,
+                          logits_ref, norm64, pair_sum, rotate)
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,92 @@ def test_weight_gradients_keep_an_infinity(dt, interleaved, heads):
     dw = mt.rotary_backward(dq, None, pos, tab, interleaved=interleaved, q=q,
                             q_weight=w, eps=1e-6)[2].tolist()
     assert {d: v for d, v in enumerate(dw) if not math.isfinite(v)} == want
+
+
+WEIGHT_SHAPES = [
+    # tokens, query heads, key heads, dim, rotary_dim: many items per warp,
+    # of a number that does not divide evenly; odd, padded and wide heads
+    (3001, 5, 3, 64, 64), (2999, 13, 2, 64, 32), (700, 33, 5, 64, 64),
+    (6007, 3, 1, 64, 64), (1999, 7, 7, 96, 48), (1003, 9, 1, 128, 128),
+    (901, 5, 2, 80, 40), (301, 6, 2, 512, 512), (303, 7, 1, 130, 66),
+    (203, 3, 2, 77, 70), (151, 3, 1, 511, 510), (12001, 1, 1, 64, 64),
+]
+
+
+def weight_sum_roundings(tokens, hq, hk):
+    """Most roundings on the way of one term into a weight's gradient: a lane
+    adds up its warp's items (a token's group of heads, at most one per head;
+    a tensor has a part of 304 blocks of 8 warps or more in proportion to its
+    groups, rounded down but at least one, so at least half its due), then 5
+    exchanges, up to 12 warps, 10 of 304 rows of partial sums, and 32 sums of
+    those."""
+    items = -(-2 * tokens * (hq + hk) // (304 * 8)) + 1
+    return items + 5 + 12 + 10 + 32
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rotary", WEIGHT_SHAPES)
+def test_weight_gradients_add_every_row_once(dt, interleaved, tokens, hq, hk,
+                                             dim, rotary):
+    """Whole numbers in dy, x of +-1 and position 0 without eps: the mean
+    square is 1 (its sum is exact, the mean within one rounding), the factor
+    1/sqrt within 2 ulp of 1, the rotation the identity, and every term a
+    whole number of 1 or more but for that factor: a row that is left out or
+    taken twice shows in every column."""
+    dtype = DTYPES[dt]
+    g = gen(dim + tokens)
+    tab = mt.rotary_frequencies(rotary)
+    pos = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    args, want = [], []
+    for h in (hq, hk):
+        x = torch.randint(0, 2, (tokens, h, dim), generator=g,
+                          device="cuda") * 2 - 1
+        dy = torch.randint(1, 3, (tokens, h, dim), generator=g,
+                           device="cuda") * (torch.randint(
+                               0, 2, (tokens, h, dim), generator=g,
+                               device="cuda") * 2 - 1)
+        args.append((x.to(dtype), dy.to(dtype)))
+        want.append(((x * dy).sum((0, 1)), dy.abs().sum((0, 1))))
+    ones = torch.ones(dim, dtype=dtype, device="cuda")
+    got = mt.rotary_backward(args[0][1], args[1][1], pos, tab,
+                             interleaved=interleaved, q=args[0][0],
+                             k=args[1][0], q_weight=ones, k_weight=ones,
+                             eps=0.0)
+    roundings = weight_sum_roundings(tokens, hq, hk)
+    for i in range(2):
+        ref, size = want[i]
+        # 1/sqrt: 2 ulp are 2^-22, half a rounding of the mean, its own; then
+        # g r, and the sums where r is not 1 exactly
+        tol = size.double() * (2.0 ** -22 + (3 + roundings) * U)
+        assert float(tol.max()) < 0.5   # a term is 1 or more
+        check(got[2 + i], ref.double(), tol, "dweight")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rotary", WEIGHT_SHAPES)
+def test_weight_gradients_to_the_longest_sum(dt, interleaved, tokens, hq, hk,
+                                             dim, rotary):
+    """Random rows, with the error that the longest way of a term into its
+    sum allows (however many rows there are)."""
+    dtype = DTYPES[dt]
+    q, k, dq, dk = backward_inputs(tokens, tokens, hq, hk, dim, dtype)
+    pos = torch.randint(0, 8192, (tokens,), generator=gen(1), device="cuda")
+    tab = mt.rotary_frequencies(rotary)
+    freqs, scale = mt.mt_rotary_frequencies(rotary, 10000.0)
+    w = torch.ones(dim, dtype=dtype, device="cuda")
+    got = mt.rotary_backward(dq, dk, pos, tab, interleaved=interleaved, q=q,
+                             k=k, q_weight=w, k_weight=w, eps=1e-6)
+    roundings = weight_sum_roundings(tokens, hq, hk)
+    for i, (x, dy) in enumerate(((q, dq), (k, dk))):
+        g = rotate(dy, pos, freqs, scale, rotary, interleaved, -1.0)
+        xr = norm64(x, None, 1e-6)[0]
+        mag = pair_sum(dy, rotary, interleaved, scale) * xr.abs()
+        # angle, 1/sqrt and its sum, g r and the term's product, the sums
+        tol = mag.sum((0, 1)) * (angle_error(dtype) + NORM +
+                                 (3 + roundings) * U)
+        terms = (g * xr).sum(1)
+        # one token left out would show
+        assert bool((terms[-1].abs() > tol).any())
+        check(got[2 + i], terms.sum(0), tol, "dweight")
