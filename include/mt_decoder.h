@@ -170,7 +170,8 @@ typedef struct mt_cache_call {
                               negative or >= slots takes no part: nothing is
                               stored for it, and a read leaves its output row
                               as it was. */
-    int64_t tokens, slots;
+    int64_t tokens, slots; /* tokens*heads*dim <= 2^40, or 2^32 where group
+                              is not a multiple of 8 */
     int32_t heads;         /* >= 1 */
     int32_t dim;           /* >= 1; heads*dim <= 2^20 */
     int32_t group;         /* divides dim */

@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;     // of the narrow kernels
 constexpr int kMaxThreads = 512;  // of the wide ones
+constexpr int64_t kNarrowGrid = 1 << 18;  // most CTAs of the narrow ones
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 // Four values times `inv` as four codes.  int8: adding 1.5 * 2^23 leaves the
@@ -252,38 +253,44 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     }
 }
 
-// Any group: a warp per group reads it twice (the second time from L1).
+// Any group: a warp at a time reads it twice (the second time from L1).  32
+// registers keep 64 warps per SM (38 and 48 warps: 13.6 us for 12.8 at 64 rows
+// of 2 x 8 heads of 128 by 4).  Bound by instructions per group, whatever its
+// size: 16384 such rows 1.6 ms.
 template <typename T, bool INT8>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     write_any_kernel(const CacheArgs a, unsigned per_row) {
     grid_launch_dependents();
     grid_wait_prerequisites();
     const int lane = threadIdx.x & 31;
-    const int64_t n = (int64_t)blockIdx.x * (kThreads >> 5) +
-                      (threadIdx.x >> 5);
-    const int64_t row = n / per_row;
-    const unsigned g = (unsigned)(n - row * per_row);
-    const int64_t t = a.tensors == 2 ? row >> 1 : row;
-    const int i = a.tensors == 2 ? (int)(row & 1) : 0;
-    if (t >= a.tokens) return;
-    const int64_t slot = a.slot[t];
-    if (slot < 0 || slot >= a.slots) return;
-    const unsigned groups = (unsigned)(a.dim / a.group);
-    const unsigned head = g / groups, part = g - head * groups;
-    const T *x = static_cast<const T *>(a.rows[i]) + t * a.ts[i] +
-                 head * a.hs[i] + part * a.group;
-    float amax = 0.f;
-    for (int e = lane; e < a.group; e += 32)
-        amax = nanmax(amax, fabsf(to_f(x[e])));
-    amax = warp_nanmax(amax);
-    float inv;
-    bool bad;
-    const float s = group_scale<INT8>(amax, inv, bad);
-    const int64_t group = slot * per_row + g;
-    uint8_t *c = a.codes[i] + group * a.group;
-    for (int e = lane; e < a.group; e += 32)
-        c[e] = bad ? 0 : (uint8_t)encode<INT8>(to_f(x[e]), inv);
-    if (lane == 0) a.scales[i][group] = s;
+    const int64_t total = a.tokens * a.tensors * (int64_t)per_row;
+#pragma unroll 1
+    for (int64_t n = (int64_t)blockIdx.x * (kThreads >> 5) +
+                     (threadIdx.x >> 5);
+         n < total; n += (int64_t)gridDim.x * (kThreads >> 5)) {
+        const int64_t row = n / per_row;
+        const unsigned g = (unsigned)(n - row * per_row);
+        const int64_t t = a.tensors == 2 ? row >> 1 : row;
+        const int i = a.tensors == 2 ? (int)(row & 1) : 0;
+        const int64_t slot = a.slot[t];
+        if (slot < 0 || slot >= a.slots) continue;
+        const unsigned groups = (unsigned)(a.dim / a.group);
+        const unsigned head = g / groups, part = g - head * groups;
+        const T *x = static_cast<const T *>(a.rows[i]) + t * a.ts[i] +
+                     head * a.hs[i] + part * a.group;
+        float amax = 0.f;
+        for (int e = lane; e < a.group; e += 32)
+            amax = nanmax(amax, fabsf(to_f(x[e])));
+        amax = warp_nanmax(amax);
+        float inv;
+        bool bad;
+        const float s = group_scale<INT8>(amax, inv, bad);
+        const int64_t group = slot * per_row + g;
+        uint8_t *c = a.codes[i] + group * a.group;
+        for (int e = lane; e < a.group; e += 32)
+            c[e] = bad ? 0 : (uint8_t)encode<INT8>(to_f(x[e]), inv);
+        if (lane == 0) a.scales[i][group] = s;
+    }
 }
 
 // Reading back.  A row's codes are contiguous (heads x dim bytes): V of them
@@ -367,25 +374,30 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     }
 }
 
-// One value per thread: any sizes, strides and addresses.
+// One value per thread at a time: any sizes, strides and addresses.
 template <typename T, bool INT8>
 __global__ void __launch_bounds__(kThreads)
     read_any_kernel(const CacheArgs a, unsigned width) {
     grid_launch_dependents();
     grid_wait_prerequisites();
-    const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t row = n / width;
-    const unsigned v = (unsigned)(n - row * width);
-    const int64_t t = a.tensors == 2 ? row >> 1 : row;
-    const int i = a.tensors == 2 ? (int)(row & 1) : 0;
-    if (t >= a.tokens) return;
-    const int64_t slot = a.slot[t];
-    if (slot < 0 || slot >= a.slots) return;
-    const unsigned head = v / (unsigned)a.dim, d = v - head * (unsigned)a.dim;
-    const float s = a.scales[i][slot * (width / (unsigned)a.group) +
-                                v / (unsigned)a.group];
-    static_cast<T *>(a.rows[i])[t * a.ts[i] + (int64_t)head * a.hs[i] + d] =
-        from_f<T>(decode<INT8>(a.codes[i][slot * width + v]) * s);
+    const int64_t total = a.tokens * a.tensors * (int64_t)width;
+#pragma unroll 1
+    for (int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x; n < total;
+         n += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = n / width;
+        const unsigned v = (unsigned)(n - row * width);
+        const int64_t t = a.tensors == 2 ? row >> 1 : row;
+        const int i = a.tensors == 2 ? (int)(row & 1) : 0;
+        const int64_t slot = a.slot[t];
+        if (slot < 0 || slot >= a.slots) continue;
+        const unsigned head = v / (unsigned)a.dim;
+        const unsigned d = v - head * (unsigned)a.dim;
+        const float s = a.scales[i][slot * (width / (unsigned)a.group) +
+                                    v / (unsigned)a.group];
+        static_cast<T *>(a.rows[i])[t * a.ts[i] + (int64_t)head * a.hs[i] +
+                                    d] =
+            from_f<T>(decode<INT8>(a.codes[i][slot * width + v]) * s);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -459,6 +471,12 @@ cudaError_t launch_shape(K kernel, const Shape &s, const CacheArgs &a,
     return cudaLaunchKernelEx(&cfg, kernel, a, s.map);
 }
 
+// CTAs of a narrow kernel that take `per` of n units at a time.
+int64_t narrow_grid(int64_t n, int64_t per) {
+    const int64_t need = (n + per - 1) / per;
+    return need < kNarrowGrid ? need : kNarrowGrid;
+}
+
 template <typename T, bool INT8>
 cudaError_t write_as(const CacheArgs &a, int vec, cudaStream_t s) {
     const unsigned per_row = (unsigned)(a.heads * (a.dim / a.group));
@@ -475,10 +493,9 @@ cudaError_t write_as(const CacheArgs &a, int vec, cudaStream_t s) {
                    ? launch_shape(write_wide_kernel<T, INT8, 16>, shape, a, s)
                    : launch_shape(write_wide_kernel<T, INT8, 8>, shape, a, s);
     }
-    const int64_t per = kThreads / 32;
     return launch_dependent(write_any_kernel<T, INT8>,
-                            (groups + per - 1) / per, kThreads, 0, s, a,
-                            per_row);
+                            narrow_grid(groups, kThreads / 32), kThreads, 0, s,
+                            a, per_row);
 }
 
 template <typename T, bool INT8>
@@ -496,7 +513,7 @@ cudaError_t read_as(const CacheArgs &a, int vec, cudaStream_t s) {
     }
     const int64_t n = a.tokens * a.tensors * (int64_t)width;
     return launch_dependent(read_any_kernel<T, INT8>,
-                            (n + kThreads - 1) / kThreads, kThreads, 0, s, a,
+                            narrow_grid(n, kThreads), kThreads, 0, s, a,
                             width);
 }
 

@@ -330,9 +330,8 @@ mt_status cache_setup(int dtype, const mt_cache_call_t *c, bool write,
     a->dim = c->dim;
     a->group = c->group;
     a->int8 = c->format == MT_CACHE_INT8;
-    // The kernels for any sizes take a warp per group (or a thread per
-    // value), which must fit a grid; the wide ones loop.
-    if (c->tokens > (1LL << (*vec ? 40 : 32)) / width)
+    // The same at every address, whichever kernel that leads to.
+    if (c->tokens > (1LL << (c->group % 8 == 0 ? 40 : 32)) / width)
         return MT_ERR_UNSUPPORTED;
     return MT_OK;
 }

@@ -162,3 +162,68 @@ def test_weight_gradients_to_the_longest_sum(dt, interleaved, tokens, hq, hk,
         # one token left out would show
         assert bool((terms[-1].abs() > tol).any())
         check(got[2 + i], terms.sum(0), tol, "dweight")
+
+
+# ---- cache: sizes do not depend on addresses ---------------------------------------
+def cache_in(buf, slots, heads, dim, group, off):
+    """A cache whose codes start `off` bytes into `buf`."""
+    return (buf[off:off + slots * heads * dim].view(slots, heads, dim),
+            torch.zeros(slots, heads, dim // group, device="cuda"))
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_cache_accepts_the_same_sizes_at_any_address(off):
+    """More than 2^32 values of one call, the codes on a 16-byte boundary and
+    off it.  (One row of values for all tokens; most have no slot.)"""
+    heads, dim, slots = 1024, 1024, 3
+    tokens = 4099                               # of 2^20 values
+    assert tokens * heads * dim > 2 ** 32
+    row = torch.randn(1, heads, dim, generator=gen(1), device="cuda").to(
+        torch.bfloat16)
+    at = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    at[0], at[2050], at[tokens - 1] = 2, 0, 1
+    buf = torch.full((slots * heads * dim + 16,), 55, dtype=torch.int8,
+                     device="cuda")
+    cache = cache_in(buf, slots, heads, dim, 256, off)
+    mt.cache_write(row.expand(tokens, -1, -1), None, cache, None, at)
+    want = cache_in(torch.zeros_like(buf), slots, heads, dim, 256, 0)
+    mt.cache_write(row.expand(3, -1, -1), None, want, None,
+                   torch.arange(3, device="cuda"))
+    assert torch.equal(cache[0], want[0]) and torch.equal(cache[1], want[1])
+    assert bool((buf[:off] == 55).all())
+    assert bool((buf[off + slots * heads * dim:] == 55).all())
+    # every token reads slot 1, but for a few that keep what was there
+    at = torch.full((tokens,), 1, dtype=torch.int64, device="cuda")
+    at[0] = at[2050] = -1
+    out = torch.full((tokens, heads, dim), 7.0, dtype=torch.bfloat16,
+                     device="cuda")
+    mt.cache_read(cache, None, at, out=out)
+    value = mt.cache_read(want, None, torch.tensor([1], device="cuda"))[0]
+    for t in range(0, tokens, 512):
+        part = out[t:t + 512]
+        keep = (at[t:t + 512] < 0)
+        assert bool((part[keep] == 7.0).all())
+        assert bool((part[~keep] == value).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_cache_of_many_odd_groups(dt, fmt):
+    """Groups of any size, many of them: every row of a call of 2200003 tokens
+    against the same rows in calls of 1000."""
+    tokens, heads, dim, group = 2_200_003, 3, 10, 5
+    dtype = DTYPES[dt]
+    g = gen(3)
+    base = torch.randn(1000, heads, dim, generator=g, device="cuda").to(dtype)
+    x = base.repeat(tokens // 1000 + 1, 1, 1)[:tokens]
+    at = torch.randperm(tokens, generator=g, device="cuda")
+    k, v = (mt.cache_alloc(tokens, heads, dim, group, fmt) for _ in range(2))
+    mt.cache_write(x, -x, k, v, at)
+    few = [mt.cache_alloc(1000, heads, dim, group, fmt) for _ in range(2)]
+    rows = torch.arange(1000, device="cuda")
+    mt.cache_write(base, -base, *few, rows)
+    kr, vr = mt.cache_read(k, v, at, dtype=dtype)
+    fk, fv = mt.cache_read(*few, rows, dtype=dtype)
+    of = torch.arange(tokens, device="cuda") % 1000
+    assert torch.equal(kr, fk[of]) and torch.equal(vr, fv[of])
+    assert torch.equal(k[1][at], few[0][1][of])
