@@ -92,7 +92,7 @@ MT_API mt_status mt_rotary_frequencies(int32_t rotary_dim, double base,
                                        double *freqs, double *factor);
 
 /* Host only.  turns[i] = freqs[i] / 2 pi in units of 2^-64 turns, modulo one
- * turn.  freqs finite, of any sign. */
+ * turn.  freqs of any sign, below 1e6 in magnitude. */
 MT_API mt_status mt_rotary_turns(const double *freqs, int32_t n,
                                  uint64_t *turns);
 
@@ -106,7 +106,7 @@ typedef struct mt_rotary_heads {
     float *dweight;     /* backward with norm: dim FP32 values, or NULL (not
                            wanted).  Otherwise NULL */
     int64_t x_token, x_head, dy_token, dy_head, y_token, y_head; /* strides */
-    int32_t heads;      /* >= 0; 0 = the tensor is absent */
+    int32_t heads;      /* 0..65536; 0 = the tensor is absent */
     int32_t reserved;   /* 0 */
 } mt_rotary_heads_t;
 
@@ -114,7 +114,7 @@ typedef struct mt_rotary_call {
     mt_rotary_heads_t q, k;
     const void *positions;  /* tokens int32 or int64 values, of any sign */
     const uint64_t *turns;  /* DEVICE pointer, rotary_dim/2 values */
-    int64_t tokens;
+    int64_t tokens;         /* 0..2^33 */
     int32_t position_bytes; /* 4 or 8 */
     int32_t dim;            /* values per head, 1..512 */
     int32_t rotary_dim;     /* even, 2..dim */
@@ -194,7 +194,8 @@ MT_API mt_status mt_cache_read(int dtype, const mt_cache_call_t *call,
  * table[s*table_stride + p/page_size] * page_size + p % page_size.  A row
  * behind offsets[sequences], before offsets[0], at a negative position, past
  * the table's width or in a negative page gets slot -1.  offsets (sequences+1
- * values, not decreasing), starts and table are int32 DEVICE arrays. */
+ * values, not decreasing), starts and table are int32 DEVICE arrays; rows at
+ * most 2^38. */
 MT_API mt_status mt_cache_slots(const int32_t *table, int64_t table_stride,
                                 int32_t pages_per_sequence,
                                 const int32_t *offsets, const int32_t *starts,
@@ -225,7 +226,7 @@ typedef enum mt_logits_mode {
 typedef struct mt_logits_call {
     const void *x;             /* rows x vocab, row stride x_stride */
     void *y;                   /* same type, row stride y_stride >= vocab */
-    int64_t rows, x_stride, y_stride;
+    int64_t rows, x_stride, y_stride; /* rows 0..2^24 */
     int32_t vocab;             /* 1..524280 */
     int32_t mode;              /* mt_logits_mode */
     const int32_t *tokens;     /* rows x history token ids, row stride

@@ -348,7 +348,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, freqs=None,
     context to the one trained on: "linear"; "ntk"; "yarn" and "bands" with
     "original_length" and the bounds "low" and "high" in turns (yarn 1 and
     32, bands 1 and 4 where not given).  freqs: frequencies of your own
-    (rotary_dim/2 radians per position) in place of base and scaling.
+    (rotary_dim/2 radians per position, below 1e6 in magnitude) in place of
+    base and scaling.
     scale: factor on rotated values in place of the scaling's own."""
     import torch
     if freqs is not None:
