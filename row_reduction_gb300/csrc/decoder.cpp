@@ -206,9 +206,9 @@ mt_status rotary_setup(int dtype, const mt_rotary_call_t *c, RotKind kind,
 
 // Warps per token (a power of two): one while the tokens fill the device,
 // more where there are few, up to one group of heads each.
-int split_log2(int64_t tokens, int groups) {
+int split_log2(int64_t tokens, int groups, int sms) {
     int l = 0;
-    while ((1 << l) < groups && (tokens << l) < 152 * 16) ++l;
+    while ((1 << l) < groups && (tokens << l) < (int64_t)sms * 16) ++l;
     return l;
 }
 
@@ -224,10 +224,10 @@ bool rotary_at_once(const RotArgs &a) {
 // 128: 4.2 for 5.1); with it, where they still fit the device at once
 // (1237 of 15 + 5 of 80: 4.5 for 5.9; many tokens 69 for 62).  Not with eight
 // angles to a lane (30000 of 5 + 5 of 160, interleaved: 51 for 46).
-void rotary_split(RotArgs *a, int V, int K, bool norm) {
-    a->log2S = split_log2(a->tokens, a->t[0].groups + a->t[1].groups);
+void rotary_split(RotArgs *a, int V, int K, bool norm, int sms) {
+    a->log2S = split_log2(a->tokens, a->t[0].groups + a->t[1].groups, sms);
     if (K != 1 || V == 8 || rotary_at_once(*a) ||
-        a->tokens << a->log2S >= (norm ? 152 * 24 : 1 << 30))
+        a->tokens << a->log2S >= (norm ? sms * 24 : 1 << 30))
         return;
     RotArgs b = *a;
     ++b.log2S;
@@ -253,11 +253,14 @@ cudaError_t rotary_launch(int dtype, const RotArgs &a, int V, int K, bool ilv,
 // 16384 of 32 + 8 of 128 51 us either way).
 cudaError_t rotary_forward(int dtype, RotArgs a, int V, int K, bool ilv,
                            bool norm, cudaStream_t s) {
-    rotary_split(&a, V, K, norm);
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    rotary_split(&a, V, K, norm, sms);
     if (V == 8) {
         RotArgs b = a;
         if (rotary_layout(&b, 4) == 1) {
-            rotary_split(&b, 4, 1, norm);
+            rotary_split(&b, 4, 1, norm, sms);
             if (rotary_at_once(b) || !norm)
                 return rotary_launch(dtype, b, 4, 1, ilv, norm, s);
         }
@@ -480,28 +483,32 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
                                                call->interleaved != 0, false,
                                                s));
     }
-    // The CTAs are shared out between queries and keys by their heads' groups.
+    // As many CTAs as are resident at once (each takes an equal share of the
+    // work), shared out between queries and keys by their heads' groups.
     // FP32 takes the larger CTAs where every warp has work: few items are
     // done sooner by warps with all their registers (333 tokens of 12 + 4
     // heads of 64: 5.8 us for 6.9).
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    const int blocks = 2 * sms < kRotBackBlocks ? 2 * sms : kRotBackBlocks;
     const int g0 = a.t[0].groups, g1 = a.t[1].groups;
     a.threads = dtype == DT_F32 && K == 1 &&
                         a.tokens * (g0 + g1) >
-                            (int64_t)kRotBackBlocks * (kRotBackThreads / 32)
+                            (int64_t)blocks * (kRotBackThreads / 32)
                     ? kRotBackThreads : kRotThreads;
     const int warps = a.threads / 32;
     for (int i = 0; i < 2; ++i) {
         const int64_t items = a.tokens * a.t[i].groups;
         const int64_t need = (items + warps - 1) / warps;
-        int64_t share = (int64_t)kRotBackBlocks * a.t[i].groups / (g0 + g1);
+        int64_t share = (int64_t)blocks * a.t[i].groups / (g0 + g1);
         if (share < 1) share = 1;
         if (share > need) share = need;
         a.blocks[i] = a.t[i].heads ? (int32_t)share : 0;
     }
-    if (a.blocks[0] + a.blocks[1] > kRotBackBlocks)
+    if (a.blocks[0] + a.blocks[1] > blocks)
         --a.blocks[a.blocks[0] < a.blocks[1]];
     a.partial = dw ? static_cast<float *>(workspace) : nullptr;
-    cudaError_t e;
     switch (dtype) {
         case DT_F32:
             e = launch_rotary_backward_f32(a, V, K, call->interleaved != 0, s);

@@ -50,7 +50,8 @@ constexpr int kRotThreads = 256;
 constexpr int kRotBackThreads = 384;
 constexpr int kRotMaxDim = 512;
 // Most CTAs of the backward pass with norm (rows of partial sums): two for
-// each of 152 SMs, as many as are resident at once.
+// each SM, as many as are resident at once, and no more than two for each of
+// 152.
 constexpr int kRotBackBlocks = 304;
 
 // Whether each warp of a token has at most so many groups of heads.

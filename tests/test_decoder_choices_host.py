@@ -32,7 +32,10 @@ cudaError_t cudaFuncSetAttribute(const void *, enum cudaFuncAttribute, int) {
 cudaError_t cudaMemsetAsync(void *, int, size_t, cudaStream_t) {
     return cudaSuccess;
 }
-void fake_device(int sms) { g_dev = sms % 64; g_dev_sms[g_dev] = sms; }
+void fake_device(int sms) {  // a device of its own for each size
+    g_dev = sms / 4;
+    g_dev_sms[g_dev] = sms;
+}
 int fake_launches() { return g_launches; }
 void fake_last(int *o) {
     const int v[] = {g_vec, g_V, g_K, g_rot.log2S, g_rot.blocks[0],
@@ -120,7 +123,8 @@ def fake(tmp_path_factory):
     (d / "fakes.cpp").write_text(FAKES)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     subprocess.run(
-        ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I",
+        ["g++", "-std=c++17", "-O1", "-shared", "-fPIC",
+         "-Wl,-Bsymbolic", "-I",  # the fakes, not a loaded CUDA runtime
          os.path.join(cuda, "include"), "-I",
          os.path.join(ROOT, "row_reduction_gb300", "csrc"),
          str(d / "fakes.cpp"), "-o", str(d / "fakes.so")], check=True)
@@ -191,3 +195,43 @@ def test_cache_limits_do_not_depend_on_addresses(fake, write, rows, codes,
     most = 2 ** (40 if group % 8 == 0 else 32) // (heads_ * dim)
     assert f(BF16, cache(most, heads_, dim, group, rows, codes)) == 0
     assert f(BF16, cache(most + 1, heads_, dim, group, rows, codes)) == UNS
+
+
+# ---- choices by the device's size --------------------------------------------------
+@pytest.mark.parametrize("sms", [20, 76, 132, 148, 152, 160])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("hq,hk", [(32, 8), (8, 1), (1, 0), (20, 5), (64, 1)])
+def test_backward_takes_the_blocks_that_are_resident(fake, sms, dtype, hq, hk):
+    """Equal shares of the work for two blocks per SM: one more would run
+    alone after the rest.  304 rows of partial sums at most."""
+    fake.lib.fake_device(sms)
+    most = min(304, 2 * sms)
+    for tokens in (1, 7, 300, 4096, 100003):
+        c = rotary(tokens, hq, hk, norm=1, back=True)
+        assert fake.rotary_backward(dtype, c, None, 0) == 0
+        got = fake.last()
+        warps = got["threads"] // 32
+        q, k = got["q_blocks"], got["k_blocks"]
+        assert 1 <= q and (k >= 1) == (hk > 0) and q + k <= most
+        for blocks, groups in ((q, got["q_groups"]), (k, got["k_groups"])):
+            assert blocks <= -(-tokens * groups // warps)
+        if tokens >= 4096:
+            assert q + k >= most - 1
+    fake.lib.fake_device(152)
+
+
+@pytest.mark.parametrize("sms", [76, 148, 152])
+def test_forward_splits_a_token_until_the_device_is_full(fake, sms):
+    """Warps per token: one more doubling while 16 per SM are not reached (a
+    last one, to ask for all heads at once, may follow)."""
+    fake.lib.fake_device(sms)
+    for tokens in (1, 8, 100, 1000, sms * 16 - 1, sms * 16, 100000):
+        for norm in (0, 1):
+            assert fake.rotary(F32, rotary(tokens, 32, 8, norm=norm)) == 0
+            got = fake.last()
+            split, groups = 1 << got["log2S"], got["q_groups"] + got["k_groups"]
+            assert split >= groups or tokens * split >= sms * 16
+            assert split == 1 or tokens * split // 4 < sms * 16 or not norm
+            if tokens >= sms * 24:
+                assert split == 1 or not norm
+    fake.lib.fake_device(152)
