@@ -501,13 +501,13 @@ mt_status mt_rotary_backward(int dtype, const mt_rotary_call_t *call,
     for (int i = 0; i < 2; ++i) {
         const int64_t items = a.tokens * a.t[i].groups;
         const int64_t need = (items + warps - 1) / warps;
+        // Rounded down, so that the two (one at least each) stay within
+        // blocks: where one is raised to 1, the other is below blocks.
         int64_t share = (int64_t)blocks * a.t[i].groups / (g0 + g1);
         if (share < 1) share = 1;
         if (share > need) share = need;
         a.blocks[i] = a.t[i].heads ? (int32_t)share : 0;
     }
-    if (a.blocks[0] + a.blocks[1] > blocks)
-        --a.blocks[a.blocks[0] < a.blocks[1]];
     a.partial = dw ? static_cast<float *>(workspace) : nullptr;
     switch (dtype) {
         case DT_F32:

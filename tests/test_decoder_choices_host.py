@@ -220,6 +220,21 @@ def test_backward_takes_the_blocks_that_are_resident(fake, sms, dtype, hq, hk):
     fake.lib.fake_device(152)
 
 
+def test_backward_shares_never_exceed_the_blocks(fake):
+    """Any numbers of groups: the two tensors' parts, rounded down but at least
+    one each, fit the rows of partial sums."""
+    for sms in (8, 28, 148, 152):
+        fake.lib.fake_device(sms)
+        most = min(304, 2 * sms)
+        for hq in [*range(1, 70), 400, 9001, 65536]:
+            for hk in [*range(0, 70, 3), 1000, 65536]:
+                c = rotary(10 ** 6, hq, hk, dim=256, norm=1, back=True)
+                assert fake.rotary_backward(F32, c, None, 0) == 0
+                got = fake.last()
+                assert got["q_blocks"] + got["k_blocks"] <= most
+    fake.lib.fake_device(152)
+
+
 @pytest.mark.parametrize("sms", [76, 148, 152])
 def test_forward_splits_a_token_until_the_device_is_full(fake, sms):
     """Warps per token: one more doubling while 16 per SM are not reached (a
