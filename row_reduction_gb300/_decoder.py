@@ -371,6 +371,11 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, freqs=None,
             if kind not in _SCALINGS:
                 raise ValueError(f"scaling type must be one of "
                                  f"{sorted(_SCALINGS)}, got {kind!r}")
+            needs = {"factor"} | ({"original_length"} if kind in
+                                  ("yarn", "bands") else set())
+            if needs - set(scaling):
+                raise ValueError(f"scaling {kind!r} needs "
+                                 f"{sorted(needs - set(scaling))}")
             s = MtRotaryScaling(
                 type=_SCALINGS[kind], factor=scaling["factor"],
                 original_length=scaling.get("original_length", 0.0),

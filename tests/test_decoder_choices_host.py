@@ -197,6 +197,16 @@ def test_cache_limits_do_not_depend_on_addresses(fake, write, rows, codes,
     assert f(BF16, cache(most + 1, heads_, dim, group, rows, codes)) == UNS
 
 
+@pytest.mark.parametrize("scaling,missing", [
+    (dict(type="linear"), "factor"), (dict(type="ntk"), "factor"),
+    (dict(type="yarn", original_length=100), "factor"),
+    (dict(type="bands", factor=2.0), "original_length"),
+    (dict(type="yarn", factor=2.0), "original_length")])
+def test_scalings_say_what_they_need(scaling, missing):
+    with pytest.raises(ValueError, match=missing):
+        mt.rotary_frequencies(8, scaling=scaling, device="cpu")
+
+
 # ---- choices by the device's size --------------------------------------------------
 @pytest.mark.parametrize("sms", [20, 76, 132, 148, 152, 160])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
