@@ -31,7 +31,10 @@
  *            zero.
  * Numerics   FP32 arithmetic with one rounding at each output store (half
  *            step, to nearest even); sums run in a fixed order, so the same
- *            call gives the same bits.  No float atomics.
+ *            call gives the same bits.  No float atomics.  That order goes by
+ *            the call's sizes and alignment and the device's SM count: in
+ *            another batch, a row's norm or softmax may differ in its last
+ *            bits.
  */
 #ifndef MT_DECODER_H
 #define MT_DECODER_H

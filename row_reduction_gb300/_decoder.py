@@ -5,8 +5,14 @@ The ``mt_*`` functions call the C functions of the same name; the functions
 under them check tensors, allocate outputs and fill the calls.  Tensors of one
 call are on one device and the work runs there, on ``stream`` (a
 ``torch.cuda.Stream``, a raw handle, or ``None`` for that device's current
-stream); what a call allocates belongs to the stream it runs on.  Nothing
-synchronises, and every call can be captured into a CUDA graph.
+stream); what a call allocates belongs to the stream it runs on.  These calls
+do not synchronise and can be captured into a CUDA graph; what is made once
+ahead of them is not part of that (:func:`rotary_frequencies` copies its table
+from the host, :func:`cache_alloc` fills its tensors with zeros).
+
+As in the rest of the package, autograd records nothing of a call: what comes
+back requires no gradient, whatever the inputs did.  :func:`rotary_backward`
+is the gradient of :func:`rotary`.
 """
 from __future__ import annotations
 
@@ -447,7 +453,8 @@ def rotary(q, k, positions, freqs, interleaved=False, q_weight=None,
     dimension dense).  With eps, each head is first RMS-normalised and
     multiplied by q_weight or k_weight (None: ones).  out: (q, k) to write to;
     the inputs themselves turn them in place.  Returns (q, k), or q alone
-    where k is None."""
+    where k is None; autograd does not record the call, its gradients are
+    :func:`rotary_backward`'s."""
     dt, index = _first(q, "q")
     handle = _here(index, stream)
     if handle is None:

@@ -18,15 +18,16 @@
 // exchange is the norm's sum over L lanes.
 //
 // Angles.  turns[i] is the pair's frequency in units of 2^-64 turns; position
-// times that, modulo 2^64, is the angle exactly (the frequency's own rounding
-// of 2^-65 turns grows to 2^-34 turns at position 2^31).  Its top 32 bits,
-// taken as signed, give the angle in [-pi, pi) to 2^-33 turns, and their
-// conversion to FP32 rounds at 2^-25 of half a turn: 1e-7 radians, whatever
-// the position.  FP32 storage then takes sincospif (2 ulp).  For 16-bit
-// storage __sinf and __cosf are enough: on [-pi, pi] they are off by at most
-// 2^-21.4 and 2^-21.2, with the angle's three roundings 1e-6 in all, where the
-// output's own rounding is up to 2^-12 (FP16) or 2^-9 (BF16); sincospif there
-// costs as much as the rest of a token.
+// times that, modulo 2^64, is the angle exactly (the frequency's own rounding,
+// at most 2^-63 turns, grows to 2^-32 turns at position 2^31).  Its top 32
+// bits, taken as signed, give the angle in [-pi, pi), cut off by less than
+// 2^-32 turns (1.5e-9 radians), and their conversion to FP32 rounds at 2^-25
+// of half a turn: 1e-7 radians in all, whatever the position.  FP32 storage
+// then takes sincospif (2 ulp).  For 16-bit storage __sinf and __cosf are
+// enough: on [-pi, pi] they are off by at most 2^-21.4 and 2^-21.2, with the
+// angle's three roundings 1e-6 in all, where the output's own rounding is up
+// to 2^-12 (FP16) or 2^-9 (BF16); sincospif there costs as much as the rest of
+// a token.
 #pragma once
 
 #include "mt_decoder.cuh"
@@ -227,10 +228,10 @@ __device__ __forceinline__ void rot_groups(
 
 // Forward (and, with the sines' sign turned, backward without norm).  Bound by
 // latency at 16 warps per SM (128 registers: coefficients, and the loads of
-// four groups; 24 warps with 8-byte packs and no norm): BF16, 16384 tokens of 32 + 8 heads of 128 with norm 60 us,
-// 5.6 TB/s, 82% of the measured copy bandwidth.  The
-// loads of U groups of heads are issued before the angles are computed and
-// before any of them is used.  HQ < U: a warp has at most HQ groups of
+// four groups; 24 warps with 8-byte packs and no norm): BF16, 16384 tokens of
+// 32 + 8 heads of 128 with norm 60 us, 5.6 TB/s, 82% of the measured copy
+// bandwidth.  The loads of U groups of heads are issued before the angles are
+// computed and before any of them is used.  HQ < U: a warp has at most HQ groups of
 // queries and U - HQ of keys, all of them asked for at once.
 template <typename T, int V, int K, bool ILV, bool NORM, int HQ>
 __global__ void __launch_bounds__(
