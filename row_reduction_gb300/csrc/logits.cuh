@@ -20,15 +20,23 @@
 // through distributed shared memory behind one cluster barrier; and each
 // thread scales its exponentials once.
 //
-// Bound.  Without history 5.3 us for 64 x 131072 BF16 (its bytes' time) and
-// 41 us for the softmax of 256 x 131072 (half the copy bandwidth).  With
-// history a CTA is a chain of short phases (count, touch, join, write), of
-// which the two CTAs that 64 registers allow per SM do not hide all: 19 us
+// Bound.  Without history 5.2 us for 64 x 131072 BF16 (33.5 MB, which L2
+// holds) and 40 us for the softmax of 256 x 131072 (half the copy bandwidth).
+// With history a CTA is a chain of short phases (count, touch, join, write),
+// of which the two CTAs that 64 registers allow per SM do not hide all: 19 us
 // with 8192 tokens and 300 biases per row, 65 us with 1024 tokens and a mask.
+// Short rows are the farthest from their bytes' time: each still holds half an
+// SM through the whole chain (459 x 2798 FP16 with 225 biases 17 us).  FP32
+// with 32 values per thread does not fit 64 registers (132 to 256 bytes of
+// spills): softmax of 256 x 65536 35 us, with 1024 tokens and a mask 63 us.
 //
 // Alignment.  Packs of V values start at 16-byte boundaries of x: pack p of
 // a row holds columns p V - shift + e, shift being the row's address modulo
-// 16 in elements, so only a row's first and last pack can be partial.
+// 16 in elements, so only a row's first and last pack can be partial; such
+// rows take guarded kernels (348 x 35405 BF16 25 us, 348 x 35408 18 us).  The
+// ids of a history are read 16 bytes at a time where every row of them starts
+// at a 16-byte boundary, else one by one (64 x 131072 with a history of 8191
+// 23 us, of 8192 19 us; 17 x 50257 with 32767 27 us, with 32768 20 us).
 #pragma once
 
 #include "mt_decoder.cuh"

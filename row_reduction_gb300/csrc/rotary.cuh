@@ -227,12 +227,14 @@ __device__ __forceinline__ void rot_groups(
 }
 
 // Forward (and, with the sines' sign turned, backward without norm).  Bound by
-// latency at 16 warps per SM (128 registers: coefficients, and the loads of
-// four groups; 24 warps with 8-byte packs and no norm): BF16, 16384 tokens of
-// 32 + 8 heads of 128 with norm 60 us, 5.6 TB/s, 82% of the measured copy
-// bandwidth.  The loads of U groups of heads are issued before the angles are
-// computed and before any of them is used.  HQ < U: a warp has at most HQ groups of
-// queries and U - HQ of keys, all of them asked for at once.
+// latency at 16 warps per SM (128 registers, and 24 bytes spilled: coefficients,
+// and the loads of four groups; 24 warps with 8-byte packs and no norm): BF16,
+// 16384 tokens of 32 + 8 heads of 128 with norm 60 us, 5.6 TB/s, 82% of the
+// measured copy bandwidth.  With few heads the angles and weights of a token
+// are worked out by each group of lanes (57359 tokens of 4 + 1 heads of 64
+// 32 us, 34%).  The loads of U groups of heads are issued before the angles
+// are computed and before any of them is used.  HQ < U: a warp has at most HQ
+// groups of queries and U - HQ of keys, all of them asked for at once.
 template <typename T, int V, int K, bool ILV, bool NORM, int HQ>
 __global__ void __launch_bounds__(
     kRotThreads, sizeof(T) == 2 && V * K <= 4 && !NORM ? 3 : 2)
@@ -353,8 +355,8 @@ __global__ void __launch_bounds__(
 // the CTA writes one row of partial sums, which rotary_dweight_kernel adds.
 // Bound by dependent arithmetic at 16 warps per SM, with one item's loads on
 // their way: BF16, 8192 tokens of 32 + 8 heads of 128 54 us, 4.6 TB/s.  FP32
-// packs hold half the values; at 80 registers (of 110) 24 warps fit: 86 us for
-// 94 there.  (BF16 with half as many per lane: 56 us at 24 warps.)
+// packs hold half the values; at 80 registers (of 110, 40 bytes spilled) 24 warps
+// fit: 86 us for 94 there.  (BF16 with half as many per lane: 56 us at 24 warps.)
 template <typename T, int V, int K, bool ILV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2)
     rotary_backward_kernel(const RotArgs a) {
