@@ -740,12 +740,13 @@ def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None,
     tokens [rows, history] int32: ids of each row's history, of which the
     first lengths[row] count (int32; None: all) and the first
     prompt_lengths[row] are the prompt (int32; None: none), both clamped to
-    0..history; ids outside the vocabulary are passed over.  repetition (ids of the whole history),
-    frequency and presence (ids after the prompt): float32 [rows].  bias_ids
-    [rows, n] int32 and bias [rows, n] float32, n <= 1024: values added to
-    single logits.  temperature: float32 [rows].  mask int32 [rows, words] or
-    [words], words >= (vocab+31)//32: bit v%32 of word v//32 allows token v.
-    The order is: repetition, frequency and presence, bias, temperature, mask.
+    0..history; ids outside the vocabulary are passed over.  repetition (ids
+    of the whole history), frequency and presence (ids after the prompt):
+    float32 [rows].  bias_ids [rows, n] int32 and bias [rows, n] float32,
+    n <= 1024: values added to single logits.  temperature: float32 [rows].
+    mask int32 [rows, words] or [words], words >= (vocab+31)//32: bit v%32 of
+    word v//32 allows token v.  The order is: repetition, frequency and
+    presence, bias, temperature, mask.
     mode: "logits", "softmax" or "log_softmax"; a row of which the mask leaves
     nothing has probabilities 0 and log-probabilities -inf.  out may be
     logits."""
