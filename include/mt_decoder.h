@@ -5,7 +5,10 @@
  * RMSNorm in front of them (forward and backward), the quantised cache
  * (rows of heads reduced to one scale per group and stored as 8-bit codes,
  * and read back), and the logits (penalties, biases, grammar mask and
- * temperature, then the row's softmax or log-softmax in the same pass).
+ * temperature, then the row's softmax or log-softmax in the same pass); and
+ * what stands around that cache: the pages of a step's tokens, attention over
+ * the cached codes, and the norms behind a block and before the next one with
+ * the block's gate and the residual's scale (forward and backward).
  * Plain C; implemented in the same library.
  *
  * Conventions, where they differ from mt_rowreduce.h
@@ -259,6 +262,178 @@ typedef struct mt_logits_call {
 
 MT_API mt_status mt_process_logits(int dtype, const mt_logits_call_t *call,
                                    mt_stream_t stream);
+
+/* ---- pages of a step ---------------------------------------------------------
+ * A cache of pages of page_size slots is shared by sequences.  Sequence s
+ * holds lengths[s] tokens, in the pages that its row of the table names, and
+ * is to hold counts[s] more.  It needs
+ *     n_s = ceil((lengths + counts) / page_size) - ceil(lengths / page_size)
+ * new pages, which are taken from the end of the list of free pages, in the
+ * order of the sequences: with e_s = n_0 + .. + n_(s-1), its i-th new page is
+ * free_pages[*free_count - 1 - e_s - i], and its row of the table takes them
+ * behind the pages that it has.  A sequence whose pages run past the table's
+ * width or whose length passes 2^31 - 1 gets none, and counts as n_s = 0; one
+ * that needs pages of which not all are left, e_s + n_s > *free_count, gets
+ * none either (nor does any after it that needs some).  A sequence that got no
+ * pages but needs some keeps its table and length, and its rows get slot -1.
+ *
+ * Rows offsets[s] .. offsets[s+1]-1 of the step's packed batch are sequence
+ * s's new tokens: slots[r] is the slot of row r and positions[r] its position
+ * in its sequence (lengths[s], lengths[s]+1, ...); behind the batch -1 and 0.
+ * A row whose page is a negative entry gets slot -1.  The table's entries of
+ * pages that are not new are read only, and only for the rows that stand in
+ * them.  Negative lengths and counts count as 0, *free_count is clamped to
+ * 0 .. free_size, and offsets end at 2^31 - 1.  Called again with the same
+ * arguments (lengths, free_count), it does the same again. */
+typedef struct mt_cache_extend_call {
+    int32_t *table;            /* sequences x pages, row stride table_stride;
+                                  takes the new pages */
+    int64_t table_stride;      /* >= pages with more than one sequence */
+    const int32_t *lengths, *counts; /* sequences each */
+    const int32_t *free_pages; /* free_size page numbers, >= 0 and different */
+    const int32_t *free_count; /* DEVICE: how many of them are free, from the
+                                  start of the list */
+    int32_t *offsets;          /* sequences + 1 */
+    int64_t *slots;            /* rows */
+    int32_t *positions;        /* rows */
+    int32_t *new_lengths;      /* sequences: lengths + counts, or lengths */
+    int32_t *new_free_count;   /* 1 */
+    int64_t rows;              /* 0..2^31 - 1 */
+    int32_t pages;             /* the table's width, >= 0 */
+    int32_t sequences;         /* 0..2^31 - 2 */
+    int32_t free_size;         /* 0..2^31 - 2 */
+    int32_t page_size;         /* >= 1 */
+} mt_cache_extend_call_t;
+
+/* The outputs must not be the inputs (the table apart). */
+MT_API mt_status mt_cache_extend(const mt_cache_extend_call_t *call,
+                                 mt_stream_t stream);
+
+/* ---- attention over the cache --------------------------------------------------
+ * Queries against the keys and values of the quantised cache, where they
+ * stand.  Rows offsets[s] .. offsets[s+1]-1 of q belong to sequence s and
+ * stand at positions p = starts[s], starts[s]+1, ...; key j of a sequence is
+ * in slot table[s*table_stride + j/page_size] * page_size + j % page_size, as
+ * in mt_cache_slots.  Query head h reads key head h / (q_heads / k_heads).
+ *     z_j = scale (q . k_j)
+ *     z_j = cap tanh(z_j / cap)             (cap > 0)
+ *     z_j -= slopes[h] |p - j|              (slopes)
+ *     o = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
+ * over the keys that the row sees: from 0, or first[row], to p, or last[row],
+ * and of those with a window the keys from p - window + 1 on.  Bounds are
+ * clamped to the keys that the sequence holds, 0 .. starts[s] + its rows - 1,
+ * so first makes a document's mask and last a prefix's; a key without a page
+ * (a negative entry, past the table's width or the cache's slots) is not
+ * seen.  A row that sees nothing gives zeros, and lse -infinity.  Rows before
+ * offsets[0] and from offsets[sequences] on are left as they were.  A query
+ * head that holds a NaN or an infinity, and a row that sees a group that reads
+ * back as NaN in the values, or in the keys, gives NaN (from a value: in that
+ * group alone); what a row does not see has no effect on it.  (The codes of
+ * e4m3 that are NaN themselves, which mt_cache_write never stores, must not
+ * stand in slots that a row of the sequence sees.) */
+typedef struct mt_attention_call {
+    const void *q;             /* rows x q_heads x dim */
+    void *out;                 /* the same type and shape */
+    float *lse;                /* rows x q_heads, contiguous, or NULL */
+    int64_t q_row, q_head, out_row, out_head; /* strides in elements */
+    const void *k_codes, *v_codes;    /* as in mt_cache_rows_t */
+    const float *k_scales, *v_scales;
+    const int32_t *table;      /* sequences x pages */
+    int64_t table_stride;
+    const int32_t *offsets;    /* sequences + 1, not decreasing */
+    const int32_t *starts;     /* sequences */
+    const int32_t *first, *last; /* rows each, or NULL */
+    const float *slopes;       /* q_heads, or NULL */
+    int64_t rows;              /* 0..2^31 - 1 */
+    int64_t slots;
+    int32_t sequences, pages, page_size;
+    int32_t q_heads;           /* a multiple of k_heads, at most 65536 */
+    int32_t k_heads;           /* >= 1 */
+    int32_t dim;               /* 1..512 */
+    int32_t group;             /* divides dim */
+    int32_t format;            /* mt_cache_format */
+    int32_t window;            /* >= 1, or 0: none */
+    float scale;               /* finite */
+    float cap;                 /* > 0 and finite, or 0: none */
+    int32_t reserved;          /* 0 */
+} mt_attention_call_t;
+
+/* dtype: mt_dtype of q and out.  The workspace is as in mt_rotary_backward
+ * (mt_cache_attention_workspace() bytes, 16-byte aligned; NULL where those
+ * are 0); its size goes by the call's sizes and the current device. */
+MT_API mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
+                                    void *workspace, size_t workspace_bytes,
+                                    mt_stream_t stream);
+MT_API mt_status mt_cache_attention_workspace(int dtype,
+                                              const mt_attention_call_t *call,
+                                              size_t *bytes);
+
+/* ---- norms around a block ------------------------------------------------------
+ * A block's output x joins the residual stream, through a norm of its own and
+ * a gate, and the stream goes through the norm before the next block, in one
+ * pass over each row:
+ *     u = x / sqrt(mean(x^2) + eps) * weight     (MT_NORM_AFTER; else u = x)
+ *     h = residual_scale * residual + gate * u
+ *     y = h / sqrt(mean(h^2) + eps) * next_weight   (MT_NORM_BEFORE)
+ * y is made from h before its rounding.  gate may be NULL (ones). */
+enum {
+    MT_NORM_AFTER = 1,  /* the norm behind the block */
+    MT_NORM_BEFORE = 2  /* the norm before the next one */
+};
+
+typedef struct mt_block_norm_call {
+    const void *x, *residual;      /* rows x cols */
+    const void *gate;              /* rows x cols, row stride 0: one for all
+                                      rows; or NULL */
+    const void *weight;            /* cols, NULL = ones (MT_NORM_AFTER) */
+    const void *next_weight;       /* cols, NULL = ones (MT_NORM_BEFORE) */
+    void *h, *y;                   /* rows x cols; y with MT_NORM_BEFORE only */
+    int64_t x_stride, residual_stride, gate_stride, h_stride, y_stride;
+    int64_t rows;                  /* 0..2^31 - 1 */
+    int32_t cols;                  /* 1..2^20 */
+    int32_t norms;                 /* MT_NORM_AFTER, MT_NORM_BEFORE or both */
+    float eps, residual_scale;
+} mt_block_norm_call_t;
+
+/* h and y may be x or residual. */
+MT_API mt_status mt_block_norm(int dtype, const mt_block_norm_call_t *call,
+                               mt_stream_t stream);
+
+/* Gradients.  dy and dh are those of y and h, h the forward call's output.
+ * r1 = 1/sqrt(mean(x^2)+eps), r2 = 1/sqrt(mean(h^2)+eps):
+ *     g  = dh + r2 (dy next_weight - h r2^2 mean(dy next_weight h))
+ *     dresidual = residual_scale g,   dgate = g u,   e = g gate
+ *     dx = r1 (e weight - x r1^2 mean(e weight x))
+ *     dweight = sum over rows of e x r1,  dnext_weight = of dy h r2;
+ * without a norm g = dh, or dx = e.  A gate of one row for all has its
+ * gradient summed over rows in FP32 (dgate_sum); else dgate has the gate's
+ * type. */
+typedef struct mt_block_norm_back {
+    const void *dy;                /* with MT_NORM_BEFORE only */
+    const void *dh;                /* NULL: zeros (MT_NORM_BEFORE) */
+    const void *x;                 /* MT_NORM_AFTER, or a gate's gradient */
+    const void *h;                 /* with MT_NORM_BEFORE only */
+    const void *gate, *weight, *next_weight;   /* as in the forward call */
+    void *dx, *dresidual;          /* rows x cols */
+    void *dgate;                   /* rows x cols, or NULL */
+    float *dgate_sum, *dweight, *dnext_weight; /* cols each, or NULL */
+    int64_t dy_stride, dh_stride, x_stride, h_stride, gate_stride, dx_stride,
+        dresidual_stride, dgate_stride;
+    int64_t rows;
+    int32_t cols, norms;
+    float eps, residual_scale;
+} mt_block_norm_back_t;
+
+/* dx, dresidual and dgate may be dy, dh, x, h or gate exactly (each at most
+ * one of them).  The workspace is as in mt_rotary_backward: needed for
+ * dgate_sum, dweight and dnext_weight. */
+MT_API mt_status mt_block_norm_backward(int dtype,
+                                        const mt_block_norm_back_t *call,
+                                        void *workspace,
+                                        size_t workspace_bytes,
+                                        mt_stream_t stream);
+MT_API mt_status mt_block_norm_backward_workspace(
+    int dtype, const mt_block_norm_back_t *call, size_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,8 @@
 """GB300 (sm_103a) per-row FP32 reductions: RMSNorm, LayerNorm, residual
 LayerNorm, softmax, row sum and cross-entropy; and the row operators between
-a decoder's matrix products: rotary positions, the quantised cache and the
-processing of logits (``include/mt_decoder.h``).
+a decoder's matrix products: rotary positions, the quantised cache, its pages
+and attention over it, the norms around a block and the processing of logits
+(``include/mt_decoder.h``).
 
 The computation is the CUDA library ``_lib/libmt_rowreduce.so`` (C ABI in
 ``include/mt_rowreduce.h``), built by :func:`row_reduction_gb300.build.build`.
@@ -49,6 +50,12 @@ from ._decoder import (  # noqa: F401
     mt_process_logits, mt_rotary, mt_rotary_backward,
     mt_rotary_backward_workspace, mt_rotary_frequencies, mt_rotary_turns,
     process_logits, rotary, rotary_backward, rotary_frequencies)
+from ._step import (  # noqa: F401
+    MT_NORM_AFTER, MT_NORM_BEFORE, CacheStep, MtAttentionCall,
+    MtBlockNormBack, MtBlockNormCall, MtCacheExtendCall, block_norm,
+    block_norm_backward, cache_attention, cache_extend, mt_block_norm,
+    mt_block_norm_backward, mt_block_norm_backward_workspace,
+    mt_cache_attention, mt_cache_attention_workspace, mt_cache_extend)
 
 
 def _shape(x):

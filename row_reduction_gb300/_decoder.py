@@ -33,6 +33,9 @@ DECODER_EXPORTS = (
     "mt_rotary_frequencies", "mt_rotary_turns", "mt_rotary",
     "mt_rotary_backward", "mt_rotary_backward_workspace", "mt_cache_write",
     "mt_cache_read", "mt_cache_slots", "mt_process_logits",
+    "mt_cache_extend", "mt_cache_attention", "mt_cache_attention_workspace",
+    "mt_block_norm", "mt_block_norm_backward",
+    "mt_block_norm_backward_workspace",
 )
 
 _P, _I64, _I32, _F, _D = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,

@@ -26,12 +26,14 @@ OPS = ("rmsnorm", "layernorm", "residual_layernorm", "softmax", "row_sum",
        "cross_entropy", "residual_rmsnorm", "log_softmax")
 DTYPES = ("f32", "f16", "bf16")
 SOURCES = (["api.cpp", "planner.cpp", "mean.cu", "probe.cu", "decoder.cpp",
-            "cache.cu"] +
-           [f"{op}_{dt}.cu" for op in ("rotary", "logits") for dt in DTYPES] +
+            "cache.cu", "step.cpp", "extend.cu", "attention.cu"] +
+           [f"{op}_{dt}.cu" for op in ("rotary", "logits", "block_norm")
+            for dt in DTYPES] +
            [f"ops_{op}_{dt}.cu" for op in OPS for dt in DTYPES])
 DEPENDS = ["mt_internal.h", "mt_kernels.cuh", "mt_stage.cuh", "plan_table.inc",
            "mt_decoder_internal.h", "mt_decoder.cuh", "rotary.cuh",
-           "logits.cuh"]
+           "logits.cuh", "mt_decoder_checks.h", "attention.cuh",
+           "block_norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler",

@@ -107,4 +107,31 @@ cudaError_t launch_logits_f32(const mt_logits_call_t &c, cudaStream_t s);
 cudaError_t launch_logits_f16(const mt_logits_call_t &c, cudaStream_t s);
 cudaError_t launch_logits_bf16(const mt_logits_call_t &c, cudaStream_t s);
 
+// ---- pages of a step ---------------------------------------------------------
+cudaError_t launch_cache_extend(const mt_cache_extend_call_t &c,
+                                cudaStream_t s);
+
+// ---- attention over the cache --------------------------------------------------
+constexpr int kAttentionMaxDim = 512;
+cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
+                                 cudaStream_t s);
+
+// ---- norms around a block ------------------------------------------------------
+constexpr int kNormMaxCols = 1 << 20;
+// Rows of partial sums of the backward pass (each of 3 x cols FP32 values).
+constexpr int kNormBackBlocks = 304;
+#define MT_DECLARE_BLOCK_NORM(dt)                                            \
+    cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &c,        \
+                                       cudaStream_t s);                      \
+    cudaError_t launch_block_norm_back_##dt(const mt_block_norm_back_t &c,   \
+                                            float *partial, int blocks,      \
+                                            cudaStream_t s);
+MT_DECLARE_BLOCK_NORM(f32)
+MT_DECLARE_BLOCK_NORM(f16)
+MT_DECLARE_BLOCK_NORM(bf16)
+#undef MT_DECLARE_BLOCK_NORM
+// d_k[i] = sum over blocks of partial[block][k][i], where d_k is wanted.
+cudaError_t launch_norm_sums(const float *partial, int cols, int blocks,
+                             float *d0, float *d1, float *d2, cudaStream_t s);
+
 }  // namespace mt

@@ -1,0 +1,246 @@
+// step.cpp -- C entry points of the operators around a decoder's cache: pages
+// of a step, attention over the cache, the norms around a block.  Argument
+// checks and choice of kernel variants.
+#include <math.h>
+#include <stdint.h>
+
+#include "mt_decoder_checks.h"
+#include "mt_decoder_internal.h"
+
+namespace mt {
+namespace {
+
+// ---- attention -------------------------------------------------------------
+mt_status attention_setup(int dtype, const mt_attention_call_t *c,
+                          bool *empty) {
+    if (c == nullptr || !known_dtype(dtype)) return MT_ERR_INVALID_ARGUMENT;
+    const int es = dtype_size(dtype);
+    if (c->rows < 0 || c->slots < 0 || c->sequences < 0 || c->pages < 0 ||
+        c->page_size < 1 || c->k_heads < 1 || c->q_heads < 1 ||
+        c->q_heads % c->k_heads != 0 || c->dim < 1 || c->group < 1 ||
+        c->dim % c->group != 0 || c->window < 0 || c->reserved != 0 ||
+        (c->format != MT_CACHE_E4M3 && c->format != MT_CACHE_INT8) ||
+        !isfinite(c->scale) || !(c->cap >= 0.f) || !isfinite(c->cap) ||
+        c->table_stride < 0)
+        return MT_ERR_INVALID_ARGUMENT;
+    if (c->dim > kAttentionMaxDim || c->q_heads > 65536 ||
+        c->rows > INT32_MAX)
+        return MT_ERR_UNSUPPORTED;
+    if (misaligned(c->q, es) || misaligned(c->out, es) ||
+        misaligned(c->lse, 4) || misaligned(c->k_scales, 4) ||
+        misaligned(c->v_scales, 4) || misaligned(c->table, 4) ||
+        misaligned(c->offsets, 4) || misaligned(c->starts, 4) ||
+        misaligned(c->first, 4) || misaligned(c->last, 4) ||
+        misaligned(c->slopes, 4))
+        return MT_ERR_INVALID_ARGUMENT;
+    const int64_t width = (int64_t)c->k_heads * c->dim;
+    if (c->slots > kMaxOffset / width ||
+        (c->sequences > 1 && c->table_stride > kMaxOffset / c->sequences))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (!reachable(c->q_row, c->q_head, c->rows, c->q_heads) ||
+        !reachable(c->out_row, c->out_head, c->rows, c->q_heads) ||
+        (c->rows > 0 &&
+         !disjoint(c->out_row, c->out_head, c->rows, c->q_heads, c->dim)))
+        return MT_ERR_INVALID_ARGUMENT;
+    *empty = c->rows == 0 || c->sequences == 0;
+    if (*empty) return MT_OK;
+    const bool keys = c->slots > 0 && c->pages > 0;
+    if (!c->q || !c->out || !c->offsets || !c->starts ||
+        (keys && (!c->k_codes || !c->v_codes || !c->k_scales ||
+                  !c->v_scales || !c->table)))
+        return MT_ERR_INVALID_ARGUMENT;
+    return MT_OK;
+}
+
+// ---- norms around a block ----------------------------------------------------
+// A matrix of a call: wanted or not, aligned, rows that are within reach and,
+// for an output, do not overlap.
+bool matrix_ok(const void *p, int64_t stride, int64_t rows, int64_t cols,
+               int es, bool output) {
+    int64_t extent = cols;
+    return !misaligned(p, es) && add_extent(stride, rows, &extent) &&
+           (!output || rows <= 1 || stride >= cols);
+}
+bool norm_sizes_ok(int dtype, int64_t rows, int64_t cols, int norms, float eps,
+                   float scale) {
+    return known_dtype(dtype) && rows >= 0 && cols >= 1 && norms >= 1 &&
+           norms <= (MT_NORM_AFTER | MT_NORM_BEFORE) && eps >= 0.f &&
+           isfinite(scale);
+}
+
+size_t norm_workspace(const mt_block_norm_back_t &c) {
+    return c.dgate_sum || c.dweight || c.dnext_weight
+               ? (size_t)kNormBackBlocks * 3 * (size_t)c.cols * sizeof(float)
+               : 0;
+}
+
+}  // namespace
+}  // namespace mt
+
+using namespace mt;
+
+extern "C" {
+
+mt_status mt_cache_extend(const mt_cache_extend_call_t *call,
+                          mt_stream_t stream) {
+    if (call == nullptr) return MT_ERR_INVALID_ARGUMENT;
+    const mt_cache_extend_call_t &c = *call;
+    if (c.rows < 0 || c.pages < 0 || c.sequences < 0 || c.free_size < 0 ||
+        c.page_size < 1 || c.table_stride < 0 ||
+        (c.sequences > 1 && (c.table_stride < c.pages ||
+                             c.table_stride > kMaxOffset / c.sequences)) ||
+        misaligned(c.table, 4) || misaligned(c.lengths, 4) ||
+        misaligned(c.counts, 4) || misaligned(c.free_pages, 4) ||
+        misaligned(c.free_count, 4) || misaligned(c.offsets, 4) ||
+        misaligned(c.slots, 8) || misaligned(c.positions, 4) ||
+        misaligned(c.new_lengths, 4) || misaligned(c.new_free_count, 4))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (!c.free_count || !c.offsets || !c.new_free_count ||
+        c.new_free_count == c.free_count ||
+        (c.free_size > 0 && !c.free_pages) ||
+        (c.rows > 0 && (!c.slots || !c.positions)) ||
+        (c.sequences > 0 && (!c.lengths || !c.counts || !c.new_lengths ||
+                             c.new_lengths == c.lengths ||
+                             c.new_lengths == c.counts ||
+                             (c.pages > 0 && !c.table))))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (c.rows > INT32_MAX || c.sequences == INT32_MAX ||
+        c.free_size == INT32_MAX)
+        return MT_ERR_UNSUPPORTED;
+    return status_from_cuda(launch_cache_extend(c, (cudaStream_t)stream));
+}
+
+mt_status mt_cache_attention_workspace(int dtype,
+                                       const mt_attention_call_t *call,
+                                       size_t *bytes) {
+    bool empty = false;
+    if (bytes == nullptr) return MT_ERR_INVALID_ARGUMENT;
+    if (mt_status st = attention_setup(dtype, call, &empty)) return st;
+    *bytes = 0;
+    return MT_OK;
+}
+
+mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
+                             void *workspace, size_t workspace_bytes,
+                             mt_stream_t stream) {
+    bool empty = false;
+    if (mt_status st = attention_setup(dtype, call, &empty)) return st;
+    if (empty) return MT_OK;
+    (void)workspace;
+    (void)workspace_bytes;
+    return status_from_cuda(
+        launch_attention_any(dtype, *call, (cudaStream_t)stream));
+}
+
+mt_status mt_block_norm(int dtype, const mt_block_norm_call_t *call,
+                        mt_stream_t stream) {
+    if (call == nullptr) return MT_ERR_INVALID_ARGUMENT;
+    const mt_block_norm_call_t &c = *call;
+    if (!norm_sizes_ok(dtype, c.rows, c.cols, c.norms, c.eps,
+                       c.residual_scale))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (c.cols > kNormMaxCols || c.rows > INT32_MAX)
+        return MT_ERR_UNSUPPORTED;
+    const int es = dtype_size(dtype);
+    const bool before = c.norms & MT_NORM_BEFORE;
+    if (!matrix_ok(c.x, c.x_stride, c.rows, c.cols, es, false) ||
+        !matrix_ok(c.residual, c.residual_stride, c.rows, c.cols, es, false) ||
+        !matrix_ok(c.gate, c.gate_stride, c.rows, c.cols, es, false) ||
+        !matrix_ok(c.h, c.h_stride, c.rows, c.cols, es, true) ||
+        (before && !matrix_ok(c.y, c.y_stride, c.rows, c.cols, es, true)) ||
+        misaligned(c.weight, es) || misaligned(c.next_weight, es) ||
+        (!(c.norms & MT_NORM_AFTER) && c.weight) ||
+        (!before && (c.next_weight || c.y)))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (c.rows == 0) return MT_OK;
+    if (!c.x || !c.residual || !c.h || (before && !c.y) || c.h == c.y)
+        return MT_ERR_INVALID_ARGUMENT;
+    cudaStream_t s = (cudaStream_t)stream;
+    return status_from_cuda(dtype == DT_F32   ? launch_block_norm_f32(c, s)
+                            : dtype == DT_F16 ? launch_block_norm_f16(c, s)
+                                              : launch_block_norm_bf16(c, s));
+}
+
+mt_status mt_block_norm_backward_workspace(int dtype,
+                                           const mt_block_norm_back_t *call,
+                                           size_t *bytes) {
+    if (call == nullptr || bytes == nullptr ||
+        !norm_sizes_ok(dtype, call->rows, call->cols, call->norms, call->eps,
+                       call->residual_scale))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (call->cols > kNormMaxCols || call->rows > INT32_MAX)
+        return MT_ERR_UNSUPPORTED;
+    *bytes = norm_workspace(*call);
+    return MT_OK;
+}
+
+mt_status mt_block_norm_backward(int dtype, const mt_block_norm_back_t *call,
+                                 void *workspace, size_t workspace_bytes,
+                                 mt_stream_t stream) {
+    if (call == nullptr) return MT_ERR_INVALID_ARGUMENT;
+    const mt_block_norm_back_t &c = *call;
+    if (!norm_sizes_ok(dtype, c.rows, c.cols, c.norms, c.eps,
+                       c.residual_scale))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (c.cols > kNormMaxCols || c.rows > INT32_MAX)
+        return MT_ERR_UNSUPPORTED;
+    const int es = dtype_size(dtype);
+    const bool before = c.norms & MT_NORM_BEFORE;
+    const bool after = c.norms & MT_NORM_AFTER;
+    const auto in = [&](const void *p, int64_t stride) {
+        return matrix_ok(p, stride, c.rows, c.cols, es, false);
+    };
+    const auto out = [&](const void *p, int64_t stride) {
+        return p == nullptr || matrix_ok(p, stride, c.rows, c.cols, es, true);
+    };
+    if (!in(c.dy, c.dy_stride) || !in(c.dh, c.dh_stride) ||
+        !in(c.x, c.x_stride) || !in(c.h, c.h_stride) ||
+        !in(c.gate, c.gate_stride) || !out(c.dx, c.dx_stride) ||
+        !out(c.dresidual, c.dresidual_stride) ||
+        !out(c.dgate, c.dgate_stride) || misaligned(c.weight, es) ||
+        misaligned(c.next_weight, es) || misaligned(c.dgate_sum, 4) ||
+        misaligned(c.dweight, 4) || misaligned(c.dnext_weight, 4))
+        return MT_ERR_INVALID_ARGUMENT;
+    // What a call without a norm, or without a gate, does not take.
+    if ((!before && (c.dy || c.h || c.next_weight || c.dnext_weight)) ||
+        (!after && (c.weight || c.dweight)) ||
+        (!c.gate && (c.dgate || c.dgate_sum)) || (c.dgate && c.dgate_sum))
+        return MT_ERR_INVALID_ARGUMENT;
+    cudaStream_t s = (cudaStream_t)stream;
+    float *sums[3] = {c.dgate_sum, c.dweight, c.dnext_weight};
+    const size_t need = norm_workspace(c);
+    if (c.rows == 0) {  // sums over no rows
+        for (float *d : sums)
+            if (d) {
+                cudaError_t e =
+                    cudaMemsetAsync(d, 0, c.cols * sizeof(float), s);
+                if (e != cudaSuccess) return status_from_cuda(e);
+            }
+        return MT_OK;
+    }
+    if (!c.dx || !c.dresidual || c.dx == c.dresidual ||
+        (c.dgate && (c.dgate == c.dx || c.dgate == c.dresidual)) ||
+        (before && (!c.dy || !c.h)) || (!before && !c.dh) ||
+        ((after || c.dgate || c.dgate_sum) && !c.x))
+        return MT_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return MT_ERR_OUT_OF_RESOURCES;
+    if (need > 0 && (workspace == nullptr || misaligned(workspace, 16)))
+        return MT_ERR_INVALID_ARGUMENT;
+    float *partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    int64_t blocks = 2 * sms < kNormBackBlocks ? 2 * sms : kNormBackBlocks;
+    if (blocks > c.rows) blocks = c.rows;
+    e = dtype == DT_F32
+            ? launch_block_norm_back_f32(c, partial, (int)blocks, s)
+        : dtype == DT_F16
+            ? launch_block_norm_back_f16(c, partial, (int)blocks, s)
+            : launch_block_norm_back_bf16(c, partial, (int)blocks, s);
+    if (e == cudaSuccess && need > 0)
+        e = launch_norm_sums(partial, c.cols, (int)blocks, sums[0], sums[1],
+                             sums[2], s);
+    return status_from_cuda(e);
+}
+
+}  // extern "C"
