@@ -1,0 +1,5 @@
+// Attention over the cache: int8 codes, FP16 and FP32 queries, 8 columns.
+#include "attention_mma.cuh"
+namespace mt {
+MT_DEFINE_ATTENTION(launch_attention_int8_p2n1, true, 2, 1)
+}  // namespace mt

@@ -115,6 +115,30 @@ cudaError_t launch_cache_extend(const mt_cache_extend_call_t &c,
 constexpr int kAttentionMaxDim = 512;
 cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
                                  cudaStream_t s);
+// A call on the matrix kernels: how its rows and query heads are cut into
+// tiles of 8 nt columns, and the CTAs that share its work.
+struct AttentionPlan {
+    int32_t nt;
+    int32_t times;  // query heads per key head
+    int32_t per;    // rows of a tile
+    int32_t parts;  // tiles that share a row's query heads
+    int32_t ctas;
+};
+// Bytes behind the partial sums, one record per CTA.
+constexpr int kAttentionRecord = 24;
+#define MT_DECLARE_ATTENTION(name)                                           \
+    cudaError_t name(const AttentionPlan &p, const mt_attention_call_t &c,   \
+                     int dtype, void *workspace, cudaStream_t s);
+// parts of FP16 that queries and weights are held in, and nt
+MT_DECLARE_ATTENTION(launch_attention_e4m3_p1n1)
+MT_DECLARE_ATTENTION(launch_attention_e4m3_p1n2)
+MT_DECLARE_ATTENTION(launch_attention_e4m3_p2n1)
+MT_DECLARE_ATTENTION(launch_attention_e4m3_p2n2)
+MT_DECLARE_ATTENTION(launch_attention_int8_p1n1)
+MT_DECLARE_ATTENTION(launch_attention_int8_p1n2)
+MT_DECLARE_ATTENTION(launch_attention_int8_p2n1)
+MT_DECLARE_ATTENTION(launch_attention_int8_p2n2)
+#undef MT_DECLARE_ATTENTION
 
 // ---- norms around a block ------------------------------------------------------
 constexpr int kNormMaxCols = 1 << 20;

@@ -52,6 +52,44 @@ mt_status attention_setup(int dtype, const mt_attention_call_t *c,
     return MT_OK;
 }
 
+// The sizes that the matrix kernels take (on any device).
+bool attention_head(const mt_attention_call_t &c) {
+    const int groups = c.dim / c.group;
+    switch (c.dim) {
+        case 64: return groups <= 2;
+        case 80: case 96: return groups == 1;
+        case 128: return groups == 1 || groups == 2 || groups == 4;
+        case 256: return groups == 1 || groups == 2 || groups == 8;
+        default: return false;
+    }
+}
+// Whether the call goes to the matrix kernels, and how: else a warp per row
+// and query head.
+mt_status attention_plan(const mt_attention_call_t &c, bool *matrix,
+                         AttentionPlan *p) {
+    *matrix = attention_head(c) && c.slots <= INT32_MAX &&
+              !misaligned(c.k_codes, 32) && !misaligned(c.v_codes, 32) &&
+              !misaligned(c.k_scales, 16) && !misaligned(c.v_scales, 16);
+    if (!*matrix) return MT_OK;
+    int sms = 0;
+    if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
+    p->times = c.q_heads / c.k_heads;
+    // 16 columns where a sequence has more than 8 on average
+    p->nt = c.dim <= 128 && (int64_t)p->times * c.rows > 8LL * c.sequences
+                ? 2 : 1;
+    const int columns = 8 * p->nt;
+    p->per = p->times < columns ? columns / p->times : 1;
+    p->parts = (p->times + columns - 1) / columns;
+    // as many as are resident at once
+    p->ctas = sms * (p->nt == 1 && c.dim <= 128 ? 3 : 2);
+    return MT_OK;
+}
+size_t attention_workspace(const mt_attention_call_t &c,
+                           const AttentionPlan &p) {
+    return (size_t)p.ctas * (2 * 8 * (size_t)p.nt * (c.dim + 2) *
+                             sizeof(float) + kAttentionRecord);
+}
+
 // ---- norms around a block ----------------------------------------------------
 // A matrix of a call: wanted or not, aligned, rows that are within reach and,
 // for an output, do not overlap.
@@ -117,6 +155,11 @@ mt_status mt_cache_attention_workspace(int dtype,
     if (bytes == nullptr) return MT_ERR_INVALID_ARGUMENT;
     if (mt_status st = attention_setup(dtype, call, &empty)) return st;
     *bytes = 0;
+    bool matrix = false;
+    AttentionPlan p = {};
+    if (empty) return MT_OK;
+    if (mt_status st = attention_plan(*call, &matrix, &p)) return st;
+    if (matrix) *bytes = attention_workspace(*call, p);
     return MT_OK;
 }
 
@@ -126,10 +169,28 @@ mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
     bool empty = false;
     if (mt_status st = attention_setup(dtype, call, &empty)) return st;
     if (empty) return MT_OK;
-    (void)workspace;
-    (void)workspace_bytes;
-    return status_from_cuda(
-        launch_attention_any(dtype, *call, (cudaStream_t)stream));
+    bool matrix = false;
+    AttentionPlan p = {};
+    if (mt_status st = attention_plan(*call, &matrix, &p)) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (!matrix)
+        return status_from_cuda(launch_attention_any(dtype, *call, s));
+    if (workspace_bytes < attention_workspace(*call, p))
+        return MT_ERR_OUT_OF_RESOURCES;
+    if (workspace == nullptr || misaligned(workspace, 16))
+        return MT_ERR_INVALID_ARGUMENT;
+    const bool int8 = call->format == MT_CACHE_INT8;
+    const auto launch =
+        dtype == DT_BF16
+            ? (int8 ? p.nt == 2 ? launch_attention_int8_p1n2
+                                : launch_attention_int8_p1n1
+                    : p.nt == 2 ? launch_attention_e4m3_p1n2
+                                : launch_attention_e4m3_p1n1)
+            : (int8 ? p.nt == 2 ? launch_attention_int8_p2n2
+                                : launch_attention_int8_p2n1
+                    : p.nt == 2 ? launch_attention_e4m3_p2n2
+                                : launch_attention_e4m3_p2n1);
+    return status_from_cuda(launch(p, *call, dtype, workspace, s));
 }
 
 mt_status mt_block_norm(int dtype, const mt_block_norm_call_t *call,
