@@ -5,7 +5,15 @@
 
 #include "mt_decoder.cuh"
 
+struct CUtensorMap_st;
+
 namespace mt {
+
+// A tensor of `rows` rows of `width` bytes, gathered in fours (rows of 128 and
+// 64 bytes swizzled).
+cudaError_t attention_map(const void *codes, int64_t rows, int width,
+                          CUtensorMap_st *map);
+
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -23,6 +31,14 @@ __device__ __forceinline__ float pow2(float t) {
 __device__ __forceinline__ float capped(float z, float cap, float inv_cap) {
     const float e = pow2(z * inv_cap * (2.f * kLog2e));
     return cap - 2.f * cap / (1.f + e);
+}
+
+// The same for z2 = 2 z / cap and cap2 = cap, both times log2(e), with the
+// hardware's reciprocal (one unit in the last place).
+__device__ __forceinline__ float capped2(float z2, float cap2) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + pow2(z2)));
+    return fmaf(-2.f * cap2, r, cap2);
 }
 
 // The sequence of a row of the batch (offsets[0] <= r < offsets[sequences]).
@@ -44,7 +60,8 @@ __device__ __forceinline__ void row_sees(const mt_attention_call_t &c,
     hi = c.last ? (int64_t)c.last[row] : p;
     if (c.window) lo = max(lo, p - c.window + 1);
     lo = max(lo, (int64_t)0);
-    hi = min(hi, min(held, (int64_t)c.pages * c.page_size) - 1);
+    hi = c.slots > 0
+             ? min(hi, min(held, (int64_t)c.pages * c.page_size) - 1) : -1;
 }
 
 // The slot of key j of a sequence, or -1.

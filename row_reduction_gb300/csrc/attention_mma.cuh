@@ -4,10 +4,14 @@
 // Scores are formed transposed, keys x queries (S^T = K Q^T), so that the
 // cache's codes, which are the long operand, fill the instruction's 16 rows and
 // the few query heads that share a key head its 8 columns.  A warp goes through
-// chunks of keys of its own: codes come straight into registers, in the order
-// of the instruction's fragments (the order of the dimensions is free as long
-// as queries have the same; see Q below), one chunk ahead of the one that is
-// worked on, and are widened to FP16 there, exactly.  What the scores give
+// chunks of keys of its own: codes are gathered into shared
+// memory of the warp's own by tensor copies, four keys' rows to a copy, a chunk
+// ahead of the one that is worked on, and widened to FP16 on the way into
+// fragments, exactly (the order of the dimensions is free as long as queries
+// have the same, so a lane reads up to 16 bytes of a key at once).  Loads into
+// registers kept too few bytes in flight (64 sequences to 16384 keys of 8 heads
+// of 128: 247 us), and copies of 16 bytes per lane took longer to issue than a
+// chunk takes to work on (351 us).  What the scores give
 // turns into the other product's operand (O^T = V^T P^T) by one transposition
 // of 8 x 8 values within the warp.
 //
@@ -17,10 +21,16 @@
 // Roundings to FP16.  Codes are exact.  Queries are held as a power of two
 // times FP16 with the head's largest value at 2^14..2^15, BF16 and FP16 values
 // exactly (down to 2^-28 of the largest), FP32 in two parts (2^-22).  Weights
-// times the values' scales are held against the chunk's largest likewise: one
-// part for BF16 output (2^-11, a quarter of its own rounding), two for FP16 and
-// FP32.  Sums over a chunk are the instruction's, in FP32; sums over chunks are
-// rounded to nearest in FP32.
+// times the values' scales are held likewise, their largest so far at
+// 2^11..2^12 or above: one part for BF16 output (2^-11, a quarter of its own
+// rounding), two for FP16 and FP32.  Sums are FP32: for BF16 output the
+// instruction's own all along, else its sums of a chunk, added up to nearest.
+//
+// References.  A column's weights are exponentials about a reference that
+// follows its largest score only where that runs 2^8 ahead, and the power of
+// two under a group's weights where they pass 2^15: one vote tells that neither
+// is so, which holds for nearly all chunks, and saves the exchange of maxima
+// among lanes and the scaling of the sums.
 //
 // Work is dealt out in units, a chunk of keys of one tile (rows of a sequence
 // and the query heads of a key head, up to 8 NT columns): every CTA takes an
@@ -30,6 +40,8 @@
 // runs is left as partial sums, which a second kernel joins in order.
 #pragma once
 
+#include <cuda.h>
+
 #include "attention.cuh"
 
 namespace mt {
@@ -38,24 +50,35 @@ namespace {
 constexpr int kWarps = 4;
 
 // ---- sums of a tile's units ----------------------------------------------------
-// sum over 0 <= t < n of floor((a t + b) / m), for a, b >= 0.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a,
-                                             int64_t b) {
-    int64_t s = 0;
+// a / b for a >= 0, b > 0; in 32 bits, many times quicker, where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((uint64_t)(a | b) >> 32) == 0)
+        return (int64_t)((unsigned)a / (unsigned)b);
+    return a / b;
+}
+// sum over 0 <= t < n of floor((a t + b) / M), for a, b >= 0: whole parts
+// aside, the points under a line, counted along the other axis in turn.
+template <int M>
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
+    int64_t s = 0, m = M;
     while (n > 0) {
-        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
+        s += (n - 1) * n / 2 * quotient(a, m) + n * quotient(b, m);
+        a -= quotient(a, m) * m;
+        b -= quotient(b, m) * m;
         const int64_t y = a * n + b;
         if (y < m) break;
-        n = y / m;
-        b = y % m;
+        n = quotient(y, m);
+        b = y - n * m;
         const int64_t x = m;
         m = a;
         a = x;
     }
     return s;
 }
+
+// A tile's begin and end (queries, the first keys' way, the warps' sums
+// joined) in units: without them runs of short sequences are the last to end.
+constexpr int64_t kExtra = 8;
 
 // How the rows of a sequence are cut into tiles and units of KEYS keys.
 struct Tiles {
@@ -69,25 +92,28 @@ struct Tiles {
     template <int KEYS>
     __device__ __forceinline__ int64_t first(int t) const {
         if (window == 0) return 0;
-        return max(start + (int64_t)t * per - window + 1, (int64_t)0) / KEYS;
+        return (int64_t)((uint64_t)max(start + (int64_t)t * per - window + 1,
+                                       (int64_t)0) / KEYS);
     }
     template <int KEYS>
     __device__ __forceinline__ int64_t last(int t) const {
         const int64_t r = all ? rows : min((int64_t)(t + 1) * per,
                                            (int64_t)rows);
-        return (start + r - 1) / KEYS;
+        return (int64_t)((uint64_t)(start + r - 1) / KEYS);
     }
-    // Units of the tiles before t (first <= last in every tile).
+    // Units of the tiles before t (first <= last in every tile), kExtra to
+    // each for what a tile costs besides.
     template <int KEYS>
     __device__ __forceinline__ int64_t before(int t) const {
         if (t <= 0) return 0;
-        int64_t s = t;
+        int64_t s = (1 + kExtra) * (int64_t)t;
+        if (t == 1) return s + last<KEYS>(0) - first<KEYS>(0);
         if (all) {
             s += t * last<KEYS>(0);
         } else {
             // all tiles but the sequence's last are whole
             const int whole = t < count ? t : count - 1;
-            s += floor_sum(whole, KEYS, per, start + per - 1);
+            s += floor_sum<KEYS>(whole, per, start + per - 1);
             if (t > whole) s += last<KEYS>(count - 1);
         }
         if (window != 0) {
@@ -95,7 +121,8 @@ struct Tiles {
             const int64_t short_of = window - 1 - start;
             const int64_t z = short_of <= 0 ? 0 : (short_of + per - 1) / per;
             if (t > z)
-                s -= floor_sum(t - z, KEYS, per, start + z * per - window + 1);
+                s -= floor_sum<KEYS>(t - z, per,
+                                         start + z * per - window + 1);
         }
         return s;
     }
@@ -176,109 +203,152 @@ __device__ __forceinline__ void widen4(unsigned w, unsigned &lo,
         lo = *reinterpret_cast<const unsigned *>(&x);
         hi = *reinterpret_cast<const unsigned *>(&y);
     } else {
-        const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(
-            (__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-        const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(
-            (__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        lo = (unsigned)x.x | (unsigned)x.y << 16;
-        hi = (unsigned)y.x | (unsigned)y.y << 16;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
     }
 }
 
-// BYTES of codes into words; zeros where not `on`.
-template <int BYTES>
-__device__ __forceinline__ void load_codes(const uint8_t *p, bool on,
+// `bytes` (a constant: 16, 8, 4 or 2) of codes from shared memory into words.
+__device__ __forceinline__ void read_codes(const uint8_t *p, int bytes,
                                            unsigned *w) {
-    if constexpr (BYTES == 32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 0;
-        if (on)
-            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, "
-                         "[%8];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]),
-                           "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                         : "l"(p));
-    } else if constexpr (BYTES == 16) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = *reinterpret_cast<const uint4 *>(p);
+    if (bytes == 32 || bytes == 16) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (BYTES == 8) {
-        uint2 v = make_uint2(0, 0);
-        if (on) v = *reinterpret_cast<const uint2 *>(p);
+    } else if (bytes == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x; w[1] = v.y;
-    } else if constexpr (BYTES == 4) {
-        w[0] = on ? *reinterpret_cast<const unsigned *>(p) : 0u;
+    } else if (bytes == 4) {
+        w[0] = *reinterpret_cast<const unsigned *>(p);
     } else {
-        w[0] = on ? *reinterpret_cast<const unsigned short *>(p) : 0u;
+        w[0] = *reinterpret_cast<const uint16_t *>(p);
     }
 }
-template <int N>
-__device__ __forceinline__ void load_scales(const float *p, bool on,
-                                            float *v) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    if (!on) return;
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(p + i);
-            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-        }
-    } else if constexpr (N == 2) {
-        const float2 f = *reinterpret_cast<const float2 *>(p);
-        v[0] = f.x; v[1] = f.y;
+
+// Four rows of a tensor of rows into shared memory, completing on `bar`.
+__device__ __forceinline__ void gather4(void *to, const CUtensorMap *map,
+                                        int r0, int r1, int r2, int r3,
+                                        uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::"
+        "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            smem_addr(to)),
+        "l"(map), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// A key's scales into shared memory, on their way; zeros where not `on`.
+template <int BYTES>
+__device__ __forceinline__ void copy_scales(void *to, const void *from,
+                                            bool on) {
+    if constexpr (BYTES > 16) {
+        copy_scales<16>(to, from, on);
+        copy_scales<BYTES - 16>(static_cast<char *>(to) + 16,
+                                static_cast<const char *>(from) + 16, on);
     } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = p[i];
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                         (unsigned)__cvta_generic_to_shared(to)),
+                     "l"(from), "n"(BYTES), "r"(on ? BYTES : 0)
+                     : "memory");
     }
 }
 
 // ---- a head's layout -------------------------------------------------------------
+struct Block {
+    int base, size;
+};
 template <int DIM_, int GROUPS_>
 struct Head {
     static constexpr int DIM = DIM_, GROUPS = GROUPS_;
     static constexpr int GROUP = DIM / GROUPS;
-    // A group is cut into blocks of B dimensions, the largest power of two
-    // that divides it, at most 128.  Of a block, lane l of a quad holds the
-    // B/4 bytes from l B/4 on of a key (two steps of the instruction take a
-    // word of 4), and lane l of eight the B/8 bytes from l B/8 on of a value.
-    static constexpr int B = (GROUP & -GROUP) > 128 ? 128 : (GROUP & -GROUP);
-    static constexpr int BLOCKS = DIM / B;
     static constexpr int KEYS = DIM > 128 ? 16 : 32;  // of a chunk
-    static constexpr int STEPS = DIM / 16;
-    static constexpr int VWORDS = B >= 32 ? DIM / 32 : BLOCKS;
+    static constexpr int STEPS = DIM / 16;            // of the instruction
+    static constexpr int PER = GROUP / 16;            // of a group
+    // A group's dimensions come in blocks of 128, 64, 32 and 16, the largest
+    // that fit first.  Of a block, lane l of a quad holds the size/4 bytes from
+    // l size/4 on of a key, a word of them for each step, and lane l of eight
+    // the size/8 bytes from l size/8 on of a value, two of them for each step.
+    static __host__ __device__ constexpr Block block(int step) {
+        int base = 0;
+        for (int size = 128; size >= 16; size /= 2)
+            while (GROUP - base >= size) {
+                if (step * 16 < base + size) return {base, size};
+                base += size;
+            }
+        return {0, 0};
+    }
+    // A chunk's codes as the copies lay them out: planes of up to 128 bytes of
+    // each key, rows of 128 or 64 bytes permuted (swizzled) so that what a
+    // quarter of a warp reads at once lies in different banks, rows of 80 in
+    // fours at a distance that the copies can start at.
+    static constexpr int PLANES = DIM > 128 ? DIM / 128 : 1;
+    static constexpr int WIDE = DIM / PLANES;
+    static constexpr int FOUR = (4 * WIDE + 127) / 128 * 128;
+    static constexpr int PLANE = KEYS / 4 * FOUR;
+    static __device__ __forceinline__ int place(int key, int byte) {
+        const int plane = PLANES > 1 ? byte / WIDE * PLANE : 0;
+        byte = PLANES > 1 ? byte % WIDE : byte;
+        if (WIDE == 128) return plane + key * 128 + (byte ^ (key & 7) << 4);
+        if (WIDE == 64) return key * 64 + (byte ^ (key >> 1 & 3) << 4);
+        return key / 4 * FOUR + key % 4 * WIDE + byte;
+    }
 };
 
 // A column of a tile: one row's query head.
 struct Column {
-    float f;            // score = f (q . k): the scale and the query's power
-    float slope;
+    float slope;        // in units of log 2
     int32_t lo, hi;     // keys that it sees
     int32_t p;          // its row's position
-    int32_t pad;
 };
 
 template <class H, int PARTS, int NT>
 struct Shared {
+    // Each warp's own: the codes of two chunks, then its sums.
+    struct Codes {
+        uint8_t k[H::PLANES * H::PLANE], v[H::PLANES * H::PLANE];
+    };
+    union Own {
+        Codes codes[2];
+        float o[8 * NT][H::DIM + 4];
+    };
+    struct Scales {
+        float k[H::KEYS][H::GROUPS], v[H::KEYS][H::GROUPS];
+    };
+    Own own[kWarps];                    // at a multiple of 1024 bytes
+    Scales scales[kWarps][2];
     uint2 q[NT][PARTS][H::STEPS][32];   // fragments
+    uint64_t bar[kWarps][2];
     Column column[8 * NT];
+    // What a column's product takes to be a score in units of log 2 (with cap,
+    // to be 2 score / cap in them): the scale and the query's power of two.
+    float f[8 * NT];
     int32_t lo_any, hi_any, lo_all, hi_all;
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    float o[kWarps][8 * NT][H::DIM + 4];
     int64_t scan[kWarps];
     int64_t at;         // place of the CTA's first unit in its sequence
     int32_t sequence;
+    static_assert(sizeof(Own) == 2 * sizeof(Codes) &&
+                  sizeof(Codes) % 1024 == 0, "swizzled rows keep their place");
+};
+
+// A key head of the cache: its codes as rows of a tensor, its scales.
+struct Cache {
+    const CUtensorMap *k, *v;
+    const float *ks, *vs;
+    int heads, head;
+    unsigned scales;  // of a slot
 };
 
 template <class H, bool INT8, int PARTS, int NT>
 struct Warp {
     static constexpr int KT = H::KEYS / 16;     // rows of 16 keys
-    static constexpr int C = 8 * NT;
-    unsigned k[KT][2][H::STEPS];
-    unsigned v[KT][4][H::VWORDS];
-    float ks[KT][2][H::GROUPS], vs[KT][2][H::GROUPS];
-    float o[NT][H::STEPS][4];
-    float m[NT][2], l[NT][2];
+    using Codes = typename Shared<H, PARTS, NT>::Codes;
+    using Scales = typename Shared<H, PARTS, NT>::Scales;
+    float o[NT][H::STEPS][4];        // in units of 2^-(up of its group)
+    float ref[NT][2], l[NT][2];
+    // Exponent bits of the largest weight times scale so far, of each column
+    // and group; four to a word.
+    unsigned most[NT][2][(H::GROUPS + 3) / 4];
 
     __device__ __forceinline__ void begin() {
 #pragma unroll
@@ -287,68 +357,72 @@ struct Warp {
             for (int i = 0; i < H::STEPS; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ref[n][h] = -INFINITY;
+                l[n][h] = 0.f;
+#pragma unroll
+                for (int i = 0; i < (H::GROUPS + 3) / 4; ++i)
+                    most[n][h][i] = 0;
+            }
         }
     }
-    // slot: of the chunk's key `lane`, or -1.
-    __device__ __forceinline__ void load_keys(const mt_attention_call_t &c,
-                                              int head, int slot) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    // All sums NaN.
+    __device__ __forceinline__ void spoil() {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int s = __shfl_sync(kFull, slot, 16 * t + 8 * i + g);
-                const int64_t at = (int64_t)s * c.k_heads + head;
-                const uint8_t *p = static_cast<const uint8_t *>(c.k_codes) +
-                                   at * H::DIM + q * (H::B / 4);
-#pragma unroll
-                for (int b = 0; b < H::BLOCKS; ++b)
-                    load_codes<H::B / 4>(p + b * H::B, s >= 0,
-                                         &k[t][i][b * (H::B / 16)]);
-                load_scales<H::GROUPS>(c.k_scales + at * H::GROUPS, s >= 0,
-                                       ks[t][i]);
-            }
+        for (int n = 0; n < NT; ++n)
+            ref[n][0] = ref[n][1] = l[n][0] = l[n][1] = NAN;
     }
-    __device__ __forceinline__ void load_values(const mt_attention_call_t &c,
-                                                int head, int slot) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    __device__ __forceinline__ unsigned exponent(int n, int h, int gr) const {
+        return max(most[n][h][gr / 4] >> gr % 4 * 8 & 0xffu, 12u);
+    }
+    // 2^11 over the power of two under the largest, and its inverse.
+    static __device__ __forceinline__ float up(unsigned e) {
+        return __uint_as_float((265u - e) << 23);
+    }
+    static __device__ __forceinline__ float down(unsigned e) {
+        return __uint_as_float((e - 11u) << 23);
+    }
+    // A chunk's codes and scales on their way.  slot: of the chunk's key
+    // `lane`, or -1; such a key takes the codes of one that is there (its
+    // weights will be zero, and those codes are numbers), of slot 0 if none is
+    // (the chunk is passed over then).
+    __device__ __forceinline__ void load(const Cache &c, int slot, Codes &to,
+                                         Scales &scales, uint64_t *bar) {
+        const int lane = threadIdx.x & 31;
+        const unsigned there = __ballot_sync(kFull, slot >= 0);
+        const int some =
+            there ? __shfl_sync(kFull, slot, __ffs(there) - 1) : 0;
+        // lanes: fours of keys, planes of keys, planes of values
+        constexpr int kFours = H::KEYS / 4;
+        const int four = lane % kFours, kind = lane / kFours;
+        int row[4];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = __shfl_sync(
-                    kFull, slot, 16 * t + 2 * q + (i & 1) + 8 * (i >> 1));
-                const uint8_t *p = static_cast<const uint8_t *>(c.v_codes) +
-                                   ((int64_t)s * c.k_heads + head) * H::DIM +
-                                   g * (H::B / 8);
-#pragma unroll
-                for (int b = 0; b < H::BLOCKS; ++b)
-                    load_codes<H::B / 8>(
-                        p + b * H::B, s >= 0,
-                        &v[t][i][H::B >= 32 ? b * (H::B / 32) : b]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int s = __shfl_sync(kFull, slot, 16 * t + 8 * i + g);
-                load_scales<H::GROUPS>(
-                    c.v_scales + ((int64_t)s * c.k_heads + head) * H::GROUPS,
-                    s >= 0, vs[t][i]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int s = __shfl_sync(kFull, slot, 4 * four + i);
+            row[i] = ((s < 0 ? some : s) * c.heads + c.head) * H::PLANES +
+                     kind % H::PLANES;
+        }
+        if (lane == 0) mbar_expect_tx(bar, 2 * H::KEYS * H::DIM);
+        __syncwarp();
+        if (kind < 2 * H::PLANES) {
+            const bool values = kind >= H::PLANES;
+            gather4((values ? to.v : to.k) + kind % H::PLANES * H::PLANE +
+                        four * H::FOUR,
+                    values ? c.v : c.k, row[0], row[1], row[2], row[3], bar);
+        }
+        if (lane < H::KEYS) {
+            const uint64_t from = (uint64_t)(unsigned)max(slot, 0) * c.scales;
+            copy_scales<4 * H::GROUPS>(scales.k[lane], c.ks + from, slot >= 0);
+            copy_scales<4 * H::GROUPS>(scales.v[lane], c.vs + from, slot >= 0);
         }
     }
     // Sums of codes times queries times the keys' scales.
-    __device__ __forceinline__ void scores(
-        const Shared<H, PARTS, NT> &sh, float (&z)[NT][KT][4]) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[n][t][e] = 0.f;
-        constexpr int kPer = H::STEPS / H::GROUPS;  // steps of a group
+    __device__ __forceinline__ void scores(const Shared<H, PARTS, NT> &sh,
+                                           const Codes &st,
+                                           const Scales &scales,
+                                           float (&z)[NT][KT][4]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
             float acc[NT][KT][4];
@@ -359,31 +433,56 @@ struct Warp {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[n][t][e] = 0.f;
 #pragma unroll
-            for (int i = gr * kPer; i < (gr + 1) * kPer; ++i) {
-                unsigned a[KT][4];
-#pragma unroll
-                for (int t = 0; t < KT; ++t) {
-                    widen4<INT8>(k[t][0][i], a[t][0], a[t][2]);
-                    widen4<INT8>(k[t][1][i], a[t][1], a[t][3]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        const uint2 b = sh.q[n][part][i][lane];
-#pragma unroll
-                        for (int t = 0; t < KT; ++t)
-                            mma16816(acc[n][t], a[t], b.x, b.y);
-                    }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int b = 0; b < H::PER;) {
+                // half a block of 128 at a time: 16 bytes of a key
+                const Block block = H::block(b);
+                const int size = block.size > 64 ? 64 : block.size;
+                const int at = gr * H::GROUP + block.base +
+                               q * (block.size / 4) +
+                               4 * (b - block.base / 16);
+                unsigned k[KT][2][4];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[n][t][e] = fmaf(acc[n][t][e], ks[t][e >> 1][gr],
-                                          z[n][t][e]);
+                    for (int i = 0; i < 2; ++i)
+                        read_codes(st.k + H::place(16 * t + 8 * i + g,
+                                                   at & ~15) + (at & 15),
+                                   size / 4, k[t][i]);
+#pragma unroll
+                for (int x = 0; x < size / 16; ++x) {
+                    unsigned a[KT][4];
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        widen4<INT8>(k[t][0][x], a[t][0], a[t][2]);
+                        widen4<INT8>(k[t][1][x], a[t][1], a[t][3]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) {
+                            const uint2 v =
+                                sh.q[n][part][gr * H::PER + b + x][lane];
+#pragma unroll
+                            for (int t = 0; t < KT; ++t)
+                                mma16816(acc[n][t], a[t], v.x, v.y);
+                        }
+                }
+                b += size / 16;
+            }
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float f = scales.k[16 * t + 8 * i + g][gr];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &to = z[n][t][2 * i + h];
+                            const float from = acc[n][t][2 * i + h];
+                            to = gr == 0 ? from * f : fmaf(from, f, to);
+                        }
+                }
         }
     }
     // Scores to exponents of two; -infinity, and a bit of `hidden`, for keys
@@ -391,8 +490,8 @@ struct Warp {
     // that have a slot.
     __device__ __forceinline__ void bend(const mt_attention_call_t &c,
                                          const Shared<H, PARTS, NT> &sh,
-                                         float inv_cap, int j0,
-                                         unsigned there, unsigned &hidden,
+                                         int j0, unsigned there,
+                                         unsigned &hidden,
                                          float (&z)[NT][KT][4]) {
         hidden = 0;
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -400,63 +499,85 @@ struct Warp {
         const bool whole = there == kAll && j0 >= sh.lo_all &&
                            j0 + H::KEYS - 1 <= sh.hi_all;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const Column &col = sh.column[8 * n + 2 * q + h];
-                const float f = col.f;
+                const float f = sh.f[8 * n + 2 * q + h];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) z[n][t][2 * i + h] *= f;
-                if (c.cap > 0.f) {
-#pragma unroll
-                    for (int t = 0; t < KT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            z[n][t][2 * i + h] =
-                                capped(z[n][t][2 * i + h], c.cap, inv_cap);
-                }
-                if (c.slopes != nullptr) {
-#pragma unroll
-                    for (int t = 0; t < KT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = j0 + 16 * t + 8 * i + g;
-                            z[n][t][2 * i + h] -=
-                                col.slope * (float)abs(col.p - j);
-                        }
-                }
-                if (!whole) {
-#pragma unroll
-                    for (int t = 0; t < KT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int at = 16 * t + 8 * i + g;
-                            const bool see = there >> at & 1u &&
-                                             j0 + at >= col.lo &&
-                                             j0 + at <= col.hi;
-                            if (!see) {
-                                z[n][t][2 * i + h] = -INFINITY;
-                                hidden |= 1u << (4 * (n * KT + t) + 2 * i + h);
-                            }
-                        }
-                }
             }
+        if (c.cap > 0.f) {
+            const float cap2 = c.cap * kLog2e;
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[n][t][e] *= kLog2e;
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[n][t][e] = capped2(z[n][t][e], cap2);
         }
-    }
-    // Weights about the running maximum, and what the sums so far take.
-    __device__ __forceinline__ void weigh(float (&z)[NT][KT][4],
-                                          float (&keep)[NT][2]) {
+        if (c.slopes == nullptr && whole) return;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float top = z[n][0][h];
+                const Column &col = sh.column[8 * n + 2 * q + h];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = 16 * t + 8 * i + g;
+                        float &v = z[n][t][2 * i + h];
+                        if (c.slopes != nullptr)
+                            v -= col.slope * (float)abs(col.p - (j0 + at));
+                        if (!whole &&
+                            !(there >> at & 1u && j0 + at >= col.lo &&
+                              j0 + at <= col.hi)) {
+                            v = -INFINITY;
+                            hidden |= 1u << (4 * (n * KT + t) + 2 * i + h);
+                        }
+                    }
+            }
+    }
+    // Weights about the columns' references, which move where a score is 2^8
+    // ahead of one (or there is none yet, or something is NaN).
+    __device__ __forceinline__ void weigh(float (&z)[NT][KT][4]) {
+        bool ahead = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        ahead |= !(z[n][t][2 * i + h] <= ref[n][h] + 8.f);
+        if (__any_sync(kFull, ahead)) move(z);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float about = ref[n][h] == -INFINITY ? 0.f : ref[n][h];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &w = z[n][t][2 * i + h];
+                        w = pow2(w - about);
+                        l[n][h] += w;
+                    }
+            }
+    }
+    // References to the columns' largest scores; sums and exponents follow.
+    __device__ __forceinline__ void move(const float (&z)[NT][KT][4]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float keep[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = ref[n][h];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -465,123 +586,194 @@ struct Warp {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     top = nanmax(top, __shfl_xor_sync(kFull, top, off));
-                top = nanmax(top, m[n][h]);
-                // nothing seen yet: all weights are 2^-infinity
-                const float ref = top == -INFINITY ? 0.f : top;
-                keep[n][h] = pow2(m[n][h] - ref);
-                m[n][h] = top;
-                float sum = 0.f;
+                keep[h] = pow2(ref[n][h] - (top == -INFINITY ? 0.f : top));
+                ref[n][h] = top;
+                l[n][h] *= keep[h];
+                // the exponents of the largest so far in the new units: down by
+                // as many powers of two, to the sums' own where that is less
+                const unsigned less =
+                    127u - min(__float_as_uint(keep[h]) >> 23, 127u);
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
+                for (int gr = 0; gr < H::GROUPS; ++gr) {
+                    const unsigned old = exponent(n, h, gr);
+                    const unsigned now = max(old > less ? old - less : 0u, 12u);
+                    set(n, h, gr, now);
+                    const float f = keep[h] * up(now) * down(old);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &w = z[n][t][2 * i + h];
-                        w = pow2(w - ref);
-                        sum += w;
+                    for (int i = gr * H::PER; i < (gr + 1) * H::PER; ++i) {
+                        o[n][i][h] *= f;
+                        o[n][i][2 + h] *= f;
                     }
-                l[n][h] = fmaf(l[n][h], keep[n][h], sum);
+                }
             }
+        }
+    }
+    __device__ __forceinline__ void set(int n, int h, int gr, unsigned e) {
+        unsigned &w = most[n][h][gr / 4];
+        w = (w & ~(0xffu << gr % 4 * 8)) | e << gr % 4 * 8;
+    }
+    // A group's weights times scales, a power of two up, within FP16's range:
+    // where they pass it, or the largest so far is left far behind by the first
+    // that come, that power moves.
+    __device__ __forceinline__ void scaled(const float (&w)[NT][KT][4],
+                                           unsigned hidden,
+                                           const Scales &scales, int gr,
+                                           float (&x)[NT][KT][4]) {
+        const int g = (threadIdx.x & 31) >> 2;
+        float scale[KT][2];
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                scale[t][i] = scales.v[16 * t + 8 * i + g][gr];
+        bool out = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float f[2] = {up(exponent(n, 0, gr)), up(exponent(n, 1, gr))};
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n][t][e] = w[n][t][e] * scale[t][e >> 1];
+                    // not seen: nothing, whatever stands in the scale
+                    if (hidden >> (4 * (n * KT + t) + e) & 1u)
+                        x[n][t][e] = 0.f;
+                    x[n][t][e] *= f[e & 1];
+                    out |= !(fabsf(x[n][t][e]) < 32768.f);
+                }
+        }
+        if (__any_sync(kFull, out)) raise(w, hidden, scale, gr, x);
+    }
+    __device__ __forceinline__ void raise(const float (&w)[NT][KT][4],
+                                       unsigned hidden,
+                                       const float (&scale)[KT][2], int gr,
+                                       float (&x)[NT][KT][4]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            unsigned e0 = 0, e1 = 0;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n][t][e] = hidden >> (4 * (n * KT + t) + e) & 1u
+                                     ? 0.f : w[n][t][e] * scale[t][e >> 1];
+                    const unsigned bits =
+                        __float_as_uint(fabsf(x[n][t][e])) >> 23;
+                    if (e & 1) e1 = max(e1, bits);
+                    else e0 = max(e0, bits);
+                }
+            unsigned ex = e0 | e1 << 16;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+                ex = __vmaxu2(ex, __shfl_xor_sync(kFull, ex, off));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                unsigned old = 0, now = 0;
+#pragma unroll
+                for (int r = 0; r < H::GROUPS; ++r)
+                    if (r == gr) {
+                        old = exponent(n, h, r);
+                        now = max(old, h ? ex >> 16 : ex & 0xffffu);
+                        set(n, h, r, now);
+                        const float f = up(now) * down(old);
+#pragma unroll
+                        for (int i = r * H::PER; i < (r + 1) * H::PER; ++i) {
+                            o[n][i][h] *= f;
+                            o[n][i][2 + h] *= f;
+                        }
+                    }
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    x[n][t][h] *= up(now);
+                    x[n][t][2 + h] *= up(now);
+                }
+            }
+        }
     }
     // Adds the chunk's weights times values.
     __device__ __forceinline__ void add(const float (&w)[NT][KT][4],
-                                        const float (&keep)[NT][2],
-                                        unsigned hidden) {
-        constexpr int kPer = H::STEPS / H::GROUPS;
+                                        unsigned hidden, const Codes &st,
+                                        const Scales &scales) {
+        const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
             unsigned b[NT][PARTS][KT][2];
-            float back[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float pv[KT][4];
-                unsigned e0 = 0, e1 = 0;
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pv[t][e] = w[n][t][e] * vs[t][e >> 1][gr];
-                        // not seen: nothing, whatever stands in the scale
-                        if (hidden >> (4 * (n * KT + t) + e) & 1u)
-                            pv[t][e] = 0.f;
-                        const unsigned bits = __float_as_uint(pv[t][e]);
-                        if (e & 1) e1 = max(e1, bits & 0x7fffffffu);
-                        else e0 = max(e0, bits & 0x7fffffffu);
-                    }
-                unsigned ex = e0 >> 23 | (e1 >> 23) << 16;
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
-                    ex = __vmaxu2(ex, __shfl_xor_sync(kFull, ex, off));
-                float up[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // the largest at 2^14..2^15
-                    const unsigned x = max(h ? ex >> 16 : ex & 0xffffu, 15u);
-                    up[h] = __uint_as_float((268u - x) << 23);
-                    back[n][h] = __uint_as_float((x - 14u) << 23);
-                }
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float x = pv[t][2 * i] * up[0];
-                        const float y = pv[t][2 * i + 1] * up[1];
-                        const unsigned hi = half_pair(x, y);
-                        b[n][0][t][i] = transpose8x8(hi);
-                        if constexpr (PARTS == 2) {
-                            const float2 r = from_half_pair(hi);
-                            b[n][1][t][i] =
-                                transpose8x8(half_pair(x - r.x, y - r.y));
-                        }
-                    }
-            }
-            // Two rows of the output per lane and step: dimensions 2 i and
-            // 2 i + 1 of its bytes; a pair of keys side by side.
-#pragma unroll
-            for (int i = gr * kPer; i < (gr + 1) * kPer; i += 2) {
-                // words with the dimensions of steps i and i + 1
-                unsigned a[2][KT][4];
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int word = H::B >= 32 ? i / 2 : i;
-                        const unsigned u = v[t][2 * y][word];
-                        const unsigned x = v[t][2 * y + 1][word];
-                        widen4<INT8>(__byte_perm(u, x, 0x5140), a[0][t][2 * y],
-                                     a[0][t][2 * y + 1]);
-                        if constexpr (H::B >= 32)
-                            widen4<INT8>(__byte_perm(u, x, 0x7362),
-                                         a[1][t][2 * y], a[1][t][2 * y + 1]);
-                        else if (i + 1 < (gr + 1) * kPer)
-                            widen4<INT8>(
-                                __byte_perm(v[t][2 * y][word + 1],
-                                            v[t][2 * y + 1][word + 1],
-                                            0x5140),
-                                a[1][t][2 * y], a[1][t][2 * y + 1]);
-                    }
+            {
+                float x[NT][KT][4];
+                scaled(w, hidden, scales, gr, x);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if (i + y >= (gr + 1) * kPer) continue;
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int t = 0; t < KT; ++t)
 #pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
+                        for (int i = 0; i < 2; ++i) {
+                            const float lo = x[n][t][2 * i];
+                            const float hi = x[n][t][2 * i + 1];
+                            const unsigned h = half_pair(lo, hi);
+                            b[n][0][t][i] = transpose8x8(h);
+                            if constexpr (PARTS == 2) {
+                                const float2 r = from_half_pair(h);
+                                b[n][1][t][i] =
+                                    transpose8x8(half_pair(lo - r.x,
+                                                           hi - r.y));
+                            }
+                        }
+            }
+            // Two rows of the output per lane and step: two bytes of its own
+            // of a value; a pair of keys side by side.
+#pragma unroll
+            for (int s = 0; s < H::PER;) {
+                const Block block = H::block(s);
+                const int at = gr * H::GROUP + block.base +
+                               g * (block.size / 8);
+                unsigned v[KT][4][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        read_codes(
+                            st.v + H::place(16 * t + 2 * q + (i & 1) +
+                                                8 * (i >> 1),
+                                            at & ~15) + (at & 15),
+                            block.size / 8, v[t][i]);
+#pragma unroll
+                for (int m = 0; m < block.size / 16; ++m) {
+                    unsigned a[KT][4];
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            widen4<INT8>(
+                                __byte_perm(v[t][2 * y][m / 2],
+                                            v[t][2 * y + 1][m / 2],
+                                            m & 1 ? 0x7362 : 0x5140),
+                                a[t][2 * y], a[t][2 * y + 1]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float (&to)[4] = o[n][gr * H::PER + s + m];
+                        if constexpr (PARTS == 1) {
 #pragma unroll
                             for (int t = 0; t < KT; ++t)
-                                mma16816(acc, a[y][t], b[n][part][t][0],
-                                         b[n][part][t][1]);
-                        float (&out)[4] = o[n][i + y];
+                                mma16816(to, a[t], b[n][0][t][0],
+                                         b[n][0][t][1]);
+                        } else {
+                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            out[e] = fmaf(acc[e], back[n][e & 1],
-                                          out[e] * keep[n][e & 1]);
+                            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                                for (int t = 0; t < KT; ++t)
+                                    mma16816(acc, a[t], b[n][part][t][0],
+                                             b[n][part][t][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) to[e] += acc[e];
+                        }
                     }
+                }
+                s += block.size / 16;
             }
         }
     }
 };
-
 
 // ---- a tile ------------------------------------------------------------------
 struct Tile {
@@ -626,133 +818,215 @@ __device__ __forceinline__ Place place_of(const Cut &cut, int first_row,
     return p;
 }
 
-// Queries and bounds of a tile into shared memory.
+// A thread's part of the queries of a tile: kPer threads to a column.
 template <class H, int PARTS, int NT>
-__device__ __forceinline__ void tile_begin(const mt_attention_call_t &c,
-                                           const Cut &cut, int dtype,
-                                           const Tile &a,
-                                           Shared<H, PARTS, NT> &sh) {
-    constexpr int C = 8 * NT, kPer = 32 * kWarps / C;  // threads per column
-    constexpr int kEach = H::DIM / kPer;
-    const int tid = threadIdx.x, col = tid / kPer, sub = tid % kPer;
-    const int from = c.offsets[a.s] + a.t * cut.per;
-    const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
-    const Place at = place_of<C>(cut, from, rows, a.head, a.part, col);
+struct Queries {
+    static constexpr int C = 8 * NT, kPer = 32 * kWarps / C;
+    static constexpr int kEach = H::DIM / kPer;
     float x[kEach];
-    float largest = 0.f;
-    const int64_t q = (int64_t)at.row * c.q_row + (int64_t)at.head * c.q_head;
+    int row, head;  // of this thread's column
+    bool used;
+    __device__ __forceinline__ void load(const mt_attention_call_t &c,
+                                         const Cut &cut, int dtype,
+                                         const Tile &a) {
+        const int col = threadIdx.x / kPer, sub = threadIdx.x % kPer;
+        const Place at = place_of<C>(
+            cut, c.offsets[a.s] + a.t * cut.per,
+            min(cut.per, a.tiles.rows - a.t * cut.per), a.head, a.part, col);
+        const int64_t q =
+            (int64_t)at.row * c.q_row + (int64_t)at.head * c.q_head;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-        x[i] = at.used ? load_as(PARTS == 1 ? (int)DT_BF16 : dtype, c.q,
-                                 q + sub + kPer * i)
-                       : 0.f;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) largest = nanmax(largest, fabsf(x[i]));
-#pragma unroll
-    for (int off = kPer / 2; off > 0; off >>= 1)
-        largest = nanmax(largest, __shfl_xor_sync(kFull, largest, off));
-    const unsigned e = max(__float_as_uint(largest) >> 23, 15u);
-    const bool bad = !(largest < INFINITY);
-    const float up = bad ? 0.f : __uint_as_float((268u - e) << 23);
-    __half *halves = reinterpret_cast<__half *>(&sh.q[col / 8][0][0][0]);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int d = sub + kPer * i, r = d % H::B;
-        const int step = d / H::B * (H::B / 16) + r % (H::B / 4) / 4;
-        const int lane = col % 8 * 4 + r / (H::B / 4);
-        const float v = bad ? 0.f : x[i] * up;
-        const __half hi = __float2half_rn(v);
-        halves[(step * 32 + lane) * 4 + r % 4] = hi;
-        if constexpr (PARTS == 2)
-            halves[((H::STEPS + step) * 32 + lane) * 4 + r % 4] =
-                __float2half_rn(v - __half2float(hi));
+        for (int i = 0; i < kEach; ++i)
+            x[i] = at.used ? load_as(PARTS == 1 ? (int)DT_BF16 : dtype, c.q,
+                                     q + sub + kPer * i)
+                           : 0.f;
     }
-    if (sub == 0) {
-        Column k = {};
-        k.lo = INT32_MIN;
-        k.hi = INT32_MAX;
-        if (at.used) {
-            const int64_t n = (int64_t)c.offsets[a.s + 1] - c.offsets[a.s];
-            const int64_t p = (int64_t)c.starts[a.s] +
-                              (at.row - c.offsets[a.s]);
-            int64_t lo, hi;
-            row_sees(c, at.row, p, c.starts[a.s] + n, lo, hi);
-            k.f = bad ? NAN : c.scale * __uint_as_float((e - 14u) << 23);
-            k.slope = c.slopes ? c.slopes[at.head] : 0.f;
-            k.lo = (int32_t)min(lo, (int64_t)INT32_MAX);
-            k.hi = (int32_t)max(min(hi, (int64_t)INT32_MAX), (int64_t)-1);
-            k.p = (int32_t)min(p, (int64_t)INT32_MAX);
-            k.pad = 1;
+    // Fragments, and the columns' factors, into shared memory.
+    __device__ __forceinline__ void put(const mt_attention_call_t &c,
+                                        Shared<H, PARTS, NT> &sh) {
+        const int col = threadIdx.x / kPer, sub = threadIdx.x % kPer;
+        float largest = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) largest = nanmax(largest, fabsf(x[i]));
+#pragma unroll
+        for (int off = kPer / 2; off > 0; off >>= 1)
+            largest = nanmax(largest, __shfl_xor_sync(kFull, largest, off));
+        const unsigned e = max(__float_as_uint(largest) >> 23, 15u);
+        const bool bad = !(largest < INFINITY);
+        const float up = bad ? 0.f : __uint_as_float((268u - e) << 23);
+        __half *halves = reinterpret_cast<__half *>(&sh.q[col / 8][0][0][0]);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int d = sub + kPer * i, r = d % H::GROUP;
+            const Block block = H::block(r / 16);
+            const int in = r - block.base, wide = block.size / 4;
+            const int step = d / H::GROUP * H::PER + block.base / 16 +
+                             in % wide / 4;
+            const int lane = col % 8 * 4 + in / wide;
+            const float v = bad ? 0.f : x[i] * up;
+            const __half hi = __float2half_rn(v);
+            halves[(step * 32 + lane) * 4 + r % 4] = hi;
+            if constexpr (PARTS == 2)
+                halves[((H::STEPS + step) * 32 + lane) * 4 + r % 4] =
+                    __float2half_rn(v - __half2float(hi));
         }
-        sh.column[col] = k;
+        if (sub == 0)
+            sh.f[col] = bad ? NAN
+                            : (c.cap > 0.f ? c.scale / c.cap * 2.f : c.scale) *
+                                  kLog2e * __uint_as_float((e - 14u) << 23);
     }
-    __syncthreads();
-    if (tid < 32) {
-        const Column k = tid < C ? sh.column[tid] : Column{};
-        const bool used = k.pad != 0, some = used && k.lo <= k.hi;
-        const int lo_any = __reduce_min_sync(kFull, some ? k.lo : INT32_MAX);
-        const int hi_any = __reduce_max_sync(kFull, some ? k.hi : -1);
-        const int lo_all = __reduce_max_sync(kFull, used ? k.lo : INT32_MIN);
-        const int hi_all = __reduce_min_sync(kFull, used ? k.hi : INT32_MAX);
-        if (tid == 0) {
-            sh.lo_any = lo_any;
-            sh.hi_any = hi_any;
-            sh.lo_all = lo_all;
-            sh.hi_all = hi_all;
-        }
+};
+
+// What the columns of a tile see, into shared memory.
+template <class H, int PARTS, int NT>
+__device__ __forceinline__ void tile_bounds(const mt_attention_call_t &c,
+                                            const Cut &cut, const Tile &a,
+                                            Shared<H, PARTS, NT> &sh) {
+    constexpr int C = 8 * NT;
+    const int col = threadIdx.x;
+    if (col >= 32) return;
+    const int from = c.offsets[a.s];
+    const Place at = place_of<C>(cut, from + a.t * cut.per,
+                                 min(cut.per, a.tiles.rows - a.t * cut.per),
+                                 a.head, a.part, col);
+    const bool used = col < C && at.used;
+    Column k = {0.f, INT32_MIN, INT32_MAX, 0};
+    if (used) {
+        const int64_t n = (int64_t)c.offsets[a.s + 1] - from;
+        const int64_t start = c.starts[a.s], p = start + (at.row - from);
+        int64_t lo, hi;
+        row_sees(c, at.row, p, start + n, lo, hi);
+        k.slope = c.slopes ? c.slopes[at.head] * kLog2e : 0.f;
+        k.lo = (int32_t)min(lo, (int64_t)INT32_MAX);
+        k.hi = (int32_t)max(min(hi, (int64_t)INT32_MAX), (int64_t)-1);
+        k.p = (int32_t)min(p, (int64_t)INT32_MAX);
     }
-    __syncthreads();
+    if (col < C) sh.column[col] = k;
+    const bool some = used && k.lo <= k.hi;
+    const int lo_any = __reduce_min_sync(kFull, some ? k.lo : INT32_MAX);
+    const int hi_any = __reduce_max_sync(kFull, some ? k.hi : -1);
+    const int lo_all = __reduce_max_sync(kFull, k.lo);
+    const int hi_all = __reduce_min_sync(kFull, k.hi);
+    if (col == 0) {
+        sh.lo_any = lo_any;
+        sh.hi_any = hi_any;
+        sh.lo_all = lo_all;
+        sh.hi_all = hi_all;
+    }
 }
 
-// The slot of key j, or -1 where no column sees it or it has none.
-__device__ __forceinline__ int slot_in(const mt_attention_call_t &c,
-                                       const int32_t *pages, int64_t j,
-                                       int lo, int hi) {
-    if (j < lo || j > hi) return -1;
-    const int page = (int)((unsigned)j / (unsigned)c.page_size);
-    const int id = pages[page];
-    const int64_t slot = (int64_t)id * c.page_size +
-                         ((int)j - page * c.page_size);
-    return id >= 0 && slot < c.slots ? (int)slot : -1;
+// A key's page, asked for a chunk before its slot is worked out (arithmetic on
+// a loaded value would hold the warp up where it stands).
+struct Page {
+    int id, at;  // number (-1: no column sees the key), place in it
+};
+__device__ __forceinline__ Page page_of(const mt_attention_call_t &c,
+                                        const int32_t *pages, int64_t j,
+                                        int lo, int hi) {
+    Page p = {-1, 0};
+    if (j >= lo && j <= hi) {
+        const unsigned page = (unsigned)j / (unsigned)c.page_size;
+        p.at = (int)((unsigned)j - page * (unsigned)c.page_size);
+        p.id = pages[page];
+    }
+    return p;
+}
+// Its slot, or -1 where it has none.
+__device__ __forceinline__ int slot_in(const mt_attention_call_t &c, Page p) {
+    const int64_t slot = (int64_t)p.id * c.page_size + p.at;
+    return p.id >= 0 && slot < c.slots ? (int)slot : -1;
 }
 
-// A warp's share of the units [u0, u1) of a tile.
+// The cache's codes as tensors of rows; a warp's waits on its two barriers.
+struct Maps {
+    const CUtensorMap *k, *v;
+};
+struct Waits {
+    unsigned phase;  // bit s: the parity that stage s completes next
+    bool gave_up;
+};
+
+// The units [u0, u1) of a tile: its queries, and each warp's share of them.
 template <class H, bool INT8, int PARTS, int NT>
 __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
+                                         const Cut &cut, int dtype,
                                          const Tile &a, int64_t u0, int64_t u1,
-                                         const Shared<H, PARTS, NT> &sh,
+                                         const Maps &maps, Waits &waits,
+                                         Shared<H, PARTS, NT> &sh,
                                          Warp<H, INT8, PARTS, NT> &w) {
     constexpr int KT = H::KEYS / 16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // The queries are asked for first and needed last: the first keys' slots
+    // and codes are on their way meanwhile.
+    Queries<H, PARTS, NT> queries;
+    queries.load(c, cut, dtype, a);
+    tile_bounds(c, cut, a, sh);
+    __syncthreads();
     const int lo = sh.lo_any, hi = sh.hi_any;
-    const float inv_cap = c.cap > 0.f ? 1.f / c.cap : 0.f;
     const int32_t *pages = c.table + a.s * c.table_stride;
-    if (lo > hi) return;
     u0 = max(u0, (int64_t)(lo / H::KEYS));
-    u1 = min(u1, (int64_t)(hi / H::KEYS) + 1);
+    u1 = lo > hi ? 0 : min(u1, (int64_t)(hi / H::KEYS) + 1);
     int64_t u = u0 + warp;
-    if (u >= u1) return;
-    const auto slot_at = [&](int64_t v) {
+    const auto page_at = [&](int64_t v) {
         return v < u1 && lane < H::KEYS
-                   ? slot_in(c, pages, v * H::KEYS + lane, lo, hi) : -1;
+                   ? page_of(c, pages, v * H::KEYS + lane, lo, hi)
+                   : Page{-1, 0};
     };
-    int slot = slot_at(u), next = slot_at(u + kWarps);
-    w.load_keys(c, a.head, slot);
-    w.load_values(c, a.head, slot);
+    Cache m;
+    m.k = maps.k;
+    m.v = maps.v;
+    m.heads = c.k_heads;
+    m.head = a.head;
+    m.ks = c.k_scales + a.head * H::GROUPS;
+    m.vs = c.v_scales + a.head * H::GROUPS;
+    m.scales = (unsigned)(c.k_heads * H::GROUPS);
+    auto &codes = sh.own[warp].codes;
+    auto &scales = sh.scales[warp];
+    uint64_t *bar = sh.bar[warp];
+    if (waits.gave_up) u = u1;
+    const Page first = page_at(u);
+    Page next = page_at(u + kWarps);
+    int slot = slot_in(c, first), stage = 0;
+    if (u < u1) w.load(m, slot, codes[0], scales[0], &bar[0]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    queries.put(c, sh);
+    __syncthreads();
 #pragma unroll 1
     for (; u < u1; u += kWarps) {
         const unsigned there = __ballot_sync(kFull, slot >= 0);
-        float z[NT][KT][4], keep[NT][2];
-        unsigned hidden;
-        w.scores(sh, z);
-        w.load_keys(c, a.head, next);
-        w.bend(c, sh, inv_cap, (int)(u * H::KEYS), there, hidden, z);
-        slot = next;
-        next = slot_at(u + 2 * kWarps);
-        w.weigh(z, keep);
-        w.add(z, keep, hidden);
-        w.load_values(c, a.head, slot);
+        slot = slot_in(c, next);
+        next = page_at(u + 2 * kWarps);
+        if (u + kWarps < u1)
+            w.load(m, slot, codes[stage ^ 1], scales[stage ^ 1],
+                   &bar[stage ^ 1]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const bool came =
+            mbar_wait_bounded(&bar[stage], waits.phase >> stage & 1u);
+        waits.phase ^= 1u << stage;
+        if (!__all_sync(kFull, came)) {
+            // Not before a fault elsewhere: no more copies, their own awaited,
+            // and NaN for what this warp had a part in.
+            if (u + kWarps < u1)
+                mbar_wait_bounded(&bar[stage ^ 1],
+                                  waits.phase >> (stage ^ 1) & 1u);
+            waits.gave_up = true;
+            break;
+        }
+        if (there != 0) {
+            float z[NT][KT][4];
+            unsigned hidden;
+            w.scores(sh, codes[stage], scales[stage], z);
+            w.bend(c, sh, (int)(u * H::KEYS), there, hidden, z);
+            w.weigh(z);
+            w.add(z, hidden, codes[stage], scales[stage]);
+        }
+        __syncwarp();  // the next round's copies go where this one read
+        stage ^= 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (waits.gave_up) w.spoil();
+    __syncwarp();  // the warp's sums take the chunks' place
 }
 
 // The warps' sums of a tile joined: written out where the tile is whole, left
@@ -776,7 +1050,7 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
             for (int off = 4; off < 32; off <<= 1)
                 sum += __shfl_xor_sync(kFull, sum, off);
             if (g == 0) {
-                sh.m[warp][8 * n + 2 * q + h] = w.m[n][h];
+                sh.m[warp][8 * n + 2 * q + h] = w.ref[n][h];
                 sh.l[warp][8 * n + 2 * q + h] = sum;
             }
         }
@@ -784,9 +1058,13 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
         for (int i = 0; i < H::STEPS; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int d = i / (H::B / 16) * H::B + g * (H::B / 8) +
-                              2 * (i % (H::B / 16)) + (e >> 1);
-                sh.o[warp][8 * n + 2 * q + (e & 1)][d] = w.o[n][i][e];
+                const int gr = i / H::PER;
+                const Block block = H::block(i % H::PER);
+                const int d = gr * H::GROUP + block.base +
+                              g * (block.size / 8) +
+                              2 * (i % H::PER - block.base / 16) + (e >> 1);
+                sh.own[warp].o[8 * n + 2 * q + (e & 1)][d] =
+                    w.o[n][i][e] * w.down(w.exponent(n, e & 1, gr));
             }
     }
     __syncthreads();
@@ -806,7 +1084,7 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
         for (int x = 0; x < kWarps; ++x) {
             const float f = pow2(sh.m[x][col] - ref);
             sum = fmaf(sh.l[x][col], f, sum);
-            o = fmaf(sh.o[x][col][d], f, o);
+            o = fmaf(sh.own[x].o[col][d], f, o);
         }
         if (whole) {
             store_as(PARTS == 1 ? (int)DT_BF16 : dtype, c.out,
@@ -825,21 +1103,36 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
             }
         }
     }
-    __syncthreads();  // shared memory is the next tile's
+    // Shared memory is the next tile's: its copies come after these accesses.
+    fence_proxy_async_smem();
+    __syncthreads();
 }
 
-// The least units that a CTA takes where there are few: one for each warp.
-constexpr int kLeastUnits = kWarps;
+// The least units that a CTA takes where there are few: a tile's own, and one
+// of keys for each warp.
+constexpr int kLeastUnits = (int)kExtra + kWarps;
 
 template <class H, bool INT8, int PARTS, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 && H::DIM <= 128 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kWarps,
+                                  attention_ctas(H::DIM, H::GROUPS, PARTS, NT))
     attention_mma_kernel(const mt_attention_call_t c, const Cut cut,
-                         const Share share, int dtype) {
+                         const Share share, int dtype,
+                         const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map) {
     constexpr int C = 8 * NT, KEYS = H::KEYS, T = 32 * kWarps;
-    __shared__ __align__(16) Shared<H, PARTS, NT> sh;
+    extern __shared__ uint8_t shared[];
+    Shared<H, PARTS, NT> &sh = *reinterpret_cast<Shared<H, PARTS, NT> *>(
+        shared + (-smem_addr(shared) & 1023u));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lane == 0) {
+        mbar_init(&sh.bar[warp][0], 1);
+        mbar_init(&sh.bar[warp][1], 1);
+        mbar_init_fence();
+    }
+    const Maps maps = {&k_map, &v_map};
+    Waits waits = {0, false};
     grid_launch_dependents();
     grid_wait_prerequisites();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Record record = {};
     // Units of the sequences of this thread, and where they begin.
     const int each = (c.sequences + T - 1) / T;
@@ -870,8 +1163,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 && H::DIM <= 128 ? 3 : 2)
                              (total + kLeastUnits - 1) / kLeastUnits);
     int64_t at = 0, end = 0;
     if (blockIdx.x < ctas) {
-        at = total * blockIdx.x / ctas;
-        end = total * (blockIdx.x + 1) / ctas;
+        at = quotient(total * blockIdx.x, ctas);
+        end = quotient(total * (blockIdx.x + 1), ctas);
     }
     if (at < end) {
         if (first <= at && at < first + mine) {
@@ -899,23 +1192,23 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 && H::DIM <= 128 ? 3 : 2)
         a.t = lo;
         off -= wide * a.tiles.template before<KEYS>(lo);
         int64_t base = a.tiles.template first<KEYS>(lo);
-        int64_t units = a.tiles.template last<KEYS>(lo) - base + 1;
-        int index = (int)(off / units);
+        int64_t units = a.tiles.template last<KEYS>(lo) - base + 1 + kExtra;
+        int index = (int)quotient(off, units);
         off -= index * units;
         Warp<H, INT8, PARTS, NT> w;
         while (at < end) {
             const int64_t n = min(units - off, end - at);
             a.head = index / cut.parts;
             a.part = index - a.head * cut.parts;
-            tile_begin<H, PARTS, NT>(c, cut, dtype, a, sh);
             w.begin();
-            tile_run<H, INT8, PARTS, NT>(c, a, base + off, base + off + n, sh,
-                                         w);
+            tile_run<H, INT8, PARTS, NT>(
+                c, cut, dtype, a, base + max(off - kExtra, (int64_t)0),
+                base + max(off + n - kExtra, (int64_t)0), maps, waits, sh, w);
             const bool whole = n == units;
             if (!whole && off == 0) {
                 const int64_t x = at + units;
                 record.valid = 1;
-                record.last = (int)((x * ctas - 1) / total);
+                record.last = (int)quotient(x * ctas - 1, total);
                 record.row = c.offsets[a.s] + a.t * cut.per;
                 record.rows = min(cut.per, a.tiles.rows - a.t * cut.per);
                 record.head = a.head;
@@ -936,50 +1229,83 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 && H::DIM <= 128 ? 3 : 2)
                     while (a.tiles.rows == 0);
                 }
                 base = a.tiles.template first<KEYS>(a.t);
-                units = a.tiles.template last<KEYS>(a.t) - base + 1;
+                units = a.tiles.template last<KEYS>(a.t) - base + 1 + kExtra;
             }
         }
     }
     if (tid == 0) share.records[blockIdx.x] = record;
 }
 
-// Joins the parts of a cut tile, in the order of the CTAs that left them.
+// Joins the parts of a cut tile, in the order of the CTAs that left them: first
+// the parts' factors, a warp to a column and a lane to a part, then the sums,
+// four values to a thread and many parts in flight.
+constexpr int kJoin = 256;
 template <int DIM, int C>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoin)
     attention_join_kernel(const mt_attention_call_t c, const Cut cut,
                           const Share share, int dtype) {
+    extern __shared__ float factors[];  // C x CTAs
+    __shared__ float tops[C], totals[C];
     grid_launch_dependents();
     grid_wait_prerequisites();
     const Record r = share.records[blockIdx.x];
     if (!r.valid) return;
     constexpr int64_t kPlace = place_floats(C, DIM);
+    // part 0 is in this CTA's second place, the others in the first places of
+    // the CTAs after it
     const float *begin = share.sums + (2 * (int64_t)blockIdx.x + 1) * kPlace;
-    const float *others = share.sums + 2 * kPlace * (blockIdx.x + 1);
-    const int more = r.last - (int)blockIdx.x;
-    const auto part = [&](int i) {
-        return i == 0 ? begin : others + 2 * kPlace * (i - 1);
+    const float *others = share.sums + 2 * kPlace * (int64_t)blockIdx.x;
+    const int parts = r.last - (int)blockIdx.x + 1;
+    const auto part = [&](int x) {
+        return x == 0 ? begin : others + 2 * kPlace * x;
     };
-    for (int i = blockIdx.y * 128 + threadIdx.x; i < C * DIM;
-         i += 128 * gridDim.y) {
+    const int lane = threadIdx.x & 31;
+    for (int col = threadIdx.x >> 5; col < C; col += kJoin / 32) {
+        float top = -INFINITY;
+        for (int x = lane; x < parts; x += 32)
+            top = nanmax(top, part(x)[col]);
+        top = warp_nanmax(top);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int x = lane; x < parts; x += 32) {
+            const float f = pow2(part(x)[col] - ref);
+            factors[col * gridDim.x + x] = f;
+            sum = fmaf(part(x)[C + col], f, sum);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            sum += __shfl_xor_sync(kFull, sum, off);
+        if (lane == 0) {
+            tops[col] = top;
+            totals[col] = sum;
+        }
+    }
+    __syncthreads();
+    for (int i = 4 * threadIdx.x; i < C * DIM; i += 4 * kJoin) {
         const int col = i / DIM, d = i % DIM;
         const Place at = place_of<C>(cut, r.row, r.rows, r.head, r.part, col);
         if (!at.used) continue;
-        float top = -INFINITY, sum = 0.f, o = 0.f;
-#pragma unroll 4
-        for (int x = 0; x <= more; ++x) {
-            const float *p = part(x);
-            const float m = p[col], l = p[C + col], v = p[2 * C + i];
-            const float next = nanmax(top, m);
-            const float ref = next == -INFINITY ? 0.f : next;
-            const float a = pow2(top - ref), b = pow2(m - ref);
-            sum = sum * a + l * b;
-            o = o * a + v * b;
-            top = next;
-        }
-        store_as(dtype, c.out,
-                 (int64_t)at.row * c.out_row + (int64_t)at.head * c.out_head +
-                     d,
-                 top == -INFINITY ? 0.f : o / sum);
+        const float *f = factors + col * gridDim.x;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        const auto add = [&](const float *p, float f) {
+            const float2 v = reinterpret_cast<const float2 *>(p)[0];
+            const float2 w = reinterpret_cast<const float2 *>(p)[1];
+            o[0] = fmaf(v.x, f, o[0]);
+            o[1] = fmaf(v.y, f, o[1]);
+            o[2] = fmaf(w.x, f, o[2]);
+            o[3] = fmaf(w.y, f, o[3]);
+        };
+        add(begin + 2 * C + i, f[0]);
+#pragma unroll 8
+        for (int x = 1; x < parts; ++x)
+            add(others + 2 * kPlace * x + 2 * C + i, f[x]);
+        const float top = tops[col], sum = totals[col];
+        const int64_t to = (int64_t)at.row * c.out_row +
+                           (int64_t)at.head * c.out_head + d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            store_as(dtype, c.out, to + e,
+                     top == -INFINITY ? 0.f : o[e] / sum);
         if (c.lse != nullptr && d == 0)
             c.lse[(int64_t)at.row * c.q_heads + at.head] =
                 top == -INFINITY ? top
@@ -991,26 +1317,31 @@ template <class H, bool INT8, int PARTS, int NT>
 cudaError_t launch_attention_as(const AttentionPlan &p,
                                 const mt_attention_call_t &c, int dtype,
                                 void *workspace, cudaStream_t s) {
+    using Sh = Shared<H, PARTS, NT>;
+    constexpr int kCtas = attention_ctas(H::DIM, H::GROUPS, PARTS, NT);
+    constexpr size_t kBytes = sizeof(Sh) + 1024;  // to a multiple of 1024
+    static_assert((kBytes + 1024) * kCtas <= 228 * 1024,
+                  "the CTAs that share an SM fit its shared memory");
     const Cut cut = {p.times, p.per, p.parts};
     Share share;
     share.sums = static_cast<float *>(workspace);
     share.records = reinterpret_cast<Record *>(
         share.sums + 2 * (int64_t)p.ctas * place_floats(8 * NT, H::DIM));
-    cudaError_t e = launch_dependent(attention_mma_kernel<H, INT8, PARTS, NT>,
-                                     p.ctas, 32 * kWarps, 0, s, c, cut, share,
-                                     dtype);
+    CUtensorMap maps[2];
+    const int64_t rows = c.slots * c.k_heads * H::PLANES;
+    cudaError_t e = attention_map(c.k_codes, rows, H::WIDE, &maps[0]);
+    if (e == cudaSuccess)
+        e = attention_map(c.v_codes, rows, H::WIDE, &maps[1]);
+    const auto kernel = attention_mma_kernel<H, INT8, PARTS, NT>;
+    if (e == cudaSuccess && kBytes > 48 * 1024)
+        e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    if (e == cudaSuccess)
+        e = launch_dependent(kernel, p.ctas, 32 * kWarps, kBytes, s, c, cut,
+                             share, dtype, maps[0], maps[1]);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas, 2);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<H::DIM, 8 * NT>, c,
-                              cut, share, dtype);
+    return launch_dependent(attention_join_kernel<H::DIM, 8 * NT>, p.ctas,
+                            kJoin, (size_t)p.ctas * 8 * NT * sizeof(float), s,
+                            c, cut, share, dtype);
 }
 
 template <bool INT8, int PARTS, int NT>

@@ -1,5 +1,19 @@
 // block_norm.cuh -- the norms around a block with its gate and the residual's
 // scale, forward and backward (one translation unit per storage type).
+//
+// A row stays in the registers of the W threads that share it, K packs of V
+// values each, asked for at once: each matrix is read and written once.  The
+// forward pass has two sums one after the other (of x^2, and of h^2, which needs
+// the first).  So has the backward pass: x^2, h^2 and dy w2 h together, then e w1
+// x.  There a CTA goes through many rows, the next one on its way while one is
+// worked on, and a thread, which has the same columns in all of them, keeps
+// their parts of the weights' and the gate's gradients, in registers, or in
+// shared memory where it has 16 columns or more; a second kernel adds up the
+// CTAs' in order.
+//
+// Packs are as wide as every row's address allows (rows of an odd length: one
+// value).  Rows that the registers do not hold are gone through in loops, once
+// per sum and once to write.
 #pragma once
 
 #include "mt_decoder.cuh"
@@ -7,7 +21,7 @@
 namespace mt {
 namespace {
 
-constexpr int kLoop = 256;  // threads of the kernels for any row
+constexpr int kLoop = 512;  // threads of the kernels for any row
 
 // Sums of N values over the CTA, the same bits in every thread.
 template <int N>
@@ -34,147 +48,655 @@ __device__ __forceinline__ void cta_sum(float (&v)[N]) {
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float at(const void *p, int64_t i, float absent) {
-    return p == nullptr ? absent : to_f(static_cast<const T *>(p)[i]);
+// V values of a matrix or vector, or the value that stands for an absent one.
+template <typename T, int V>
+__device__ __forceinline__ void values(const void *p, int64_t i, float absent,
+                                       float *v) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = absent;
+    } else {
+        ld_vec<T, V>(static_cast<const T *>(p) + i, v);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void put(void *p, int64_t i, const float *v) {
+    st_vec<T, V>(static_cast<T *>(p) + i, v);
 }
 
 // Any row: a CTA per row, which reads it once per sum and once to write.
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(kLoop)
-    norm_any_kernel(const mt_block_norm_call_t c) {
+    norm_loop_kernel(const mt_block_norm_call_t c) {
     grid_launch_dependents();
     grid_wait_prerequisites();
     const int64_t r = blockIdx.x;
     const int64_t x = r * c.x_stride, res = r * c.residual_stride;
     const int64_t gate = r * c.gate_stride;
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
     const float inv = 1.f / (float)c.cols;
     float r1 = 1.f;
-    if (c.norms & MT_NORM_AFTER) {
+    if (after) {
         float s[1] = {0.f};
-        for (int i = threadIdx.x; i < c.cols; i += kLoop) {
-            const float v = at<T>(c.x, x + i, 0.f);
-            s[0] = fmaf(v, v, s[0]);
+        for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+            float v[V];
+            values<T, V>(c.x, x + i, 0.f, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[0] = fmaf(v[e], v[e], s[0]);
         }
         cta_sum(s);
         r1 = rsqrtf(fmaf(s[0], inv, c.eps));
     }
-    const auto stream = [&](int i) {
-        const float u = at<T>(c.x, x + i, 0.f) * r1 * at<T>(c.weight, i, 1.f);
-        return fmaf(at<T>(c.residual, res + i, 0.f), c.residual_scale,
-                    u * at<T>(c.gate, gate + i, 1.f));
+    const auto stream = [&](int i, float *h) {
+        float u[V], f[V];
+        values<T, V>(c.x, x + i, 0.f, u);
+        if (after) {
+            values<T, V>(c.weight, i, 1.f, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] = u[e] * r1 * f[e];
+        }
+        values<T, V>(c.gate, gate + i, 1.f, f);
+        values<T, V>(c.residual, res + i, 0.f, h);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            h[e] = fmaf(h[e], c.residual_scale, u[e] * f[e]);
     };
     float r2 = 0.f;
-    if (c.norms & MT_NORM_BEFORE) {
+    if (before) {
         float s[1] = {0.f};
-        for (int i = threadIdx.x; i < c.cols; i += kLoop) {
-            const float h = stream(i);
-            s[0] = fmaf(h, h, s[0]);
+        for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+            float h[V];
+            stream(i, h);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[0] = fmaf(h[e], h[e], s[0]);
         }
         cta_sum(s);
         r2 = rsqrtf(fmaf(s[0], inv, c.eps));
     }
-    for (int i = threadIdx.x; i < c.cols; i += kLoop) {
-        const float h = stream(i);
-        static_cast<T *>(c.h)[r * c.h_stride + i] = from_f<T>(h);
-        if (c.norms & MT_NORM_BEFORE)
-            static_cast<T *>(c.y)[r * c.y_stride + i] =
-                from_f<T>(h * r2 * at<T>(c.next_weight, i, 1.f));
+    for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+        float h[V], f[V];
+        stream(i, h);
+        put<T, V>(c.h, r * c.h_stride + i, h);
+        if (!before) continue;
+        values<T, V>(c.next_weight, i, 1.f, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = h[e] * r2 * f[e];
+        put<T, V>(c.y, r * c.y_stride + i, h);
     }
 }
 
 // Any row, backward: a CTA takes every gridDim.x-th row and adds its weights'
-// gradients up in its own row of partial sums.
-template <typename T>
+// gradients up in shared memory where 3 x cols of them fit (`room`), else in
+// its own row of partial sums.
+template <typename T, int V>
 __global__ void __launch_bounds__(kLoop)
-    norm_back_any_kernel(const mt_block_norm_back_t c, float *partial) {
+    norm_back_loop_kernel(const mt_block_norm_back_t c, float *partial,
+                          int room) {
+    extern __shared__ float shared[];
     grid_launch_dependents();
     grid_wait_prerequisites();
     const float inv = 1.f / (float)c.cols;
-    const bool after = c.norms & MT_NORM_AFTER, before = c.norms & MT_NORM_BEFORE;
-    float *sums = partial + (int64_t)blockIdx.x * 3 * c.cols;
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
+    float *own = partial + (int64_t)blockIdx.x * 3 * c.cols;
+    float *sums = room ? shared : own;
     if (partial != nullptr)
         for (int i = threadIdx.x; i < 3 * c.cols; i += kLoop) sums[i] = 0.f;
     __syncthreads();
     for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
         const int64_t x = r * c.x_stride, h = r * c.h_stride;
-        const int64_t gate = r * c.gate_stride;
+        const int64_t dy = r * c.dy_stride, gate = r * c.gate_stride;
         float s[3] = {0.f, 0.f, 0.f};
-        for (int i = threadIdx.x; i < c.cols; i += kLoop) {
+        for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+            float v[V], d[V], f[V];
             if (after) {
-                const float v = at<T>(c.x, x + i, 0.f);
-                s[0] = fmaf(v, v, s[0]);
+                values<T, V>(c.x, x + i, 0.f, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0] = fmaf(v[e], v[e], s[0]);
             }
             if (before) {
-                const float v = at<T>(c.h, h + i, 0.f);
-                s[1] = fmaf(v, v, s[1]);
-                s[2] = fmaf(at<T>(c.dy, r * c.dy_stride + i, 0.f) *
-                                at<T>(c.next_weight, i, 1.f), v, s[2]);
+                values<T, V>(c.h, h + i, 0.f, v);
+                values<T, V>(c.dy, dy + i, 0.f, d);
+                values<T, V>(c.next_weight, i, 1.f, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    s[1] = fmaf(v[e], v[e], s[1]);
+                    s[2] = fmaf(d[e] * f[e], v[e], s[2]);
+                }
             }
         }
         cta_sum(s);
         const float r1 = after ? rsqrtf(fmaf(s[0], inv, c.eps)) : 1.f;
         const float r2 = before ? rsqrtf(fmaf(s[1], inv, c.eps)) : 0.f;
         const float m2 = s[2] * inv * r2 * r2;
-        const auto grad = [&](int i) {
-            float g = at<T>(c.dh, r * c.dh_stride + i, 0.f);
-            if (before)
-                g += r2 * (at<T>(c.dy, r * c.dy_stride + i, 0.f) *
-                               at<T>(c.next_weight, i, 1.f) -
-                           at<T>(c.h, h + i, 0.f) * m2);
-            return g;
+        // The stream's gradient; dy and h on the way.
+        const auto grad = [&](int i, float *g, float *d, float *v) {
+            values<T, V>(c.dh, r * c.dh_stride + i, 0.f, g);
+            if (!before) return;
+            float f[V];
+            values<T, V>(c.dy, dy + i, 0.f, d);
+            values<T, V>(c.h, h + i, 0.f, v);
+            values<T, V>(c.next_weight, i, 1.f, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                g[e] += r2 * (d[e] * f[e] - v[e] * m2);
         };
         float m1 = 0.f;
         if (after) {
             float t[1] = {0.f};
-            for (int i = threadIdx.x; i < c.cols; i += kLoop)
-                t[0] = fmaf(grad(i) * at<T>(c.gate, gate + i, 1.f) *
-                                at<T>(c.weight, i, 1.f),
-                            at<T>(c.x, x + i, 0.f), t[0]);
+            for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+                float g[V], d[V], v[V], f[V], w[V];
+                grad(i, g, d, v);
+                values<T, V>(c.gate, gate + i, 1.f, f);
+                values<T, V>(c.weight, i, 1.f, w);
+                values<T, V>(c.x, x + i, 0.f, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    t[0] = fmaf(g[e] * f[e] * w[e], v[e], t[0]);
+            }
             cta_sum(t);
             m1 = t[0] * inv * r1 * r1;
         }
-        for (int i = threadIdx.x; i < c.cols; i += kLoop) {
-            const float g = grad(i), xv = at<T>(c.x, x + i, 0.f);
-            const float w = at<T>(c.weight, i, 1.f);
-            const float e = g * at<T>(c.gate, gate + i, 1.f);
-            const float dg = g * xv * r1 * w;
-            if (partial != nullptr) {
-                if (c.dgate_sum) sums[i] += dg;
-                if (c.dweight) sums[c.cols + i] += e * xv * r1;
+        for (int i = threadIdx.x * V; i < c.cols; i += kLoop * V) {
+            float g[V], d[V], v[V], xv[V], f[V], w[V], o[V], dg[V];
+            grad(i, g, d, v);
+            values<T, V>(c.x, x + i, 0.f, xv);
+            values<T, V>(c.weight, i, 1.f, w);
+            values<T, V>(c.gate, gate + i, 1.f, f);
+            float dx[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                dg[e] = g[e] * (xv[e] * r1 * w[e]);
+                dx[e] = g[e] * f[e];
+                if (c.dgate_sum) sums[i + e] += dg[e];
+                if (c.dweight)
+                    sums[c.cols + i + e] += dx[e] * xv[e] * r1;
                 if (c.dnext_weight)
-                    sums[2 * c.cols + i] +=
-                        at<T>(c.dy, r * c.dy_stride + i, 0.f) *
-                        at<T>(c.h, h + i, 0.f) * r2;
+                    sums[2 * c.cols + i + e] += d[e] * v[e] * r2;
+                o[e] = g[e] * c.residual_scale;
+                if (after) dx[e] = r1 * (dx[e] * w[e] - xv[e] * m1);
             }
-            const float dx = after ? r1 * (e * w - xv * m1) : e;
-            static_cast<T *>(c.dx)[r * c.dx_stride + i] = from_f<T>(dx);
-            static_cast<T *>(c.dresidual)[r * c.dresidual_stride + i] =
-                from_f<T>(g * c.residual_scale);
-            if (c.dgate)
-                static_cast<T *>(c.dgate)[r * c.dgate_stride + i] =
-                    from_f<T>(dg);
+            put<T, V>(c.dx, r * c.dx_stride + i, dx);
+            put<T, V>(c.dresidual, r * c.dresidual_stride + i, o);
+            if (c.dgate) put<T, V>(c.dgate, r * c.dgate_stride + i, dg);
         }
+    }
+    if (partial == nullptr || !room) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 3 * c.cols; i += kLoop) own[i] = shared[i];
+}
+
+// ---- rows in registers -------------------------------------------------------
+// Sums of N values over the W threads of a row: lanes of a warp (W <= 32) or
+// the whole CTA; `turn` alternates between two places of the exchange, so that
+// one barrier per call is enough.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int W, int &turn) {
+    __shared__ float part[2][N][32];
+    if (W <= 32) {
+        for (int o = W >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] += __shfl_xor_sync(kFull, v[i], o);
+        return;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = (int)blockDim.x >> 5;
+    float (&to)[N][32] = part[turn];
+    turn ^= 1;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) to[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane < warps ? to[i][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
+}
+
+// How a row's packs lie: pack k of thread `w` of a row has the columns from
+// (w + k W) V on.
+struct Lay {
+    int W, rows;  // threads of a row, rows of a CTA
+};
+
+template <typename T, int V, int K>
+struct Packs {
+    Raw<T, V> p[K];
+    __device__ __forceinline__ void load(const void *m, int64_t at, int w,
+                                         int W, int cols, bool on) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * W) * V;
+            if (on && col < cols)
+                p[k].load(static_cast<const T *>(m) + at + col);
+            else
+                p[k].zero();
+        }
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ void vector_pack(const void *p, int col, float *v) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = 1.f;
+    } else {
+        ld_vec<T, V, true>(static_cast<const T *>(p) + col, v);
     }
 }
 
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(K * V >= 32 ? 512 : 1024)
+    norm_kernel(const mt_block_norm_call_t c, const Lay lay) {
+    grid_launch_dependents();
+    grid_wait_prerequisites();
+    const int w = (int)threadIdx.x & (lay.W <= 32 ? lay.W - 1 : ~0);
+    const int64_t r = (int64_t)blockIdx.x * lay.rows +
+                      (lay.W <= 32 ? (int)threadIdx.x / lay.W : 0);
+    const bool on = r < c.rows;
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
+    const float inv = 1.f / (float)c.cols;
+    int turn = 0;
+    Packs<T, V, K> x, res;
+    x.load(c.x, r * c.x_stride, w, lay.W, c.cols, on);
+    res.load(c.residual, r * c.residual_stride, w, lay.W, c.cols, on);
+    float r1 = 1.f;
+    if (after) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float v[V];
+            x.p[k].widen(v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[0] = fmaf(v[e], v[e], s[0]);
+        }
+        row_sums(s, lay.W, turn);
+        r1 = rsqrtf(fmaf(s[0], inv, c.eps));
+    }
+    float h[K][V];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = (w + k * lay.W) * V;
+        if (!on || col >= c.cols) continue;
+        float u[V], f[V];
+        x.p[k].widen(u);
+        if (after) {
+            vector_pack<T, V>(c.weight, col, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] = u[e] * r1 * f[e];
+        }
+        if (c.gate != nullptr) {
+            vector_pack<T, V>(static_cast<const T *>(c.gate) +
+                                  r * c.gate_stride, col, f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] *= f[e];
+        }
+        res.p[k].widen(f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            h[k][e] = fmaf(f[e], c.residual_scale, u[e]);
+            s[0] = fmaf(h[k][e], h[k][e], s[0]);
+        }
+        st_vec<T, V>(static_cast<T *>(c.h) + r * c.h_stride + col, h[k]);
+    }
+    if (!before) return;
+    row_sums(s, lay.W, turn);
+    const float r2 = rsqrtf(fmaf(s[0], inv, c.eps));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = (w + k * lay.W) * V;
+        if (!on || col >= c.cols) continue;
+        float f[V];
+        vector_pack<T, V>(c.next_weight, col, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[k][e] = h[k][e] * r2 * f[e];
+        st_vec<T, V>(static_cast<T *>(c.y) + r * c.y_stride + col, h[k]);
+    }
+}
+
+// The matrices of a row of the backward pass.
+template <typename T, int V, int K>
+struct BackRow {
+    Packs<T, V, K> dy, dh, x, h;
+    __device__ __forceinline__ void load(const mt_block_norm_back_t &c,
+                                         int64_t r, int w, int W) {
+        const bool on = r < c.rows;
+        if (c.dy) dy.load(c.dy, r * c.dy_stride, w, W, c.cols, on);
+        if (c.h) h.load(c.h, r * c.h_stride, w, W, c.cols, on);
+        if (c.dh) dh.load(c.dh, r * c.dh_stride, w, W, c.cols, on);
+        if (c.x) x.load(c.x, r * c.x_stride, w, W, c.cols, on);
+    }
+};
+
+// Where a thread's sums of its columns are: registers, or shared memory (value
+// i of every thread side by side).
+template <int N, bool SHARED>
+struct Sums {
+    float v[SHARED ? 1 : N];
+    float *at;
+    __device__ __forceinline__ void begin(float *shared) {
+        at = shared + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (SHARED) at[i * blockDim.x] = 0.f;
+            else v[i] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void add(int i, float d) {
+        if constexpr (SHARED) at[i * blockDim.x] += d;
+        else v[i] += d;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (SHARED) return at[i * blockDim.x];
+        else return v[i];
+    }
+};
+
+// 16 columns' sums and the rows of a thread do not fit its registers.
+__host__ __device__ constexpr bool norm_sums_shared(int columns) {
+    return columns >= 16;
+}
+
+// The next row is on its way where both fit (8 words of each matrix or less).
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(512)
+    norm_back_kernel(const mt_block_norm_back_t c, const Lay lay,
+                     float *partial) {
+    constexpr bool kShared = norm_sums_shared(K * V);
+    constexpr bool kAhead = Raw<T, V>::kWords * K <= 8;
+    extern __shared__ float shared[];
+    grid_launch_dependents();
+    grid_wait_prerequisites();
+    const int w = (int)threadIdx.x & (lay.W <= 32 ? lay.W - 1 : ~0);
+    const int group = lay.W <= 32 ? (int)threadIdx.x / lay.W : 0;
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
+    const float inv = 1.f / (float)c.cols;
+    int turn = 0;
+    // dgate, dweight, dnext_weight of the thread's columns
+    Sums<3 * K * V, kShared> sums;
+    if (partial != nullptr) sums.begin(shared);
+    BackRow<T, V, K> a, next;
+    const int64_t step = (int64_t)gridDim.x * lay.rows;
+    int64_t base = (int64_t)blockIdx.x * lay.rows;
+    if (kAhead) next.load(c, base + group, w, lay.W);
+    for (; base < c.rows; base += step) {
+        const int64_t r = base + group;
+        const bool on = r < c.rows;
+        if (kAhead) {
+            a = next;
+            next.load(c, r + step, w, lay.W);
+        } else {
+            a.load(c, r, w, lay.W);
+        }
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            if (!on || col >= c.cols) continue;
+            if (after) {
+                float v[V];
+                a.x.p[k].widen(v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0] = fmaf(v[e], v[e], s[0]);
+            }
+            if (before) {
+                float v[V], d[V], f[V];
+                a.h.p[k].widen(v);
+                a.dy.p[k].widen(d);
+                vector_pack<T, V>(c.next_weight, col, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    s[1] = fmaf(v[e], v[e], s[1]);
+                    s[2] = fmaf(d[e] * f[e], v[e], s[2]);
+                }
+            }
+        }
+        row_sums(s, lay.W, turn);
+        const float r1 = after ? rsqrtf(fmaf(s[0], inv, c.eps)) : 1.f;
+        const float r2 = before ? rsqrtf(fmaf(s[1], inv, c.eps)) : 0.f;
+        const float m2 = s[2] * inv * r2 * r2;
+        float g[K][V];
+        float t[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            if (!on || col >= c.cols) continue;
+            float x[V];
+            if (c.dh != nullptr) {
+                a.dh.p[k].widen(g[k]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[k][e] = 0.f;
+            }
+            if (before) {
+                float v[V], d[V], f[V];
+                a.h.p[k].widen(v);
+                a.dy.p[k].widen(d);
+                vector_pack<T, V>(c.next_weight, col, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    g[k][e] += r2 * (d[e] * f[e] - v[e] * m2);
+                if (c.dnext_weight != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        sums.add((2 * K + k) * V + e, d[e] * v[e] * r2);
+                }
+            }
+            // outputs may lie on inputs: nothing is written before the gate is
+            // read
+            float o[V], down[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) down[e] = g[k][e] * c.residual_scale;
+            if (c.x != nullptr) a.x.p[k].widen(x);
+            if (c.gate != nullptr) {
+                float f[V];
+                if (c.dgate != nullptr || c.dgate_sum != nullptr) {
+                    vector_pack<T, V>(c.weight, col, f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        o[e] = g[k][e] * (x[e] * r1 * f[e]);
+                    if (c.dgate_sum != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) sums.add(k * V + e, o[e]);
+                    }
+                }
+                vector_pack<T, V>(static_cast<const T *>(c.gate) +
+                                      r * c.gate_stride, col, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[k][e] *= f[e];
+                if (c.dgate != nullptr)
+                    st_vec<T, V>(static_cast<T *>(c.dgate) +
+                                     r * c.dgate_stride + col, o);
+            }
+            st_vec<T, V>(static_cast<T *>(c.dresidual) +
+                             r * c.dresidual_stride + col, down);
+            if (after) {
+                float f[V];
+                vector_pack<T, V>(c.weight, col, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (c.dweight != nullptr)
+                        sums.add((K + k) * V + e, g[k][e] * x[e] * r1);
+                    g[k][e] *= f[e];
+                    t[0] = fmaf(g[k][e], x[e], t[0]);
+                }
+            }
+        }
+        float m1 = 0.f;
+        if (after) {
+            row_sums(t, lay.W, turn);
+            m1 = t[0] * inv * r1 * r1;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            if (!on || col >= c.cols) continue;
+            if (after) {
+                float x[V];
+                a.x.p[k].widen(x);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    g[k][e] = r1 * (g[k][e] - x[e] * m1);
+            }
+            st_vec<T, V>(static_cast<T *>(c.dx) + r * c.dx_stride + col, g[k]);
+        }
+    }
+    if (partial == nullptr) return;
+    // Groups of a CTA's rows one after the other, then the CTA's row of sums.
+    float *to = partial + (int64_t)blockIdx.x * 3 * c.cols;
+#pragma unroll 1
+    for (int q = 0; q < lay.rows; ++q) {
+        if (q == group) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const int col = (w + k * lay.W) * V + e;
+                        if (col >= c.cols) continue;
+                        float &p = to[(int64_t)i * c.cols + col];
+                        const float v = sums.get((i * K + k) * V + e);
+                        p = q == 0 ? v : p + v;
+                    }
+        }
+        __syncthreads();
+    }
+}
+
+// Threads per row and rows per CTA for K packs of V values.
+inline Lay lay_of(int cols, int V, int K, int small) {
+    const int packs = (cols + V - 1) / V;
+    const int need = (packs + K - 1) / K;
+    Lay l;
+    if (need <= 32) {
+        l.W = 1;
+        while (l.W < need) l.W *= 2;
+        l.rows = small / l.W;
+    } else {
+        l.W = (need + 31) / 32 * 32;
+        l.rows = 1;
+    }
+    return l;
+}
+
+template <typename T, int V, int K>
+cudaError_t norm_launch(const mt_block_norm_call_t &c, cudaStream_t s) {
+    const Lay l = lay_of(c.cols, V, K, 128);
+    return launch_dependent(norm_kernel<T, V, K>,
+                            (c.rows + l.rows - 1) / l.rows, l.W * l.rows, 0, s,
+                            c, l);
+}
+
+template <typename T, int V>
+cudaError_t norm_packs(const mt_block_norm_call_t &c, cudaStream_t s) {
+    const int packs = (c.cols + V - 1) / V;
+    if (packs <= 256) return norm_launch<T, V, 1>(c, s);
+    if (packs <= 1024) return norm_launch<T, V, 2>(c, s);
+    if (packs <= 2048) return norm_launch<T, V, 4>(c, s);
+    if constexpr (V < 8)
+        if (packs <= 4096) return norm_launch<T, V, 8>(c, s);
+    if constexpr (V == 1)
+        if (packs <= 8192) return norm_launch<T, V, 16>(c, s);
+    return launch_dependent(norm_loop_kernel<T, V>, c.rows, kLoop, 0, s, c);
+}
+
 template <typename T>
-cudaError_t norm_as(const mt_block_norm_call_t &c, cudaStream_t s) {
-    return launch_dependent(norm_any_kernel<T>, c.rows, kLoop, 0, s, c);
+cudaError_t norm_as(const mt_block_norm_call_t &c, int V, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (V == 8) return norm_packs<T, 8>(c, s);
+    if (V >= 4) return norm_packs<T, 4>(c, s);
+    if (V >= 2) return norm_packs<T, 2>(c, s);
+    return norm_packs<T, 1>(c, s);
+}
+
+// CTAs of the backward pass that share an SM: as many as 128 registers per
+// thread and the sums in shared memory allow, two at most (each leaves a row
+// of partial sums).
+inline int back_grid(int64_t rows, int threads, size_t smem, int sms) {
+    const int per_sm = threads <= 256 && smem <= 100 * 1024 ? 2 : 1;
+    int64_t grid = (int64_t)sms * per_sm;
+    if (grid > kNormBackBlocks) grid = kNormBackBlocks;
+    return (int)(grid < rows ? grid : rows);
+}
+
+template <typename T, int V, int K>
+cudaError_t norm_back_launch(const mt_block_norm_back_t &c, float *partial,
+                             int *blocks, cudaStream_t s) {
+    const Lay l = lay_of(c.cols, V, K, 256);
+    const int threads = l.W * l.rows;
+    const auto kernel = norm_back_kernel<T, V, K>;
+    size_t smem = 0;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (norm_sums_shared(K * V) && partial != nullptr) {
+        smem = (size_t)3 * K * V * threads * sizeof(float);
+        if (smem > 40 * 1024 && e == cudaSuccess)
+            e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    }
+    if (e != cudaSuccess) return e;
+    *blocks = back_grid((c.rows + l.rows - 1) / l.rows, threads, smem, sms);
+    return launch_dependent(kernel, *blocks, threads, smem, s, c, l, partial);
+}
+
+template <typename T, int V>
+cudaError_t norm_back_packs(const mt_block_norm_back_t &c, float *partial,
+                            int *blocks, cudaStream_t s) {
+    constexpr int kWords = Raw<T, V>::kWords;  // of a pack
+    const int packs = (c.cols + V - 1) / V;
+    if (packs <= 512) return norm_back_launch<T, V, 1>(c, partial, blocks, s);
+    if (packs <= 1024) return norm_back_launch<T, V, 2>(c, partial, blocks, s);
+    if (packs <= 2048) return norm_back_launch<T, V, 4>(c, partial, blocks, s);
+    if constexpr (kWords * 8 <= 16)
+        if (packs <= 4096)
+            return norm_back_launch<T, V, 8>(c, partial, blocks, s);
+    if constexpr (kWords * 16 <= 16)
+        if (packs <= 8192)
+            return norm_back_launch<T, V, 16>(c, partial, blocks, s);
+    const auto kernel = norm_back_loop_kernel<T, V>;
+    const size_t need = (size_t)3 * c.cols * sizeof(float);
+    const bool room = partial != nullptr && need <= 200 * 1024;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e == cudaSuccess && room)
+        e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    if (e != cudaSuccess) return e;
+    *blocks = back_grid(c.rows, kLoop, room ? need : 0, sms);
+    return launch_dependent(kernel, *blocks, kLoop, room ? need : 0, s, c,
+                            partial, room ? 1 : 0);
+}
+
+template <typename T>
+cudaError_t norm_back_as(const mt_block_norm_back_t &c, int V, float *partial,
+                         int *blocks, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (V == 8) return norm_back_packs<T, 8>(c, partial, blocks, s);
+    if (V >= 4) return norm_back_packs<T, 4>(c, partial, blocks, s);
+    if (V >= 2) return norm_back_packs<T, 2>(c, partial, blocks, s);
+    return norm_back_packs<T, 1>(c, partial, blocks, s);
 }
 
 }  // namespace
 
 #define MT_DEFINE_BLOCK_NORM(T, dt)                                          \
-    cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &c,        \
+    cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &c, int V, \
                                        cudaStream_t s) {                     \
-        return norm_as<T>(c, s);                                             \
+        return norm_as<T>(c, V, s);                                          \
     }                                                                        \
     cudaError_t launch_block_norm_back_##dt(const mt_block_norm_back_t &c,   \
-                                            float *partial, int blocks,      \
-                                            cudaStream_t s) {                \
-        return launch_dependent(norm_back_any_kernel<T>, blocks, kLoop, 0,   \
-                                s, c, partial);                              \
+                                            int V, float *partial,           \
+                                            int *blocks, cudaStream_t s) {   \
+        return norm_back_as<T>(c, V, partial, blocks, s);                    \
     }
 
 }  // namespace mt

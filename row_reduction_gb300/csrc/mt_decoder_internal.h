@@ -124,6 +124,11 @@ struct AttentionPlan {
     int32_t parts;  // tiles that share a row's query heads
     int32_t ctas;
 };
+// CTAs of the matrix kernels that share an SM: three as far as registers (two
+// column tiles or wide heads take more than 168) and shared memory go.
+constexpr int attention_ctas(int dim, int groups, int parts, int nt) {
+    return nt > 1 || dim >= 128 ? 2 : 3;
+}
 // Bytes behind the partial sums, one record per CTA.
 constexpr int kAttentionRecord = 24;
 #define MT_DECLARE_ATTENTION(name)                                           \
@@ -144,12 +149,14 @@ MT_DECLARE_ATTENTION(launch_attention_int8_p2n2)
 constexpr int kNormMaxCols = 1 << 20;
 // Rows of partial sums of the backward pass (each of 3 x cols FP32 values).
 constexpr int kNormBackBlocks = 304;
+// V: values that every access of a row can take at once.  blocks: on return how
+// many rows of partial sums there are.
 #define MT_DECLARE_BLOCK_NORM(dt)                                            \
-    cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &c,        \
+    cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &c, int V, \
                                        cudaStream_t s);                      \
     cudaError_t launch_block_norm_back_##dt(const mt_block_norm_back_t &c,   \
-                                            float *partial, int blocks,      \
-                                            cudaStream_t s);
+                                            int V, float *partial,           \
+                                            int *blocks, cudaStream_t s);
 MT_DECLARE_BLOCK_NORM(f32)
 MT_DECLARE_BLOCK_NORM(f16)
 MT_DECLARE_BLOCK_NORM(bf16)

@@ -65,9 +65,10 @@ bool attention_head(const mt_attention_call_t &c) {
 }
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
-mt_status attention_plan(const mt_attention_call_t &c, bool *matrix,
+mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
                          AttentionPlan *p) {
-    *matrix = attention_head(c) && c.slots <= INT32_MAX &&
+    *matrix = attention_head(c) && c.slots > 0 && c.pages > 0 &&
+              c.slots <= INT32_MAX / ((int64_t)c.k_heads * 2) &&
               !misaligned(c.k_codes, 32) && !misaligned(c.v_codes, 32) &&
               !misaligned(c.k_scales, 16) && !misaligned(c.v_scales, 16);
     if (!*matrix) return MT_OK;
@@ -81,7 +82,8 @@ mt_status attention_plan(const mt_attention_call_t &c, bool *matrix,
     p->per = p->times < columns ? columns / p->times : 1;
     p->parts = (p->times + columns - 1) / columns;
     // as many as are resident at once
-    p->ctas = sms * (p->nt == 1 && c.dim <= 128 ? 3 : 2);
+    p->ctas = sms * attention_ctas(c.dim, c.dim / c.group,
+                                   dtype == DT_BF16 ? 1 : 2, p->nt);
     return MT_OK;
 }
 size_t attention_workspace(const mt_attention_call_t &c,
@@ -105,6 +107,19 @@ bool norm_sizes_ok(int dtype, int64_t rows, int64_t cols, int norms, float eps,
            norms <= (MT_NORM_AFTER | MT_NORM_BEFORE) && eps >= 0.f &&
            isfinite(scale);
 }
+
+// Values of a row that every access can take at once: the widest pack that
+// fits all rows' addresses and divides the row.
+struct Widest {
+    int es;
+    int64_t rows;
+    uint64_t bits;
+    void add(const void *p, int64_t stride) {
+        bits |= (uint64_t)(reinterpret_cast<uintptr_t>(p) / es);
+        if (p && rows > 1) bits |= (uint64_t)stride;
+    }
+    int values() const { return widest(bits, 16 / es); }
+};
 
 size_t norm_workspace(const mt_block_norm_back_t &c) {
     return c.dgate_sum || c.dweight || c.dnext_weight
@@ -158,7 +173,7 @@ mt_status mt_cache_attention_workspace(int dtype,
     bool matrix = false;
     AttentionPlan p = {};
     if (empty) return MT_OK;
-    if (mt_status st = attention_plan(*call, &matrix, &p)) return st;
+    if (mt_status st = attention_plan(dtype, *call, &matrix, &p)) return st;
     if (matrix) *bytes = attention_workspace(*call, p);
     return MT_OK;
 }
@@ -171,7 +186,7 @@ mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
     if (empty) return MT_OK;
     bool matrix = false;
     AttentionPlan p = {};
-    if (mt_status st = attention_plan(*call, &matrix, &p)) return st;
+    if (mt_status st = attention_plan(dtype, *call, &matrix, &p)) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if (!matrix)
         return status_from_cuda(launch_attention_any(dtype, *call, s));
@@ -217,9 +232,18 @@ mt_status mt_block_norm(int dtype, const mt_block_norm_call_t *call,
     if (!c.x || !c.residual || !c.h || (before && !c.y) || c.h == c.y)
         return MT_ERR_INVALID_ARGUMENT;
     cudaStream_t s = (cudaStream_t)stream;
-    return status_from_cuda(dtype == DT_F32   ? launch_block_norm_f32(c, s)
-                            : dtype == DT_F16 ? launch_block_norm_f16(c, s)
-                                              : launch_block_norm_bf16(c, s));
+    Widest w{es, c.rows, (uint64_t)c.cols};
+    w.add(c.x, c.x_stride);
+    w.add(c.residual, c.residual_stride);
+    w.add(c.gate, c.gate_stride);
+    w.add(c.h, c.h_stride);
+    w.add(c.y, c.y_stride);
+    w.add(c.weight, 0);
+    w.add(c.next_weight, 0);
+    return status_from_cuda(
+        dtype == DT_F32   ? launch_block_norm_f32(c, w.values(), s)
+        : dtype == DT_F16 ? launch_block_norm_f16(c, w.values(), s)
+                          : launch_block_norm_bf16(c, w.values(), s));
 }
 
 mt_status mt_block_norm_backward_workspace(int dtype,
@@ -288,18 +312,27 @@ mt_status mt_block_norm_backward(int dtype, const mt_block_norm_back_t *call,
     if (need > 0 && (workspace == nullptr || misaligned(workspace, 16)))
         return MT_ERR_INVALID_ARGUMENT;
     float *partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
-    int sms = 0;
-    cudaError_t e = current_sm_count(&sms);
-    if (e != cudaSuccess) return status_from_cuda(e);
-    int64_t blocks = 2 * sms < kNormBackBlocks ? 2 * sms : kNormBackBlocks;
-    if (blocks > c.rows) blocks = c.rows;
-    e = dtype == DT_F32
-            ? launch_block_norm_back_f32(c, partial, (int)blocks, s)
+    int blocks = 0;
+    Widest w{es, c.rows, (uint64_t)c.cols};
+    w.add(c.dy, c.dy_stride);
+    w.add(c.dh, c.dh_stride);
+    w.add(c.x, c.x_stride);
+    w.add(c.h, c.h_stride);
+    w.add(c.gate, c.gate_stride);
+    w.add(c.dx, c.dx_stride);
+    w.add(c.dresidual, c.dresidual_stride);
+    w.add(c.dgate, c.dgate_stride);
+    w.add(c.weight, 0);
+    w.add(c.next_weight, 0);
+    const int V = w.values();
+    cudaError_t e =
+        dtype == DT_F32
+            ? launch_block_norm_back_f32(c, V, partial, &blocks, s)
         : dtype == DT_F16
-            ? launch_block_norm_back_f16(c, partial, (int)blocks, s)
-            : launch_block_norm_back_bf16(c, partial, (int)blocks, s);
+            ? launch_block_norm_back_f16(c, V, partial, &blocks, s)
+            : launch_block_norm_back_bf16(c, V, partial, &blocks, s);
     if (e == cudaSuccess && need > 0)
-        e = launch_norm_sums(partial, c.cols, (int)blocks, sums[0], sums[1],
+        e = launch_norm_sums(partial, c.cols, blocks, sums[0], sums[1],
                              sums[2], s);
     return status_from_cuda(e);
 }
