@@ -1,41 +1,8 @@
 // attention.cu -- attention over the quantised cache for any head and group: a
 // warp per row and query head.
-#include <cuda.h>
-
-#include <atomic>
-
 #include "attention.cuh"
 
 namespace mt {
-
-// The driver's encoder, found once (the library itself does not link to the
-// driver).
-cudaError_t attention_map(const void *codes, int64_t rows, int width,
-                          CUtensorMap *map) {
-    using Encode = decltype(&cuTensorMapEncodeTiled);
-    static std::atomic<void *> found{nullptr};
-    void *fn = found.load(std::memory_order_relaxed);
-    if (fn == nullptr) {
-        cudaDriverEntryPointQueryResult r;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion(
-            "cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r);
-        if (e != cudaSuccess) return e;
-        if (r != cudaDriverEntryPointSuccess || fn == nullptr)
-            return cudaErrorNotSupported;
-        found.store(fn, std::memory_order_relaxed);
-    }
-    const cuuint64_t sizes[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)width};
-    const cuuint32_t box[2] = {(cuuint32_t)width, 1}, steps[2] = {1, 1};
-    const CUresult r = reinterpret_cast<Encode>(fn)(
-        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes),
-        sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-        : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                      : CU_TENSOR_MAP_SWIZZLE_NONE,
-        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 
 namespace {
 

@@ -5,14 +5,7 @@
 
 #include "mt_decoder.cuh"
 
-struct CUtensorMap_st;
-
 namespace mt {
-
-// A tensor of `rows` rows of `width` bytes, gathered in fours (rows of 128 and
-// 64 bytes swizzled).
-cudaError_t attention_map(const void *codes, int64_t rows, int width,
-                          CUtensorMap_st *map);
 
 namespace {
 

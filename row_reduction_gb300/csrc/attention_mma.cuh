@@ -40,8 +40,6 @@
 // runs is left as partial sums, which a second kernel joins in order.
 #pragma once
 
-#include <cuda.h>
-
 #include "attention.cuh"
 
 namespace mt {
@@ -225,17 +223,12 @@ __device__ __forceinline__ void read_codes(const uint8_t *p, int bytes,
     }
 }
 
-// Four rows of a tensor of rows into shared memory, completing on `bar`.
-__device__ __forceinline__ void gather4(void *to, const CUtensorMap *map,
-                                        int r0, int r1, int r2, int r3,
-                                        uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::"
-        "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-            smem_addr(to)),
-        "l"(map), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
-        "r"(smem_addr(bar))
-        : "memory");
+// 16 bytes from global into shared memory, on their way; zeros where not `on`.
+__device__ __forceinline__ void copy16(void *to, const void *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_addr(to)),
+                 "l"(from), "r"(on ? 16 : 0)
+                 : "memory");
 }
 // A key's scales into shared memory, on their way; zeros where not `on`.
 template <int BYTES>
@@ -277,20 +270,13 @@ struct Head {
             }
         return {0, 0};
     }
-    // A chunk's codes as the copies lay them out: planes of up to 128 bytes of
-    // each key, rows of 128 or 64 bytes permuted (swizzled) so that what a
-    // quarter of a warp reads at once lies in different banks, rows of 80 in
-    // fours at a distance that the copies can start at.
-    static constexpr int PLANES = DIM > 128 ? DIM / 128 : 1;
-    static constexpr int WIDE = DIM / PLANES;
-    static constexpr int FOUR = (4 * WIDE + 127) / 128 * 128;
-    static constexpr int PLANE = KEYS / 4 * FOUR;
+    // Where byte `byte` of key `key` of a chunk is in shared memory: units of
+    // 16 bytes permuted by the key, so that what a quarter of a warp reads at
+    // once lies in different banks.
     static __device__ __forceinline__ int place(int key, int byte) {
-        const int plane = PLANES > 1 ? byte / WIDE * PLANE : 0;
-        byte = PLANES > 1 ? byte % WIDE : byte;
-        if (WIDE == 128) return plane + key * 128 + (byte ^ (key & 7) << 4);
-        if (WIDE == 64) return key * 64 + (byte ^ (key >> 1 & 3) << 4);
-        return key / 4 * FOUR + key % 4 * WIDE + byte;
+        if (DIM % 128 == 0) return key * DIM + (byte ^ (key & 7) << 4);
+        if (DIM == 64) return key * 64 + (byte ^ (key >> 1 & 3) << 4);
+        return key * DIM + byte;
     }
 };
 
@@ -305,7 +291,7 @@ template <class H, int PARTS, int NT>
 struct Shared {
     // Each warp's own: the codes of two chunks, then its sums.
     struct Codes {
-        uint8_t k[H::PLANES * H::PLANE], v[H::PLANES * H::PLANE];
+        uint8_t k[H::KEYS * H::DIM], v[H::KEYS * H::DIM];
     };
     union Own {
         Codes codes[2];
@@ -314,10 +300,9 @@ struct Shared {
     struct Scales {
         float k[H::KEYS][H::GROUPS], v[H::KEYS][H::GROUPS];
     };
-    Own own[kWarps];                    // at a multiple of 1024 bytes
+    Own own[kWarps];
     Scales scales[kWarps][2];
     uint2 q[NT][PARTS][H::STEPS][32];   // fragments
-    uint64_t bar[kWarps][2];
     Column column[8 * NT];
     // What a column's product takes to be a score in units of log 2 (with cap,
     // to be 2 score / cap in them): the scale and the query's power of two.
@@ -327,16 +312,14 @@ struct Shared {
     int64_t scan[kWarps];
     int64_t at;         // place of the CTA's first unit in its sequence
     int32_t sequence;
-    static_assert(sizeof(Own) == 2 * sizeof(Codes) &&
-                  sizeof(Codes) % 1024 == 0, "swizzled rows keep their place");
+    static_assert(sizeof(Own) == 2 * sizeof(Codes), "room for the sums");
 };
 
-// A key head of the cache: its codes as rows of a tensor, its scales.
+// A key head of the cache, at slot 0, and the strides of slots.
 struct Cache {
-    const CUtensorMap *k, *v;
+    const uint8_t *k, *v;
     const float *ks, *vs;
-    int heads, head;
-    unsigned scales;  // of a slot
+    unsigned row, scales;
 };
 
 template <class H, bool INT8, int PARTS, int NT>
@@ -367,12 +350,6 @@ struct Warp {
             }
         }
     }
-    // All sums NaN.
-    __device__ __forceinline__ void spoil() {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            ref[n][0] = ref[n][1] = l[n][0] = l[n][1] = NAN;
-    }
     __device__ __forceinline__ unsigned exponent(int n, int h, int gr) const {
         return max(most[n][h][gr / 4] >> gr % 4 * 8 & 0xffu, 12u);
     }
@@ -383,33 +360,21 @@ struct Warp {
     static __device__ __forceinline__ float down(unsigned e) {
         return __uint_as_float((e - 11u) << 23);
     }
-    // A chunk's codes and scales on their way.  slot: of the chunk's key
-    // `lane`, or -1; such a key takes the codes of one that is there (its
-    // weights will be zero, and those codes are numbers), of slot 0 if none is
-    // (the chunk is passed over then).
+    // A chunk's codes and scales on their way; slot: of the chunk's key `lane`,
+    // or -1, whose place is filled with zeros (its weights will be zero, but
+    // what stands elsewhere may be NaN).
     __device__ __forceinline__ void load(const Cache &c, int slot, Codes &to,
-                                         Scales &scales, uint64_t *bar) {
+                                         Scales &scales) {
+        constexpr int kPieces = H::DIM / 16;  // of a key
         const int lane = threadIdx.x & 31;
-        const unsigned there = __ballot_sync(kFull, slot >= 0);
-        const int some =
-            there ? __shfl_sync(kFull, slot, __ffs(there) - 1) : 0;
-        // lanes: fours of keys, planes of keys, planes of values
-        constexpr int kFours = H::KEYS / 4;
-        const int four = lane % kFours, kind = lane / kFours;
-        int row[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = __shfl_sync(kFull, slot, 4 * four + i);
-            row[i] = ((s < 0 ? some : s) * c.heads + c.head) * H::PLANES +
-                     kind % H::PLANES;
-        }
-        if (lane == 0) mbar_expect_tx(bar, 2 * H::KEYS * H::DIM);
-        __syncwarp();
-        if (kind < 2 * H::PLANES) {
-            const bool values = kind >= H::PLANES;
-            gather4((values ? to.v : to.k) + kind % H::PLANES * H::PLANE +
-                        four * H::FOUR,
-                    values ? c.v : c.k, row[0], row[1], row[2], row[3], bar);
+        for (int i = 0; i < H::KEYS * kPieces / 32; ++i) {
+            const int piece = lane + 32 * i;
+            const int key = piece / kPieces, at = piece % kPieces * 16;
+            const int s = __shfl_sync(kFull, slot, key);
+            const uint64_t from = (uint64_t)(unsigned)max(s, 0) * c.row + at;
+            copy16(to.k + H::place(key, at), c.k + from, s >= 0);
+            copy16(to.v + H::place(key, at), c.v + from, s >= 0);
         }
         if (lane < H::KEYS) {
             const uint64_t from = (uint64_t)(unsigned)max(slot, 0) * c.scales;
@@ -417,12 +382,54 @@ struct Warp {
             copy_scales<4 * H::GROUPS>(scales.v[lane], c.vs + from, slot >= 0);
         }
     }
+    // A group's products from step S on: half a block of 128 at a time, 16
+    // bytes of a key (steps as template arguments: in loops whose step varies
+    // the fragments went through local memory).
+    template <int S>
+    __device__ __forceinline__ void score_blocks(
+        const Shared<H, PARTS, NT> &sh, const Codes &st, int gr,
+        float (&acc)[NT][KT][4]) {
+        if constexpr (S < H::PER) {
+            constexpr Block block = H::block(S);
+            constexpr int size = block.size > 64 ? 64 : block.size;
+            const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+            const int at = gr * H::GROUP + block.base + q * (block.size / 4) +
+                           4 * (S - block.base / 16);
+            unsigned k[KT][2][4];
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    read_codes(st.k + H::place(16 * t + 8 * i + g, at & ~15) +
+                                   (at & 15),
+                               size / 4, k[t][i]);
+#pragma unroll
+            for (int x = 0; x < size / 16; ++x) {
+                unsigned a[KT][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    widen4<INT8>(k[t][0][x], a[t][0], a[t][2]);
+                    widen4<INT8>(k[t][1][x], a[t][1], a[t][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        const uint2 v = sh.q[n][part][gr * H::PER + S + x][lane];
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            mma16816(acc[n][t], a[t], v.x, v.y);
+                    }
+            }
+            score_blocks<S + size / 16>(sh, st, gr, acc);
+        }
+    }
     // Sums of codes times queries times the keys' scales.
     __device__ __forceinline__ void scores(const Shared<H, PARTS, NT> &sh,
                                            const Codes &st,
                                            const Scales &scales,
                                            float (&z)[NT][KT][4]) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+        const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
             float acc[NT][KT][4];
@@ -432,43 +439,7 @@ struct Warp {
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[n][t][e] = 0.f;
-#pragma unroll
-            for (int b = 0; b < H::PER;) {
-                // half a block of 128 at a time: 16 bytes of a key
-                const Block block = H::block(b);
-                const int size = block.size > 64 ? 64 : block.size;
-                const int at = gr * H::GROUP + block.base +
-                               q * (block.size / 4) +
-                               4 * (b - block.base / 16);
-                unsigned k[KT][2][4];
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        read_codes(st.k + H::place(16 * t + 8 * i + g,
-                                                   at & ~15) + (at & 15),
-                                   size / 4, k[t][i]);
-#pragma unroll
-                for (int x = 0; x < size / 16; ++x) {
-                    unsigned a[KT][4];
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        widen4<INT8>(k[t][0][x], a[t][0], a[t][2]);
-                        widen4<INT8>(k[t][1][x], a[t][1], a[t][3]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part) {
-                            const uint2 v =
-                                sh.q[n][part][gr * H::PER + b + x][lane];
-#pragma unroll
-                            for (int t = 0; t < KT; ++t)
-                                mma16816(acc[n][t], a[t], v.x, v.y);
-                        }
-                }
-                b += size / 16;
-            }
+            score_blocks<0>(sh, st, gr, acc);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -690,11 +661,63 @@ struct Warp {
             }
         }
     }
+    // A group's weighted values from step S on.  Two rows of the output per
+    // lane and step: two bytes of its own of a value; a pair of keys side by
+    // side.
+    template <int S>
+    __device__ __forceinline__ void value_blocks(
+        const Codes &st, int gr, const unsigned (&b)[NT][PARTS][KT][2]) {
+        if constexpr (S < H::PER) {
+            constexpr Block block = H::block(S);
+            const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
+            const int at = gr * H::GROUP + block.base + g * (block.size / 8);
+            unsigned v[KT][4][4];
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    read_codes(st.v + H::place(16 * t + 2 * q + (i & 1) +
+                                                   8 * (i >> 1),
+                                               at & ~15) + (at & 15),
+                               block.size / 8, v[t][i]);
+#pragma unroll
+            for (int m = 0; m < block.size / 16; ++m) {
+                unsigned a[KT][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        widen4<INT8>(__byte_perm(v[t][2 * y][m / 2],
+                                                 v[t][2 * y + 1][m / 2],
+                                                 m & 1 ? 0x7362 : 0x5140),
+                                     a[t][2 * y], a[t][2 * y + 1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float (&to)[4] = o[n][gr * H::PER + S + m];
+                    if constexpr (PARTS == 1) {
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            mma16816(to, a[t], b[n][0][t][0], b[n][0][t][1]);
+                    } else {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                            for (int t = 0; t < KT; ++t)
+                                mma16816(acc, a[t], b[n][part][t][0],
+                                         b[n][part][t][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) to[e] += acc[e];
+                    }
+                }
+            }
+            value_blocks<S + block.size / 16>(st, gr, b);
+        }
+    }
     // Adds the chunk's weights times values.
     __device__ __forceinline__ void add(const float (&w)[NT][KT][4],
                                         unsigned hidden, const Codes &st,
                                         const Scales &scales) {
-        const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
             unsigned b[NT][PARTS][KT][2];
@@ -719,58 +742,7 @@ struct Warp {
                             }
                         }
             }
-            // Two rows of the output per lane and step: two bytes of its own
-            // of a value; a pair of keys side by side.
-#pragma unroll
-            for (int s = 0; s < H::PER;) {
-                const Block block = H::block(s);
-                const int at = gr * H::GROUP + block.base +
-                               g * (block.size / 8);
-                unsigned v[KT][4][4];
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        read_codes(
-                            st.v + H::place(16 * t + 2 * q + (i & 1) +
-                                                8 * (i >> 1),
-                                            at & ~15) + (at & 15),
-                            block.size / 8, v[t][i]);
-#pragma unroll
-                for (int m = 0; m < block.size / 16; ++m) {
-                    unsigned a[KT][4];
-#pragma unroll
-                    for (int t = 0; t < KT; ++t)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            widen4<INT8>(
-                                __byte_perm(v[t][2 * y][m / 2],
-                                            v[t][2 * y + 1][m / 2],
-                                            m & 1 ? 0x7362 : 0x5140),
-                                a[t][2 * y], a[t][2 * y + 1]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float (&to)[4] = o[n][gr * H::PER + s + m];
-                        if constexpr (PARTS == 1) {
-#pragma unroll
-                            for (int t = 0; t < KT; ++t)
-                                mma16816(to, a[t], b[n][0][t][0],
-                                         b[n][0][t][1]);
-                        } else {
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                                for (int t = 0; t < KT; ++t)
-                                    mma16816(acc, a[t], b[n][part][t][0],
-                                             b[n][part][t][1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) to[e] += acc[e];
-                        }
-                    }
-                }
-                s += block.size / 16;
-            }
+            value_blocks<0>(st, gr, b);
         }
     }
 };
@@ -937,21 +909,11 @@ __device__ __forceinline__ int slot_in(const mt_attention_call_t &c, Page p) {
     return p.id >= 0 && slot < c.slots ? (int)slot : -1;
 }
 
-// The cache's codes as tensors of rows; a warp's waits on its two barriers.
-struct Maps {
-    const CUtensorMap *k, *v;
-};
-struct Waits {
-    unsigned phase;  // bit s: the parity that stage s completes next
-    bool gave_up;
-};
-
 // The units [u0, u1) of a tile: its queries, and each warp's share of them.
 template <class H, bool INT8, int PARTS, int NT>
 __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
                                          const Cut &cut, int dtype,
                                          const Tile &a, int64_t u0, int64_t u1,
-                                         const Maps &maps, Waits &waits,
                                          Shared<H, PARTS, NT> &sh,
                                          Warp<H, INT8, PARTS, NT> &w) {
     constexpr int KT = H::KEYS / 16;
@@ -973,21 +935,18 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
                    : Page{-1, 0};
     };
     Cache m;
-    m.k = maps.k;
-    m.v = maps.v;
-    m.heads = c.k_heads;
-    m.head = a.head;
+    m.row = (unsigned)(c.k_heads * H::DIM);
+    m.scales = (unsigned)(c.k_heads * H::GROUPS);
+    m.k = static_cast<const uint8_t *>(c.k_codes) + a.head * H::DIM;
+    m.v = static_cast<const uint8_t *>(c.v_codes) + a.head * H::DIM;
     m.ks = c.k_scales + a.head * H::GROUPS;
     m.vs = c.v_scales + a.head * H::GROUPS;
-    m.scales = (unsigned)(c.k_heads * H::GROUPS);
     auto &codes = sh.own[warp].codes;
     auto &scales = sh.scales[warp];
-    uint64_t *bar = sh.bar[warp];
-    if (waits.gave_up) u = u1;
     const Page first = page_at(u);
     Page next = page_at(u + kWarps);
     int slot = slot_in(c, first), stage = 0;
-    if (u < u1) w.load(m, slot, codes[0], scales[0], &bar[0]);
+    if (u < u1) w.load(m, slot, codes[0], scales[0]);
     asm volatile("cp.async.commit_group;" ::: "memory");
     queries.put(c, sh);
     __syncthreads();
@@ -997,22 +956,10 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
         slot = slot_in(c, next);
         next = page_at(u + 2 * kWarps);
         if (u + kWarps < u1)
-            w.load(m, slot, codes[stage ^ 1], scales[stage ^ 1],
-                   &bar[stage ^ 1]);
+            w.load(m, slot, codes[stage ^ 1], scales[stage ^ 1]);
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const bool came =
-            mbar_wait_bounded(&bar[stage], waits.phase >> stage & 1u);
-        waits.phase ^= 1u << stage;
-        if (!__all_sync(kFull, came)) {
-            // Not before a fault elsewhere: no more copies, their own awaited,
-            // and NaN for what this warp had a part in.
-            if (u + kWarps < u1)
-                mbar_wait_bounded(&bar[stage ^ 1],
-                                  waits.phase >> (stage ^ 1) & 1u);
-            waits.gave_up = true;
-            break;
-        }
+        __syncwarp();
         if (there != 0) {
             float z[NT][KT][4];
             unsigned hidden;
@@ -1025,7 +972,6 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
         stage ^= 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (waits.gave_up) w.spoil();
     __syncwarp();  // the warp's sums take the chunks' place
 }
 
@@ -1103,9 +1049,7 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
             }
         }
     }
-    // Shared memory is the next tile's: its copies come after these accesses.
-    fence_proxy_async_smem();
-    __syncthreads();
+    __syncthreads();  // shared memory is the next tile's
 }
 
 // The least units that a CTA takes where there are few: a tile's own, and one
@@ -1116,22 +1060,12 @@ template <class H, bool INT8, int PARTS, int NT>
 __global__ void __launch_bounds__(32 * kWarps,
                                   attention_ctas(H::DIM, H::GROUPS, PARTS, NT))
     attention_mma_kernel(const mt_attention_call_t c, const Cut cut,
-                         const Share share, int dtype,
-                         const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map) {
+                         const Share share, int dtype) {
     constexpr int C = 8 * NT, KEYS = H::KEYS, T = 32 * kWarps;
-    extern __shared__ uint8_t shared[];
-    Shared<H, PARTS, NT> &sh = *reinterpret_cast<Shared<H, PARTS, NT> *>(
-        shared + (-smem_addr(shared) & 1023u));
+    extern __shared__ __align__(16) uint8_t shared[];
+    Shared<H, PARTS, NT> &sh =
+        *reinterpret_cast<Shared<H, PARTS, NT> *>(shared);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (lane == 0) {
-        mbar_init(&sh.bar[warp][0], 1);
-        mbar_init(&sh.bar[warp][1], 1);
-        mbar_init_fence();
-    }
-    const Maps maps = {&k_map, &v_map};
-    Waits waits = {0, false};
-    grid_launch_dependents();
     grid_wait_prerequisites();
     Record record = {};
     // Units of the sequences of this thread, and where they begin.
@@ -1183,11 +1117,17 @@ __global__ void __launch_bounds__(32 * kWarps,
         a.s = sh.sequence;
         int64_t off = sh.at;
         a.tiles = tiles_of(c, cut, a.s);
-        int lo = 0, hi = a.tiles.count;  // before(lo) <= off < before(hi)
+        // before(lo) <= off < before(hi): every thread looks at one place of
+        // the range, until it has one tile.
+        int lo = 0, hi = a.tiles.count;
         while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (wide * a.tiles.template before<KEYS>(mid) <= off) lo = mid;
-            else hi = mid;
+            const int each_ = (hi - lo + T - 1) / T;
+            const int mid = min(lo + (tid + 1) * each_, hi);
+            const int fewer = __syncthreads_count(
+                mid < hi &&
+                wide * a.tiles.template before<KEYS>(mid) <= off);
+            lo += fewer * each_;
+            hi = min(lo + each_, hi);
         }
         a.t = lo;
         off -= wide * a.tiles.template before<KEYS>(lo);
@@ -1203,7 +1143,7 @@ __global__ void __launch_bounds__(32 * kWarps,
             w.begin();
             tile_run<H, INT8, PARTS, NT>(
                 c, cut, dtype, a, base + max(off - kExtra, (int64_t)0),
-                base + max(off + n - kExtra, (int64_t)0), maps, waits, sh, w);
+                base + max(off + n - kExtra, (int64_t)0), sh, w);
             const bool whole = n == units;
             if (!whole && off == 0) {
                 const int64_t x = at + units;
@@ -1233,6 +1173,9 @@ __global__ void __launch_bounds__(32 * kWarps,
             }
         }
     }
+    // Not before: the next kernel's CTAs would take the place of this one's
+    // (64 sequences to 16384 keys with three CTAs per SM: 331 us).
+    grid_launch_dependents();
     if (tid == 0) share.records[blockIdx.x] = record;
 }
 
@@ -1319,7 +1262,7 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
                                 void *workspace, cudaStream_t s) {
     using Sh = Shared<H, PARTS, NT>;
     constexpr int kCtas = attention_ctas(H::DIM, H::GROUPS, PARTS, NT);
-    constexpr size_t kBytes = sizeof(Sh) + 1024;  // to a multiple of 1024
+    constexpr size_t kBytes = sizeof(Sh);
     static_assert((kBytes + 1024) * kCtas <= 228 * 1024,
                   "the CTAs that share an SM fit its shared memory");
     const Cut cut = {p.times, p.per, p.parts};
@@ -1327,17 +1270,13 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
     share.sums = static_cast<float *>(workspace);
     share.records = reinterpret_cast<Record *>(
         share.sums + 2 * (int64_t)p.ctas * place_floats(8 * NT, H::DIM));
-    CUtensorMap maps[2];
-    const int64_t rows = c.slots * c.k_heads * H::PLANES;
-    cudaError_t e = attention_map(c.k_codes, rows, H::WIDE, &maps[0]);
-    if (e == cudaSuccess)
-        e = attention_map(c.v_codes, rows, H::WIDE, &maps[1]);
+    cudaError_t e = cudaSuccess;
     const auto kernel = attention_mma_kernel<H, INT8, PARTS, NT>;
-    if (e == cudaSuccess && kBytes > 48 * 1024)
+    if (kBytes > 48 * 1024)
         e = allow_max_smem(reinterpret_cast<const void *>(kernel));
     if (e == cudaSuccess)
         e = launch_dependent(kernel, p.ctas, 32 * kWarps, kBytes, s, c, cut,
-                             share, dtype, maps[0], maps[1]);
+                             share, dtype);
     if (e != cudaSuccess) return e;
     return launch_dependent(attention_join_kernel<H::DIM, 8 * NT>, p.ctas,
                             kJoin, (size_t)p.ctas * 8 * NT * sizeof(float), s,

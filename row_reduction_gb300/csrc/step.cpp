@@ -68,7 +68,7 @@ bool attention_head(const mt_attention_call_t &c) {
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
                          AttentionPlan *p) {
     *matrix = attention_head(c) && c.slots > 0 && c.pages > 0 &&
-              c.slots <= INT32_MAX / ((int64_t)c.k_heads * 2) &&
+              c.slots <= INT32_MAX &&
               !misaligned(c.k_codes, 32) && !misaligned(c.v_codes, 32) &&
               !misaligned(c.k_scales, 16) && !misaligned(c.v_scales, 16);
     if (!*matrix) return MT_OK;
