@@ -4,16 +4,18 @@
 // Scores are formed transposed, keys x queries (S^T = K Q^T), so that the
 // cache's codes, which are the long operand, fill the instruction's 16 rows and
 // the few query heads that share a key head its 8 columns.  A warp goes through
-// chunks of keys of its own: codes are gathered into shared
-// memory of the warp's own by tensor copies, four keys' rows to a copy, a chunk
-// ahead of the one that is worked on, and widened to FP16 on the way into
-// fragments, exactly (the order of the dimensions is free as long as queries
-// have the same, so a lane reads up to 16 bytes of a key at once).  Loads into
-// registers kept too few bytes in flight (64 sequences to 16384 keys of 8 heads
-// of 128: 247 us), and copies of 16 bytes per lane took longer to issue than a
-// chunk takes to work on (351 us).  What the scores give
+// chunks of keys of its own: codes are copied into shared
+// memory of the warp's own by asynchronous copies, a chunk ahead of the one that
+// is worked on, and widened to FP16 on the way into fragments, exactly (the
+// order of the dimensions is free as long as queries have the same, so a lane
+// reads up to 16 bytes of a key at once).  What the scores give
 // turns into the other product's operand (O^T = V^T P^T) by one transposition
 // of 8 x 8 values within the warp.
+//
+// The four warps of a CTA take key heads of the same keys, as many as divide the
+// call's (4, 2 or 1; the warps that are left share a head's keys): rows and
+// scales of neighbouring heads lie side by side, and a head's scale alone is 4
+// bytes of a sector of 32, which the other heads' CTAs would fetch again.
 //
 // Scales.  A key's factor multiplies its score's sum of each group, a value's
 // the weight that goes into the product of that group.
@@ -32,8 +34,9 @@
 // is so, which holds for nearly all chunks, and saves the exchange of maxima
 // among lanes and the scaling of the sums.
 //
-// Work is dealt out in units, a chunk of keys of one tile (rows of a sequence
-// and the query heads of a key head, up to 8 NT columns): every CTA takes an
+// Work is dealt out in units, one chunk for each warp of one tile (rows of a
+// sequence and the query heads of a key head, up to 8 NT columns, for each of
+// the CTA's key heads): every CTA takes an
 // equal run of all units of the batch in their order, wherever sequences begin
 // and end in it, so that lengths of any mixture fill the device and nothing
 // about them need be known on the host.  A tile that is cut by the ends of
@@ -54,11 +57,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
         return (int64_t)((unsigned)a / (unsigned)b);
     return a / b;
 }
-// sum over 0 <= t < n of floor((a t + b) / M), for a, b >= 0: whole parts
+// sum over 0 <= t < n of floor((a t + b) / m), for a, b >= 0: whole parts
 // aside, the points under a line, counted along the other axis in turn.
-template <int M>
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
-    int64_t s = 0, m = M;
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a,
+                                             int64_t b) {
+    int64_t s = 0;
     while (n > 0) {
         s += (n - 1) * n / 2 * quotient(a, m) + n * quotient(b, m);
         a -= quotient(a, m) * m;
@@ -76,61 +79,62 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
 
 // A tile's begin and end (queries, the first keys' way, the warps' sums
 // joined) in units: without them runs of short sequences are the last to end.
-constexpr int64_t kExtra = 8;
+constexpr int64_t kExtra = 2;
 
-// How the rows of a sequence are cut into tiles and units of KEYS keys.
+// How the call's rows and heads are cut.
+struct Cut {
+    int32_t times;   // query heads per key head
+    int32_t per;     // rows of a tile
+    int32_t parts;   // tiles that share a row's query heads
+    int32_t heads;   // key heads of a CTA: 4, 2 or 1
+    int32_t log2;    // keys of a unit
+    int32_t wide;    // tiles of the same rows: groups of key heads, parts
+    int32_t whole;   // out takes 4 values at a time
+};
+
+// How the rows of a sequence are cut into tiles and units.
 struct Tiles {
     int64_t start;   // position of the first row
     int32_t rows;    // of the sequence
     int32_t per;     // rows of a tile
     int32_t count;   // tiles
     int32_t window;
+    int32_t log2;
     bool all;        // every tile goes through all keys (last bounds)
     // Tile t's first and last unit of keys (of what its rows may see).
-    template <int KEYS>
     __device__ __forceinline__ int64_t first(int t) const {
         if (window == 0) return 0;
-        return (int64_t)((uint64_t)max(start + (int64_t)t * per - window + 1,
-                                       (int64_t)0) / KEYS);
+        return max(start + (int64_t)t * per - window + 1, (int64_t)0) >> log2;
     }
-    template <int KEYS>
     __device__ __forceinline__ int64_t last(int t) const {
         const int64_t r = all ? rows : min((int64_t)(t + 1) * per,
                                            (int64_t)rows);
-        return (int64_t)((uint64_t)(start + r - 1) / KEYS);
+        return (start + r - 1) >> log2;
     }
     // Units of the tiles before t (first <= last in every tile), kExtra to
     // each for what a tile costs besides.
-    template <int KEYS>
     __device__ __forceinline__ int64_t before(int t) const {
         if (t <= 0) return 0;
         int64_t s = (1 + kExtra) * (int64_t)t;
-        if (t == 1) return s + last<KEYS>(0) - first<KEYS>(0);
+        if (t == 1) return s + last(0) - first(0);
         if (all) {
-            s += t * last<KEYS>(0);
+            s += t * last(0);
         } else {
             // all tiles but the sequence's last are whole
             const int whole = t < count ? t : count - 1;
-            s += floor_sum<KEYS>(whole, per, start + per - 1);
-            if (t > whole) s += last<KEYS>(count - 1);
+            s += floor_sum(whole, 1LL << log2, per, start + per - 1);
+            if (t > whole) s += last(count - 1);
         }
         if (window != 0) {
             // from tile z on the window's begin is not negative
             const int64_t short_of = window - 1 - start;
             const int64_t z = short_of <= 0 ? 0 : (short_of + per - 1) / per;
             if (t > z)
-                s -= floor_sum<KEYS>(t - z, per,
-                                         start + z * per - window + 1);
+                s -= floor_sum(t - z, 1LL << log2, per,
+                               start + z * per - window + 1);
         }
         return s;
     }
-};
-
-// What the call's tiles have in common.
-struct Cut {
-    int32_t times;   // query heads per key head
-    int32_t per;     // rows of a tile
-    int32_t parts;   // tiles that share a row's query heads
 };
 
 __device__ __forceinline__ Tiles tiles_of(const mt_attention_call_t &c,
@@ -142,6 +146,7 @@ __device__ __forceinline__ Tiles tiles_of(const mt_attention_call_t &c,
     t.per = cut.per;
     t.count = (t.rows + cut.per - 1) / cut.per;
     t.window = c.window;
+    t.log2 = cut.log2;
     t.all = c.last != nullptr;
     return t;
 }
@@ -150,15 +155,16 @@ __device__ __forceinline__ Tiles tiles_of(const mt_attention_call_t &c,
 struct Record {
     int32_t valid, last;      // last: the CTA that holds its end
     int32_t row, rows;        // rows of the batch
-    int32_t head, part;       // key head; part of the row's query heads
+    int32_t head, part;       // first key head; part of the row's query heads
 };
 struct Share {
     Record *records;          // one per CTA
-    float *sums;              // two places per CTA: m, l, O of each column
+    float *sums;              // two places per CTA: m, l, O of each column of
+                              // each of its key heads
 };
 
 __host__ __device__ constexpr int place_floats(int columns, int dim) {
-    return columns * (dim + 2);
+    return kWarps * columns * (dim + 2);
 }
 
 // ---- instructions --------------------------------------------------------------
@@ -282,9 +288,9 @@ struct Head {
 
 // A column of a tile: one row's query head.
 struct Column {
-    float slope;        // in units of log 2
     int32_t lo, hi;     // keys that it sees
     int32_t p;          // its row's position
+    int32_t pad;
 };
 
 template <class H, int PARTS, int NT>
@@ -302,11 +308,12 @@ struct Shared {
     };
     Own own[kWarps];
     Scales scales[kWarps][2];
-    uint2 q[NT][PARTS][H::STEPS][32];   // fragments
+    uint2 q[kWarps][NT][PARTS][H::STEPS][32];  // fragments, of each key head
     Column column[8 * NT];
-    // What a column's product takes to be a score in units of log 2 (with cap,
-    // to be 2 score / cap in them): the scale and the query's power of two.
-    float f[8 * NT];
+    // Of each key head's columns: what the product takes to be a score in units
+    // of log 2 (with cap, to be 2 score / cap in them), the scale and the
+    // query's power of two; the slope in those units.
+    float f[kWarps][8 * NT], slope[kWarps][8 * NT];
     int32_t lo_any, hi_any, lo_all, hi_all;
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     int64_t scan[kWarps];
@@ -329,6 +336,7 @@ struct Warp {
     using Scales = typename Shared<H, PARTS, NT>::Scales;
     float o[NT][H::STEPS][4];        // in units of 2^-(up of its group)
     float ref[NT][2], l[NT][2];
+    int hs;                          // which of the CTA's key heads
     // Exponent bits of the largest weight times scale so far, of each column
     // and group; four to a word.
     unsigned most[NT][2][(H::GROUPS + 3) / 4];
@@ -415,7 +423,8 @@ struct Warp {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
-                        const uint2 v = sh.q[n][part][gr * H::PER + S + x][lane];
+                        const uint2 v =
+                            sh.q[hs][n][part][gr * H::PER + S + x][lane];
 #pragma unroll
                         for (int t = 0; t < KT; ++t)
                             mma16816(acc[n][t], a[t], v.x, v.y);
@@ -473,7 +482,7 @@ struct Warp {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float f = sh.f[8 * n + 2 * q + h];
+                const float f = sh.f[hs][8 * n + 2 * q + h];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -495,6 +504,7 @@ struct Warp {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const Column &col = sh.column[8 * n + 2 * q + h];
+                const float slope = sh.slope[hs][8 * n + 2 * q + h];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -502,7 +512,7 @@ struct Warp {
                         const int at = 16 * t + 8 * i + g;
                         float &v = z[n][t][2 * i + h];
                         if (c.slopes != nullptr)
-                            v -= col.slope * (float)abs(col.p - (j0 + at));
+                            v -= slope * (float)abs(col.p - (j0 + at));
                         if (!whole &&
                             !(there >> at & 1u && j0 + at >= col.lo &&
                               j0 + at <= col.hi)) {
@@ -749,7 +759,9 @@ struct Warp {
 
 // ---- a tile ------------------------------------------------------------------
 struct Tile {
-    int s, t, head, part;
+    int s, t;
+    int head;       // the first of the CTA's key heads
+    int part;
     Tiles tiles;
 };
 
@@ -790,62 +802,85 @@ __device__ __forceinline__ Place place_of(const Cut &cut, int first_row,
     return p;
 }
 
-// A thread's part of the queries of a tile: kPer threads to a column.
+// Columns of a tile that stand for something; they are the first ones.
+template <int C>
+__device__ __forceinline__ int columns_of(const Cut &cut, int rows, int part) {
+    return cut.times <= C ? rows * cut.times : min(cut.times - part * C, C);
+}
+
+// A warp's part of the queries of a tile: the columns of its key head that are
+// its own among the warps of that head; a lane has every 32nd value.
 template <class H, int PARTS, int NT>
 struct Queries {
-    static constexpr int C = 8 * NT, kPer = 32 * kWarps / C;
-    static constexpr int kEach = H::DIM / kPer;
-    float x[kEach];
-    int row, head;  // of this thread's column
-    bool used;
+    static constexpr int C = 8 * NT, kEach = (H::DIM + 31) / 32;
+    float x[C][kEach];
     __device__ __forceinline__ void load(const mt_attention_call_t &c,
                                          const Cut &cut, int dtype,
-                                         const Tile &a) {
-        const int col = threadIdx.x / kPer, sub = threadIdx.x % kPer;
-        const Place at = place_of<C>(
-            cut, c.offsets[a.s] + a.t * cut.per,
-            min(cut.per, a.tiles.rows - a.t * cut.per), a.head, a.part, col);
-        const int64_t q =
-            (int64_t)at.row * c.q_row + (int64_t)at.head * c.q_head;
+                                         const Tile &a, int hs, int ks,
+                                         int warps) {
+        const int from = c.offsets[a.s] + a.t * cut.per;
+        const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            x[i] = at.used ? load_as(PARTS == 1 ? (int)DT_BF16 : dtype, c.q,
-                                     q + sub + kPer * i)
-                           : 0.f;
+        for (int col = 0; col < C; ++col) {
+            const Place at =
+                place_of<C>(cut, from, rows, a.head + hs, a.part, col);
+            const bool on = at.used && (col & (warps - 1)) == ks;
+            const int64_t q =
+                (int64_t)at.row * c.q_row + (int64_t)at.head * c.q_head;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int d = (threadIdx.x & 31) + 32 * i;
+                x[col][i] = on && d < H::DIM
+                                ? load_as(PARTS == 1 ? (int)DT_BF16 : dtype,
+                                          c.q, q + d)
+                                : 0.f;
+            }
+        }
     }
     // Fragments, and the columns' factors, into shared memory.
     __device__ __forceinline__ void put(const mt_attention_call_t &c,
-                                        Shared<H, PARTS, NT> &sh) {
-        const int col = threadIdx.x / kPer, sub = threadIdx.x % kPer;
-        float largest = 0.f;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) largest = nanmax(largest, fabsf(x[i]));
-#pragma unroll
-        for (int off = kPer / 2; off > 0; off >>= 1)
-            largest = nanmax(largest, __shfl_xor_sync(kFull, largest, off));
-        const unsigned e = max(__float_as_uint(largest) >> 23, 15u);
-        const bool bad = !(largest < INFINITY);
-        const float up = bad ? 0.f : __uint_as_float((268u - e) << 23);
-        __half *halves = reinterpret_cast<__half *>(&sh.q[col / 8][0][0][0]);
+                                        Shared<H, PARTS, NT> &sh, int hs,
+                                        int ks, int warps) {
+        const int lane = threadIdx.x & 31;
+        int place[kEach];  // of the lane's values in a column's fragments
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int d = sub + kPer * i, r = d % H::GROUP;
+            const int d = min(lane + 32 * i, H::DIM - 1), r = d % H::GROUP;
             const Block block = H::block(r / 16);
             const int in = r - block.base, wide = block.size / 4;
             const int step = d / H::GROUP * H::PER + block.base / 16 +
                              in % wide / 4;
-            const int lane = col % 8 * 4 + in / wide;
-            const float v = bad ? 0.f : x[i] * up;
-            const __half hi = __float2half_rn(v);
-            halves[(step * 32 + lane) * 4 + r % 4] = hi;
-            if constexpr (PARTS == 2)
-                halves[((H::STEPS + step) * 32 + lane) * 4 + r % 4] =
-                    __float2half_rn(v - __half2float(hi));
+            place[i] = (step * 32 + in / wide) * 4 + r % 4;
         }
-        if (sub == 0)
-            sh.f[col] = bad ? NAN
-                            : (c.cap > 0.f ? c.scale / c.cap * 2.f : c.scale) *
-                                  kLog2e * __uint_as_float((e - 14u) << 23);
+#pragma unroll
+        for (int col = 0; col < C; ++col) {
+            if ((col & (warps - 1)) != ks) continue;
+            float largest = 0.f;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                largest = nanmax(largest, fabsf(x[col][i]));
+            largest = warp_nanmax(largest);
+            const unsigned e = max(__float_as_uint(largest) >> 23, 15u);
+            const bool bad = !(largest < INFINITY);
+            const float up = bad ? 0.f : __uint_as_float((268u - e) << 23);
+            __half *halves = reinterpret_cast<__half *>(
+                                 &sh.q[hs][col / 8][0][0][0]) + col % 8 * 16;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (lane + 32 * i >= H::DIM) continue;
+                const float v = bad ? 0.f : x[col][i] * up;
+                const __half hi = __float2half_rn(v);
+                halves[place[i]] = hi;
+                if constexpr (PARTS == 2)
+                    halves[H::STEPS * 128 + place[i]] =
+                        __float2half_rn(v - __half2float(hi));
+            }
+            if (lane == 0)
+                sh.f[hs][col] =
+                    bad ? NAN
+                        : (c.cap > 0.f ? c.scale / c.cap * 2.f : c.scale) *
+                              kLog2e * __uint_as_float((e - 14u) << 23);
+        }
     }
 };
 
@@ -853,22 +888,24 @@ struct Queries {
 template <class H, int PARTS, int NT>
 __device__ __forceinline__ void tile_bounds(const mt_attention_call_t &c,
                                             const Cut &cut, const Tile &a,
+                                            int hs, int ks,
                                             Shared<H, PARTS, NT> &sh) {
     constexpr int C = 8 * NT;
-    const int col = threadIdx.x;
-    if (col >= 32) return;
+    const int col = threadIdx.x & 31;
     const int from = c.offsets[a.s];
     const Place at = place_of<C>(cut, from + a.t * cut.per,
                                  min(cut.per, a.tiles.rows - a.t * cut.per),
-                                 a.head, a.part, col);
+                                 a.head + hs, a.part, col);
     const bool used = col < C && at.used;
-    Column k = {0.f, INT32_MIN, INT32_MAX, 0};
+    if (c.slopes != nullptr && ks == 0 && col < C)
+        sh.slope[hs][col] = used ? c.slopes[at.head] * kLog2e : 0.f;
+    if (threadIdx.x >= 32) return;
+    Column k = {INT32_MIN, INT32_MAX, 0, 0};
     if (used) {
         const int64_t n = (int64_t)c.offsets[a.s + 1] - from;
         const int64_t start = c.starts[a.s], p = start + (at.row - from);
         int64_t lo, hi;
         row_sees(c, at.row, p, start + n, lo, hi);
-        k.slope = c.slopes ? c.slopes[at.head] * kLog2e : 0.f;
         k.lo = (int32_t)min(lo, (int64_t)INT32_MAX);
         k.hi = (int32_t)max(min(hi, (int64_t)INT32_MAX), (int64_t)-1);
         k.p = (int32_t)min(p, (int64_t)INT32_MAX);
@@ -918,44 +955,51 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
                                          Warp<H, INT8, PARTS, NT> &w) {
     constexpr int KT = H::KEYS / 16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = kWarps / cut.heads;  // of a key head
+    const int hs = warp / warps, ks = warp & (warps - 1);
+    w.hs = hs;
     // The queries are asked for first and needed last: the first keys' slots
     // and codes are on their way meanwhile.
     Queries<H, PARTS, NT> queries;
-    queries.load(c, cut, dtype, a);
-    tile_bounds(c, cut, a, sh);
+    queries.load(c, cut, dtype, a, hs, ks, warps);
+    tile_bounds(c, cut, a, hs, ks, sh);
     __syncthreads();
     const int lo = sh.lo_any, hi = sh.hi_any;
     const int32_t *pages = c.table + a.s * c.table_stride;
-    u0 = max(u0, (int64_t)(lo / H::KEYS));
-    u1 = lo > hi ? 0 : min(u1, (int64_t)(hi / H::KEYS) + 1);
-    int64_t u = u0 + warp;
+    // chunks
+    int64_t u = max(u0 * warps, (int64_t)(lo / H::KEYS));
+    const int64_t end =
+        lo > hi ? 0 : min(u1 * warps, (int64_t)(hi / H::KEYS) + 1);
+    u += (ks - u) & (warps - 1);
     const auto page_at = [&](int64_t v) {
-        return v < u1 && lane < H::KEYS
+        return v < end && lane < H::KEYS
                    ? page_of(c, pages, v * H::KEYS + lane, lo, hi)
                    : Page{-1, 0};
     };
+    const int head = a.head + hs;
     Cache m;
     m.row = (unsigned)(c.k_heads * H::DIM);
     m.scales = (unsigned)(c.k_heads * H::GROUPS);
-    m.k = static_cast<const uint8_t *>(c.k_codes) + a.head * H::DIM;
-    m.v = static_cast<const uint8_t *>(c.v_codes) + a.head * H::DIM;
-    m.ks = c.k_scales + a.head * H::GROUPS;
-    m.vs = c.v_scales + a.head * H::GROUPS;
+    m.k = static_cast<const uint8_t *>(c.k_codes) + head * H::DIM;
+    m.v = static_cast<const uint8_t *>(c.v_codes) + head * H::DIM;
+    m.ks = c.k_scales + head * H::GROUPS;
+    m.vs = c.v_scales + head * H::GROUPS;
     auto &codes = sh.own[warp].codes;
     auto &scales = sh.scales[warp];
     const Page first = page_at(u);
-    Page next = page_at(u + kWarps);
+    Page next = page_at(u + warps);
     int slot = slot_in(c, first), stage = 0;
-    if (u < u1) w.load(m, slot, codes[0], scales[0]);
+    if (u < end) w.load(m, slot, codes[0], scales[0]);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    queries.put(c, sh);
+    queries.put(c, sh, hs, ks, warps);
     __syncthreads();
+    w.begin();
 #pragma unroll 1
-    for (; u < u1; u += kWarps) {
+    for (; u < end; u += warps) {
         const unsigned there = __ballot_sync(kFull, slot >= 0);
         slot = slot_in(c, next);
-        next = page_at(u + 2 * kWarps);
-        if (u + kWarps < u1)
+        next = page_at(u + 2 * warps);
+        if (u + warps < end)
             w.load(m, slot, codes[stage ^ 1], scales[stage ^ 1]);
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -973,6 +1017,34 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();  // the warp's sums take the chunks' place
+}
+
+// Four values of a row of the output.
+__device__ __forceinline__ void store4(int dtype, bool whole, void *p,
+                                       int64_t i, const float *v) {
+    if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_as(dtype, p, i + e, v[e]);
+    } else if (dtype == DT_BF16) {
+        st_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(p) + i, v);
+    } else if (dtype == DT_F16) {
+        st_vec<__half, 4>(static_cast<__half *>(p) + i, v);
+    } else {
+        st_vec<float, 4>(static_cast<float *>(p) + i, v);
+    }
+}
+// A column's sums about `top` (-infinity: nothing seen), out.
+__device__ __forceinline__ void finish(const mt_attention_call_t &c,
+                                       const Cut &cut, int dtype,
+                                       const Place &at, int d, float top,
+                                       float sum, float *o) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = top == -INFINITY ? 0.f : o[e] / sum;
+    store4(dtype, cut.whole != 0, c.out,
+           (int64_t)at.row * c.out_row + (int64_t)at.head * c.out_head + d, o);
+    if (c.lse != nullptr && d == 0)
+        c.lse[(int64_t)at.row * c.q_heads + at.head] =
+            top == -INFINITY ? top : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // The warps' sums of a tile joined: written out where the tile is whole, left
@@ -1016,52 +1088,56 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
     __syncthreads();
     const int from = c.offsets[a.s] + a.t * cut.per;
     const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
+    const int columns = columns_of<C>(cut, rows, a.part);
+    const int warps = kWarps / cut.heads;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < C * H::DIM; i += 32 * kWarps) {
-        const int col = i / H::DIM, d = i % H::DIM;
-        const Place at = place_of<C>(cut, from, rows, a.head, a.part, col);
-        if (!at.used) continue;
-        float top = sh.m[0][col];
-#pragma unroll
-        for (int x = 1; x < kWarps; ++x) top = nanmax(top, sh.m[x][col]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, o = 0.f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-            const float f = pow2(sh.m[x][col] - ref);
-            sum = fmaf(sh.l[x][col], f, sum);
-            o = fmaf(sh.own[x].o[col][d], f, o);
-        }
-        if (whole) {
-            store_as(PARTS == 1 ? (int)DT_BF16 : dtype, c.out,
-                     (int64_t)at.row * c.out_row +
-                         (int64_t)at.head * c.out_head + d,
-                     top == -INFINITY ? 0.f : o / sum);
-            if (c.lse != nullptr && d == 0)
-                c.lse[(int64_t)at.row * c.q_heads + at.head] =
-                    top == -INFINITY ? top
-                                     : (top + log2f(sum)) * 0.6931471805599453f;
-        } else {
-            sums[2 * C + i] = o;
-            if (d == 0) {
-                sums[col] = top;
-                sums[C + col] = sum;
+    for (int hs = 0; hs < cut.heads; ++hs)
+#pragma unroll 1
+        for (int i = 4 * threadIdx.x; i < columns * H::DIM;
+             i += 128 * kWarps) {
+            const int col = i / H::DIM, d = i % H::DIM, w0 = hs * warps;
+            float top = sh.m[w0][col];
+            for (int x = 1; x < warps; ++x)
+                top = nanmax(top, sh.m[w0 + x][col]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int x = 0; x < warps; ++x) {
+                const float f = pow2(sh.m[w0 + x][col] - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    &sh.own[w0 + x].o[col][d]);
+                sum = fmaf(sh.l[w0 + x][col], f, sum);
+                o[0] = fmaf(v.x, f, o[0]);
+                o[1] = fmaf(v.y, f, o[1]);
+                o[2] = fmaf(v.z, f, o[2]);
+                o[3] = fmaf(v.w, f, o[3]);
+            }
+            if (whole) {
+                finish(c, cut, PARTS == 1 ? (int)DT_BF16 : dtype,
+                       place_of<C>(cut, from, rows, a.head + hs, a.part, col),
+                       d, top, sum, o);
+            } else {
+                const int at = hs * C + col;
+                *reinterpret_cast<float4 *>(sums + 2 * kWarps * C +
+                                            at * H::DIM + d) =
+                    make_float4(o[0], o[1], o[2], o[3]);
+                if (d == 0) {
+                    sums[at] = top;
+                    sums[kWarps * C + at] = sum;
+                }
             }
         }
-    }
     __syncthreads();  // shared memory is the next tile's
 }
 
-// The least units that a CTA takes where there are few: a tile's own, and one
-// of keys for each warp.
-constexpr int kLeastUnits = (int)kExtra + kWarps;
+// The least units that a CTA takes where there are few: a tile's own, and one.
+constexpr int kLeastUnits = (int)kExtra + 1;
 
 template <class H, bool INT8, int PARTS, int NT>
 __global__ void __launch_bounds__(32 * kWarps,
                                   attention_ctas(H::DIM, H::GROUPS, PARTS, NT))
     attention_mma_kernel(const mt_attention_call_t c, const Cut cut,
                          const Share share, int dtype) {
-    constexpr int C = 8 * NT, KEYS = H::KEYS, T = 32 * kWarps;
+    constexpr int C = 8 * NT, T = 32 * kWarps;
     extern __shared__ __align__(16) uint8_t shared[];
     Shared<H, PARTS, NT> &sh =
         *reinterpret_cast<Shared<H, PARTS, NT> *>(shared);
@@ -1072,10 +1148,10 @@ __global__ void __launch_bounds__(32 * kWarps,
     const int each = (c.sequences + T - 1) / T;
     const int s0 = min(tid * each, c.sequences);
     const int s1 = min(s0 + each, c.sequences);
-    const int64_t wide = (int64_t)c.k_heads * cut.parts;
+    const int64_t wide = cut.wide;
     const auto units_of = [&](int s) {
         const Tiles t = tiles_of(c, cut, s);
-        return wide * t.template before<KEYS>(t.count);
+        return wide * t.before(t.count);
     };
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) mine += units_of(s);
@@ -1121,18 +1197,17 @@ __global__ void __launch_bounds__(32 * kWarps,
         // the range, until it has one tile.
         int lo = 0, hi = a.tiles.count;
         while (hi - lo > 1) {
-            const int each_ = (hi - lo + T - 1) / T;
-            const int mid = min(lo + (tid + 1) * each_, hi);
+            const int step = (hi - lo + T - 1) / T;
+            const int mid = min(lo + (tid + 1) * step, hi);
             const int fewer = __syncthreads_count(
-                mid < hi &&
-                wide * a.tiles.template before<KEYS>(mid) <= off);
-            lo += fewer * each_;
-            hi = min(lo + each_, hi);
+                mid < hi && wide * a.tiles.before(mid) <= off);
+            lo += fewer * step;
+            hi = min(lo + step, hi);
         }
         a.t = lo;
-        off -= wide * a.tiles.template before<KEYS>(lo);
-        int64_t base = a.tiles.template first<KEYS>(lo);
-        int64_t units = a.tiles.template last<KEYS>(lo) - base + 1 + kExtra;
+        off -= wide * a.tiles.before(lo);
+        int64_t base = a.tiles.first(lo);
+        int64_t units = a.tiles.last(lo) - base + 1 + kExtra;
         int index = (int)quotient(off, units);
         off -= index * units;
         Warp<H, INT8, PARTS, NT> w;
@@ -1140,7 +1215,7 @@ __global__ void __launch_bounds__(32 * kWarps,
             const int64_t n = min(units - off, end - at);
             a.head = index / cut.parts;
             a.part = index - a.head * cut.parts;
-            w.begin();
+            a.head *= cut.heads;
             tile_run<H, INT8, PARTS, NT>(
                 c, cut, dtype, a, base + max(off - kExtra, (int64_t)0),
                 base + max(off + n - kExtra, (int64_t)0), sh, w);
@@ -1168,92 +1243,148 @@ __global__ void __launch_bounds__(32 * kWarps,
                     do a.tiles = tiles_of(c, cut, ++a.s);
                     while (a.tiles.rows == 0);
                 }
-                base = a.tiles.template first<KEYS>(a.t);
-                units = a.tiles.template last<KEYS>(a.t) - base + 1 + kExtra;
+                base = a.tiles.first(a.t);
+                units = a.tiles.last(a.t) - base + 1 + kExtra;
             }
         }
     }
     // Not before: the next kernel's CTAs would take the place of this one's
-    // (64 sequences to 16384 keys with three CTAs per SM: 331 us).
+    // (64 sequences to 16384 keys with three CTAs per SM: 331 us for 251).
     grid_launch_dependents();
     if (tid == 0) share.records[blockIdx.x] = record;
 }
 
-// Joins the parts of a cut tile, in the order of the CTAs that left them: first
-// the parts' factors, a warp to a column and a lane to a part, then the sums,
-// four values to a thread and many parts in flight.
-constexpr int kJoin = 256;
+// Joins the parts of cut tiles, in the order of the CTAs that left them: a
+// column to a warp, four values to a lane, a part's factor in each lane first;
+// where there are few columns, the warps of a CTA share the parts of one.
+constexpr int kJoin = 256, kJoinWarps = kJoin / 32;
 template <int DIM, int C>
 __global__ void __launch_bounds__(kJoin)
     attention_join_kernel(const mt_attention_call_t c, const Cut cut,
                           const Share share, int dtype) {
-    extern __shared__ float factors[];  // C x CTAs
-    __shared__ float tops[C], totals[C];
-    grid_launch_dependents();
+    constexpr int kQuads = (DIM / 4 + 31) / 32;  // of a lane
+    __shared__ int16_t cuts[kAttentionMaxCtas];
+    __shared__ int counts[kJoinWarps];
+    __shared__ float tops[kJoinWarps], totals[kJoinWarps];
+    __shared__ float4 part_o[kJoinWarps][DIM / 4];
     grid_wait_prerequisites();
-    const Record r = share.records[blockIdx.x];
-    if (!r.valid) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = (int)gridDim.x;
+    // The cut tiles, by the CTA in which they begin.
+    int n = 0;
+    for (int b0 = 0; b0 < ctas; b0 += kJoin) {
+        const int b = b0 + tid;
+        const bool on = b < ctas && share.records[b].valid != 0;
+        const unsigned mask = __ballot_sync(kFull, on);
+        if (lane == 0) counts[warp] = __popc(mask);
+        __syncthreads();
+        int before = n;
+        for (int x = 0; x < kJoinWarps; ++x) {
+            if (x < warp) before += counts[x];
+            n += counts[x];
+        }
+        if (on)
+            cuts[before + __popc(mask & ((1u << lane) - 1u))] = (int16_t)b;
+        __syncthreads();
+    }
     constexpr int64_t kPlace = place_floats(C, DIM);
-    // part 0 is in this CTA's second place, the others in the first places of
-    // the CTAs after it
-    const float *begin = share.sums + (2 * (int64_t)blockIdx.x + 1) * kPlace;
-    const float *others = share.sums + 2 * kPlace * (int64_t)blockIdx.x;
-    const int parts = r.last - (int)blockIdx.x + 1;
-    const auto part = [&](int x) {
-        return x == 0 ? begin : others + 2 * kPlace * x;
-    };
-    const int lane = threadIdx.x & 31;
-    for (int col = threadIdx.x >> 5; col < C; col += kJoin / 32) {
+    const int columns = n * cut.heads * C;
+    const bool few = columns <= ctas;
+    const int share_of = few ? kJoinWarps : 1;
+    const int mine = few ? warp : 0;  // which of the parts
+    for (int p = few ? (int)blockIdx.x
+                     : (int)blockIdx.x * kJoinWarps + warp;
+         p < columns; p += ctas * (few ? 1 : kJoinWarps)) {
+        const int b = cuts[p / (cut.heads * C)];
+        const int hs = p / C % cut.heads, col = p % C;
+        const Record r = share.records[b];
+        const Place at =
+            place_of<C>(cut, r.row, r.rows, r.head + hs, r.part, col);
+        if (!at.used) continue;  // the same for all that share the column
+        const int parts = r.last - b + 1, i = hs * C + col;
+        // part 0 is in its CTA's second place, the others in the first places
+        // of the CTAs after it
+        const auto part = [&](int x) {
+            return share.sums + (2 * (int64_t)(b + x) + (x == 0 ? 1 : 0)) *
+                                    kPlace;
+        };
         float top = -INFINITY;
-        for (int x = lane; x < parts; x += 32)
-            top = nanmax(top, part(x)[col]);
+        for (int x = mine + share_of * lane; x < parts; x += share_of * 32)
+            top = nanmax(top, part(x)[i]);
         top = warp_nanmax(top);
         const float ref = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
-        for (int x = lane; x < parts; x += 32) {
-            const float f = pow2(part(x)[col] - ref);
-            factors[col * gridDim.x + x] = f;
-            sum = fmaf(part(x)[C + col], f, sum);
+        float4 o[kQuads] = {};
+        for (int x0 = mine; x0 < parts; x0 += share_of * 32) {
+            const int x = x0 + share_of * lane;
+            const bool on = x < parts;
+            const float f = on ? pow2(part(x)[i] - ref) : 0.f;
+            if (on) sum = fmaf(part(x)[kWarps * C + i], f, sum);
+            const int many = min(32, (parts - x0 + share_of - 1) / share_of);
+#pragma unroll 8
+            for (int y = 0; y < many; ++y) {
+                const float g = __shfl_sync(kFull, f, y);
+                const float *from = part(x0 + share_of * y) + 2 * kWarps * C +
+                                    i * DIM;
+#pragma unroll
+                for (int k = 0; k < kQuads; ++k) {
+                    const int at4 = lane + 32 * k;
+                    if (at4 >= DIM / 4) continue;
+                    const float4 v =
+                        *reinterpret_cast<const float4 *>(from + 4 * at4);
+                    o[k].x = fmaf(v.x, g, o[k].x);
+                    o[k].y = fmaf(v.y, g, o[k].y);
+                    o[k].z = fmaf(v.z, g, o[k].z);
+                    o[k].w = fmaf(v.w, g, o[k].w);
+                }
+            }
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             sum += __shfl_xor_sync(kFull, sum, off);
-        if (lane == 0) {
-            tops[col] = top;
-            totals[col] = sum;
-        }
-    }
-    __syncthreads();
-    for (int i = 4 * threadIdx.x; i < C * DIM; i += 4 * kJoin) {
-        const int col = i / DIM, d = i % DIM;
-        const Place at = place_of<C>(cut, r.row, r.rows, r.head, r.part, col);
-        if (!at.used) continue;
-        const float *f = factors + col * gridDim.x;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        const auto add = [&](const float *p, float f) {
-            const float2 v = reinterpret_cast<const float2 *>(p)[0];
-            const float2 w = reinterpret_cast<const float2 *>(p)[1];
-            o[0] = fmaf(v.x, f, o[0]);
-            o[1] = fmaf(v.y, f, o[1]);
-            o[2] = fmaf(w.x, f, o[2]);
-            o[3] = fmaf(w.y, f, o[3]);
-        };
-        add(begin + 2 * C + i, f[0]);
-#pragma unroll 8
-        for (int x = 1; x < parts; ++x)
-            add(others + 2 * kPlace * x + 2 * C + i, f[x]);
-        const float top = tops[col], sum = totals[col];
-        const int64_t to = (int64_t)at.row * c.out_row +
-                           (int64_t)at.head * c.out_head + d;
+        if (few) {
+            if (lane == 0) {
+                tops[warp] = top;
+                totals[warp] = sum;
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            store_as(dtype, c.out, to + e,
-                     top == -INFINITY ? 0.f : o[e] / sum);
-        if (c.lse != nullptr && d == 0)
-            c.lse[(int64_t)at.row * c.q_heads + at.head] =
-                top == -INFINITY ? top
-                                 : (top + log2f(sum)) * 0.6931471805599453f;
+            for (int k = 0; k < kQuads; ++k)
+                if (lane + 32 * k < DIM / 4) part_o[warp][lane + 32 * k] = o[k];
+            __syncthreads();
+            if (warp == 0) {
+                for (int x = 0; x < kJoinWarps; ++x)
+                    top = nanmax(top, tops[x]);
+                const float about = top == -INFINITY ? 0.f : top;
+                sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < kQuads; ++k)
+                    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = 0; x < kJoinWarps; ++x) {
+                    const float g = pow2(tops[x] - about);
+                    sum = fmaf(totals[x], g, sum);
+#pragma unroll
+                    for (int k = 0; k < kQuads; ++k) {
+                        if (lane + 32 * k >= DIM / 4) continue;
+                        const float4 v = part_o[x][lane + 32 * k];
+                        o[k].x = fmaf(v.x, g, o[k].x);
+                        o[k].y = fmaf(v.y, g, o[k].y);
+                        o[k].z = fmaf(v.z, g, o[k].z);
+                        o[k].w = fmaf(v.w, g, o[k].w);
+                    }
+                }
+            }
+        }
+        if (!few || warp == 0) {
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) {
+                const int at4 = lane + 32 * k;
+                if (at4 < DIM / 4)
+                    finish(c, cut, dtype, at, 4 * at4, top, sum, &o[k].x);
+            }
+        }
+        if (few) __syncthreads();  // the next column's
     }
+    grid_launch_dependents();
 }
 
 template <class H, bool INT8, int PARTS, int NT>
@@ -1265,22 +1396,25 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
     constexpr size_t kBytes = sizeof(Sh);
     static_assert((kBytes + 1024) * kCtas <= 228 * 1024,
                   "the CTAs that share an SM fit its shared memory");
-    const Cut cut = {p.times, p.per, p.parts};
+    const int warps = kWarps / p.heads;
+    const Cut cut = {p.times, p.per, p.parts, p.heads,
+                     (H::KEYS == 32 ? 5 : 4) + (warps == 4   ? 2
+                                                : warps == 2 ? 1 : 0),
+                     c.k_heads / p.heads * p.parts, p.whole};
     Share share;
     share.sums = static_cast<float *>(workspace);
     share.records = reinterpret_cast<Record *>(
         share.sums + 2 * (int64_t)p.ctas * place_floats(8 * NT, H::DIM));
     cudaError_t e = cudaSuccess;
     const auto kernel = attention_mma_kernel<H, INT8, PARTS, NT>;
-    if (kBytes > 48 * 1024)
+    if (kBytes > 40 * 1024)
         e = allow_max_smem(reinterpret_cast<const void *>(kernel));
     if (e == cudaSuccess)
         e = launch_dependent(kernel, p.ctas, 32 * kWarps, kBytes, s, c, cut,
                              share, dtype);
     if (e != cudaSuccess) return e;
     return launch_dependent(attention_join_kernel<H::DIM, 8 * NT>, p.ctas,
-                            kJoin, (size_t)p.ctas * 8 * NT * sizeof(float), s,
-                            c, cut, share, dtype);
+                            kJoin, 0, s, c, cut, share, dtype);
 }
 
 template <bool INT8, int PARTS, int NT>

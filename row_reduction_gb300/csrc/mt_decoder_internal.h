@@ -122,8 +122,11 @@ struct AttentionPlan {
     int32_t times;  // query heads per key head
     int32_t per;    // rows of a tile
     int32_t parts;  // tiles that share a row's query heads
+    int32_t heads;  // key heads that a CTA works at once
+    int32_t whole;  // out takes four values at a time
     int32_t ctas;
 };
+constexpr int kAttentionMaxCtas = 1024;
 // CTAs of the matrix kernels that share an SM: three as far as registers (two
 // column tiles or wide heads take more than 168) and shared memory go.
 constexpr int attention_ctas(int dim, int groups, int parts, int nt) {

@@ -81,14 +81,22 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     const int columns = 8 * p->nt;
     p->per = p->times < columns ? columns / p->times : 1;
     p->parts = (p->times + columns - 1) / columns;
+    p->heads = c.k_heads % 4 == 0 ? 4 : c.k_heads % 2 == 0 ? 2 : 1;
+    const int es = dtype_size(dtype);
+    const uint64_t places =
+        (uint64_t)(reinterpret_cast<uintptr_t>(c.out) / es) |
+        (c.rows > 1 ? (uint64_t)c.out_row : 0) |
+        (c.q_heads > 1 ? (uint64_t)c.out_head : 0);
+    p->whole = (places & 3) == 0;
     // as many as are resident at once
     p->ctas = sms * attention_ctas(c.dim, c.dim / c.group,
                                    dtype == DT_BF16 ? 1 : 2, p->nt);
+    if (p->ctas > kAttentionMaxCtas) p->ctas = kAttentionMaxCtas;
     return MT_OK;
 }
 size_t attention_workspace(const mt_attention_call_t &c,
                            const AttentionPlan &p) {
-    return (size_t)p.ctas * (2 * 8 * (size_t)p.nt * (c.dim + 2) *
+    return (size_t)p.ctas * (2 * 4 * 8 * (size_t)p.nt * (c.dim + 2) *
                              sizeof(float) + kAttentionRecord);
 }
 
