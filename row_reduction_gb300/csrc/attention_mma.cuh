@@ -57,22 +57,23 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
         return (int64_t)((unsigned)a / (unsigned)b);
     return a / b;
 }
-// sum over 0 <= t < n of floor((a t + b) / m), for a, b >= 0: whole parts
-// aside, the points under a line, counted along the other axis in turn.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a,
+// sum over 0 <= t < n of floor((a t + b) / 2^log2), for a, b >= 0: whole parts
+// aside, the points under a line, counted along the other axis in turn (slopes
+// below 2^log2 from there on).
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int log2, int64_t a,
                                              int64_t b) {
-    int64_t s = 0;
-    while (n > 0) {
-        s += (n - 1) * n / 2 * quotient(a, m) + n * quotient(b, m);
-        a -= quotient(a, m) * m;
-        b -= quotient(b, m) * m;
-        const int64_t y = a * n + b;
-        if (y < m) break;
+    const int64_t low = (1LL << log2) - 1;
+    int64_t s = (n - 1) * n / 2 * (a >> log2) + n * (b >> log2);
+    int m = 1 << log2, slope = (int)(a & low), at = (int)(b & low);
+    for (int64_t y = slope * n + at; y >= m; y = slope * n + at) {
         n = quotient(y, m);
-        b = y - n * m;
-        const int64_t x = m;
-        m = a;
-        a = x;
+        at = (int)(y - n * m);
+        const int x = m / slope;
+        s += (n - 1) * n / 2 * x + n * (at / slope);
+        const int rest = m - x * slope;
+        at %= slope;
+        m = slope;
+        slope = rest;
     }
     return s;
 }
@@ -89,7 +90,7 @@ struct Cut {
     int32_t heads;   // key heads of a CTA: 4, 2 or 1
     int32_t log2;    // keys of a unit
     int32_t wide;    // tiles of the same rows: groups of key heads, parts
-    int32_t whole;   // out takes 4 values at a time
+    int32_t whole;   // bits: q, out take 4 values at a time
 };
 
 // How the rows of a sequence are cut into tiles and units.
@@ -122,7 +123,7 @@ struct Tiles {
         } else {
             // all tiles but the sequence's last are whole
             const int whole = t < count ? t : count - 1;
-            s += floor_sum(whole, 1LL << log2, per, start + per - 1);
+            s += floor_sum(whole, log2, per, start + per - 1);
             if (t > whole) s += last(count - 1);
         }
         if (window != 0) {
@@ -130,7 +131,7 @@ struct Tiles {
             const int64_t short_of = window - 1 - start;
             const int64_t z = short_of <= 0 ? 0 : (short_of + per - 1) / per;
             if (t > z)
-                s -= floor_sum(t - z, 1LL << log2, per,
+                s -= floor_sum(t - z, log2, per,
                                start + z * per - window + 1);
         }
         return s;
@@ -153,12 +154,13 @@ __device__ __forceinline__ Tiles tiles_of(const mt_attention_call_t &c,
 
 // A cut tile that begins in a CTA's run: where its parts lie and what it is.
 struct Record {
-    int32_t valid, last;      // last: the CTA that holds its end
+    int32_t last;             // the CTA that holds its end
     int32_t row, rows;        // rows of the batch
     int32_t head, part;       // first key head; part of the row's query heads
 };
 struct Share {
-    Record *records;          // one per CTA
+    Record *records;          // one per CTA, where it has a cut tile
+    int32_t *cut;             // one per CTA: whether it has
     float *sums;              // two places per CTA: m, l, O of each column of
                               // each of its key heads
 };
@@ -809,17 +811,38 @@ __device__ __forceinline__ int columns_of(const Cut &cut, int rows, int part) {
 }
 
 // A warp's part of the queries of a tile: the columns of its key head that are
-// its own among the warps of that head; a lane has every 32nd value.
+// its own among the warps of that head, four values to a lane (one access each
+// where they can: the CTAs of a sequence all ask for the same few lines).
 template <class H, int PARTS, int NT>
 struct Queries {
-    static constexpr int C = 8 * NT, kEach = (H::DIM + 31) / 32;
-    float x[C][kEach];
+    static constexpr int C = 8 * NT, kEach = (H::DIM / 4 + 31) / 32;
+    static constexpr int kWords = PARTS == 1 ? 2 : 4;
+    unsigned x[C][kEach][kWords];
+    template <typename T>
+    static __device__ __forceinline__ void four(const void *q, int64_t at,
+                                                bool whole, unsigned *w) {
+        const T *p = static_cast<const T *>(q) + at;
+        Raw<T, 4> r;
+        if (whole) {
+            r.load(p);
+        } else {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = to_f(p[e]);
+#pragma unroll
+            for (int i = 0; i < r.kWords; ++i)
+                r.w[i] = Pack<T>::pack(v + i * Pack<T>::kPerWord);
+        }
+#pragma unroll
+        for (int i = 0; i < r.kWords; ++i) w[i] = r.w[i];
+    }
     __device__ __forceinline__ void load(const mt_attention_call_t &c,
                                          const Cut &cut, int dtype,
                                          const Tile &a, int hs, int ks,
                                          int warps) {
         const int from = c.offsets[a.s] + a.t * cut.per;
         const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
+        const bool whole = cut.whole & 1;
 #pragma unroll
         for (int col = 0; col < C; ++col) {
             const Place at =
@@ -829,51 +852,87 @@ struct Queries {
                 (int64_t)at.row * c.q_row + (int64_t)at.head * c.q_head;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const int d = (threadIdx.x & 31) + 32 * i;
-                x[col][i] = on && d < H::DIM
-                                ? load_as(PARTS == 1 ? (int)DT_BF16 : dtype,
-                                          c.q, q + d)
-                                : 0.f;
+                const int d = 4 * ((threadIdx.x & 31) + 32 * i);
+#pragma unroll
+                for (int e = 0; e < kWords; ++e) x[col][i][e] = 0;
+                if (!on || d >= H::DIM) continue;
+                if constexpr (PARTS == 1)
+                    four<__nv_bfloat16>(c.q, q + d, whole, x[col][i]);
+                else if (dtype == DT_F16)
+                    four<__half>(c.q, q + d, whole, x[col][i]);
+                else
+                    four<float>(c.q, q + d, whole, x[col][i]);
             }
         }
     }
-    // Fragments, and the columns' factors, into shared memory.
+    __device__ __forceinline__ void widen(const unsigned *w, int dtype,
+                                          float *v) const {
+        if constexpr (PARTS == 1) {
+            Pack<__nv_bfloat16>::unpack(w[0], v);
+            Pack<__nv_bfloat16>::unpack(w[1], v + 2);
+        } else if (dtype == DT_F16) {
+            Pack<__half>::unpack(w[0], v);
+            Pack<__half>::unpack(w[1], v + 2);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+        }
+    }
+    // Fragments, and the columns' factors, into shared memory; columns from
+    // `columns` on stand for nothing.
     __device__ __forceinline__ void put(const mt_attention_call_t &c,
-                                        Shared<H, PARTS, NT> &sh, int hs,
-                                        int ks, int warps) {
+                                        Shared<H, PARTS, NT> &sh, int dtype,
+                                        int columns, int hs, int ks,
+                                        int warps) {
         const int lane = threadIdx.x & 31;
-        int place[kEach];  // of the lane's values in a column's fragments
+        int place[kEach];  // of the lane's fours in a column's fragments
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int d = min(lane + 32 * i, H::DIM - 1), r = d % H::GROUP;
+            const int d = min(4 * (lane + 32 * i), H::DIM - 4);
+            const int r = d % H::GROUP;
             const Block block = H::block(r / 16);
             const int in = r - block.base, wide = block.size / 4;
             const int step = d / H::GROUP * H::PER + block.base / 16 +
                              in % wide / 4;
-            place[i] = (step * 32 + in / wide) * 4 + r % 4;
+            place[i] = step * 32 + in / wide;
         }
 #pragma unroll
         for (int col = 0; col < C; ++col) {
             if ((col & (warps - 1)) != ks) continue;
+            float v[kEach][4];
             float largest = 0.f;
+            if (col < columns) {
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                largest = nanmax(largest, fabsf(x[col][i]));
-            largest = warp_nanmax(largest);
+                for (int i = 0; i < kEach; ++i) {
+                    widen(x[col][i], dtype, v[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        largest = nanmax(largest, fabsf(v[i][e]));
+                }
+                largest = warp_nanmax(largest);
+            }
             const unsigned e = max(__float_as_uint(largest) >> 23, 15u);
             const bool bad = !(largest < INFINITY);
-            const float up = bad ? 0.f : __uint_as_float((268u - e) << 23);
-            __half *halves = reinterpret_cast<__half *>(
-                                 &sh.q[hs][col / 8][0][0][0]) + col % 8 * 16;
+            const bool none = bad || col >= columns;
+            const float up = __uint_as_float((268u - e) << 23);
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                if (lane + 32 * i >= H::DIM) continue;
-                const float v = bad ? 0.f : x[col][i] * up;
-                const __half hi = __float2half_rn(v);
-                halves[place[i]] = hi;
+                if (4 * (lane + 32 * i) >= H::DIM) continue;
+                uint2 hi = make_uint2(0, 0), lo = hi;
+                if (!none) {
+                    const float a = v[i][0] * up, b = v[i][1] * up;
+                    const float c_ = v[i][2] * up, d = v[i][3] * up;
+                    hi = make_uint2(half_pair(a, b), half_pair(c_, d));
+                    if constexpr (PARTS == 2) {
+                        const float2 p = from_half_pair(hi.x);
+                        const float2 q = from_half_pair(hi.y);
+                        lo = make_uint2(half_pair(a - p.x, b - p.y),
+                                        half_pair(c_ - q.x, d - q.y));
+                    }
+                }
+                sh.q[hs][col / 8][0][0][place[i] + col % 8 * 4] = hi;
                 if constexpr (PARTS == 2)
-                    halves[H::STEPS * 128 + place[i]] =
-                        __float2half_rn(v - __half2float(hi));
+                    sh.q[hs][col / 8][1][0][place[i] + col % 8 * 4] = lo;
             }
             if (lane == 0)
                 sh.f[hs][col] =
@@ -991,7 +1050,10 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
     int slot = slot_in(c, first), stage = 0;
     if (u < end) w.load(m, slot, codes[0], scales[0]);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    queries.put(c, sh, hs, ks, warps);
+    queries.put(c, sh, dtype,
+                columns_of<8 * NT>(
+                    cut, min(cut.per, a.tiles.rows - a.t * cut.per), a.part),
+                hs, ks, warps);
     __syncthreads();
     w.begin();
 #pragma unroll 1
@@ -1040,7 +1102,7 @@ __device__ __forceinline__ void finish(const mt_attention_call_t &c,
                                        float sum, float *o) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = top == -INFINITY ? 0.f : o[e] / sum;
-    store4(dtype, cut.whole != 0, c.out,
+    store4(dtype, (cut.whole & 2) != 0, c.out,
            (int64_t)at.row * c.out_row + (int64_t)at.head * c.out_head + d, o);
     if (c.lse != nullptr && d == 0)
         c.lse[(int64_t)at.row * c.q_heads + at.head] =
@@ -1143,7 +1205,7 @@ __global__ void __launch_bounds__(32 * kWarps,
         *reinterpret_cast<Shared<H, PARTS, NT> *>(shared);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_wait_prerequisites();
-    Record record = {};
+    int cut_here = 0;
     // Units of the sequences of this thread, and where they begin.
     const int each = (c.sequences + T - 1) / T;
     const int s0 = min(tid * each, c.sequences);
@@ -1196,16 +1258,22 @@ __global__ void __launch_bounds__(32 * kWarps,
         // before(lo) <= off < before(hi): every thread looks at one place of
         // the range, until it has one tile.
         int lo = 0, hi = a.tiles.count;
+        int64_t units_before = 0;
         while (hi - lo > 1) {
             const int step = (hi - lo + T - 1) / T;
             const int mid = min(lo + (tid + 1) * step, hi);
-            const int fewer = __syncthreads_count(
-                mid < hi && wide * a.tiles.before(mid) <= off);
+            const int64_t here = mid < hi ? wide * a.tiles.before(mid) : 0;
+            const int fewer = __syncthreads_count(mid < hi && here <= off);
+            if (fewer > 0) {
+                if (tid == fewer - 1) sh.at = here;
+                __syncthreads();
+                units_before = sh.at;
+            }
             lo += fewer * step;
             hi = min(lo + step, hi);
         }
         a.t = lo;
-        off -= wide * a.tiles.before(lo);
+        off -= units_before;
         int64_t base = a.tiles.first(lo);
         int64_t units = a.tiles.last(lo) - base + 1 + kExtra;
         int index = (int)quotient(off, units);
@@ -1222,12 +1290,13 @@ __global__ void __launch_bounds__(32 * kWarps,
             const bool whole = n == units;
             if (!whole && off == 0) {
                 const int64_t x = at + units;
-                record.valid = 1;
-                record.last = (int)quotient(x * ctas - 1, total);
-                record.row = c.offsets[a.s] + a.t * cut.per;
-                record.rows = min(cut.per, a.tiles.rows - a.t * cut.per);
-                record.head = a.head;
-                record.part = a.part;
+                cut_here = 1;
+                if (tid == 0)
+                    share.records[blockIdx.x] = {
+                        (int)quotient(x * ctas - 1, total),
+                        c.offsets[a.s] + a.t * cut.per,
+                        min(cut.per, a.tiles.rows - a.t * cut.per), a.head,
+                        a.part};
             }
             tile_end<H, INT8, PARTS, NT>(
                 c, cut, dtype, a, whole,
@@ -1251,7 +1320,7 @@ __global__ void __launch_bounds__(32 * kWarps,
     // Not before: the next kernel's CTAs would take the place of this one's
     // (64 sequences to 16384 keys with three CTAs per SM: 331 us for 251).
     grid_launch_dependents();
-    if (tid == 0) share.records[blockIdx.x] = record;
+    if (tid == 0) share.cut[blockIdx.x] = cut_here;
 }
 
 // Joins the parts of cut tiles, in the order of the CTAs that left them: a
@@ -1274,7 +1343,7 @@ __global__ void __launch_bounds__(kJoin)
     int n = 0;
     for (int b0 = 0; b0 < ctas; b0 += kJoin) {
         const int b = b0 + tid;
-        const bool on = b < ctas && share.records[b].valid != 0;
+        const bool on = b < ctas && share.cut[b] != 0;
         const unsigned mask = __ballot_sync(kFull, on);
         if (lane == 0) counts[warp] = __popc(mask);
         __syncthreads();
@@ -1405,6 +1474,8 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
     share.sums = static_cast<float *>(workspace);
     share.records = reinterpret_cast<Record *>(
         share.sums + 2 * (int64_t)p.ctas * place_floats(8 * NT, H::DIM));
+    share.cut = reinterpret_cast<int32_t *>(share.records + p.ctas);
+    static_assert(sizeof(Record) + sizeof(int32_t) == kAttentionRecord, "");
     cudaError_t e = cudaSuccess;
     const auto kernel = attention_mma_kernel<H, INT8, PARTS, NT>;
     if (kBytes > 40 * 1024)

@@ -123,7 +123,7 @@ struct AttentionPlan {
     int32_t per;    // rows of a tile
     int32_t parts;  // tiles that share a row's query heads
     int32_t heads;  // key heads that a CTA works at once
-    int32_t whole;  // out takes four values at a time
+    int32_t whole;  // bits: q, out take four values at a time
     int32_t ctas;
 };
 constexpr int kAttentionMaxCtas = 1024;
@@ -132,7 +132,7 @@ constexpr int kAttentionMaxCtas = 1024;
 constexpr int attention_ctas(int dim, int groups, int parts, int nt) {
     return nt > 1 || dim >= 128 ? 2 : 3;
 }
-// Bytes behind the partial sums, one record per CTA.
+// Bytes behind the partial sums for each CTA: what it left there.
 constexpr int kAttentionRecord = 24;
 #define MT_DECLARE_ATTENTION(name)                                           \
     cudaError_t name(const AttentionPlan &p, const mt_attention_call_t &c,   \

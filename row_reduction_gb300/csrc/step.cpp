@@ -83,11 +83,15 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     p->parts = (p->times + columns - 1) / columns;
     p->heads = c.k_heads % 4 == 0 ? 4 : c.k_heads % 2 == 0 ? 2 : 1;
     const int es = dtype_size(dtype);
-    const uint64_t places =
-        (uint64_t)(reinterpret_cast<uintptr_t>(c.out) / es) |
-        (c.rows > 1 ? (uint64_t)c.out_row : 0) |
-        (c.q_heads > 1 ? (uint64_t)c.out_head : 0);
-    p->whole = (places & 3) == 0;
+    const auto fours = [&](const void *q, int64_t row, int64_t head) {
+        const uint64_t bits =
+            (uint64_t)(reinterpret_cast<uintptr_t>(q) / es) |
+            (c.rows > 1 ? (uint64_t)row : 0) |
+            (c.q_heads > 1 ? (uint64_t)head : 0);
+        return (bits & 3) == 0;
+    };
+    p->whole = (fours(c.q, c.q_row, c.q_head) ? 1 : 0) |
+               (fours(c.out, c.out_row, c.out_head) ? 2 : 0);
     // as many as are resident at once
     p->ctas = sms * attention_ctas(c.dim, c.dim / c.group,
                                    dtype == DT_BF16 ? 1 : 2, p->nt);
