@@ -1339,33 +1339,52 @@ __global__ void __launch_bounds__(kJoin)
     grid_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)gridDim.x;
-    // The cut tiles, by the CTA in which they begin.
+    // The cut tiles, by the CTA in which they begin: a warp looks at a run of
+    // them, four for each lane at a time.
+    constexpr int kLooks = 4;
     int n = 0;
-    for (int b0 = 0; b0 < ctas; b0 += kJoin) {
-        const int b = b0 + tid;
-        const bool on = b < ctas && share.cut[b] != 0;
-        const unsigned mask = __ballot_sync(kFull, on);
-        if (lane == 0) counts[warp] = __popc(mask);
+    for (int b0 = 0; b0 < ctas; b0 += kLooks * kJoin) {
+        bool on[kLooks];
+        unsigned mask[kLooks];
+        int found = 0;
+#pragma unroll
+        for (int y = 0; y < kLooks; ++y) {
+            const int b = b0 + (warp * kLooks + y) * 32 + lane;
+            on[y] = b < ctas && share.cut[b] != 0;
+        }
+#pragma unroll
+        for (int y = 0; y < kLooks; ++y) {
+            mask[y] = __ballot_sync(kFull, on[y]);
+            found += __popc(mask[y]);
+        }
+        if (lane == 0) counts[warp] = found;
         __syncthreads();
         int before = n;
         for (int x = 0; x < kJoinWarps; ++x) {
             if (x < warp) before += counts[x];
             n += counts[x];
         }
-        if (on)
-            cuts[before + __popc(mask & ((1u << lane) - 1u))] = (int16_t)b;
+#pragma unroll
+        for (int y = 0; y < kLooks; ++y) {
+            if (on[y])
+                cuts[before + __popc(mask[y] & ((1u << lane) - 1u))] =
+                    (int16_t)(b0 + (warp * kLooks + y) * 32 + lane);
+            before += __popc(mask[y]);
+        }
         __syncthreads();
     }
+    // columns that a tile has at most
+    const int most = cut.times <= C ? cut.per * cut.times : C;
     constexpr int64_t kPlace = place_floats(C, DIM);
-    const int columns = n * cut.heads * C;
+    const int columns = n * cut.heads * most;
     const bool few = columns <= ctas;
     const int share_of = few ? kJoinWarps : 1;
     const int mine = few ? warp : 0;  // which of the parts
     for (int p = few ? (int)blockIdx.x
                      : (int)blockIdx.x * kJoinWarps + warp;
          p < columns; p += ctas * (few ? 1 : kJoinWarps)) {
-        const int b = cuts[p / (cut.heads * C)];
-        const int hs = p / C % cut.heads, col = p % C;
+        const int tile = p / (cut.heads * most), in = p - tile * cut.heads * most;
+        const int b = cuts[tile], hs = in / most, col = in - hs * most;
         const Record r = share.records[b];
         const Place at =
             place_of<C>(cut, r.row, r.rows, r.head + hs, r.part, col);
