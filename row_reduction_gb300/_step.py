@@ -16,7 +16,7 @@ from collections import namedtuple
 from . import _decoder as _d
 from ._binding import _check
 from ._decoder import (_F, _I32, _I64, _P, _cache, _dense, _first, _heads,
-                       _here, _new_like, _On, _opt, _rows, _tensor, _three)
+                       _here, _On, _opt, _rows, _tensor, _three)
 
 MT_NORM_AFTER, MT_NORM_BEFORE = 1, 2
 
@@ -192,6 +192,14 @@ def _on(index, stream, run):
     return run(handle)
 
 
+def _length(t, name, dtype):
+    """Values of a vector (the rest is checked with its address)."""
+    sh = getattr(t, "shape", None)
+    if sh is None or len(sh) != 1 or not t.is_cuda:
+        _tensor(t, name, dtype, (None,))
+    return sh[0]
+
+
 def _table(table, sequences, index):
     """(address, row stride, width) of a page table."""
     try:
@@ -235,35 +243,40 @@ def cache_extend(table, lengths, counts, free_pages, free_count, page_size,
         _d._setup()
     torch = _d._torch
     i32, i64 = torch.int32, torch.int64
-    _tensor(lengths, "lengths", i32, (None,))
-    n, index = lengths.shape[0], lengths.get_device()
+    n = _length(lengths, "lengths", i32)
+    index = lengths.get_device()
     at, stride, pages = _table(table, n, index)
     lens = _dense(lengths, "lengths", i32, (n,), index)
     more = _dense(counts, "counts", i32, (n,), index)
-    _tensor(free_pages, "free_pages", i32, (None,), index)
-    size = free_pages.shape[0]
+    size = _length(free_pages, "free_pages", i32)
     free = _dense(free_pages, "free_pages", i32, (size,), index)
     left = _dense(free_count, "free_count", i32, (1,), index)
 
     def run(handle):
         if out is None:
+            # one block for the int32 ones: addresses by their places in it
             flat = torch.empty(rows + 2 * n + 2, dtype=i32,
                                device=lengths.device)
             place, offsets, lengths_, count = flat.split_with_sizes(
                 (rows, n + 1, n, 1))
-            step = CacheStep(
-                offsets, torch.empty(rows, dtype=i64, device=flat.device),
-                place, lengths_, count)
+            slots = torch.empty(rows, dtype=i64, device=flat.device)
+            step = CacheStep(offsets, slots, place, lengths_, count)
+            p = flat.data_ptr()
+            q = p + 4 * rows
+            places = (q, slots.data_ptr(), p, q + 4 * (n + 1),
+                      q + 4 * (2 * n + 1))
         else:
             step = CacheStep(*out)
-        _call("mt_cache_extend", _EXTEND.pack(
-            at, stride, lens, more, free, left,
-            _dense(step.offsets, "offsets", i32, (n + 1,), index),
-            _dense(step.slots, "slots", i64, (rows,), index),
-            _dense(step.positions, "positions", i32, (rows,), index),
-            _dense(step.lengths, "new lengths", i32, (n,), index),
-            _dense(step.free_count, "new free_count", i32, (1,), index),
-            rows, pages, n, size, page_size), handle)
+            places = (_dense(step.offsets, "offsets", i32, (n + 1,), index),
+                      _dense(step.slots, "slots", i64, (rows,), index),
+                      _dense(step.positions, "positions", i32, (rows,),
+                             index),
+                      _dense(step.lengths, "new lengths", i32, (n,), index),
+                      _dense(step.free_count, "new free_count", i32, (1,),
+                             index))
+        _call("mt_cache_extend",
+              _EXTEND.pack(at, stride, lens, more, free, left, *places, rows,
+                           pages, n, size, page_size), handle)
         return step
     return _on(index, stream, run)
 
@@ -308,8 +321,7 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
         raise ValueError(f"{q_heads} query heads are no multiple of the "
                          f"cache's {heads}")
     i32 = torch.int32
-    _tensor(starts, "starts", i32, (None,), index)
-    n = starts.shape[0]
+    n = _length(starts, "starts", i32)
     at, stride, pages = _table(table, n, index)
     offs = _dense(offsets, "offsets", i32, (n + 1,), index)
     from_ = _dense(starts, "starts", i32, (n,), index)
@@ -324,10 +336,12 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
         scale = dim ** -0.5
 
     def run(handle):
-        y = out
-        if y is None:
+        if out is None:
             y = torch.zeros(shape, dtype=dtype, device=q.device)
-        o, orow, oh = _heads(y, "out", dtype, shape, index)
+            o, orow, oh = y.data_ptr(), q_heads * dim, dim
+        else:
+            y = out
+            o, orow, oh = _heads(y, "out", dtype, shape, index)
         lse = torch.full((rows, q_heads), -torch.inf, device=q.device) \
             if return_lse else None
         call = _ATTENTION.pack(
@@ -392,8 +406,10 @@ def block_norm(x, residual, weight=None, gate=None, next_weight=None,
     (ones).  Returns (y, h), with norms "after" h alone.  out and h_out: where
     to write y and h; either may be x or residual."""
     dt, index = _first(x, "x")
-    _tensor(x, "x", shape=(None, None))
+    torch = _d._torch
     dtype, shape = x.dtype, x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [rows, cols], got {tuple(shape)}")
     kind = _kind(norms, weight, next_weight)
     px, xs = _matrix(x, "x", dtype, shape, index)
     pr, rs = _matrix(residual, "residual", dtype, shape, index)
@@ -407,13 +423,16 @@ def block_norm(x, residual, weight=None, gate=None, next_weight=None,
 
     def run(handle):
         h, y = h_out, out
-        if h is None:
-            h = _new_like(x, shape, xs, 1)
-        ph, hs = _matrix(h, "h_out", dtype, shape, index)
         py = ys = 0
-        if before:
-            if y is None:
-                y = _new_like(x, shape, xs, 1)
+        if h is None:
+            h = torch.empty(shape, dtype=dtype, device=x.device)
+            ph, hs = h.data_ptr(), shape[1]
+        else:
+            ph, hs = _matrix(h, "h_out", dtype, shape, index)
+        if before and y is None:
+            y = torch.empty(shape, dtype=dtype, device=x.device)
+            py, ys = y.data_ptr(), shape[1]
+        elif before:
             py, ys = _matrix(y, "out", dtype, shape, index)
         _call("mt_block_norm", dt, _NORM.pack(
             px, pr, pg, pw, pn, ph, py, xs, rs, gs, hs, ys, shape[0],
@@ -448,9 +467,11 @@ def block_norm_backward(dy, dh, x, h, weight=None, gate=None,
         raise ValueError("x is needed")
     one = dy if before else dh
     dt, index = _first(one, "dy" if before else "dh")
-    _tensor(one, "dy" if before else "dh", shape=(None, None))
     torch = _d._torch
     dtype, shape, f32 = one.dtype, one.shape, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"gradients must be [rows, cols], got "
+                         f"{tuple(shape)}")
     pdy, dys = _matrix(dy, "dy", dtype, shape, index) if before else (0, 0)
     pdh, dhs = (0, 0) if dh is None else \
         _matrix(dh, "dh", dtype, shape, index)
@@ -462,21 +483,26 @@ def block_norm_backward(dy, dh, x, h, weight=None, gate=None,
 
     def run(handle):
         dx, dres = (None, None) if out is None else out
+        device, cols = one.device, shape[1]
         if dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=one.device)
+            dx = torch.empty(shape, dtype=dtype, device=device)
+            pdx, dxs = dx.data_ptr(), cols
+        else:
+            pdx, dxs = _matrix(dx, "out (dx)", dtype, shape, index)
         if dres is None:
-            dres = torch.empty(shape, dtype=dtype, device=one.device)
-        pdx, dxs = _matrix(dx, "out (dx)", dtype, shape, index)
-        pdr, drs = _matrix(dres, "out (dresidual)", dtype, shape, index)
+            dres = torch.empty(shape, dtype=dtype, device=device)
+            pdr, drs = dres.data_ptr(), cols
+        else:
+            pdr, drs = _matrix(dres, "out (dresidual)", dtype, shape, index)
         got, sums, pdg, dgs = [dx, dres], [0, 0, 0], 0, 0
         wide = gate is not None and gate.dim() == 2
         if wide:
-            dgate = torch.empty(shape, dtype=dtype, device=one.device)
-            pdg, dgs = dgate.data_ptr(), shape[1]
+            dgate = torch.empty(shape, dtype=dtype, device=device)
+            pdg, dgs = dgate.data_ptr(), cols
             got.append(dgate)
         for i, t in enumerate((None if wide else gate, weight, next_weight)):
             if t is not None:
-                d = torch.empty(shape[1], dtype=f32, device=one.device)
+                d = torch.empty(cols, dtype=f32, device=device)
                 sums[i] = d.data_ptr()
                 got.append(d)
         call = _NORM_BACK.pack(

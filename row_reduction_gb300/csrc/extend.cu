@@ -3,9 +3,16 @@
 //   n_s = ceil((lengths + counts) / page) - ceil(lengths / page),
 //   e_s = n_0 + .. + n_(s-1)
 //
-// One CTA adds up the sequences in order (two prefix sums: tokens and pages)
-// and gives out the pages; then a thread per row finds its sequence by halving
-// among the offsets.
+// Up to kOne sequences take one kernel: every CTA adds up all of them for
+// itself (two prefix sums, tokens and pages, kept in shared memory; the counts
+// come from L2) and then has its share of the new pages and of the rows, each
+// of which finds its sequence by halving.  A row in a new page takes it from the
+// list, as the CTA that writes the table does, so that no CTA waits for
+// another.  More sequences take two kernels: one CTA goes through them in order
+// and gives out the pages, then a thread per row.
+//
+// Bound: latency.  256 sequences of a token each 4 us, 1024 with 174k rows 7
+// (two kernels: 8 and 13).
 #include "mt_decoder.cuh"
 
 namespace mt {
@@ -135,10 +142,116 @@ __global__ void __launch_bounds__(kRowThreads)
     c.positions[r] = place;
 }
 
+// The last place of an ascending array (n + 1 values) whose value is at most
+// v < at[n].
+__device__ __forceinline__ int place_in(const int32_t *at, int n, int64_t v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= v) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+constexpr int kOne = 4096;          // sequences of the one kernel
+constexpr int kOneThreads = 256;
+__global__ void __launch_bounds__(kOneThreads)
+    extend_one_kernel(const mt_cache_extend_call_t c) {
+    extern __shared__ int32_t sums[];
+    int32_t *offsets = sums, *pages = sums + c.sequences + 1;
+    __shared__ int32_t most[kOneThreads / 32];
+    grid_launch_dependents();
+    grid_wait_prerequisites();
+    const int n = c.sequences, tid = threadIdx.x;
+    const int32_t held_free = min(max(*c.free_count, 0), c.free_size);
+    // A run of sequences per thread; the sums stop at the type's largest.
+    const int each = (n + kOneThreads - 1) / kOneThreads;
+    const int s0 = min(tid * each, n), s1 = min(s0 + each, n);
+    Pair mine = {0, 0};
+    for (int s = s0; s < s1; ++s) {
+        const Asked a = asked(c, s);
+        mine.tokens += a.count;
+        mine.pages += a.need;
+    }
+    Pair total;
+    Pair at = scan(mine, total);
+    int32_t used = 0;  // pages of the list that are given out
+    for (int s = s0; s < s1; ++s) {
+        const Asked a = asked(c, s);
+        const bool served =
+            a.fits && (a.need == 0 || at.pages + a.need <= held_free);
+        offsets[s] = (int32_t)min(at.tokens, kMost);
+        pages[s] = (int32_t)min(at.pages, kMost);
+        if (served && a.need > 0) used = (int32_t)(at.pages + a.need);
+        if (s % (int)gridDim.x == (int)blockIdx.x) {
+            c.offsets[s] = offsets[s];
+            c.new_lengths[s] = (int32_t)(a.length + (served ? a.count : 0));
+        }
+        at.tokens += a.count;
+        at.pages += a.need;
+    }
+    used = __reduce_max_sync(kFull, used);
+    if ((tid & 31) == 0) most[tid >> 5] = used;
+    if (tid == 0) {
+        offsets[n] = (int32_t)min(total.tokens, kMost);
+        pages[n] = (int32_t)min(total.pages, kMost);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kOneThreads / 32; ++x) used = max(used, most[x]);
+    if (tid == 0 && blockIdx.x == 0) {
+        c.offsets[n] = offsets[n];
+        *c.new_free_count = held_free - used;
+    }
+    const int64_t step = (int64_t)gridDim.x * kOneThreads;
+    const int64_t first = (int64_t)blockIdx.x * kOneThreads + tid;
+    for (int64_t i = first; i < used; i += step) {
+        const int s = place_in(pages, n, i);
+        c.table[s * c.table_stride + asked(c, s).held + (i - pages[s])] =
+            c.free_pages[held_free - 1 - i];
+    }
+    for (int64_t r = first; r < c.rows; r += step) {
+        int64_t slot = -1;
+        int32_t place = 0;
+        if (n > 0 && r < offsets[n]) {
+            const int s = place_in(offsets, n, r);
+            const Asked a = asked(c, s);
+            const int64_t p = a.length + (r - offsets[s]);
+            const int64_t page = p / c.page_size;
+            place = (int32_t)min(p, kMost);
+            if (a.fits && page < c.pages &&
+                (a.need == 0 || pages[s] + a.need <= held_free)) {
+                const int32_t id =
+                    page < a.held
+                        ? c.table[s * c.table_stride + page]
+                        : c.free_pages[held_free - 1 - pages[s] -
+                                       (page - a.held)];
+                if (id >= 0)
+                    slot = (int64_t)id * c.page_size + (p - page * c.page_size);
+            }
+        }
+        c.slots[r] = slot;
+        c.positions[r] = place;
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_cache_extend(const mt_cache_extend_call_t &c,
                                 cudaStream_t s) {
+    if (c.sequences <= kOne) {
+        int sms = 0;
+        const cudaError_t e = current_sm_count(&sms);
+        if (e != cudaSuccess) return e;
+        // a thread for each row, up to four CTAs on an SM
+        int64_t grid = (c.rows + kOneThreads - 1) / kOneThreads;
+        if (grid < c.sequences / 32) grid = c.sequences / 32;
+        if (grid > 4LL * sms) grid = 4LL * sms;
+        if (grid < 1) grid = 1;
+        return launch_dependent(extend_one_kernel, grid, kOneThreads,
+                                (size_t)2 * (c.sequences + 1) *
+                                    sizeof(int32_t), s, c);
+    }
     cudaError_t e = launch_dependent(extend_kernel, 1, kScan, 0, s, c);
     if (e == cudaSuccess && c.rows > 0)
         e = launch_dependent(extend_rows_kernel,
