@@ -574,6 +574,240 @@ __global__ void __launch_bounds__(512)
     }
 }
 
+// The same for rows of whole 16-byte packs, with the rows on their way in shared
+// memory: each thread copies and reads its own packs (no barrier), two rows
+// ahead.  Its columns' weights stay widened, arithmetic goes in pairs, and a
+// gate of one row and the weight have one sum between them, A = sum of g x r1:
+// dgate = weight A, dweight = gate A.  Packs past the row's end are zeros, which
+// add nothing; only what is stored is guarded.
+//
+// Bound by instructions: some 25 for a value.  BF16 8192 x 4096 with one gate
+// and both weights 68 us, where the kernel that widened everything for each row
+// took 135.
+__device__ __forceinline__ void copy_pack(void *to, const void *from,
+                                          bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_addr(to)),
+                 "l"(from), "r"(on ? 16 : 0)
+                 : "memory");
+}
+constexpr int kAheadRows = 2;
+enum { GATE_NONE, GATE_ROW, GATE_MATRIX };
+// Threads of a CTA: 256, two CTAs to an SM, where a row needs no more.
+template <typename T, int K, int THREADS, int NORMS, int GATE>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+    norm_back_ahead_kernel(const mt_block_norm_back_t c, const Lay lay,
+                           float *partial) {
+    constexpr int V = 16 / (int)sizeof(T);
+    constexpr bool after = NORMS & MT_NORM_AFTER;
+    constexpr bool before = NORMS & MT_NORM_BEFORE;
+    constexpr int kMatrices = GATE == GATE_MATRIX ? 5 : 4;
+    extern __shared__ __align__(16) uint4 packs[];
+    grid_wait_prerequisites();
+    const int w = (int)threadIdx.x & (lay.W <= 32 ? lay.W - 1 : ~0);
+    const int group = lay.W <= 32 ? (int)threadIdx.x / lay.W : 0;
+    const float inv = 1.f / (float)c.cols;
+    int turn = 0;
+    enum { DY, DH, X, H, G };
+    // pack k of matrix m of the row in place `stage`
+    const auto pack = [&](int stage, int m, int k) -> uint4 * {
+        return packs + ((stage * kMatrices + m) * K + k) * blockDim.x +
+               threadIdx.x;
+    };
+    const auto load = [&](int64_t r, int stage) {
+        const bool on = r < c.rows;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            const bool in = on && col < c.cols;
+            const auto one = [&](const void *m, int64_t stride, int which) {
+                copy_pack(pack(stage, which, k),
+                          static_cast<const T *>(m) +
+                              (in ? r * stride + col : 0), in);
+            };
+            if (before) one(c.dy, c.dy_stride, DY);
+            if (before) one(c.h, c.h_stride, H);
+            if (after || GATE != GATE_NONE) one(c.x, c.x_stride, X);
+            if (c.dh != nullptr) one(c.dh, c.dh_stride, DH);
+            if (GATE == GATE_MATRIX) one(c.gate, c.gate_stride, G);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto get = [&](int stage, int m, int k, float *v) {
+        ld_vec<T, V>(reinterpret_cast<const T *>(pack(stage, m, k)), v);
+    };
+    // next_weight; weight times a gate of one row.
+    float w2[K][V], wg[K][V], shared_sum[K][V], next_sum[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = (w + k * lay.W) * V;
+        float f[V];
+        const bool in = col < c.cols;
+        vector_pack<T, V>(in ? c.next_weight : nullptr, in ? col : 0, w2[k]);
+        vector_pack<T, V>(in ? c.weight : nullptr, in ? col : 0, wg[k]);
+        vector_pack<T, V>(in && GATE == GATE_ROW ? c.gate : nullptr,
+                          in ? col : 0, f);
+        mul_n<V>(wg[k], wg[k], f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) shared_sum[k][e] = next_sum[k][e] = 0.f;
+        if (c.dh == nullptr)
+#pragma unroll
+            for (int i = 0; i < kAheadRows; ++i)
+                *pack(i, DH, k) = make_uint4(0, 0, 0, 0);
+    }
+    const int64_t step = (int64_t)gridDim.x * lay.rows;
+    int64_t base = (int64_t)blockIdx.x * lay.rows;
+#pragma unroll
+    for (int i = 0; i < kAheadRows; ++i) load(base + group + i * step, i);
+    int stage = 0;
+#pragma unroll 1
+    for (; base < c.rows; base += step) {
+        const int64_t r = base + group;
+        const bool on = r < c.rows;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAheadRows - 1)
+                     : "memory");
+        float r1 = 1.f, r2 = 0.f, m2 = 0.f;
+        if (after || before) {
+            float2 q[3] = {};
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float v[V], d[V];
+                if (after) {
+                    get(stage, X, k, v);
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 p = make_float2(v[e], v[e + 1]);
+                        q[0] = fma2(p, p, q[0]);
+                    }
+                }
+                if (before) {
+                    get(stage, H, k, v);
+                    get(stage, DY, k, d);
+                    mul_n<V>(d, d, w2[k]);
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 p = make_float2(v[e], v[e + 1]);
+                        q[1] = fma2(p, p, q[1]);
+                        q[2] = fma2(make_float2(d[e], d[e + 1]), p, q[2]);
+                    }
+                }
+            }
+            float s[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) s[i] = q[i].x + q[i].y;
+            row_sums(s, lay.W, turn);
+            if (after) r1 = rsqrtf(fmaf(s[0], inv, c.eps));
+            if (before) r2 = rsqrtf(fmaf(s[1], inv, c.eps));
+            m2 = s[2] * inv * r2 * r2;
+            if (!on) r1 = r2 = m2 = 0.f;
+        }
+        float g[K][V];
+        float2 t2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            const bool in = on && col < c.cols;
+            float x[V], f[V], o[V];
+            get(stage, DH, k, g[k]);
+            if (before) {
+                float v[V], d[V];
+                get(stage, H, k, v);
+                get(stage, DY, k, d);
+                mul_n<V>(o, d, w2[k]);
+                scale_add_n<V>(o, v, -m2, o);
+                scale_add_n<V>(g[k], o, r2, g[k]);
+                scale_n<V>(v, v, r2);
+                fma_n<V>(next_sum[k], d, v, next_sum[k]);
+            }
+            if (after || GATE != GATE_NONE) {
+                get(stage, X, k, x);
+                scale_n<V>(f, x, r1);     // x r1
+            }
+            if (in) {
+                scale_n<V>(o, g[k], c.residual_scale);
+                st_vec<T, V>(static_cast<T *>(c.dresidual) +
+                                 r * c.dresidual_stride + col, o);
+            }
+            if (GATE == GATE_MATRIX) {
+                float gate[V];
+                get(stage, G, k, gate);
+                mul_n<V>(o, g[k], f);
+                mul_n<V>(o, o, wg[k]);
+                if (in)
+                    st_vec<T, V>(static_cast<T *>(c.dgate) +
+                                     r * c.dgate_stride + col, o);
+                mul_n<V>(g[k], g[k], gate);
+            }
+            if (after || GATE == GATE_ROW)
+                fma_n<V>(shared_sum[k], g[k], f, shared_sum[k]);
+            mul_n<V>(g[k], g[k], wg[k]);
+            if (after) {
+#pragma unroll
+                for (int e = 0; e < V; e += 2)
+                    t2 = fma2(make_float2(g[k][e], g[k][e + 1]),
+                              make_float2(x[e], x[e + 1]), t2);
+            }
+        }
+        float m1 = 0.f;
+        if (after) {
+            float t[1] = {t2.x + t2.y};
+            row_sums(t, lay.W, turn);
+            m1 = t[0] * inv * r1 * r1;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = (w + k * lay.W) * V;
+            if (after) {
+                float x[V];
+                get(stage, X, k, x);
+                scale_add_n<V>(g[k], x, -m1, g[k]);
+                scale_n<V>(g[k], g[k], r1);
+            }
+            if (on && col < c.cols)
+                st_vec<T, V>(static_cast<T *>(c.dx) + r * c.dx_stride + col,
+                             g[k]);
+        }
+        load(r + kAheadRows * step, stage);
+        stage = stage + 1 == kAheadRows ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    grid_launch_dependents();
+    if (partial == nullptr) return;
+    // Groups of a CTA's rows one after the other, then the CTA's row of sums.
+    float *to = partial + (int64_t)blockIdx.x * 3 * c.cols;
+#pragma unroll 1
+    for (int q = 0; q < lay.rows; ++q) {
+        if (q == group) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int col = (w + k * lay.W) * V;
+                if (col >= c.cols) continue;
+                float f[V], u[V];
+                vector_pack<T, V>(c.weight, col, u);
+                vector_pack<T, V>(GATE == GATE_ROW ? c.gate : nullptr, col, f);
+                mul_n<V>(u, u, shared_sum[k]);
+                mul_n<V>(f, f, shared_sum[k]);
+                const float *v[3] = {u, f, next_sum[k]};
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; e += 4) {
+                        float4 *p = reinterpret_cast<float4 *>(
+                            to + (int64_t)i * c.cols + col + e);
+                        float4 a = make_float4(v[i][e], v[i][e + 1],
+                                               v[i][e + 2], v[i][e + 3]);
+                        if (q != 0) {
+                            const float4 b = *p;
+                            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+                        }
+                        *p = a;
+                    }
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Threads per row and rows per CTA for K packs of V values.
 inline Lay lay_of(int cols, int V, int K, int small) {
     const int packs = (cols + V - 1) / V;
@@ -649,13 +883,71 @@ cudaError_t norm_back_launch(const mt_block_norm_back_t &c, float *partial,
     return launch_dependent(kernel, *blocks, threads, smem, s, c, l, partial);
 }
 
+template <typename T, int K, int THREADS, int NORMS, int GATE>
+cudaError_t norm_back_ahead_as(const mt_block_norm_back_t &c, float *partial,
+                               int *blocks, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const Lay l = lay_of(c.cols, V, K, 256);
+    const int threads = l.W * l.rows;
+    const auto kernel = norm_back_ahead_kernel<T, K, THREADS, NORMS, GATE>;
+    const size_t smem = (size_t)kAheadRows * (GATE == GATE_MATRIX ? 5 : 4) *
+                        K * 16 * threads;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e == cudaSuccess && smem > 40 * 1024)
+        e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    if (e != cudaSuccess) return e;
+    int64_t grid = (int64_t)sms * (512 / THREADS);
+    const int64_t need = (c.rows + l.rows - 1) / l.rows;
+    if (grid > kNormBackBlocks) grid = kNormBackBlocks;
+    if (grid > need) grid = need;
+    *blocks = (int)grid;
+    return launch_dependent(kernel, grid, threads, smem, s, c, l, partial);
+}
+template <typename T, int K, int THREADS>
+cudaError_t norm_back_ahead(const mt_block_norm_back_t &c, float *partial,
+                            int *blocks, cudaStream_t s) {
+    const int gate = c.gate == nullptr     ? GATE_NONE
+                     : c.dgate == nullptr ? GATE_ROW : GATE_MATRIX;
+#define MT_NORM_AHEAD(n, g)                                                  \
+    if (c.norms == n && gate == g)                                           \
+        return norm_back_ahead_as<T, K, THREADS, n, g>(c, partial, blocks, s);
+    MT_NORM_AHEAD(1, GATE_NONE)
+    MT_NORM_AHEAD(1, GATE_ROW)
+    MT_NORM_AHEAD(1, GATE_MATRIX)
+    MT_NORM_AHEAD(2, GATE_NONE)
+    MT_NORM_AHEAD(2, GATE_ROW)
+    MT_NORM_AHEAD(2, GATE_MATRIX)
+    MT_NORM_AHEAD(3, GATE_NONE)
+    MT_NORM_AHEAD(3, GATE_ROW)
+    MT_NORM_AHEAD(3, GATE_MATRIX)
+#undef MT_NORM_AHEAD
+    return cudaErrorInvalidValue;
+}
+
 template <typename T, int V>
 cudaError_t norm_back_packs(const mt_block_norm_back_t &c, float *partial,
                             int *blocks, cudaStream_t s) {
     constexpr int kWords = Raw<T, V>::kWords;  // of a pack
     const int packs = (c.cols + V - 1) / V;
-    if (packs <= 512) return norm_back_launch<T, V, 1>(c, partial, blocks, s);
-    if (packs <= 1024) return norm_back_launch<T, V, 2>(c, partial, blocks, s);
+    // (A gate matrix without its gradient, which only the C call can ask for,
+    // goes the other way.)
+    const bool plain = c.gate == nullptr || c.dgate != nullptr ||
+                       c.gate_stride == 0 || c.rows == 1;
+    if (V * sizeof(T) == 16 && packs <= 1024 && plain) {
+        if constexpr (V * sizeof(T) == 16)
+            return packs <= 256 ? norm_back_ahead<T, 1, 256>(c, partial,
+                                                             blocks, s)
+                   : packs <= 512 ? norm_back_ahead<T, 2, 256>(c, partial,
+                                                               blocks, s)
+                                  : norm_back_ahead<T, 2, 512>(c, partial,
+                                                               blocks, s);
+    } else {
+        if (packs <= 512)
+            return norm_back_launch<T, V, 1>(c, partial, blocks, s);
+        if (packs <= 1024)
+            return norm_back_launch<T, V, 2>(c, partial, blocks, s);
+    }
     if (packs <= 2048) return norm_back_launch<T, V, 4>(c, partial, blocks, s);
     if constexpr (kWords * 8 <= 16)
         if (packs <= 4096)
