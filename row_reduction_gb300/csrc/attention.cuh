@@ -19,6 +19,13 @@ __device__ __forceinline__ float pow2(float t) {
     return r;
 }
 
+// The largest of three; NaN where one is.
+__device__ __forceinline__ float nanmax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // cap tanh(z / cap) as cap (1 - 2 / (1 + e^(2 z / cap))): off by a few
 // roundings of cap, where tanh.approx would be off by 2^-11 of it.
 __device__ __forceinline__ float capped(float z, float cap, float inv_cap) {

@@ -469,8 +469,8 @@ struct Warp {
     }
     // Scores to exponents of two; -infinity, and a bit of `hidden`, for keys
     // that a column does not see.  j0: the chunk's first key; there: its keys
-    // that have a slot.
-    __device__ __forceinline__ void bend(const mt_attention_call_t &c,
+    // that have a slot.  Returns whether there may be any such key.
+    __device__ __forceinline__ bool bend(const mt_attention_call_t &c,
                                          const Shared<H, PARTS, NT> &sh,
                                          int j0, unsigned there,
                                          unsigned &hidden,
@@ -500,7 +500,7 @@ struct Warp {
                     for (int e = 0; e < 4; ++e)
                         z[n][t][e] = capped2(z[n][t][e], cap2);
         }
-        if (c.slopes == nullptr && whole) return;
+        if (c.slopes == nullptr && whole) return false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -523,6 +523,7 @@ struct Warp {
                         }
                     }
             }
+        return !whole;
     }
     // Weights about the columns' references, which move where a score is 2^8
     // ahead of one (or there is none yet, or something is NaN).
@@ -531,12 +532,13 @@ struct Warp {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                float top = nanmax(z[n][0][h], z[n][0][2 + h]);
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        ahead |= !(z[n][t][2 * i + h] <= ref[n][h] + 8.f);
+                for (int t = 1; t < KT; ++t)
+                    top = nanmax3(top, z[n][t][h], z[n][t][2 + h]);
+                ahead |= !(top <= ref[n][h] + 8.f);
+            }
         if (__any_sync(kFull, ahead)) move(z);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -600,6 +602,7 @@ struct Warp {
     // that come, that power moves.
     __device__ __forceinline__ void scaled(const float (&w)[NT][KT][4],
                                            unsigned hidden,
+                                           bool masked,
                                            const Scales &scales, int gr,
                                            float (&x)[NT][KT][4]) {
         const int g = (threadIdx.x & 31) >> 2;
@@ -609,22 +612,37 @@ struct Warp {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 scale[t][i] = scales.v[16 * t + 8 * i + g][gr];
-        bool out = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[n][t][e] = w[n][t][e] * scale[t][e >> 1];
+        if (masked) {
+            // not seen: nothing, whatever stands in the scale
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (hidden >> (4 * (n * KT + t) + e) & 1u)
+                            x[n][t][e] = 0.f;
+        }
+        float most_x = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float f[2] = {up(exponent(n, 0, gr)), up(exponent(n, 1, gr))};
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
+            for (int t = 0; t < KT; ++t) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[n][t][e] = w[n][t][e] * scale[t][e >> 1];
-                    // not seen: nothing, whatever stands in the scale
-                    if (hidden >> (4 * (n * KT + t) + e) & 1u)
-                        x[n][t][e] = 0.f;
-                    x[n][t][e] *= f[e & 1];
-                    out |= !(fabsf(x[n][t][e]) < 32768.f);
-                }
+                for (int e = 0; e < 4; ++e) x[n][t][e] *= f[e & 1];
+                most_x = nanmax3(most_x, fabsf(x[n][t][0]), fabsf(x[n][t][1]));
+                most_x = nanmax3(most_x, fabsf(x[n][t][2]), fabsf(x[n][t][3]));
+            }
         }
+        const bool out = !(most_x < 32768.f);
         if (__any_sync(kFull, out)) raise(w, hidden, scale, gr, x);
     }
     __device__ __forceinline__ void raise(const float (&w)[NT][KT][4],
@@ -728,14 +746,15 @@ struct Warp {
     }
     // Adds the chunk's weights times values.
     __device__ __forceinline__ void add(const float (&w)[NT][KT][4],
-                                        unsigned hidden, const Codes &st,
+                                        unsigned hidden, bool masked,
+                                        const Codes &st,
                                         const Scales &scales) {
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
             unsigned b[NT][PARTS][KT][2];
             {
                 float x[NT][KT][4];
-                scaled(w, hidden, scales, gr, x);
+                scaled(w, hidden, masked, scales, gr, x);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1070,9 +1089,10 @@ __device__ __forceinline__ void tile_run(const mt_attention_call_t &c,
             float z[NT][KT][4];
             unsigned hidden;
             w.scores(sh, codes[stage], scales[stage], z);
-            w.bend(c, sh, (int)(u * H::KEYS), there, hidden, z);
+            const bool masked =
+                w.bend(c, sh, (int)(u * H::KEYS), there, hidden, z);
             w.weigh(z);
-            w.add(z, hidden, codes[stage], scales[stage]);
+            w.add(z, hidden, masked, codes[stage], scales[stage]);
         }
         __syncwarp();  // the next round's copies go where this one read
         stage ^= 1;
