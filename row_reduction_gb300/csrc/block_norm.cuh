@@ -11,9 +11,12 @@
 // shared memory where it has 16 columns or more; a second kernel adds up the
 // CTAs' in order.
 //
-// Packs are as wide as every row's address allows (rows of an odd length: one
-// value).  Rows that the registers do not hold are gone through in loops, once
-// per sum and once to write.
+// Packs are as wide as every row's address allows.  Rows that 16-byte packs do
+// not divide, from 512 columns on, are copied into shared memory with what lies
+// around them up to the packs' bounds and read there value by value (one value
+// per access of global memory: 12000 x 5001 BF16 350 us, backward 6000 x 5001
+// 930 us).  Rows that neither registers nor that hold are gone through in
+// loops, once per sum and once to write.
 #pragma once
 
 #include "mt_decoder.cuh"
@@ -808,6 +811,288 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
     }
 }
 
+// ---- rows off the packs' bounds ----------------------------------------------
+// A CTA goes through many rows, the next one on its way where there is room for
+// two (`places`); a thread has every THREADS-th column of all of them, K at
+// most, and its weights in registers.
+//
+// A row in shared memory: its place among 16-byte packs is kept, so that whole
+// packs can be copied (the first of them with the end of the row before it, of
+// the last one only what is the row's).
+template <typename T>
+struct OddRow {
+    const uint8_t *at;  // the row's first value
+    template <int THREADS>
+    __device__ __forceinline__ void load(uint8_t *to, const void *m,
+                                         int64_t row, int64_t stride,
+                                         int cols) const {
+        const uintptr_t first = reinterpret_cast<uintptr_t>(m) +
+                                (uintptr_t)(row * stride) * sizeof(T);
+        const unsigned shift = (unsigned)(first & 15);
+        const unsigned bytes = (unsigned)cols * (unsigned)sizeof(T);
+        for (unsigned j = threadIdx.x * 16; j < shift + bytes;
+             j += THREADS * 16) {
+            const uintptr_t from = first - shift + j;
+            if (j == 0 && row == 0 && shift != 0) {
+                // nothing of the matrix before it: value by value
+                for (unsigned b = shift; b < 16 && b < shift + bytes;
+                     b += sizeof(T))
+                    *reinterpret_cast<T *>(to + b) =
+                        *reinterpret_cast<const T *>(from + b);
+                continue;
+            }
+            const unsigned left = shift + bytes - j;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_addr(to + j)),
+                         "l"(from), "r"(left < 16 ? left : 16u)
+                         : "memory");
+        }
+    }
+    __device__ __forceinline__ void begin(const uint8_t *region, const void *m,
+                                          int64_t row, int64_t stride) {
+        at = region + ((reinterpret_cast<uintptr_t>(m) +
+                        (uintptr_t)(row * stride) * sizeof(T)) & 15);
+    }
+    __device__ __forceinline__ float operator[](int col) const {
+        return to_f(reinterpret_cast<const T *>(at)[col]);
+    }
+};
+
+template <typename T, int K, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    norm_odd_kernel(const mt_block_norm_call_t c, int region, int places) {
+    extern __shared__ __align__(16) uint8_t rows[];
+    grid_wait_prerequisites();
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
+    const bool wide = c.gate != nullptr && c.gate_stride != 0;
+    const float inv = 1.f / (float)c.cols;
+    const int tid = threadIdx.x;
+    int turn = 0;
+    float wg[K], w2[K];  // weight times a gate of one row; next_weight
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = tid + k * THREADS;
+        const bool in = col < c.cols;
+        wg[k] = in ? param_at(static_cast<const T *>(c.weight), col, 1.f) : 1.f;
+        if (in && !wide)
+            wg[k] *= param_at(static_cast<const T *>(c.gate), col, 1.f);
+        w2[k] = in ? param_at(static_cast<const T *>(c.next_weight), col, 1.f)
+                   : 1.f;
+    }
+    OddRow<T> x, res, gate;
+    const auto load = [&](int64_t r, int stage) {
+        uint8_t *to = rows + stage * 3 * region;
+        if (r < c.rows) {
+            x.template load<THREADS>(to, c.x, r, c.x_stride, c.cols);
+            res.template load<THREADS>(to + region, c.residual, r,
+                                       c.residual_stride, c.cols);
+            if (wide)
+                gate.template load<THREADS>(to + 2 * region, c.gate, r,
+                                            c.gate_stride, c.cols);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int stage = 0;
+    if (places == 2) load(blockIdx.x, 0);
+#pragma unroll 1
+    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+        if (places == 1) {
+            __syncthreads();  // the row before is done with
+            load(r, 0);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // this row is there, the one before is done with
+        if (places == 2) {
+            stage ^= 1;
+            load(r + gridDim.x, stage);
+        }
+        const uint8_t *from = rows + (stage ^ (places - 1)) * 3 * region;
+        x.begin(from, c.x, r, c.x_stride);
+        res.begin(from + region, c.residual, r, c.residual_stride);
+        gate.begin(from + 2 * region, c.gate, r, c.gate_stride);
+        float h[K];
+        float s[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            h[k] = col < c.cols ? x[col] : 0.f;
+            s[0] = fmaf(h[k], h[k], s[0]);
+        }
+        float r1 = 1.f;
+        if (after) {
+            row_sums(s, THREADS, turn);
+            r1 = rsqrtf(fmaf(s[0], inv, c.eps));
+        }
+        s[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            if (col >= c.cols) continue;
+            float u = h[k] * r1 * wg[k];
+            if (wide) u *= gate[col];
+            h[k] = fmaf(res[col], c.residual_scale, u);
+            s[0] = fmaf(h[k], h[k], s[0]);
+            static_cast<T *>(c.h)[r * c.h_stride + col] = from_f<T>(h[k]);
+        }
+        if (!before) continue;
+        row_sums(s, THREADS, turn);
+        const float r2 = rsqrtf(fmaf(s[0], inv, c.eps));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            if (col < c.cols)
+                static_cast<T *>(c.y)[r * c.y_stride + col] =
+                    from_f<T>(h[k] * r2 * w2[k]);
+        }
+    }
+    grid_launch_dependents();
+}
+
+template <typename T, int K, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+    norm_back_odd_kernel(const mt_block_norm_back_t c, float *partial,
+                         int region, int places) {
+    extern __shared__ __align__(16) uint8_t rows[];
+    grid_wait_prerequisites();
+    const bool after = c.norms & MT_NORM_AFTER;
+    const bool before = c.norms & MT_NORM_BEFORE;
+    const bool wide = c.dgate != nullptr;
+    const bool takes_x = after || c.gate != nullptr;
+    const float inv = 1.f / (float)c.cols;
+    const int tid = threadIdx.x;
+    int turn = 0;
+    float wg[K], w2[K], shared_sum[K], next_sum[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = tid + k * THREADS;
+        const bool in = col < c.cols;
+        wg[k] = in ? param_at(static_cast<const T *>(c.weight), col, 1.f) : 1.f;
+        if (in && !wide)
+            wg[k] *= param_at(static_cast<const T *>(c.gate), col, 1.f);
+        w2[k] = in ? param_at(static_cast<const T *>(c.next_weight), col, 1.f)
+                   : 1.f;
+        shared_sum[k] = next_sum[k] = 0.f;
+    }
+    OddRow<T> dy, dh, x, h, gate;
+    const auto load = [&](int64_t r, int stage) {
+        uint8_t *to = rows + stage * 5 * region;
+        if (r < c.rows) {
+            const auto one = [&](const OddRow<T> &m, const void *p,
+                                 int64_t stride, int i) {
+                m.template load<THREADS>(to + i * region, p, r, stride,
+                                         c.cols);
+            };
+            if (before) one(dy, c.dy, c.dy_stride, 0);
+            if (before) one(h, c.h, c.h_stride, 1);
+            if (takes_x) one(x, c.x, c.x_stride, 2);
+            if (c.dh) one(dh, c.dh, c.dh_stride, 3);
+            if (wide) one(gate, c.gate, c.gate_stride, 4);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int stage = 0;
+    if (places == 2) load(blockIdx.x, 0);
+#pragma unroll 1
+    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+        if (places == 1) {
+            __syncthreads();  // the row before is done with
+            load(r, 0);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // this row is there, the one before is done with
+        if (places == 2) {
+            stage ^= 1;
+            load(r + gridDim.x, stage);
+        }
+        const uint8_t *from = rows + (stage ^ (places - 1)) * 5 * region;
+        dy.begin(from, c.dy, r, c.dy_stride);
+        h.begin(from + region, c.h, r, c.h_stride);
+        x.begin(from + 2 * region, c.x, r, c.x_stride);
+        dh.begin(from + 3 * region, c.dh, r, c.dh_stride);
+        gate.begin(from + 4 * region, c.gate, r, c.gate_stride);
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            if (col >= c.cols) continue;
+            if (after) s[0] = fmaf(x[col], x[col], s[0]);
+            if (before) {
+                const float v = h[col];
+                s[1] = fmaf(v, v, s[1]);
+                s[2] = fmaf(dy[col] * w2[k], v, s[2]);
+            }
+        }
+        row_sums(s, THREADS, turn);
+        const float r1 = after ? rsqrtf(fmaf(s[0], inv, c.eps)) : 1.f;
+        const float r2 = before ? rsqrtf(fmaf(s[1], inv, c.eps)) : 0.f;
+        const float m2 = s[2] * inv * r2 * r2;
+        float g[K];
+        float t[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            if (col >= c.cols) continue;
+            g[k] = c.dh ? dh[col] : 0.f;
+            if (before) {
+                const float d = dy[col], v = h[col];
+                g[k] = fmaf(r2, fmaf(-v, m2, d * w2[k]), g[k]);
+                next_sum[k] = fmaf(d, v * r2, next_sum[k]);
+            }
+            // outputs may lie on inputs: the row itself is in shared memory
+            static_cast<T *>(c.dresidual)[r * c.dresidual_stride + col] =
+                from_f<T>(g[k] * c.residual_scale);
+            if (!takes_x) continue;
+            const float v = x[col], u = v * r1;
+            if (wide) {
+                static_cast<T *>(c.dgate)[r * c.dgate_stride + col] =
+                    from_f<T>(g[k] * u * wg[k]);
+                g[k] *= gate[col];
+            }
+            shared_sum[k] = fmaf(g[k], u, shared_sum[k]);
+            g[k] *= wg[k];
+            t[0] = fmaf(g[k], v, t[0]);
+        }
+        float m1 = 0.f;
+        if (after) {
+            row_sums(t, THREADS, turn);
+            m1 = t[0] * inv * r1 * r1;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = tid + k * THREADS;
+            if (col >= c.cols) continue;
+            if (after) g[k] = r1 * fmaf(-x[col], m1, g[k]);
+            static_cast<T *>(c.dx)[r * c.dx_stride + col] = from_f<T>(g[k]);
+        }
+    }
+    grid_launch_dependents();
+    if (partial == nullptr) return;
+    float *to = partial + (int64_t)blockIdx.x * 3 * c.cols;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int col = tid + k * THREADS;
+        if (col >= c.cols) continue;
+        to[col] = shared_sum[k] *
+                  param_at(static_cast<const T *>(c.weight), col, 1.f);
+        to[c.cols + col] =
+            shared_sum[k] *
+            (wide ? 1.f : param_at(static_cast<const T *>(c.gate), col, 1.f));
+        to[2 * c.cols + col] = next_sum[k];
+    }
+}
+
+// Bytes of a row's place in shared memory.
+inline int odd_region(int cols, int es) {
+    return (int)(((int64_t)cols * es + 15 + 15) / 16 * 16);
+}
+// Whether a matrix's rows follow one another, so that what lies before a row
+// but the first is the matrix's too.
+inline bool odd_ok(const void *p, int64_t stride, int64_t rows, int cols) {
+    return p == nullptr || rows <= 1 || stride >= cols;
+}
+constexpr int kOddFrom = 512, kOddMost = 8192;
+
 // Threads per row and rows per CTA for K packs of V values.
 inline Lay lay_of(int cols, int V, int K, int small) {
     const int packs = (cols + V - 1) / V;
@@ -832,9 +1117,38 @@ cudaError_t norm_launch(const mt_block_norm_call_t &c, cudaStream_t s) {
                             c, l);
 }
 
+template <typename T, int K, int THREADS>
+cudaError_t norm_odd(const mt_block_norm_call_t &c, cudaStream_t s) {
+    const auto kernel = norm_odd_kernel<T, K, THREADS>;
+    const int region = odd_region(c.cols, sizeof(T));
+    const int places = (int64_t)6 * region <= 200 * 1024 ? 2 : 1;
+    const size_t smem = (size_t)places * 3 * region;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e == cudaSuccess && smem > 40 * 1024)
+        e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    if (e != cudaSuccess) return e;
+    int64_t grid = (int64_t)sms * (1024 / THREADS);
+    const int64_t fit = 220 * 1024 / (int64_t)(smem + 2048);
+    if (grid > sms * fit) grid = sms * fit;
+    if (grid > c.rows) grid = c.rows;
+    return launch_dependent(kernel, grid, THREADS, smem, s, c, region, places);
+}
+
 template <typename T, int V>
 cudaError_t norm_packs(const mt_block_norm_call_t &c, cudaStream_t s) {
     const int packs = (c.cols + V - 1) / V;
+    if constexpr (V * sizeof(T) < 16) {
+        if (c.cols >= kOddFrom && c.cols <= kOddMost &&
+            odd_ok(c.x, c.x_stride, c.rows, c.cols) &&
+            odd_ok(c.residual, c.residual_stride, c.rows, c.cols) &&
+            (c.gate_stride == 0 ||
+             odd_ok(c.gate, c.gate_stride, c.rows, c.cols)))
+            return c.cols <= 1024   ? norm_odd<T, 4, 256>(c, s)
+                   : c.cols <= 2048 ? norm_odd<T, 8, 256>(c, s)
+                   : c.cols <= 4096 ? norm_odd<T, 8, 512>(c, s)
+                                    : norm_odd<T, 16, 512>(c, s);
+    }
     if (packs <= 256) return norm_launch<T, V, 1>(c, s);
     if (packs <= 1024) return norm_launch<T, V, 2>(c, s);
     if (packs <= 2048) return norm_launch<T, V, 4>(c, s);
@@ -883,6 +1197,17 @@ cudaError_t norm_back_launch(const mt_block_norm_back_t &c, float *partial,
     return launch_dependent(kernel, *blocks, threads, smem, s, c, l, partial);
 }
 
+inline int back_grid_of(int64_t rows, int cols, int64_t grid) {
+    if (grid > norm_back_blocks(cols)) grid = norm_back_blocks(cols);
+    return (int)(grid < rows ? grid : rows);
+}
+// A gate matrix without its gradient, which only the C call can ask for, goes
+// the general way.
+inline bool gate_plain(const mt_block_norm_back_t &c) {
+    return c.gate == nullptr || c.dgate != nullptr || c.gate_stride == 0 ||
+           c.rows == 1;
+}
+
 template <typename T, int K, int THREADS, int NORMS, int GATE>
 cudaError_t norm_back_ahead_as(const mt_block_norm_back_t &c, float *partial,
                                int *blocks, cudaStream_t s) {
@@ -925,16 +1250,49 @@ cudaError_t norm_back_ahead(const mt_block_norm_back_t &c, float *partial,
     return cudaErrorInvalidValue;
 }
 
+template <typename T, int K, int THREADS>
+cudaError_t norm_back_odd(const mt_block_norm_back_t &c, float *partial,
+                          int *blocks, cudaStream_t s) {
+    const auto kernel = norm_back_odd_kernel<T, K, THREADS>;
+    const int region = odd_region(c.cols, sizeof(T));
+    const int places = (int64_t)10 * region <= 200 * 1024 ? 2 : 1;
+    const size_t smem = (size_t)places * 5 * region;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e == cudaSuccess && smem > 40 * 1024)
+        e = allow_max_smem(reinterpret_cast<const void *>(kernel));
+    if (e != cudaSuccess) return e;
+    // 62, 80 and 112 registers for 4, 8 and 16 columns
+    int per_sm = THREADS == 512 ? 1 : K == 4 ? 4 : K == 8 ? 3 : 2;
+    while (per_sm > 1 && per_sm * (smem + 2048) > 228 * 1024) --per_sm;
+    *blocks = back_grid_of(c.rows, c.cols, (int64_t)sms * per_sm);
+    return launch_dependent(kernel, *blocks, THREADS, smem, s, c, partial,
+                            region, places);
+}
+
 template <typename T, int V>
 cudaError_t norm_back_packs(const mt_block_norm_back_t &c, float *partial,
                             int *blocks, cudaStream_t s) {
     constexpr int kWords = Raw<T, V>::kWords;  // of a pack
     const int packs = (c.cols + V - 1) / V;
-    // (A gate matrix without its gradient, which only the C call can ask for,
-    // goes the other way.)
-    const bool plain = c.gate == nullptr || c.dgate != nullptr ||
-                       c.gate_stride == 0 || c.rows == 1;
-    if (V * sizeof(T) == 16 && packs <= 1024 && plain) {
+    if (V * sizeof(T) < 16 && c.cols >= kOddFrom && c.cols <= kOddMost &&
+        gate_plain(c) &&
+        odd_ok(c.dy, c.dy_stride, c.rows, c.cols) &&
+        odd_ok(c.dh, c.dh_stride, c.rows, c.cols) &&
+        odd_ok(c.x, c.x_stride, c.rows, c.cols) &&
+        odd_ok(c.h, c.h_stride, c.rows, c.cols) &&
+        (c.dgate == nullptr ||
+         odd_ok(c.gate, c.gate_stride, c.rows, c.cols))) {
+        if constexpr (V * sizeof(T) < 16)
+            return c.cols <= 1024
+                       ? norm_back_odd<T, 4, 256>(c, partial, blocks, s)
+                   : c.cols <= 2048
+                       ? norm_back_odd<T, 8, 256>(c, partial, blocks, s)
+                   : c.cols <= 4096
+                       ? norm_back_odd<T, 16, 256>(c, partial, blocks, s)
+                       : norm_back_odd<T, 16, 512>(c, partial, blocks, s);
+    }
+    if (V * sizeof(T) == 16 && packs <= 1024 && gate_plain(c)) {
         if constexpr (V * sizeof(T) == 16)
             return packs <= 256 ? norm_back_ahead<T, 1, 256>(c, partial,
                                                              blocks, s)

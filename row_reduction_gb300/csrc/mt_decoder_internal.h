@@ -150,8 +150,12 @@ MT_DECLARE_ATTENTION(launch_attention_int8_p2n2)
 
 // ---- norms around a block ------------------------------------------------------
 constexpr int kNormMaxCols = 1 << 20;
-// Rows of partial sums of the backward pass (each of 3 x cols FP32 values).
+// Rows of partial sums of the backward pass (each of 3 x cols FP32 values): two
+// for each of 152 SMs, four of short rows, whose CTAs wait more than they work.
 constexpr int kNormBackBlocks = 304;
+constexpr int norm_back_blocks(int cols) {
+    return cols <= 2048 ? 2 * kNormBackBlocks : kNormBackBlocks;
+}
 // V: values that every access of a row can take at once.  blocks: on return how
 // many rows of partial sums there are.
 #define MT_DECLARE_BLOCK_NORM(dt)                                            \

@@ -135,7 +135,8 @@ struct Widest {
 
 size_t norm_workspace(const mt_block_norm_back_t &c) {
     return c.dgate_sum || c.dweight || c.dnext_weight
-               ? (size_t)kNormBackBlocks * 3 * (size_t)c.cols * sizeof(float)
+               ? (size_t)norm_back_blocks(c.cols) * 3 * (size_t)c.cols *
+                     sizeof(float)
                : 0;
 }
 
