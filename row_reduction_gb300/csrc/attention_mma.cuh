@@ -165,8 +165,9 @@ struct Share {
                               // each of its key heads
 };
 
+// columns: of all of a CTA's key heads.
 __host__ __device__ constexpr int place_floats(int columns, int dim) {
-    return kWarps * columns * (dim + 2);
+    return columns * (dim + 2);
 }
 
 // ---- instructions --------------------------------------------------------------
@@ -295,6 +296,12 @@ struct Column {
     int32_t pad;
 };
 
+struct Deal {
+    int64_t scan[kWarps];
+    int64_t at;         // place of the CTA's first unit in its sequence
+    int32_t sequence;
+};
+
 template <class H, int PARTS, int NT>
 struct Shared {
     // Each warp's own: the codes of two chunks, then its sums.
@@ -318,9 +325,7 @@ struct Shared {
     float f[kWarps][8 * NT], slope[kWarps][8 * NT];
     int32_t lo_any, hi_any, lo_all, hi_all;
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int64_t scan[kWarps];
-    int64_t at;         // place of the CTA's first unit in its sequence
-    int32_t sequence;
+    Deal deal;
     static_assert(sizeof(Own) == 2 * sizeof(Codes), "room for the sums");
 };
 
@@ -1214,17 +1219,15 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
 // The least units that a CTA takes where there are few: a tile's own, and one.
 constexpr int kLeastUnits = (int)kExtra + 1;
 
-template <class H, bool INT8, int PARTS, int NT>
-__global__ void __launch_bounds__(32 * kWarps,
-                                  attention_ctas(H::DIM, H::GROUPS, PARTS, NT))
-    attention_mma_kernel(const mt_attention_call_t c, const Cut cut,
-                         const Share share, int dtype) {
-    constexpr int C = 8 * NT, T = 32 * kWarps;
-    extern __shared__ __align__(16) uint8_t shared[];
-    Shared<H, PARTS, NT> &sh =
-        *reinterpret_cast<Shared<H, PARTS, NT> *>(shared);
+// Deals the call's units out and goes through the CTA's run of them:
+// body(tile, u0, u1, whole, place) for the units [u0, u1) of a tile, whole or
+// not, whose partial sums belong in the CTA's place 0 or 1.
+template <class Body>
+__device__ __forceinline__ void deal_units(const mt_attention_call_t &c,
+                                           const Cut &cut, const Share &share,
+                                           Deal &sh, Body body) {
+    constexpr int T = 32 * kWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_wait_prerequisites();
     int cut_here = 0;
     // Units of the sequences of this thread, and where they begin.
     const int each = (c.sequences + T - 1) / T;
@@ -1298,15 +1301,11 @@ __global__ void __launch_bounds__(32 * kWarps,
         int64_t units = a.tiles.last(lo) - base + 1 + kExtra;
         int index = (int)quotient(off, units);
         off -= index * units;
-        Warp<H, INT8, PARTS, NT> w;
         while (at < end) {
             const int64_t n = min(units - off, end - at);
             a.head = index / cut.parts;
             a.part = index - a.head * cut.parts;
             a.head *= cut.heads;
-            tile_run<H, INT8, PARTS, NT>(
-                c, cut, dtype, a, base + max(off - kExtra, (int64_t)0),
-                base + max(off + n - kExtra, (int64_t)0), sh, w);
             const bool whole = n == units;
             if (!whole && off == 0) {
                 const int64_t x = at + units;
@@ -1318,11 +1317,9 @@ __global__ void __launch_bounds__(32 * kWarps,
                         min(cut.per, a.tiles.rows - a.t * cut.per), a.head,
                         a.part};
             }
-            tile_end<H, INT8, PARTS, NT>(
-                c, cut, dtype, a, whole,
-                share.sums + (2 * (int64_t)blockIdx.x + (off == 0 ? 1 : 0)) *
-                                 place_floats(C, H::DIM),
-                sh, w);
+            body(a, base + max(off - kExtra, (int64_t)0),
+                 base + max(off + n - kExtra, (int64_t)0), whole,
+                 off == 0 ? 1 : 0);
             at += n;
             off = 0;
             if (at < end && ++index == wide) {
@@ -1343,11 +1340,34 @@ __global__ void __launch_bounds__(32 * kWarps,
     if (tid == 0) share.cut[blockIdx.x] = cut_here;
 }
 
+template <class H, bool INT8, int PARTS, int NT>
+__global__ void __launch_bounds__(32 * kWarps,
+                                  attention_ctas(H::DIM, H::GROUPS, PARTS, NT))
+    attention_mma_kernel(const mt_attention_call_t c, const Cut cut,
+                         const Share share, int dtype) {
+    extern __shared__ __align__(16) uint8_t shared[];
+    Shared<H, PARTS, NT> &sh =
+        *reinterpret_cast<Shared<H, PARTS, NT> *>(shared);
+    grid_wait_prerequisites();
+    Warp<H, INT8, PARTS, NT> w;
+    deal_units(c, cut, share, sh.deal,
+               [&](const Tile &a, int64_t u0, int64_t u1, bool whole,
+                   int place) {
+                   tile_run<H, INT8, PARTS, NT>(c, cut, dtype, a, u0, u1, sh,
+                                                w);
+                   tile_end<H, INT8, PARTS, NT>(
+                       c, cut, dtype, a, whole,
+                       share.sums + (2 * (int64_t)blockIdx.x + place) *
+                                        place_floats(kWarps * 8 * NT, H::DIM),
+                       sh, w);
+               });
+}
+
 // Joins the parts of cut tiles, in the order of the CTAs that left them: a
 // column to a warp, four values to a lane, a part's factor in each lane first;
 // where there are few columns, the warps of a CTA share the parts of one.
 constexpr int kJoin = 256, kJoinWarps = kJoin / 32;
-template <int DIM, int C>
+template <int DIM, int C, int SLOTS>
 __global__ void __launch_bounds__(kJoin)
     attention_join_kernel(const mt_attention_call_t c, const Cut cut,
                           const Share share, int dtype) {
@@ -1395,7 +1415,7 @@ __global__ void __launch_bounds__(kJoin)
     }
     // columns that a tile has at most
     const int most = cut.times <= C ? cut.per * cut.times : C;
-    constexpr int64_t kPlace = place_floats(C, DIM);
+    constexpr int64_t kPlace = place_floats(SLOTS * C, DIM);
     const int columns = n * cut.heads * most;
     const bool few = columns <= ctas;
     const int share_of = few ? kJoinWarps : 1;
@@ -1427,12 +1447,12 @@ __global__ void __launch_bounds__(kJoin)
             const int x = x0 + share_of * lane;
             const bool on = x < parts;
             const float f = on ? pow2(part(x)[i] - ref) : 0.f;
-            if (on) sum = fmaf(part(x)[kWarps * C + i], f, sum);
+            if (on) sum = fmaf(part(x)[SLOTS * C + i], f, sum);
             const int many = min(32, (parts - x0 + share_of - 1) / share_of);
 #pragma unroll 8
             for (int y = 0; y < many; ++y) {
                 const float g = __shfl_sync(kFull, f, y);
-                const float *from = part(x0 + share_of * y) + 2 * kWarps * C +
+                const float *from = part(x0 + share_of * y) + 2 * SLOTS * C +
                                     i * DIM;
 #pragma unroll
                 for (int k = 0; k < kQuads; ++k) {
@@ -1512,7 +1532,8 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
     Share share;
     share.sums = static_cast<float *>(workspace);
     share.records = reinterpret_cast<Record *>(
-        share.sums + 2 * (int64_t)p.ctas * place_floats(8 * NT, H::DIM));
+        share.sums +
+        2 * (int64_t)p.ctas * place_floats(kWarps * 8 * NT, H::DIM));
     share.cut = reinterpret_cast<int32_t *>(share.records + p.ctas);
     static_assert(sizeof(Record) + sizeof(int32_t) == kAttentionRecord, "");
     cudaError_t e = cudaSuccess;
@@ -1523,7 +1544,8 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
         e = launch_dependent(kernel, p.ctas, 32 * kWarps, kBytes, s, c, cut,
                              share, dtype);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attention_join_kernel<H::DIM, 8 * NT>, p.ctas,
+    return launch_dependent(attention_join_kernel<H::DIM, 8 * NT, kWarps>,
+                            p.ctas,
                             kJoin, 0, s, c, cut, share, dtype);
 }
 

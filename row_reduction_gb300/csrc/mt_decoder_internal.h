@@ -118,7 +118,7 @@ cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
 // A call on the matrix kernels: how its rows and query heads are cut into
 // tiles of 8 nt columns, and the CTAs that share its work.
 struct AttentionPlan {
-    int32_t nt;
+    int32_t nt;     // 0: the kernel for many rows, tiles of 64 columns
     int32_t times;  // query heads per key head
     int32_t per;    // rows of a tile
     int32_t parts;  // tiles that share a row's query heads
@@ -132,6 +132,7 @@ constexpr int kAttentionMaxCtas = 1024;
 constexpr int attention_ctas(int dim, int groups, int parts, int nt) {
     return nt > 1 || dim >= 128 ? 2 : 3;
 }
+constexpr int kAttentionRowCtas = 2;
 // Bytes behind the partial sums for each CTA: what it left there.
 constexpr int kAttentionRecord = 24;
 #define MT_DECLARE_ATTENTION(name)                                           \
@@ -146,6 +147,10 @@ MT_DECLARE_ATTENTION(launch_attention_int8_p1n1)
 MT_DECLARE_ATTENTION(launch_attention_int8_p1n2)
 MT_DECLARE_ATTENTION(launch_attention_int8_p2n1)
 MT_DECLARE_ATTENTION(launch_attention_int8_p2n2)
+MT_DECLARE_ATTENTION(launch_attention_rows_e4m3_p1)
+MT_DECLARE_ATTENTION(launch_attention_rows_e4m3_p2)
+MT_DECLARE_ATTENTION(launch_attention_rows_int8_p1)
+MT_DECLARE_ATTENTION(launch_attention_rows_int8_p2)
 #undef MT_DECLARE_ATTENTION
 
 // ---- norms around a block ------------------------------------------------------

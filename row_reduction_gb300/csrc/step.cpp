@@ -63,6 +63,7 @@ bool attention_head(const mt_attention_call_t &c) {
         default: return false;
     }
 }
+constexpr int64_t kManyColumns = 32;
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
@@ -75,13 +76,17 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     int sms = 0;
     if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
     p->times = c.q_heads / c.k_heads;
-    // 16 columns where a sequence has more than 8 on average
-    p->nt = c.dim <= 128 && (int64_t)p->times * c.rows > 8LL * c.sequences
-                ? 2 : 1;
-    const int columns = 8 * p->nt;
+    // Columns that a sequence has on average: the kernel for many rows, which
+    // fills tiles of 64 of them, from ROWS_FROM on; else 16 where there are more
+    // than 8.
+    const int64_t columns_all = (int64_t)p->times * c.rows;
+    const bool many = c.dim <= 128 && c.dim % 32 == 0 &&
+                      columns_all >= kManyColumns * (int64_t)c.sequences;
+    p->nt = many ? 0 : c.dim <= 128 && columns_all > 8LL * c.sequences ? 2 : 1;
+    const int columns = many ? 64 : 8 * p->nt;
     p->per = p->times < columns ? columns / p->times : 1;
     p->parts = (p->times + columns - 1) / columns;
-    p->heads = c.k_heads % 4 == 0 ? 4 : c.k_heads % 2 == 0 ? 2 : 1;
+    p->heads = many ? 1 : c.k_heads % 4 == 0 ? 4 : c.k_heads % 2 == 0 ? 2 : 1;
     const int es = dtype_size(dtype);
     const auto fours = [&](const void *q, int64_t row, int64_t head) {
         const uint64_t bits =
@@ -93,15 +98,18 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     p->whole = (fours(c.q, c.q_row, c.q_head) ? 1 : 0) |
                (fours(c.out, c.out_row, c.out_head) ? 2 : 0);
     // as many as are resident at once
-    p->ctas = sms * attention_ctas(c.dim, c.dim / c.group,
-                                   dtype == DT_BF16 ? 1 : 2, p->nt);
+    const int halves = dtype == DT_BF16 ? 1 : 2;
+    p->ctas = sms * (many ? kAttentionRowCtas
+                          : attention_ctas(c.dim, c.dim / c.group, halves,
+                                           p->nt));
     if (p->ctas > kAttentionMaxCtas) p->ctas = kAttentionMaxCtas;
     return MT_OK;
 }
 size_t attention_workspace(const mt_attention_call_t &c,
                            const AttentionPlan &p) {
-    return (size_t)p.ctas * (2 * 4 * 8 * (size_t)p.nt * (c.dim + 2) *
-                             sizeof(float) + kAttentionRecord);
+    const size_t columns = p.nt ? 4 * 8 * (size_t)p.nt : 64;
+    return (size_t)p.ctas * (2 * columns * (c.dim + 2) * sizeof(float) +
+                             kAttentionRecord);
 }
 
 // ---- norms around a block ----------------------------------------------------
@@ -209,7 +217,12 @@ mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
         return MT_ERR_INVALID_ARGUMENT;
     const bool int8 = call->format == MT_CACHE_INT8;
     const auto launch =
-        dtype == DT_BF16
+        p.nt == 0
+            ? (dtype == DT_BF16 ? int8 ? launch_attention_rows_int8_p1
+                                       : launch_attention_rows_e4m3_p1
+                                : int8 ? launch_attention_rows_int8_p2
+                                       : launch_attention_rows_e4m3_p2)
+        : dtype == DT_BF16
             ? (int8 ? p.nt == 2 ? launch_attention_int8_p1n2
                                 : launch_attention_int8_p1n1
                     : p.nt == 2 ? launch_attention_e4m3_p1n2
