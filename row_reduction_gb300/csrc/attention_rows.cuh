@@ -4,16 +4,21 @@
 // Here the queries are many enough to fill the instruction's 16 rows: a tile has
 // 64 columns (rows of a sequence times the query heads of a key head), 16 to a
 // warp, and all four warps go through the same chunks of 64 keys.  A chunk's
-// codes are copied as they are, a chunk ahead, widened to FP16 once for all
-// warps, and read from there as fragments by matrix loads (rows permuted so that
-// those touch every bank once).  Scores, references, scales and roundings are
-// as in attention_mma.cuh; what the scores give is the other product's first
-// operand as it lies.  Units, cut tiles and their joining are the same too.
+// codes are copied as they are while the one before is worked on, widened to
+// FP16 once for all warps, and read from there as fragments by matrix loads
+// (rows permuted so that those touch every bank once).  Scores, references,
+// scales and roundings are as in attention_mma.cuh; what the scores give is the
+// other product's first operand as it lies.  Units, cut tiles and their joining
+// are the same too.
 //
-// Bound: the instructions around the products, some 15 to a score and lane of
-// them; where attention_mma.cuh widens a chunk for 16 columns at a time, this
-// does for 64.  BF16, two sequences of 512 rows at 4096 keys, 32 + 8 heads of
-// 128, capped: MEASURED.
+// Taken from 48 columns per sequence on, on average: 32 rows of two sequences 34
+// us for 41 on tiles of 16 columns, 16 rows of 16 sequences (34 columns) 73 for
+// 66.
+//
+// Bound: shared memory (64% of its throughput: every warp reads all of a chunk
+// for its 16 columns) and the instructions around the products; those have 33%
+// of the tensor pipe.  BF16, two sequences of up to 512 rows at 4096 keys, 32 + 8
+// heads of 128, capped: 308 us, 185 TFLOP/s (372 us on tiles of 16 columns).
 #pragma once
 
 #include "attention_mma.cuh"
@@ -23,7 +28,7 @@ namespace {
 
 constexpr int kRowColumns = 64, kRowKeys = 64;
 
-template <class H>
+template <class H, int PARTS>
 struct RowShared {
     // 16-byte units of FP16 of a key, and the room that a row of them takes
     // (a multiple of 8 units, so that they can be permuted by the key).
@@ -33,9 +38,11 @@ struct RowShared {
         uint8_t k[kRowKeys * H::DIM], v[kRowKeys * H::DIM];
         float ks[kRowKeys][H::GROUPS], vs[kRowKeys][H::GROUPS];
     };
-    Codes codes[2];
+    Codes codes;
     uint4 k[kRowKeys * ROOM], v[kRowKeys * ROOM];
-    unsigned there[2][kWarps];       // keys with a slot, 16 to a warp
+    float ks[kRowKeys][H::GROUPS], vs[kRowKeys][H::GROUPS];
+    uint4 q[kWarps][PARTS][H::STEPS][32];  // fragments
+    unsigned there[kWarps];          // keys with a slot, 16 to a warp
     int32_t lo_any[2], hi_any[2], lo_all[2], hi_all[2];
     Deal deal;
     static __device__ __forceinline__ int place(int key, int unit) {
@@ -48,16 +55,14 @@ __device__ __forceinline__ void load_matrices(unsigned (&r)[4],
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, "
                  "[%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(smem_addr(p))
-                 : "memory");
+                 : "r"(smem_addr(p)));
 }
 __device__ __forceinline__ void load_matrices_t(unsigned (&r)[4],
                                                 const void *p) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, "
                  "%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(smem_addr(p))
-                 : "memory");
+                 : "r"(smem_addr(p)));
 }
 // Two values of a row of queries.
 __device__ __forceinline__ float2 load2(int dtype, bool whole, const void *p,
@@ -94,8 +99,7 @@ template <class H, bool INT8, int PARTS>
 struct RowWarp {
     static constexpr int N = kRowKeys / 8;      // tiles of 8 keys of a chunk
     static constexpr int TILES = H::DIM / 8;    // of the output
-    using Sh = RowShared<H>;
-    unsigned qf[PARTS][H::STEPS][4];
+    using Sh = RowShared<H, PARTS>;
     float o[TILES][4];              // in units of 2^-(up of its group)
     float ref[2], l[2], f[2], slope[2];
     int lo[2], hi[2], p[2];
@@ -125,7 +129,7 @@ struct RowWarp {
     // The tile's queries as fragments, its columns' factors and bounds.
     __device__ __forceinline__ void begin(const mt_attention_call_t &c,
                                           const Cut &cut, int dtype,
-                                          const Tile &a) {
+                                          const Tile &a, Sh &sh) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
         const int from = c.offsets[a.s];
         const int first = from + a.t * cut.per;
@@ -167,10 +171,12 @@ struct RowWarp {
                     const float u = bad ? 0.f : x[s][h].x * by;
                     const float v = bad ? 0.f : x[s][h].y * by;
                     const unsigned w = half_pair(u, v);
-                    qf[0][s][2 * h + i] = w;
+                    unsigned *to = &sh.q[threadIdx.x >> 5][0][s][lane].x;
+                    to[2 * h + i] = w;
                     if constexpr (PARTS == 2) {
                         const float2 r = from_half_pair(w);
-                        qf[1][s][2 * h + i] = half_pair(u - r.x, v - r.y);
+                        to[H::STEPS * 128 + 2 * h + i] =
+                            half_pair(u - r.x, v - r.y);
                     }
                 }
             f[i] = bad ? NAN
@@ -201,36 +207,49 @@ struct RowWarp {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     }
-    __device__ __forceinline__ void scores(const Sh &sh,
-                                           const typename Sh::Codes &st,
-                                           float (&z)[N][4]) {
+    __device__ __forceinline__ void scores(const Sh &sh, float (&z)[N][4]) {
         const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int n0 = 0; n0 < N; n0 += 4) {
+                // four tiles in turn, so that no product waits for the last
+                float acc[4][4] = {};
 #pragma unroll
                 for (int s = gr * H::PER; s < (gr + 1) * H::PER; s += 2) {
                     // 8 keys, four units: two steps
-                    unsigned b[4];
-                    load_matrices(b, &sh.k[Sh::place(8 * n + (lane & 7),
-                                                     2 * s + (lane >> 3))]);
+                    unsigned b[4][4];
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        mma16816(acc, qf[part][s], b[0], b[1]);
-                        mma16816(acc, qf[part][s + 1], b[2], b[3]);
+                    for (int y = 0; y < 4; ++y)
+                        load_matrices(
+                            b[y], &sh.k[Sh::place(8 * (n0 + y) + (lane & 7),
+                                                  2 * s + (lane >> 3))]);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 f4 =
+                                sh.q[threadIdx.x >> 5][part][s + h][lane];
+                            const unsigned q4[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                mma16816(acc[y], q4, b[y][2 * h],
+                                         b[y][2 * h + 1]);
+                        }
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int n = n0 + y;
+                        const float k = sh.ks[8 * n + 2 * q + e][gr];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &to = z[n][2 * i + e];
+                            const float from = acc[y][2 * i + e];
+                            to = gr == 0 ? from * k : fmaf(from, k, to);
+                        }
                     }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float k = st.ks[8 * n + 2 * q + e][gr];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        z[n][2 * i + e] =
-                            gr == 0 ? acc[2 * i + e] * k
-                                    : fmaf(acc[2 * i + e], k, z[n][2 * i + e]);
-                }
             }
         }
     }
@@ -313,8 +332,7 @@ struct RowWarp {
     }
     __device__ __forceinline__ void add(const float (&w)[N][4],
                                         unsigned hidden, bool masked,
-                                        const Sh &sh,
-                                        const typename Sh::Codes &st) {
+                                        const Sh &sh) {
         const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
         for (int gr = 0; gr < H::GROUPS; ++gr) {
@@ -323,7 +341,7 @@ struct RowWarp {
             for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x[n][e] = w[n][e] * st.vs[8 * n + 2 * q + (e & 1)][gr];
+                    x[n][e] = w[n][e] * sh.vs[8 * n + 2 * q + (e & 1)][gr];
             if (masked) {
                 // not seen: nothing, whatever stands in the scale
 #pragma unroll
@@ -370,27 +388,32 @@ struct RowWarp {
                 }
 #pragma unroll
             for (int d = gr * (H::GROUP / 8); d < (gr + 1) * (H::GROUP / 8);
-                 d += 2) {
-                float acc[2][4];
+                 d += 4) {
+                float acc[4][4];
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 4; ++y)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         acc[y][e] = PARTS == 1 ? o[d + y][e] : 0.f;
 #pragma unroll
                 for (int t = 0; t < N / 2; ++t) {
-                    // 16 keys, two units: two tiles of the output
-                    unsigned b[4];
-                    load_matrices_t(b, &sh.v[Sh::place(16 * t + (lane & 15),
-                                                       d + (lane >> 4))]);
+                    // 16 keys, two units each: four tiles of the output
+                    unsigned b[2][4];
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        mma16816(acc[0], pf[part][t], b[0], b[1]);
-                        mma16816(acc[1], pf[part][t], b[2], b[3]);
-                    }
+                    for (int y = 0; y < 2; ++y)
+                        load_matrices_t(
+                            b[y],
+                            &sh.v[Sh::place(16 * t + (lane & 15),
+                                            d + 2 * y + (lane >> 4))]);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            mma16816(acc[y], pf[part][t], b[y / 2][2 * (y & 1)],
+                                     b[y / 2][2 * (y & 1) + 1]);
                 }
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 4; ++y)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         o[d + y][e] = PARTS == 1 ? acc[y][e]
@@ -446,12 +469,12 @@ template <class H, bool INT8, int PARTS>
 __device__ __forceinline__ void rows_run(const mt_attention_call_t &c,
                                          const Cut &cut, int dtype,
                                          const Tile &a, int64_t u0, int64_t u1,
-                                         RowShared<H> &sh,
+                                         RowShared<H, PARTS> &sh,
                                          RowWarp<H, INT8, PARTS> &w) {
-    using Sh = RowShared<H>;
+    using Sh = RowShared<H, PARTS>;
     constexpr int N = kRowKeys / 8, kOwn = kRowKeys / kWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    w.begin(c, cut, dtype, a);
+    w.begin(c, cut, dtype, a, sh);
     // What the columns see: two warps look at 32 each.
     if (warp < 2) {
         const int from = c.offsets[a.s];
@@ -500,10 +523,10 @@ __device__ __forceinline__ void rows_run(const mt_attention_call_t &c,
                         a.head * H::DIM;
     const uint8_t *vp = static_cast<const uint8_t *>(c.v_codes) +
                         a.head * H::DIM;
-    const auto load = [&](Page page, int stage) {
+    const auto load = [&](Page page) {
         constexpr int kPieces = H::DIM / 16;
         const int slot = slot_in(c, page);
-        typename Sh::Codes &to = sh.codes[stage];
+        typename Sh::Codes &to = sh.codes;
 #pragma unroll
         for (int i = 0; i < kOwn * kPieces / 32; ++i) {
             const int piece = lane + 32 * i;
@@ -523,26 +546,25 @@ __device__ __forceinline__ void rows_run(const mt_attention_call_t &c,
                 to.vs[key], c.v_scales + a.head * H::GROUPS + from, slot >= 0);
         }
         const unsigned there = __ballot_sync(kFull, slot >= 0);
-        if (lane == 0) sh.there[stage][warp] = there & 0xffffu;
+        if (lane == 0) sh.there[warp] = there & 0xffffu;
     };
     const Page first = page_at(u);
     Page next = page_at(u + 1);
-    int stage = 0;
-    if (u < end) load(first, 0);
+    if (u < end) load(first);
     asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll 1
-    for (; u < end; ++u, stage ^= 1) {
+    for (; u < end; ++u) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the chunk is there, the one before is done with
-        const Page then = next;
-        next = page_at(u + 2);
-        if (u + 1 < end) load(then, stage ^ 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const typename Sh::Codes &st = sh.codes[stage];
+        const typename Sh::Codes &st = sh.codes;
         uint64_t there = 0;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x)
-            there |= (uint64_t)sh.there[stage][x] << (kOwn * x);
+            there |= (uint64_t)sh.there[x] << (kOwn * x);
+        for (int x = tid; x < kRowKeys * H::GROUPS; x += 32 * kWarps) {
+            sh.ks[0][x] = st.ks[0][x];
+            sh.vs[0][x] = st.vs[0][x];
+        }
         // Widened once for all: 16 codes are two units.
         constexpr int kPieces = H::DIM / 16;
 #pragma unroll
@@ -564,26 +586,33 @@ __device__ __forceinline__ void rows_run(const mt_attention_call_t &c,
             to[Sh::place(key, 2 * unit + 1)] = x1;
         }
         __syncthreads();
+        // The codes' place is free: the next chunk is on its way while this
+        // one is worked on.
+        const Page then = next;
+        next = page_at(u + 2);
+        if (u + 1 < end) load(then);
+        asm volatile("cp.async.commit_group;" ::: "memory");
         if (there == 0) continue;
         const int j0 = (int)(u * kRowKeys);
         const bool whole = ~there == 0 && j0 >= lo_all &&
                            j0 + kRowKeys - 1 <= hi_all;
         float z[N][4];
         unsigned hidden;
-        w.scores(sh, st, z);
+        w.scores(sh, z);
         const bool masked = w.bend(c, whole, j0, there, hidden, z);
         w.weigh(z);
-        w.add(z, hidden, masked, sh, st);
+        w.add(z, hidden, masked, sh);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <class H, bool INT8, int PARTS>
-__global__ void __launch_bounds__(32 * kWarps, kAttentionRowCtas)
+__global__ void __launch_bounds__(32 * kWarps, attention_row_ctas(H::DIM, H::GROUPS, PARTS))
     attention_rows_kernel(const mt_attention_call_t c, const Cut cut,
                           const Share share, int dtype) {
     extern __shared__ __align__(16) uint8_t shared[];
-    RowShared<H> &sh = *reinterpret_cast<RowShared<H> *>(shared);
+    RowShared<H, PARTS> &sh =
+        *reinterpret_cast<RowShared<H, PARTS> *>(shared);
     grid_wait_prerequisites();
     RowWarp<H, INT8, PARTS> w;
     deal_units(c, cut, share, sh.deal,
@@ -601,8 +630,8 @@ template <class H, bool INT8, int PARTS>
 cudaError_t launch_rows_as(const AttentionPlan &p,
                            const mt_attention_call_t &c, int dtype,
                            void *workspace, cudaStream_t s) {
-    constexpr size_t kBytes = sizeof(RowShared<H>);
-    static_assert((kBytes + 1024) * kAttentionRowCtas <= 228 * 1024,
+    constexpr size_t kBytes = sizeof(RowShared<H, PARTS>);
+    static_assert((kBytes + 1024) * attention_row_ctas(H::DIM, H::GROUPS, PARTS) <= 228 * 1024,
                   "the CTAs that share an SM fit its shared memory");
     const Cut cut = {p.times, p.per, p.parts, 1, 6, c.k_heads * p.parts,
                      p.whole};

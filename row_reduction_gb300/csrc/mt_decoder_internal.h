@@ -132,7 +132,9 @@ constexpr int kAttentionMaxCtas = 1024;
 constexpr int attention_ctas(int dim, int groups, int parts, int nt) {
     return nt > 1 || dim >= 128 ? 2 : 3;
 }
-constexpr int kAttentionRowCtas = 2;
+constexpr int attention_row_ctas(int dim, int groups, int parts) {
+    return parts == 1 && (dim < 128 || groups == 1) ? 3 : 2;
+}
 // Bytes behind the partial sums for each CTA: what it left there.
 constexpr int kAttentionRecord = 24;
 #define MT_DECLARE_ATTENTION(name)                                           \

@@ -63,7 +63,7 @@ bool attention_head(const mt_attention_call_t &c) {
         default: return false;
     }
 }
-constexpr int64_t kManyColumns = 32;
+constexpr int64_t kManyColumns = 48;
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
@@ -76,9 +76,9 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     int sms = 0;
     if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
     p->times = c.q_heads / c.k_heads;
-    // Columns that a sequence has on average: the kernel for many rows, which
-    // fills tiles of 64 of them, from ROWS_FROM on; else 16 where there are more
-    // than 8.
+    // Columns that a sequence has on average: from 48 on the kernel for many
+    // rows, which fills tiles of 64 of them (34 us for 41 at 132 columns, 73 for
+    // 66 at 34); else tiles of 16 where there are more than 8.
     const int64_t columns_all = (int64_t)p->times * c.rows;
     const bool many = c.dim <= 128 && c.dim % 32 == 0 &&
                       columns_all >= kManyColumns * (int64_t)c.sequences;
@@ -99,7 +99,7 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
                (fours(c.out, c.out_row, c.out_head) ? 2 : 0);
     // as many as are resident at once
     const int halves = dtype == DT_BF16 ? 1 : 2;
-    p->ctas = sms * (many ? kAttentionRowCtas
+    p->ctas = sms * (many ? attention_row_ctas(c.dim, c.dim / c.group, halves)
                           : attention_ctas(c.dim, c.dim / c.group, halves,
                                            p->nt));
     if (p->ctas > kAttentionMaxCtas) p->ctas = kAttentionMaxCtas;

@@ -264,6 +264,44 @@ def test_attention_options(dt, shape, batch, kind):
     attention_check(a, **kw)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("heads", [(80, 1), (70, 2), (9, 3), (130, 1)],
+                         ids=str)
+@pytest.mark.parametrize("batch", ["tokens", "chunk"])
+def test_attention_many_query_heads(dt, fmt, heads, batch):
+    """Query heads of a key head that take several tiles, and numbers that
+    fill none."""
+    rows = [(r, max(r, k)) for r, k in BATCHES[batch]]
+    a = attention_inputs(sum(heads), rows, *heads, 64, 64, 16, fmt,
+                         DTYPES[dt], behind=2)
+    attention_check(a, window=100)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(8, 2, 128, 128), (4, 1, 96, 96),
+                                   (6, 2, 64, 32)], ids=str)
+@pytest.mark.parametrize("kind", ["plain", "prefix", "documents", "window"])
+def test_attention_prompts(dt, shape, kind):
+    """Prompts whose rows fill tiles of 64 columns, cut wherever the CTAs'
+    shares of the work end."""
+    hq, hk, dim, group = shape
+    rows = [(200, 900), (64, 64), (0, 0), (65, 1000), (1, 700), (130, 131)]
+    a = attention_inputs(dim, rows, hq, hk, dim, group, 16, "e4m3",
+                         DTYPES[dt], before=1, behind=2)
+    p = [0] + [v for r, k in rows for v in range(k - r, k)] + [0, 0]
+    kw = {}
+    if kind == "prefix":
+        kw = dict(last=i32([max(v, 333) for v in p]), cap=5.0)
+    elif kind == "documents":
+        kw = dict(first=i32([v // 50 * 50 for v in p]),
+                  slopes=torch.rand(hq, generator=gen(1), device="cuda") / 9)
+    elif kind == "window":
+        kw = dict(window=70)
+    out = attention_check(a, **kw).clone()
+    assert torch.equal(out, attention_check(a, **kw))
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("dim,group", [(128, 128), (64, 32), (30, 10)])
 def test_attention_strided_views(dt, dim, group):
@@ -495,6 +533,40 @@ def test_block_norm(dt, gate, norms, shape):
 def test_block_norm_backward(dt, gate, norms, shape):
     a = norm_inputs(sum(shape), *shape, DTYPES[dt], gate, norms)
     back_check(a, 1, residual_scale=0.7)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [1, 2, 3, 7])
+@pytest.mark.parametrize("cols", [513, 1026, 3001, 8190])
+def test_block_norm_off_the_packs_bounds(dt, off, cols):
+    """Matrices that begin anywhere among 16-byte packs, each somewhere else,
+    rows one after the other and apart; more rows than CTAs; in place."""
+    dtype, rows = DTYPES[dt], 700 if cols < 2000 else 310
+    a = norm_inputs(off, rows, cols, dtype, "matrix", "both")
+
+    def moved(t, by, stride):
+        flat = torch.full((rows * stride + by + 8,), 5.0, dtype=dtype,
+                          device="cuda")
+        v = flat.as_strided((rows, cols), (stride, 1), by)
+        v.copy_(t)
+        return v
+    b = dict(a, x=moved(a["x"], off, cols),
+             residual=moved(a["residual"], off + 2, cols + 1),
+             gate=moved(a["gate"], 2 * off, cols + 3))
+    out = moved(a["x"], off + 1, cols + 1)
+    y, h = norm_check(b, out=out, h_out=b["residual"].clone())
+    y0, h0 = norm_check(a)
+    assert torch.equal(y, y0) and torch.equal(h, h0)
+    got = back_check(b, 1)
+    assert len(got) == 5
+    g = gen(1)
+    dy, dh = (randn(g, rows, cols, dtype=dtype) for _ in range(2))
+    args = (a["weight"], a["gate"], a["next_weight"])
+    want = mt.block_norm_backward(dy, dh, a["x"], h0, *args)
+    dy, dh = moved(dy, off, cols), moved(dh, off + 5, cols)
+    got = mt.block_norm_backward(dy, dh, a["x"], h0, *args, out=(dy, dh))
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
