@@ -16,7 +16,7 @@ from collections import namedtuple
 from . import _decoder as _d
 from ._binding import _check
 from ._decoder import (_F, _I32, _I64, _P, _cache, _dense, _first, _heads,
-                       _here, _On, _opt, _rows, _tensor, _three)
+                       _On, _opt, _rows, _tensor, _three)
 
 MT_NORM_AFTER, MT_NORM_BEFORE = 1, 2
 
@@ -185,11 +185,10 @@ def _workspace(name, dt, call, like):
 
 def _on(index, stream, run):
     """run(handle) on the call's device and stream."""
-    handle = _here(index, stream)
-    if handle is None:
-        with _On(index, stream) as handle:
-            return run(handle)
-    return run(handle)
+    if stream is None and _d._torch._C._cuda_getDevice() == index:
+        return run(_d._torch._C._cuda_getCurrentRawStream(index))
+    with _On(index, stream) as handle:
+        return run(handle)
 
 
 def _length(t, name, dtype):
@@ -376,11 +375,26 @@ def _kind(norms, weight, next_weight):
 
 def _matrix(t, name, dtype, shape, index):
     """(address, row stride) of a matrix with dense rows."""
+    try:
+        st = t.stride()
+        if (st[1] == 1 and t.dtype is dtype and t.shape == shape and
+                t.get_device() == index):
+            return t.data_ptr(), st[0]
+    except (AttributeError, IndexError):
+        pass
     at, stride, width = _rows(t, name, dtype, shape[0], index)
     if width != shape[1]:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
     return at, stride
+
+
+def _dense_like(t, shape, stride):
+    """A new dense matrix of t's shape, type and device (empty_like, the
+    quicker call, where t is dense)."""
+    if stride == shape[1]:
+        return _d._torch.empty_like(t)
+    return _d._torch.empty(shape, dtype=t.dtype, device=t.device)
 
 
 def _gate(gate, dtype, shape, index):
@@ -406,7 +420,6 @@ def block_norm(x, residual, weight=None, gate=None, next_weight=None,
     (ones).  Returns (y, h), with norms "after" h alone.  out and h_out: where
     to write y and h; either may be x or residual."""
     dt, index = _first(x, "x")
-    torch = _d._torch
     dtype, shape = x.dtype, x.shape
     if len(shape) != 2:
         raise ValueError(f"x must be [rows, cols], got {tuple(shape)}")
@@ -425,12 +438,12 @@ def block_norm(x, residual, weight=None, gate=None, next_weight=None,
         h, y = h_out, out
         py = ys = 0
         if h is None:
-            h = torch.empty(shape, dtype=dtype, device=x.device)
+            h = _dense_like(x, shape, xs)
             ph, hs = h.data_ptr(), shape[1]
         else:
             ph, hs = _matrix(h, "h_out", dtype, shape, index)
         if before and y is None:
-            y = torch.empty(shape, dtype=dtype, device=x.device)
+            y = _dense_like(x, shape, xs)
             py, ys = y.data_ptr(), shape[1]
         elif before:
             py, ys = _matrix(y, "out", dtype, shape, index)
@@ -480,29 +493,30 @@ def block_norm_backward(dy, dh, x, h, weight=None, gate=None,
     pg, gs = _gate(gate, dtype, shape, index)
     pw = _opt(weight, "weight", dtype, shape[1:], index)
     pn = _opt(next_weight, "next_weight", dtype, shape[1:], index)
+    stride = dys if before else dhs
 
     def run(handle):
         dx, dres = (None, None) if out is None else out
-        device, cols = one.device, shape[1]
+        cols = shape[1]
         if dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=device)
+            dx = _dense_like(one, shape, stride)
             pdx, dxs = dx.data_ptr(), cols
         else:
             pdx, dxs = _matrix(dx, "out (dx)", dtype, shape, index)
         if dres is None:
-            dres = torch.empty(shape, dtype=dtype, device=device)
+            dres = _dense_like(one, shape, stride)
             pdr, drs = dres.data_ptr(), cols
         else:
             pdr, drs = _matrix(dres, "out (dresidual)", dtype, shape, index)
         got, sums, pdg, dgs = [dx, dres], [0, 0, 0], 0, 0
         wide = gate is not None and gate.dim() == 2
         if wide:
-            dgate = torch.empty(shape, dtype=dtype, device=device)
+            dgate = _dense_like(one, shape, stride)
             pdg, dgs = dgate.data_ptr(), cols
             got.append(dgate)
         for i, t in enumerate((None if wide else gate, weight, next_weight)):
             if t is not None:
-                d = torch.empty(cols, dtype=f32, device=device)
+                d = torch.empty(cols, dtype=f32, device=one.device)
                 sums[i] = d.data_ptr()
                 got.append(d)
         call = _NORM_BACK.pack(
