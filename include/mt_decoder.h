@@ -305,7 +305,9 @@ typedef struct mt_cache_extend_call {
     int32_t page_size;         /* >= 1 */
 } mt_cache_extend_call_t;
 
-/* The outputs must not be the inputs (the table apart). */
+/* The outputs, and the table, must not be inputs or each other.  With fewer
+ * rows than the counts add up to, only so many are written out; the lengths
+ * and pages are those of all. */
 MT_API mt_status mt_cache_extend(const mt_cache_extend_call_t *call,
                                  mt_stream_t stream);
 
@@ -333,15 +335,17 @@ MT_API mt_status mt_cache_extend(const mt_cache_extend_call_t *call,
  * stand in slots that a row of the sequence sees.) */
 typedef struct mt_attention_call {
     const void *q;             /* rows x q_heads x dim */
-    void *out;                 /* the same type and shape */
+    void *out;                 /* the same type and shape; not q */
     float *lse;                /* rows x q_heads, contiguous, or NULL */
     int64_t q_row, q_head, out_row, out_head; /* strides in elements */
     const void *k_codes, *v_codes;    /* as in mt_cache_rows_t */
     const float *k_scales, *v_scales;
     const int32_t *table;      /* sequences x pages */
     int64_t table_stride;
-    const int32_t *offsets;    /* sequences + 1, not decreasing */
-    const int32_t *starts;     /* sequences */
+    const int32_t *offsets;    /* sequences + 1, not decreasing; clamped to
+                                  0 .. rows */
+    const int32_t *starts;     /* sequences; a row at a negative position sees
+                                  nothing */
     const int32_t *first, *last; /* rows each, or NULL */
     const float *slopes;       /* q_heads, or NULL */
     int64_t rows;              /* 0..2^31 - 1 */
@@ -354,7 +358,8 @@ typedef struct mt_attention_call {
     int32_t format;            /* mt_cache_format */
     int32_t window;            /* >= 1, or 0: none */
     float scale;               /* finite */
-    float cap;                 /* > 0 and finite, or 0: none */
+    float cap;                 /* > 0 and finite, as is 4 scale / cap; or 0:
+                                  none */
     int32_t reserved;          /* 0 */
 } mt_attention_call_t;
 

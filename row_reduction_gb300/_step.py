@@ -145,6 +145,15 @@ _NORM = struct.Struct("@7P6q2i2f")
 _NORM_BACK = struct.Struct("@13P9q2i2f")
 
 
+def _pack(form, *values):
+    """A call's structure."""
+    try:
+        return form.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is out of its type's range: {e}") \
+            from None
+
+
 def _call(name, *args):
     st = _calls[name](*args)
     if st != _d.MT_OK:
@@ -234,7 +243,8 @@ def cache_extend(table, lengths, counts, free_pages, free_count, page_size,
     :class:`CacheStep`: where the step's rows, packed sequence by sequence,
     stand, for :func:`cache_write`, :func:`rotary` and :func:`cache_attention`
     (whose starts are the old lengths); rows behind the batch, up to `rows`,
-    get slot -1.  A sequence for which there are not enough pages, in the list
+    get slot -1 (with fewer rows than the counts add up to, only so many are
+    written out).  A sequence for which there are not enough pages, in the list
     or in the table's width, gets none: its length stays and its rows have
     slot -1.  The lists themselves stay: pass the new lengths and free_count
     to the next call.  out: a CacheStep to write to."""
@@ -274,8 +284,8 @@ def cache_extend(table, lengths, counts, free_pages, free_count, page_size,
                       _dense(step.free_count, "new free_count", i32, (1,),
                              index))
         _call("mt_cache_extend",
-              _EXTEND.pack(at, stride, lens, more, free, left, *places, rows,
-                           pages, n, size, page_size), handle)
+              _pack(_EXTEND, at, stride, lens, more, free, left, *places, rows,
+                    pages, n, size, page_size), handle)
         return step
     return _on(index, stream, run)
 
@@ -303,7 +313,7 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
     slopes[head] times the distance in positions.  Returns [rows, q_heads,
     dim], zeros for a row that sees nothing, and with return_lse also the
     logarithm of the sum of the exponentials of its scores (float32 [rows,
-    q_heads], then -inf).  out: where to write; rows outside the batch
+    q_heads], then -inf).  out: where to write, not q; rows outside the batch
     (offsets[0] .. offsets[-1]) are left as they were (in new outputs:
     zeros)."""
     dt, index = _first(q, "q")
@@ -327,8 +337,8 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
     lo = _opt(first, "first", i32, (rows,), index)
     hi = _opt(last, "last", i32, (rows,), index)
     sl = _opt(slopes, "slopes", torch.float32, (q_heads,), index)
-    if cap is not None and not cap > 0:
-        raise ValueError(f"cap must be above 0, got {cap}")
+    if cap is not None and not cap >= 2.0 ** -126:
+        raise ValueError(f"cap must be above 0 (from 2^-126 on), got {cap}")
     if window is not None and window < 1:
         raise ValueError(f"window must be at least 1, got {window}")
     if scale is None:
@@ -343,11 +353,12 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
             o, orow, oh = _heads(y, "out", dtype, shape, index)
         lse = torch.full((rows, q_heads), -torch.inf, device=q.device) \
             if return_lse else None
-        call = _ATTENTION.pack(
-            x, o, 0 if lse is None else lse.data_ptr(), xr, xh, orow, oh, kc,
-            vc, ks, vs, at, stride, offs, from_, lo, hi, sl, rows, slots, n,
+        call = _pack(
+            _ATTENTION, x, o, 0 if lse is None else lse.data_ptr(), xr, xh,
+            orow, oh, kc, vc, ks, vs, at, stride, offs, from_, lo, hi, sl, rows, slots, n,
             pages, page_size, q_heads, heads, dim, dim // like[2][2],
-            _d._FORMATS[like[0]], window or 0, scale, cap or 0.0, 0)
+            _d._FORMATS[like[0]], min(window or 0, 2 ** 31 - 1), scale,
+            cap or 0.0, 0)
         held, address, size = _workspace("mt_cache_attention_workspace", dt,
                                          call, q)
         _call("mt_cache_attention", dt, call, address, size, handle)
@@ -447,8 +458,8 @@ def block_norm(x, residual, weight=None, gate=None, next_weight=None,
             py, ys = y.data_ptr(), shape[1]
         elif before:
             py, ys = _matrix(y, "out", dtype, shape, index)
-        _call("mt_block_norm", dt, _NORM.pack(
-            px, pr, pg, pw, pn, ph, py, xs, rs, gs, hs, ys, shape[0],
+        _call("mt_block_norm", dt, _pack(
+            _NORM, px, pr, pg, pw, pn, ph, py, xs, rs, gs, hs, ys, shape[0],
             shape[1], kind, eps, residual_scale), handle)
         return (y, h) if before else h
     return _on(index, stream, run)
@@ -519,8 +530,8 @@ def block_norm_backward(dy, dh, x, h, weight=None, gate=None,
                 d = torch.empty(cols, dtype=f32, device=one.device)
                 sums[i] = d.data_ptr()
                 got.append(d)
-        call = _NORM_BACK.pack(
-            pdy, pdh, px, ph, pg, pw, pn, pdx, pdr, pdg, *sums, dys, dhs, xs,
+        call = _pack(
+            _NORM_BACK, pdy, pdh, px, ph, pg, pw, pn, pdx, pdr, pdg, *sums, dys, dhs, xs,
             hs, gs, dxs, drs, dgs, shape[0], shape[1], kind, eps,
             residual_scale)
         held, address, size = _workspace("mt_block_norm_backward_workspace",

@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(kAnyThreads)
         row >= c.offsets[c.sequences])
         return;
     const int s = sequence_of(c.offsets, c.sequences, row);
-    const int64_t start = c.starts[s], from = c.offsets[s];
+    const int64_t start = c.starts[s], from = begin_of(c, s);
     const int64_t p = start + (row - from);
     int64_t lo, hi;
-    row_sees(c, row, p, start + (c.offsets[s + 1] - from), lo, hi);
+    row_sees(c, row, p, start + (begin_of(c, s + 1) - from), lo, hi);
     const int key_head = head / (c.q_heads / c.k_heads);
     const int groups = c.dim / c.group;
     const int32_t *pages = c.table + s * c.table_stride;

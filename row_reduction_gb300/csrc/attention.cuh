@@ -41,6 +41,13 @@ __device__ __forceinline__ float capped2(float z2, float cap2) {
     return fmaf(-2.f * cap2, r, cap2);
 }
 
+// Where sequence s begins among the call's rows (ends at s + 1): whatever
+// stands in offsets, no row is past them.
+__device__ __forceinline__ int32_t begin_of(const mt_attention_call_t &c,
+                                            int s) {
+    return min(max(c.offsets[s], 0), (int32_t)c.rows);
+}
+
 // The sequence of a row of the batch (offsets[0] <= r < offsets[sequences]).
 __device__ __forceinline__ int sequence_of(const int32_t *offsets, int n,
                                            int64_t r) {

@@ -151,12 +151,13 @@ struct Tiles {
 __device__ __forceinline__ Tiles tiles_of(const mt_attention_call_t &c,
                                           const Cut &cut, int s) {
     Tiles t;
-    const int64_t n = (int64_t)c.offsets[s + 1] - c.offsets[s];
+    const int64_t n = (int64_t)begin_of(c, s + 1) - begin_of(c, s);
     t.start = max(c.starts[s], 0);
     t.rows = (int32_t)max(n, (int64_t)0);
     t.per = cut.per;
     t.count = (t.rows + cut.per - 1) / cut.per;
-    t.window = c.window;
+    // rows at negative positions see nothing; their tiles begin at key 0
+    t.window = c.starts[s] < 0 ? 0 : c.window;
     t.log2 = cut.log2;
     t.all = c.last != nullptr;
     return t;
@@ -874,7 +875,7 @@ struct Queries {
                                          const Cut &cut, int dtype,
                                          const Tile &a, int hs, int ks,
                                          int warps) {
-        const int from = c.offsets[a.s] + a.t * cut.per;
+        const int from = begin_of(c, a.s) + a.t * cut.per;
         const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
         const bool whole = cut.whole & 1;
 #pragma unroll
@@ -985,7 +986,7 @@ __device__ __forceinline__ void tile_bounds(const mt_attention_call_t &c,
                                             Shared<H, PARTS, NT> &sh) {
     constexpr int C = 8 * NT;
     const int col = threadIdx.x & 31;
-    const int from = c.offsets[a.s];
+    const int from = begin_of(c, a.s);
     const Place at = place_of<C>(cut, from + a.t * cut.per,
                                  min(cut.per, a.tiles.rows - a.t * cut.per),
                                  a.head + hs, a.part, col);
@@ -995,7 +996,7 @@ __device__ __forceinline__ void tile_bounds(const mt_attention_call_t &c,
     if (threadIdx.x >= 32) return;
     Column k = {INT32_MIN, INT32_MAX, 0, 0};
     if (used) {
-        const int64_t n = (int64_t)c.offsets[a.s + 1] - from;
+        const int64_t n = (int64_t)begin_of(c, a.s + 1) - from;
         const int64_t start = c.starts[a.s], p = start + (at.row - from);
         int64_t lo, hi;
         row_sees(c, at.row, p, start + n, lo, hi);
@@ -1183,7 +1184,7 @@ __device__ __forceinline__ void tile_end(const mt_attention_call_t &c,
             }
     }
     __syncthreads();
-    const int from = c.offsets[a.s] + a.t * cut.per;
+    const int from = begin_of(c, a.s) + a.t * cut.per;
     const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
     const int columns = columns_of<C>(cut, rows, a.part);
     const int warps = kWarps / cut.heads;
@@ -1323,7 +1324,7 @@ __device__ __forceinline__ void deal_units(const mt_attention_call_t &c,
                 if (tid == 0)
                     share.records[blockIdx.x] = {
                         (int)quotient(x * ctas - 1, total),
-                        c.offsets[a.s] + a.t * cut.per,
+                        begin_of(c, a.s) + a.t * cut.per,
                         min(cut.per, a.tiles.rows - a.t * cut.per), a.head,
                         a.part};
             }

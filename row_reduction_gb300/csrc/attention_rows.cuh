@@ -131,7 +131,7 @@ struct RowWarp {
                                           const Cut &cut, int dtype,
                                           const Tile &a, Sh &sh) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-        const int from = c.offsets[a.s];
+        const int from = begin_of(c, a.s);
         const int first = from + a.t * cut.per;
         const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
         const int dt = PARTS == 1 ? (int)DT_BF16 : dtype;
@@ -187,7 +187,7 @@ struct RowWarp {
             hi[i] = INT32_MAX;
             p[i] = 0;
             if (at.used) {
-                const int64_t n = (int64_t)c.offsets[a.s + 1] - from;
+                const int64_t n = (int64_t)begin_of(c, a.s + 1) - from;
                 const int64_t start = c.starts[a.s];
                 const int64_t pos = start + (at.row - from);
                 int64_t b0, b1;
@@ -426,7 +426,7 @@ struct RowWarp {
                                         const Tile &a, bool whole,
                                         float *sums) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-        const int first = c.offsets[a.s] + a.t * cut.per;
+        const int first = begin_of(c, a.s) + a.t * cut.per;
         const int rows = min(cut.per, a.tiles.rows - a.t * cut.per);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -477,13 +477,13 @@ __device__ __forceinline__ void rows_run(const mt_attention_call_t &c,
     w.begin(c, cut, dtype, a, sh);
     // What the columns see: two warps look at 32 each.
     if (warp < 2) {
-        const int from = c.offsets[a.s];
+        const int from = begin_of(c, a.s);
         const Place at = place_of<kRowColumns>(
             cut, from + a.t * cut.per,
             min(cut.per, a.tiles.rows - a.t * cut.per), a.head, a.part, tid);
         int lo = INT32_MIN, hi = INT32_MAX;
         if (at.used) {
-            const int64_t n = (int64_t)c.offsets[a.s + 1] - from;
+            const int64_t n = (int64_t)begin_of(c, a.s + 1) - from;
             const int64_t start = c.starts[a.s];
             int64_t b0, b1;
             row_sees(c, at.row, start + (at.row - from), start + n, b0, b1);

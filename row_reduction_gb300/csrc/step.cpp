@@ -21,6 +21,7 @@ mt_status attention_setup(int dtype, const mt_attention_call_t *c,
         c->dim % c->group != 0 || c->window < 0 || c->reserved != 0 ||
         (c->format != MT_CACHE_E4M3 && c->format != MT_CACHE_INT8) ||
         !isfinite(c->scale) || !(c->cap >= 0.f) || !isfinite(c->cap) ||
+        (c->cap > 0.f && !isfinite(c->scale / c->cap * 4.f)) ||
         c->table_stride < 0)
         return MT_ERR_INVALID_ARGUMENT;
     if (c->dim > kAttentionMaxDim || c->q_heads > 65536 ||
@@ -45,7 +46,8 @@ mt_status attention_setup(int dtype, const mt_attention_call_t *c,
     *empty = c->rows == 0 || c->sequences == 0;
     if (*empty) return MT_OK;
     const bool keys = c->slots > 0 && c->pages > 0;
-    if (!c->q || !c->out || !c->offsets || !c->starts ||
+    // other tiles' rows of q may be read after a tile is written
+    if (!c->q || !c->out || c->out == c->q || !c->offsets || !c->starts ||
         (keys && (!c->k_codes || !c->v_codes || !c->k_scales ||
                   !c->v_scales || !c->table)))
         return MT_ERR_INVALID_ARGUMENT;
@@ -148,6 +150,26 @@ size_t norm_workspace(const mt_block_norm_back_t &c) {
                : 0;
 }
 
+// Whether no output of the call is one of its inputs or another output (those
+// without a value are no matter).
+bool apart(const mt_cache_extend_call_t &c) {
+    const void *in[] = {c.lengths, c.counts, c.free_pages, c.free_count};
+    const void *out[] = {c.offsets, c.new_free_count,
+                         c.sequences > 0 ? c.new_lengths : nullptr,
+                         c.rows > 0 ? c.slots : nullptr,
+                         c.rows > 0 ? c.positions : nullptr,
+                         c.sequences > 0 && c.pages > 0 ? c.table : nullptr};
+    constexpr int kOut = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < kOut; ++i) {
+        if (out[i] == nullptr) continue;
+        for (const void *p : in)
+            if (p == out[i]) return false;
+        for (int j = 0; j < i; ++j)
+            if (out[j] == out[i]) return false;
+    }
+    return true;
+}
+
 }  // namespace
 }  // namespace mt
 
@@ -170,13 +192,11 @@ mt_status mt_cache_extend(const mt_cache_extend_call_t *call,
         misaligned(c.new_lengths, 4) || misaligned(c.new_free_count, 4))
         return MT_ERR_INVALID_ARGUMENT;
     if (!c.free_count || !c.offsets || !c.new_free_count ||
-        c.new_free_count == c.free_count ||
         (c.free_size > 0 && !c.free_pages) ||
         (c.rows > 0 && (!c.slots || !c.positions)) ||
         (c.sequences > 0 && (!c.lengths || !c.counts || !c.new_lengths ||
-                             c.new_lengths == c.lengths ||
-                             c.new_lengths == c.counts ||
-                             (c.pages > 0 && !c.table))))
+                             (c.pages > 0 && !c.table))) ||
+        !apart(c))
         return MT_ERR_INVALID_ARGUMENT;
     if (c.rows > INT32_MAX || c.sequences == INT32_MAX ||
         c.free_size == INT32_MAX)

@@ -883,6 +883,78 @@ def test_explicit_streams():
         assert all(torch.equal(p, q) for p, q in zip(ge, we))
 
 
+# ---- what device arrays may hold -----------------------------------------------
+@pytest.mark.parametrize("dim,group", [(128, 64), (64, 64), (40, 40)])
+@pytest.mark.parametrize("rows", [(3, 5), (100, 130)])
+@pytest.mark.parametrize("window", [None, 20, 2 ** 40])
+def test_attention_negative_starts(dim, group, rows, window):
+    """Rows at negative positions see nothing; those behind them, in the same
+    sequence, what a window leaves."""
+    batch = [(rows[0], rows[0] - 2), (rows[1], rows[1] // 2), (4, 60)]
+    a = attention_inputs(dim, batch, 4, 1, dim, group, 16, "e4m3",
+                         torch.bfloat16)
+    assert a["starts"].tolist()[:2] == [-2, rows[1] // 2 - rows[1]]
+    attention_check(a, window=window)
+
+
+@pytest.mark.parametrize("dim,group", [(128, 64), (64, 64), (40, 40)])
+@pytest.mark.parametrize("rows", [5, 150])
+def test_attention_offsets_past_the_rows(dim, group, rows):
+    """Offsets that leave the call's rows are cut at them: fewer rows of q
+    than the step has."""
+    a = attention_inputs(dim, [(rows, rows + 40), (rows, 2 * rows)], 4, 1, dim,
+                         group, 16, "int8", torch.float16)
+    q = a["q"][:rows + 3]
+    args = (a["k_cache"], a["v_cache"], a["table"])
+    want = mt.cache_attention(q, *args, i32([0, rows, rows + 3]), a["starts"],
+                              16)
+    for offs in ([0, rows, 2 * rows], [-7, rows, 2 ** 31 - 1]):
+        room = torch.full((2 * rows, 4, dim), 3.0, dtype=q.dtype,
+                          device="cuda")
+        mt.cache_attention(q, *args, i32(offs), a["starts"], 16,
+                           out=room[:rows + 3])
+        assert torch.equal(room[:rows + 3], want)
+        assert bool((room[rows + 3:] == 3).all())
+
+
+@pytest.mark.parametrize("sequences", [3, 5000])
+def test_extend_fewer_rows_than_tokens(sequences):
+    n = torch.arange(sequences, dtype=torch.int32, device="cuda") % 5
+    free = torch.arange(2 * sequences, dtype=torch.int32, device="cuda")
+    count = i32([2 * sequences])
+    got = []
+    for rows in (int(n.sum()), 4):
+        table = torch.full((sequences, 2), -1, dtype=torch.int32,
+                           device="cuda")
+        got.append((mt.cache_extend(table, n, n, free, count, 4, rows), table))
+    (all_, t0), (few, t1) = got
+    assert torch.equal(t0, t1)
+    for name in ("offsets", "lengths", "free_count"):
+        assert torch.equal(getattr(all_, name), getattr(few, name))
+    n = min(4, all_.slots.shape[0])   # behind all of them: padding
+    assert torch.equal(all_.slots[:n], few.slots[:n])
+    assert torch.equal(all_.positions[:n], few.positions[:n])
+
+
+def test_more_refusals():
+    a = attention_inputs(51, [(1, 9), (2, 5)], 4, 2, 64, 32, 16, "e4m3",
+                         torch.bfloat16)
+    args = (a["q"], a["k_cache"], a["v_cache"], a["table"], a["offsets"],
+            a["starts"])
+    with pytest.raises(mt.MTError):
+        mt.cache_attention(*args, 16, out=a["q"])
+    for kw in (dict(page_size=2 ** 31), dict(page_size=16, cap=1e-50),
+               dict(page_size=16, scale=1e39)):
+        with pytest.raises((ValueError, mt.MTError)):
+            mt.cache_attention(*args, **kw)
+    x = torch.ones(2, 8, device="cuda")
+    with pytest.raises((ValueError, mt.MTError)):
+        mt.block_norm(x, x, residual_scale=1e39)
+    one = i32([0])
+    with pytest.raises(ValueError):
+        mt.cache_extend(i32([[0]]), one, one, i32([]), i32([0]), 2 ** 31, 1)
+
+
 # ---- refusals of the binding -------------------------------------------------
 def test_extend_refuses():
     t, n, f, c = i32([[-1, -1]]), i32([0]), i32([4, 3]), i32([2])

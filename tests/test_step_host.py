@@ -276,3 +276,19 @@ def test_plain_gradients_match_differences(norms, gate):
                         for s in (1, -1))
             want = (loss(up) - loss(down)) / (2 * step)
             assert float(d.flatten()[i]) == pytest.approx(want, abs=1e-7)
+
+
+@pytest.mark.parametrize("change", [
+    dict(offsets=2 * A), dict(offsets=10 * A), dict(slots=3 * A),
+    dict(positions=4 * A), dict(positions=7 * A), dict(new_lengths=5 * A),
+    dict(new_free_count=A), dict(table=4 * A), dict(table=6 * A)], ids=str)
+def test_extend_refuses_outputs_that_are_inputs(change):
+    refused(INV, mt.mt_cache_extend, changed(EXTEND, **change), None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=ATTENTION.q), dict(cap=1e-40), dict(cap=1e-3, scale=1e38)],
+    ids=str)
+def test_attention_refuses_more(change):
+    c = changed(ATTENTION, **change)
+    refused(INV, mt.mt_cache_attention, BF16, c, A, 1 << 30, None)
