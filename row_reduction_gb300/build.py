@@ -33,11 +33,13 @@ SOURCES = (["api.cpp", "planner.cpp", "mean.cu", "probe.cu", "decoder.cpp",
             for parts in (1, 2) for nt in (1, 2)] +
            [f"attention_rows_{fmt}_p{parts}.cu" for fmt in ("e4m3", "int8")
             for parts in (1, 2)] +
+           [f"attention_tiles_{fmt}.cu" for fmt in ("e4m3", "int8")] +
            [f"ops_{op}_{dt}.cu" for op in OPS for dt in DTYPES])
 DEPENDS = ["mt_internal.h", "mt_kernels.cuh", "mt_stage.cuh", "plan_table.inc",
            "mt_decoder_internal.h", "mt_decoder.cuh", "rotary.cuh",
            "logits.cuh", "mt_decoder_checks.h", "attention.cuh",
-           "attention_mma.cuh", "attention_rows.cuh", "block_norm.cuh"]
+           "attention_mma.cuh", "attention_rows.cuh", "attention_tiles.cuh",
+           "block_norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler",

@@ -308,7 +308,7 @@ struct Column {
 };
 
 struct Deal {
-    int64_t scan[kWarps];
+    int64_t scan[2 * kWarps];
     int64_t at;         // place of the CTA's first unit in its sequence
     int32_t sequence;
 };
@@ -1233,11 +1233,11 @@ constexpr int kLeastUnits = (int)kExtra + 1;
 // Deals the call's units out and goes through the CTA's run of them:
 // body(tile, u0, u1, whole, place) for the units [u0, u1) of a tile, whole or
 // not, whose partial sums belong in the CTA's place 0 or 1.
-template <class Body>
+template <int WARPS = kWarps, class Body>
 __device__ __forceinline__ void deal_units(const mt_attention_call_t &c,
                                            const Cut &cut, const Share &share,
                                            Deal &sh, Body body) {
-    constexpr int T = 32 * kWarps;
+    constexpr int T = 32 * WARPS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int cut_here = 0;
     // Units of the sequences of this thread, and where they begin.
@@ -1261,7 +1261,7 @@ __device__ __forceinline__ void deal_units(const mt_attention_call_t &c,
     __syncthreads();
     int64_t total = 0, first = upto - mine;
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
+    for (int x = 0; x < WARPS; ++x) {
         if (x < warp) first += sh.scan[x];
         total += sh.scan[x];
     }

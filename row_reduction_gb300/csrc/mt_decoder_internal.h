@@ -153,6 +153,8 @@ MT_DECLARE_ATTENTION(launch_attention_rows_e4m3_p1)
 MT_DECLARE_ATTENTION(launch_attention_rows_e4m3_p2)
 MT_DECLARE_ATTENTION(launch_attention_rows_int8_p1)
 MT_DECLARE_ATTENTION(launch_attention_rows_int8_p2)
+MT_DECLARE_ATTENTION(launch_attention_tiles_e4m3)
+MT_DECLARE_ATTENTION(launch_attention_tiles_int8)
 #undef MT_DECLARE_ATTENTION
 
 // ---- norms around a block ------------------------------------------------------

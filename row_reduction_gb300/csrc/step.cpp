@@ -65,7 +65,7 @@ bool attention_head(const mt_attention_call_t &c) {
         default: return false;
     }
 }
-constexpr int64_t kManyColumns = 48;
+constexpr int64_t kManyColumns = 48, kTensorColumnsLeast = 128;
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
@@ -84,8 +84,12 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     const int64_t columns_all = (int64_t)p->times * c.rows;
     const bool many = c.dim <= 128 && c.dim % 32 == 0 &&
                       columns_all >= kManyColumns * (int64_t)c.sequences;
-    p->nt = many ? 0 : c.dim <= 128 && columns_all > 8LL * c.sequences ? 2 : 1;
-    const int columns = many ? 64 : 8 * p->nt;
+    const bool tensor = dtype == DT_BF16 && c.group == c.dim &&
+                        (c.dim == 64 || c.dim == 128) &&
+                        columns_all >= kTensorColumnsLeast *
+                                           (int64_t)c.sequences;
+    p->nt = tensor ? -1 : many ? 0 : c.dim <= 128 && columns_all > 8LL * c.sequences ? 2 : 1;
+    const int columns = tensor ? 128 : many ? 64 : 8 * p->nt;
     p->per = p->times < columns ? columns / p->times : 1;
     p->parts = (p->times + columns - 1) / columns;
     p->heads = many ? 1 : c.k_heads % 4 == 0 ? 4 : c.k_heads % 2 == 0 ? 2 : 1;
@@ -101,7 +105,8 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
                (fours(c.out, c.out_row, c.out_head) ? 2 : 0);
     // as many as are resident at once
     const int halves = dtype == DT_BF16 ? 1 : 2;
-    p->ctas = sms * (many ? attention_row_ctas(c.dim, c.dim / c.group, halves)
+    p->ctas = sms * (tensor ? 2
+                     : many ? attention_row_ctas(c.dim, c.dim / c.group, halves)
                           : attention_ctas(c.dim, c.dim / c.group, halves,
                                            p->nt));
     if (p->ctas > kAttentionMaxCtas) p->ctas = kAttentionMaxCtas;
@@ -109,7 +114,8 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
 }
 size_t attention_workspace(const mt_attention_call_t &c,
                            const AttentionPlan &p) {
-    const size_t columns = p.nt ? 4 * 8 * (size_t)p.nt : 64;
+    const size_t columns = p.nt < 0    ? 128
+                           : p.nt == 0 ? 64 : 4 * 8 * (size_t)p.nt;
     return (size_t)p.ctas * (2 * columns * (c.dim + 2) * sizeof(float) +
                              kAttentionRecord);
 }
@@ -153,7 +159,10 @@ size_t norm_workspace(const mt_block_norm_back_t &c) {
 // Whether no output of the call is one of its inputs or another output (those
 // without a value are no matter).
 bool apart(const mt_cache_extend_call_t &c) {
-    const void *in[] = {c.lengths, c.counts, c.free_pages, c.free_count};
+    const void *in[] = {c.sequences > 0 ? c.lengths : nullptr,
+                        c.sequences > 0 ? c.counts : nullptr,
+                        c.free_size > 0 ? c.free_pages : nullptr,
+                        c.free_count};
     const void *out[] = {c.offsets, c.new_free_count,
                          c.sequences > 0 ? c.new_lengths : nullptr,
                          c.rows > 0 ? c.slots : nullptr,
@@ -237,7 +246,9 @@ mt_status mt_cache_attention(int dtype, const mt_attention_call_t *call,
         return MT_ERR_INVALID_ARGUMENT;
     const bool int8 = call->format == MT_CACHE_INT8;
     const auto launch =
-        p.nt == 0
+        p.nt < 0 ? (int8 ? launch_attention_tiles_int8
+                         : launch_attention_tiles_e4m3)
+        : p.nt == 0
             ? (dtype == DT_BF16 ? int8 ? launch_attention_rows_int8_p1
                                        : launch_attention_rows_e4m3_p1
                                 : int8 ? launch_attention_rows_int8_p2
