@@ -48,6 +48,16 @@ __device__ __forceinline__ void tensor_product(unsigned d, uint64_t a,
         "l"(a), "l"(b), "r"(kind), "r"(add ? 1 : 0)
         : "memory");
 }
+// The same with the first operand in tensor memory, two values to a column.
+__device__ __forceinline__ void tensor_product(unsigned d, unsigned a,
+                                               uint64_t b, unsigned kind,
+                                               bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::
+            "r"(d), "r"(a), "l"(b), "r"(kind), "r"(add ? 1 : 0)
+        : "memory");
+}
 // The products so far arrive at `bar`.
 __device__ __forceinline__ void tensor_arrive(uint64_t *bar) {
     asm volatile(
@@ -89,34 +99,6 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// The 64 columns from `at` on of the thread's own lane.
-__device__ __forceinline__ void tensor_load(unsigned (&r)[64], unsigned at) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
-        "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-          "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-          "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]),
-          "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]),
-          "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-          "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]),
-          "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
-          "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
-          "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]),
-          "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]),
-          "=r"(r[62]), "=r"(r[63])
-        : "r"(at)
-        : "memory");
-}
 // The 32 columns from `at` on of the thread's own lane.
 __device__ __forceinline__ void tensor_load(unsigned (&r)[32], unsigned at) {
     asm volatile(
@@ -157,13 +139,12 @@ struct TileShared {
     static constexpr int BLOCKS = DIM / 64;    // of 64 values, 128 bytes
     uint4 q[BLOCKS][kTileColumns * 8];
     uint4 k[BLOCKS][kTileKeys * 8], v[BLOCKS][kTileKeys * 8];
-    uint4 p[kTileColumns * 8];
     uint8_t k_codes[kTileKeys * DIM], v_codes[kTileKeys * DIM];
     float ks[4][kTileKeys], vs[4][kTileKeys];  // of four chunks in turn
-    unsigned there[4][kWarps];                 // keys with a slot, 16 to a warp
+    alignas(16) unsigned there[4][kWarps];                 // keys with a slot, 16 to a warp
     int32_t lo_any[kWarps], hi_any[kWarps], lo_all[kWarps], hi_all[kWarps];
     Deal deal;
-    uint64_t score_done[2], score_free[2], weights_there, value_done;
+    uint64_t score_done[2], weights_there, value_done;
     unsigned tensor;
     int failed;                                // a wait ran out
     static_assert(DIM == 64 || DIM == 128, "whole blocks, 128 columns of sums");
@@ -177,7 +158,6 @@ struct TileRun {
     Sh &sh;
     unsigned scores_at, sums_at;               // in tensor memory, own lanes
     unsigned score_phase = 0, value_phase = 0, weights_phase = 0;
-    unsigned free_phase = 3;                   // a new barrier's phase before
     // the thread's column
     float ref, l, f, slope;
     unsigned most;                             // exponent, as in Warp
@@ -328,21 +308,27 @@ struct TileRun {
                                            unsigned (&out)[kTileKeys / 2]) {
         constexpr int N = kTileKeys / 2;
         float2 z[N];
-        {
-            unsigned r[kTileKeys];
-            tensor_load(r, scores_at + (i & 1) * kTileKeys);
-            tensor_before();
-            arrive(&sh.score_free[i & 1]);
+        // Half of them at a time, as far as registers go; scales are asked for
+        // ahead.
 #pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const float4 k =
-                    *reinterpret_cast<const float4 *>(&sh.ks[ring][2 * j]);
-                z[j] = mul2(make_float2(__uint_as_float(r[2 * j]),
-                                        __uint_as_float(r[2 * j + 1])),
-                            make_float2(k.x, k.y));
-                z[j + 1] = mul2(make_float2(__uint_as_float(r[2 * j + 2]),
-                                            __uint_as_float(r[2 * j + 3])),
-                                make_float2(k.z, k.w));
+        for (int h = 0; h < 2; ++h) {
+            float4 k[N / 4];
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                k[j] = *reinterpret_cast<const float4 *>(
+                    &sh.ks[ring][h * N + 4 * j]);
+            unsigned r[N];
+            tensor_load(r, scores_at + (i & 1) * kTileKeys + h * N);
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) {
+                z[h * (N / 2) + 2 * j] =
+                    mul2(make_float2(__uint_as_float(r[4 * j]),
+                                     __uint_as_float(r[4 * j + 1])),
+                         make_float2(k[j].x, k[j].y));
+                z[h * (N / 2) + 2 * j + 1] =
+                    mul2(make_float2(__uint_as_float(r[4 * j + 2]),
+                                     __uint_as_float(r[4 * j + 3])),
+                         make_float2(k[j].z, k[j].w));
             }
         }
         // Exponents of two, less the reference (none yet: 0).
@@ -365,10 +351,10 @@ struct TileRun {
 #pragma unroll
             for (int j = 0; j < N; ++j) z[j] = fma2(z[j], f2, less);
         }
-        uint64_t there = 0;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x)
-            there |= (uint64_t)sh.there[ring][x] << (OWN * x);
+        const uint4 by_warp = *reinterpret_cast<const uint4 *>(sh.there[ring]);
+        static_assert(kWarps == 4 && OWN == 16, "a word of each");
+        uint64_t there = (uint64_t)(by_warp.z | by_warp.w << 16) << 32 |
+                         (by_warp.x | by_warp.y << 16);
         const bool whole = ~there == 0 && j0 >= lo_all &&
                            j0 + kTileKeys - 1 <= hi_all;
         if (c.slopes != nullptr) {
@@ -394,9 +380,14 @@ struct TileRun {
                 if (!(w & 2u)) z[j].y = -INFINITY;
             }
         }
-        float top = nanmax(z[0].x, z[0].y);
+        float tops[4];
 #pragma unroll
-        for (int j = 1; j < N; ++j) top = nanmax3(top, z[j].x, z[j].y);
+        for (int j = 0; j < 4; ++j) tops[j] = nanmax(z[j].x, z[j].y);
+#pragma unroll
+        for (int j = 4; j < N; ++j)
+            tops[j & 3] = nanmax3(tops[j & 3], z[j].x, z[j].y);
+        const float top = nanmax(nanmax(tops[0], tops[1]),
+                                 nanmax(tops[2], tops[3]));
         float times = 1.f;
         if (ref == -INFINITY ? !(top == -INFINITY) : !(top <= 8.f)) {
             // the reference up to the largest so far, by what that really is
@@ -415,15 +406,23 @@ struct TileRun {
         }
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            const float4 v =
-                *reinterpret_cast<const float4 *>(&sh.vs[ring][2 * j]);
-            z[j] = make_float2(pow2(z[j].x), pow2(z[j].y));
-            z[j + 1] = make_float2(pow2(z[j + 1].x), pow2(z[j + 1].y));
-            sum[0] = add2(sum[0], z[j]);
-            sum[1] = add2(sum[1], z[j + 1]);
-            z[j] = mul2(z[j], make_float2(v.x, v.y));
-            z[j + 1] = mul2(z[j + 1], make_float2(v.z, v.w));
+        for (int h = 0; h < 2; ++h) {
+            float4 v[N / 4];
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                v[j] = *reinterpret_cast<const float4 *>(
+                    &sh.vs[ring][h * N + 4 * j]);
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) {
+                float2 &a = z[h * (N / 2) + 2 * j];
+                float2 &b = z[h * (N / 2) + 2 * j + 1];
+                a = make_float2(pow2(a.x), pow2(a.y));
+                b = make_float2(pow2(b.x), pow2(b.y));
+                sum[0] = add2(sum[0], a);
+                sum[1] = add2(sum[1], b);
+                a = mul2(a, make_float2(v[j].x, v[j].y));
+                b = mul2(b, make_float2(v[j].z, v[j].w));
+            }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (!whole) {
@@ -435,10 +434,12 @@ struct TileRun {
                 if (!(w & 2u)) z[j].y = 0.f;
             }
         }
-        float big = 0.f;
+        float bigs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            big = nanmax3(big, fabsf(z[j].x), fabsf(z[j].y));
+            bigs[j & 3] = nanmax3(bigs[j & 3], fabsf(z[j].x), fabsf(z[j].y));
+        const float big = nanmax(nanmax(bigs[0], bigs[1]),
+                                 nanmax(bigs[2], bigs[3]));
         if (!(big * up(most) < 32768.f)) {
             const unsigned now =
                 max(most, __float_as_uint(big) >> 23 & 0xffu);
@@ -511,12 +512,12 @@ struct TileRun {
             asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
         };
         const unsigned q_at = smem_addr(sh.q), k_at = smem_addr(sh.k);
-        const unsigned v_at = smem_addr(sh.v), p_at = smem_addr(sh.p);
+        const unsigned v_at = smem_addr(sh.v);
         // (a warp's keys and scales: each warp arrives, and the products)
         const auto scores = [&](int i) {
             arrive(&sh.score_done[i & 1]);
             if (tid != 0) return;
-            wait(&sh.score_free[i & 1], free_phase, i & 1);
+            tensor_after();
 #pragma unroll
             for (int s = 0; s < DIM / 16; ++s)
                 tensor_product(
@@ -532,7 +533,7 @@ struct TileRun {
 #pragma unroll
             for (int s = 0; s < kTileKeys / 16; ++s)
                 tensor_product(sh.tensor + 2 * kTileKeys,
-                               operand(p_at + s * 32, 0),
+                               sh.tensor + (i & 1) * kTileKeys + s * 8,
                                operand(v_at + s * 2048, kTileKeys * 128),
                                product_of(DIM, true), i > 0 || s > 0);
             tensor_arrive(&sh.value_done);
@@ -571,6 +572,9 @@ struct TileRun {
                 if (i + 2 < n) load_keys(slot_next, i + 2 & 3);
             }
             commit();
+            // the sums of the chunk before are through: its values' place and
+            // its weights', which is that of the next scores, are free
+            if (i > 0) wait_all(&sh.value_done, value_phase);
             if (i + 1 < n) {
                 written();
                 scores(i + 1);
@@ -578,7 +582,6 @@ struct TileRun {
             }
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
-            if (i > 0) wait_all(&sh.value_done, value_phase);
             widen(sh.v_codes, sh.v, warp);
             __syncwarp();
             if (i + 1 < n) copy(vp, sh.v_codes, slot_v);
@@ -592,7 +595,6 @@ struct TileRun {
     // Four warps: a column to a thread.
     __device__ __forceinline__ void weights(const mt_attention_call_t &c,
                                             const Span &t) {
-        const int tid = threadIdx.x;
 #pragma unroll 1
         for (int i = 0; i < t.n; ++i) {
             wait_all(&sh.score_done[i & 1], score_phase, i & 1);
@@ -600,8 +602,10 @@ struct TileRun {
             const float times = weigh(c, i, (int)((t.u + i) * kTileKeys), i & 3,
                                       t.lo_all, t.hi_all, w);
             if (i > 0) {
-                wait_all(&sh.value_done, value_phase);
+                // sums so far: complete before they are touched
                 if (__any_sync(kFull, !(times == 1.f))) {
+                    unsigned phase = value_phase;
+                    wait_all(&sh.value_done, phase);
 #pragma unroll 1
                     for (int d = 0; d < DIM; d += 32) {
                         unsigned o[32];
@@ -613,12 +617,10 @@ struct TileRun {
                         tensor_store(sums_at + d, o);
                     }
                 }
+                value_phase ^= 1;
             }
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                sh.p[tid * 8 + (x ^ (tid & 7))] = make_uint4(
-                    w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-            fence_proxy_async_smem();
+            // in the scores' place
+            tensor_store(scores_at + (i & 1) * kTileKeys, w);
             tensor_before();
             arrive(&sh.weights_there);
         }
@@ -724,10 +726,8 @@ __global__ void __launch_bounds__(64 * kWarps, 2)
             : "memory");
     }
     if (threadIdx.x == 0) {
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2; ++b)
             mbar_init(&sh.score_done[b], 1 + kWarps);
-            mbar_init(&sh.score_free[b], kWarps);
-        }
         mbar_init(&sh.weights_there, kWarps);
         mbar_init(&sh.value_done, 1);
         mbar_init_fence();
