@@ -602,10 +602,11 @@ struct TileRun {
             const float times = weigh(c, i, (int)((t.u + i) * kTileKeys), i & 3,
                                       t.lo_all, t.hi_all, w);
             if (i > 0) {
-                // sums so far: complete before they are touched
+                // The sums so far are complete before they are touched, and
+                // the chunk before has been taken before this one arrives: no
+                // barrier gets two phases ahead of who waits for it.
+                wait_all(&sh.value_done, value_phase);
                 if (__any_sync(kFull, !(times == 1.f))) {
-                    unsigned phase = value_phase;
-                    wait_all(&sh.value_done, phase);
 #pragma unroll 1
                     for (int d = 0; d < DIM; d += 32) {
                         unsigned o[32];
@@ -617,7 +618,6 @@ struct TileRun {
                         tensor_store(sums_at + d, o);
                     }
                 }
-                value_phase ^= 1;
             }
             // in the scores' place
             tensor_store(scores_at + (i & 1) * kTileKeys, w);
