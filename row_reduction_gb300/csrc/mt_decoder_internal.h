@@ -118,7 +118,8 @@ cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
 // A call on the matrix kernels: how its rows and query heads are cut into
 // tiles of 8 nt columns, and the CTAs that share its work.
 struct AttentionPlan {
-    int32_t nt;     // 0: the kernel for many rows, tiles of 64 columns
+    int32_t nt;     // 0: the kernel for many rows, tiles of 64 columns; -1: the
+                    // one on tensor memory, of 128
     int32_t times;  // query heads per key head
     int32_t per;    // rows of a tile
     int32_t parts;  // tiles that share a row's query heads

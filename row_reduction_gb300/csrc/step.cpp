@@ -65,7 +65,7 @@ bool attention_head(const mt_attention_call_t &c) {
         default: return false;
     }
 }
-constexpr int64_t kManyColumns = 48, kTensorColumnsLeast = 128;
+constexpr int64_t kManyColumns = 48, kTensorColumns = 384;
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
@@ -78,17 +78,21 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     int sms = 0;
     if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
     p->times = c.q_heads / c.k_heads;
-    // Columns that a sequence has on average: from 48 on the kernel for many
-    // rows, which fills tiles of 64 of them (34 us for 41 at 132 columns, 73 for
-    // 66 at 34); else tiles of 16 where there are more than 8.
+    // Columns that a sequence has on average.  BF16 with one group a head from
+    // 384 on: tiles of 128 on tensor memory (2 x 128 rows of 4 query heads a key
+    // head 63 us for 73, 2 x 512 185 for 308, 2 x 512 of one query head 75 for
+    // 97; at some 200 columns 62 for 48).  From 48 on the kernel for many rows,
+    // which fills tiles of 64 (34 us for 41 at 132 columns, 73 for 66 at 34);
+    // else tiles of 16 where there are more than 8.
     const int64_t columns_all = (int64_t)p->times * c.rows;
     const bool many = c.dim <= 128 && c.dim % 32 == 0 &&
                       columns_all >= kManyColumns * (int64_t)c.sequences;
     const bool tensor = dtype == DT_BF16 && c.group == c.dim &&
                         (c.dim == 64 || c.dim == 128) &&
-                        columns_all >= kTensorColumnsLeast *
-                                           (int64_t)c.sequences;
-    p->nt = tensor ? -1 : many ? 0 : c.dim <= 128 && columns_all > 8LL * c.sequences ? 2 : 1;
+                        columns_all >= kTensorColumns * (int64_t)c.sequences;
+    p->nt = tensor ? -1
+            : many ? 0
+            : c.dim <= 128 && columns_all > 8LL * c.sequences ? 2 : 1;
     const int columns = tensor ? 128 : many ? 64 : 8 * p->nt;
     p->per = p->times < columns ? columns / p->times : 1;
     p->parts = (p->times + columns - 1) / columns;

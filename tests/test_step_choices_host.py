@@ -57,6 +57,7 @@ FAKE(launch_attention_int8_p1n1, 211) FAKE(launch_attention_int8_p1n2, 212)
 FAKE(launch_attention_int8_p2n1, 221) FAKE(launch_attention_int8_p2n2, 222)
 FAKE(launch_attention_rows_e4m3_p1, 110) FAKE(launch_attention_rows_e4m3_p2, 120)
 FAKE(launch_attention_rows_int8_p1, 210) FAKE(launch_attention_rows_int8_p2, 220)
+FAKE(launch_attention_tiles_e4m3, 109) FAKE(launch_attention_tiles_int8, 209)
 #define FAKE_NORM(dt)                                                         \
     cudaError_t launch_block_norm_##dt(const mt_block_norm_call_t &, int V,   \
                                        cudaStream_t) {                        \
@@ -216,3 +217,31 @@ def test_norms_take_the_widest_packs(fake, es, dtype):
     assert back(cols=60) == 4 and back(cols=61) == 1
     assert forward(x_stride=66) == 2 and back(dx_stride=65) == 1
     assert forward(rows=1, x_stride=65) == full
+
+
+@pytest.mark.parametrize("q_heads,k_heads,rows,sequences,dim,group,dtype,takes", [
+    (32, 8, 96, 1, 128, 128, BF16, True), (32, 8, 95, 1, 128, 128, BF16, False),
+    (32, 8, 192, 2, 64, 64, BF16, True), (32, 8, 191, 2, 64, 64, BF16, False),
+    (32, 8, 1000, 1, 128, 64, BF16, False), (32, 8, 1000, 1, 96, 96, BF16, False),
+    (32, 8, 1000, 1, 256, 256, BF16, False), (32, 8, 1000, 1, 128, 128, F16, False),
+    (32, 8, 1000, 1, 128, 128, F32, False), (390, 2, 7, 1, 128, 128, BF16, True),
+    (8, 8, 384, 1, 128, 128, BF16, True)])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_attention_on_tensor_memory(fake, q_heads, k_heads, rows, sequences, dim,
+                                    group, dtype, takes, fmt):
+    c = changed(ATTENTION, q_heads=q_heads, k_heads=k_heads, rows=rows,
+                sequences=sequences, q_row=q_heads * dim, q_head=dim,
+                out_row=q_heads * dim, out_head=dim, dim=dim, group=group,
+                format=fmt)
+    status, size, got = attend(fake, dtype, c)
+    assert status == 0
+    assert (got["which"] == 100 * (fmt + 1) + 9) == takes
+    if not takes:
+        assert got["nt"] >= 0
+        return
+    times = q_heads // k_heads
+    assert got["nt"] == -1 and got["heads"] == 1 and got["ctas"] == 2 * 152
+    assert size == got["ctas"] * (2 * 128 * (dim + 2) * 4 + 24)
+    assert got["per"] * min(times, 128) <= 128
+    assert got["parts"] * 128 >= times
+    assert attend(fake, dtype, c, size - 1)[0] == OOR

@@ -883,9 +883,147 @@ def test_explicit_streams():
         assert all(torch.equal(p, q) for p, q in zip(ge, we))
 
 
+# ---- prompts on tensor memory -----------------------------------------------------
+TALL = [(200, 900), (0, 0), (130, 131), (257, 64 * 12)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("shape", [(8, 2, 128, 16), (6, 1, 64, 24), (3, 3, 128, 1),
+                                   (140, 1, 64, 16), (7, 1, 128, 32)], ids=str)
+@pytest.mark.parametrize("kind", ["plain", "cap", "prefix", "documents",
+                                  "window", "empty", "holes"])
+def test_attention_tall(fmt, shape, kind):
+    """BF16 prompts of several tiles of 128 columns, cut wherever the CTAs'
+    shares end; chunks that some rows, or none, see."""
+    hq, hk, dim, page = shape
+    rows = TALL if hq < 100 else [(5, 300), (3, 64)]
+    if hq == hk:
+        rows = [(500, 700), (410, 410)]
+    a = attention_inputs(dim + hq, rows, hq, hk, dim, dim, page, fmt,
+                         torch.bfloat16, before=1, behind=2)
+    p = [0] + [v for r, k in rows for v in range(k - r, k)] + [0, 0]
+    rng, kw = random.Random(hq), {}
+    if kind == "cap":
+        kw = dict(cap=1.5)
+    elif kind == "prefix":
+        kw = dict(last=i32([max(v, 333) for v in p]), cap=5.0)
+    elif kind == "documents":
+        kw = dict(first=i32([v // 50 * 50 for v in p]),
+                  slopes=torch.rand(hq, generator=gen(1), device="cuda") / 9)
+    elif kind == "window":
+        kw = dict(window=70, slopes=torch.rand(hq, generator=gen(2),
+                                               device="cuda"))
+    elif kind == "empty":
+        kw = dict(first=i32([rng.choice([v + 1, 2 ** 31 - 1, 0]) for v in p]),
+                  last=i32([rng.choice([v, -1, -2 ** 31]) for v in p]))
+    elif kind == "holes":
+        t = a["table"]
+        t[torch.rand(t.shape, generator=gen(3), device="cuda") < 0.4] = -1
+        t[-1, 0] = 2 ** 31 - 1
+        kw["scale"] = -0.2
+    out = attention_check(a, **kw).clone()
+    assert torch.equal(out, attention_check(a, **kw))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("grow", [1e-4, 1.0, 30.0])
+@pytest.mark.parametrize("values", [1e-30, 1.0, 1e30])
+def test_attention_tall_moving_references(dim, grow, values):
+    """Scores that run ahead of every chunk's reference, values' scales that
+    leave the power of two of the chunks before, up and down."""
+    a = attention_inputs(9, [(250, 640), (170, 170)], 4, 1, dim, dim, 16, "e4m3",
+                         torch.bfloat16)
+    a["q"] = a["q"].abs()
+    a["k_cache"][0].copy_(a["k_cache"][0].float().abs().to(torch.float8_e4m3fn))
+    # a key's place in its sequence, by its slot
+    place = torch.zeros(a["k_cache"][0].shape[0], device="cuda")
+    for row in a["table"]:
+        for j, page in enumerate(row.tolist()):
+            if page >= 0:
+                place[page * 16:page * 16 + 16] = \
+                    j * 16 + torch.arange(16, device="cuda")
+    ks, vs = a["k_cache"][1], a["v_cache"][1]
+    ks.mul_((1 + grow * place / 64)[:, None, None])
+    vs.mul_((values * torch.exp2(12 * torch.sin(place / 40)))[:, None, None])
+    attention_check(a)
+
+
+def test_attention_tall_not_a_number():
+    """What a row does not see has no effect on it; what it does has, on its own
+    columns alone."""
+    a = attention_inputs(10, [(300, 400)], 4, 2, 128, 128, 16, "int8",
+                         torch.bfloat16)
+    clean = attention_check(a).clone()
+    at = int(a["table"][0, 250 // 16]) * 16 + 250 % 16   # seen from row 150 on
+    for which, value in (("v_cache", math.nan), ("k_cache", math.nan),
+                         ("v_cache", math.inf)):
+        s = a[which][1]
+        old = s[at, 1].clone()
+        s[at, 1] = value
+        got = mt.cache_attention(a["q"], a["k_cache"], a["v_cache"], a["table"],
+                                 a["offsets"], a["starts"], 16)
+        s[at, 1] = old
+        assert torch.equal(got[:, :2], clean[:, :2])
+        assert torch.equal(got[:150], clean[:150])
+        assert not bool(torch.isfinite(got[150:, 2:]).any())
+    q = a["q"].clone()
+    q[7, 3, 5], q[200, 0, 0] = math.nan, -math.inf
+    got = mt.cache_attention(q, a["k_cache"], a["v_cache"], a["table"],
+                             a["offsets"], a["starts"], 16)
+    bad = torch.zeros(300, 4, dtype=torch.bool, device="cuda")
+    bad[7, 3] = bad[200, 0] = True
+    assert torch.equal(got.isnan().all(-1), bad)
+    assert torch.equal(got[~bad], clean[~bad])
+
+
+def test_attention_tall_streams_and_graphs():
+    """Two calls at once on two streams, of both head sizes (tensor memory is
+    shared by what runs on an SM), and a captured one, replayed."""
+    a = [attention_inputs(11 + d, [(300, 900), (200, 333)], 8, 2, d, d, 16,
+                          "e4m3", torch.bfloat16) for d in (64, 128)]
+
+    def call(x, out=None):
+        return mt.cache_attention(x["q"], x["k_cache"], x["v_cache"], x["table"],
+                                  x["offsets"], x["starts"], 16, out=out)
+    want = [call(x) for x in a]
+    streams = [torch.cuda.Stream() for _ in a]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for x, s in zip(a, streams):
+            with torch.cuda.stream(s):
+                got.append(call(x))
+    torch.cuda.synchronize()
+    for i, t in enumerate(got):
+        assert torch.equal(t, want[i % 2])
+    out = torch.zeros_like(want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(a[1], out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_tall_strided_views(dim):
+    a = attention_inputs(12, [(150, 300), (60, 61)], 6, 1, dim, dim, 16, "int8",
+                         torch.bfloat16)
+    q = a["q"]
+    wide = randn(gen(5), 210, 9, dim + 1, dtype=torch.bfloat16)
+    wide[:, 2:8, 1:] = q
+    a["q"] = wide[:, 2:8, 1:]       # off any bound
+    room = torch.full((6, 210, dim + 3), 3.0, dtype=torch.bfloat16,
+                      device="cuda")
+    attention_check(a, out=room[:, :, 1:-2].transpose(0, 1))
+    assert bool((room[:, :, 0] == 3).all() and (room[:, :, -2:] == 3).all())
+
+
 # ---- what device arrays may hold -----------------------------------------------
 @pytest.mark.parametrize("dim,group", [(128, 64), (64, 64), (40, 40)])
-@pytest.mark.parametrize("rows", [(3, 5), (100, 130)])
+@pytest.mark.parametrize("rows", [(3, 5), (100, 130), (400, 300)])
 @pytest.mark.parametrize("window", [None, 20, 2 ** 40])
 def test_attention_negative_starts(dim, group, rows, window):
     """Rows at negative positions see nothing; those behind them, in the same
