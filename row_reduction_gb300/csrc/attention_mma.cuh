@@ -1378,10 +1378,14 @@ __global__ void __launch_bounds__(32 * kWarps,
 // column to a warp, four values to a lane, a part's factor in each lane first;
 // where there are few columns, the warps of a CTA share the parts of one.
 constexpr int kJoin = 256, kJoinWarps = kJoin / 32;
+// CTAs that join for each that left parts, behind tiles of 64 and 128 columns:
+// there a warp has many columns one after the other, each a chain of reads (two
+// prompts of 512 rows 186 us with one, 175 with two, 173 with eight).
+constexpr int kJoinCtas = 2;
 template <int DIM, int C, int SLOTS>
 __global__ void __launch_bounds__(kJoin)
     attention_join_kernel(const mt_attention_call_t c, const Cut cut,
-                          const Share share, int dtype) {
+                          const Share share, int dtype, int records) {
     constexpr int kQuads = (DIM / 4 + 31) / 32;  // of a lane
     __shared__ int16_t cuts[kAttentionMaxCtas];
     __shared__ int counts[kJoinWarps];
@@ -1394,14 +1398,14 @@ __global__ void __launch_bounds__(kJoin)
     // them, four for each lane at a time.
     constexpr int kLooks = 4;
     int n = 0;
-    for (int b0 = 0; b0 < ctas; b0 += kLooks * kJoin) {
+    for (int b0 = 0; b0 < records; b0 += kLooks * kJoin) {
         bool on[kLooks];
         unsigned mask[kLooks];
         int found = 0;
 #pragma unroll
         for (int y = 0; y < kLooks; ++y) {
             const int b = b0 + (warp * kLooks + y) * 32 + lane;
-            on[y] = b < ctas && share.cut[b] != 0;
+            on[y] = b < records && share.cut[b] != 0;
         }
 #pragma unroll
         for (int y = 0; y < kLooks; ++y) {
@@ -1556,8 +1560,7 @@ cudaError_t launch_attention_as(const AttentionPlan &p,
                              share, dtype);
     if (e != cudaSuccess) return e;
     return launch_dependent(attention_join_kernel<H::DIM, 8 * NT, kWarps>,
-                            p.ctas,
-                            kJoin, 0, s, c, cut, share, dtype);
+                            p.ctas, kJoin, 0, s, c, cut, share, dtype, p.ctas);
 }
 
 template <bool INT8, int PARTS, int NT>

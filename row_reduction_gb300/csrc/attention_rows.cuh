@@ -13,12 +13,12 @@
 //
 // Taken from 48 columns per sequence on, on average: 32 rows of two sequences 34
 // us for 41 on tiles of 16 columns, 16 rows of 16 sequences (34 columns) 73 for
-// 66.
+// 66; BF16 with one group a head only to 384 (attention_tiles.cuh).
 //
-// Bound: shared memory (64% of its throughput: every warp reads all of a chunk
-// for its 16 columns) and the instructions around the products; those have 33%
-// of the tensor pipe.  BF16, two sequences of up to 512 rows at 4096 keys, 32 + 8
-// heads of 128, capped: 308 us, 185 TFLOP/s (372 us on tiles of 16 columns).
+// Bound: shared memory (73% of its throughput: every warp reads all of a chunk
+// for its 16 columns) and the instructions around the products; those have 34%
+// of the tensor pipe.  Two sequences of up to 512 rows at 4096 keys, 32 + 8 heads
+// of 128, FP16, causal: 380 us (BF16 capped 308 here, 372 on tiles of 16).
 #pragma once
 
 #include "attention_mma.cuh"
@@ -649,7 +649,8 @@ cudaError_t launch_rows_as(const AttentionPlan &p,
                              share, dtype);
     if (e != cudaSuccess) return e;
     return launch_dependent(attention_join_kernel<H::DIM, kRowColumns, 1>,
-                            p.ctas, kJoin, 0, s, c, cut, share, dtype);
+                            kJoinCtas * p.ctas, kJoin, 0, s, c, cut, share,
+                            dtype, p.ctas);
 }
 
 template <bool INT8, int PARTS>

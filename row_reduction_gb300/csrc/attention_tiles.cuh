@@ -2,20 +2,31 @@
 // tensor memory (one translation unit per code format).
 //
 // A tile has 128 columns (rows of a sequence times the query heads of a key
-// head), one to a thread and to a lane of tensor memory.  Chunks of 64 keys: a
-// warp copies the codes of 16 of them and widens these to FP16 itself, the
-// scores S = Q K^T come from one product of 128 x 64 and the sums O += P V from
-// one of 128 x dim, whose operands all lie in shared memory, swizzled by 128
-// bytes.  The next chunk's scores are worked out while a chunk's become weights,
-// and a chunk's sums while the next one is widened.  A column's statistics are
-// its thread's own: nothing is exchanged among lanes.
+// head) and goes through chunks of 64 keys.  Four warps have a column to a thread
+// and to a lane of tensor memory: they take a chunk's scores from there, make
+// weights of them and put these, as FP16, in the scores' place.  Nothing is
+// exchanged among lanes for that.  Four other warps copy codes, widen them to
+// FP16 in shared memory (swizzled by 128 bytes), 16 keys each, and issue the
+// products: S = Q K^T, 128 x 64, a chunk ahead, and O += P V, 128 x dim, with P
+// out of tensor memory.  Two CTAs to an SM share its 512 columns.
 //
 // Scores, references, scales and roundings are as in attention_mma.cuh, for one
 // group a head and BF16; sums stay in tensor memory, and are brought out to be
 // scaled only where a reference or a power of two has moved.  Units, cut tiles
 // and their joining are the same as there.
 //
-// Waits for the products have a limit; a CTA whose wait ran out gives NaN.
+// Bound.  Two sequences of up to 512 rows at 4096 keys, 32 + 8 heads of 128,
+// capped: 175 us, 340 TFLOP/s, 308 on tiles of 64 columns with mma.sync (uncapped
+// and causal 164 for 283); 2 x 2048 rows at 8192 keys 816 us, 440 TFLOP/s.  A
+// chunk's weights take 4000 cycles of a warp for 650 instructions, of which a
+// quarter wait for scales from shared memory (53% of that pipe's throughput:
+// operands, codes and scales share it), a quarter for the two exponentials and
+// the reciprocal of a capped score; issue slots are 44% busy.  All eight warps on
+// weights, halves of a column each, took 239 us, all four on everything 214.
+//
+// Waits have a limit; a CTA whose wait ran out gives NaN.  No barrier gets two
+// phases ahead of who waits for it: weights of a chunk arrive only after the sums
+// of the chunk before are through.
 #pragma once
 
 #include "attention_mma.cuh"
@@ -781,8 +792,9 @@ cudaError_t launch_tiles_as(const AttentionPlan &p,
         e = launch_dependent(kernel, p.ctas, 64 * kWarps, kBytes, s, c, cut,
                              share, dtype);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attention_join_kernel<DIM, kTileColumns, 1>, p.ctas,
-                            kJoin, 0, s, c, cut, share, dtype);
+    return launch_dependent(attention_join_kernel<DIM, kTileColumns, 1>,
+                            kJoinCtas * p.ctas, kJoin, 0, s, c, cut, share,
+                            dtype, p.ctas);
 }
 
 }  // namespace
