@@ -13,7 +13,7 @@
 //
 // Taken from 48 columns per sequence on, on average: 32 rows of two sequences 34
 // us for 41 on tiles of 16 columns, 16 rows of 16 sequences (34 columns) 73 for
-// 66; BF16 with one group a head only to 384 (attention_tiles.cuh).
+// 66; BF16 with one group a head only to 256 (attention_tiles.cuh).
 //
 // Bound: shared memory (73% of its throughput: every warp reads all of a chunk
 // for its 16 columns) and the instructions around the products; those have 34%

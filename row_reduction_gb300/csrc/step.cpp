@@ -65,7 +65,7 @@ bool attention_head(const mt_attention_call_t &c) {
         default: return false;
     }
 }
-constexpr int64_t kManyColumns = 48, kTensorColumns = 384;
+constexpr int64_t kManyColumns = 48, kTensorColumns = 256;
 // Whether the call goes to the matrix kernels, and how: else a warp per row
 // and query head.
 mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
@@ -79,9 +79,8 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
     p->times = c.q_heads / c.k_heads;
     // Columns that a sequence has on average.  BF16 with one group a head from
-    // 384 on: tiles of 128 on tensor memory (2 x 128 rows of 4 query heads a key
-    // head 63 us for 73, 2 x 512 185 for 308, 2 x 512 of one query head 75 for
-    // 97; at some 200 columns 62 for 48).  From 48 on the kernel for many rows,
+    // 256 on: tiles of 128 on tensor memory (at 304 columns 61 us for 71, at 482
+    // 75 for 97, at 1930 175 for 308; at 190 56 for 49).  From 48 on the kernel for many rows,
     // which fills tiles of 64 (34 us for 41 at 132 columns, 73 for 66 at 34);
     // else tiles of 16 where there are more than 8.
     const int64_t columns_all = (int64_t)p->times * c.rows;

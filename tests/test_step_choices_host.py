@@ -220,12 +220,12 @@ def test_norms_take_the_widest_packs(fake, es, dtype):
 
 
 @pytest.mark.parametrize("q_heads,k_heads,rows,sequences,dim,group,dtype,takes", [
-    (32, 8, 96, 1, 128, 128, BF16, True), (32, 8, 95, 1, 128, 128, BF16, False),
-    (32, 8, 192, 2, 64, 64, BF16, True), (32, 8, 191, 2, 64, 64, BF16, False),
+    (32, 8, 64, 1, 128, 128, BF16, True), (32, 8, 63, 1, 128, 128, BF16, False),
+    (32, 8, 128, 2, 64, 64, BF16, True), (32, 8, 127, 2, 64, 64, BF16, False),
     (32, 8, 1000, 1, 128, 64, BF16, False), (32, 8, 1000, 1, 96, 96, BF16, False),
     (32, 8, 1000, 1, 256, 256, BF16, False), (32, 8, 1000, 1, 128, 128, F16, False),
     (32, 8, 1000, 1, 128, 128, F32, False), (390, 2, 7, 1, 128, 128, BF16, True),
-    (8, 8, 384, 1, 128, 128, BF16, True)])
+    (8, 8, 256, 1, 128, 128, BF16, True)])
 @pytest.mark.parametrize("fmt", [0, 1])
 def test_attention_on_tensor_memory(fake, q_heads, k_heads, rows, sequences, dim,
                                     group, dtype, takes, fmt):
