@@ -1204,13 +1204,6 @@ inline int back_grid_of(int64_t rows, int cols, int64_t grid) {
     if (grid > norm_back_blocks(cols)) grid = norm_back_blocks(cols);
     return (int)(grid < rows ? grid : rows);
 }
-// A gate matrix without its gradient, which only the C call can ask for, goes
-// the general way.
-inline bool gate_plain(const mt_block_norm_back_t &c) {
-    return c.gate == nullptr || c.dgate != nullptr || c.gate_stride == 0 ||
-           c.rows == 1;
-}
-
 template <typename T, int K, int THREADS, int NORMS, int GATE>
 cudaError_t norm_back_ahead_as(const mt_block_norm_back_t &c, float *partial,
                                int *blocks, cudaStream_t s) {

@@ -166,6 +166,16 @@ constexpr int kNormBackBlocks = 304;
 constexpr int norm_back_blocks(int cols) {
     return cols <= 2048 ? 2 * kNormBackBlocks : kNormBackBlocks;
 }
+// What the kernels with rows on their way ahead take of a gate: its gradient
+// comes with it, or it is one row for all, and there is an x beside it, which
+// they read with every gate.  The rest (a gate matrix without its gradient, a
+// gate without any gradient and without x), which only the C call can ask for,
+// goes the general way.
+inline bool gate_plain(const mt_block_norm_back_t &c) {
+    return c.gate == nullptr ||
+           (c.x != nullptr &&
+            (c.dgate != nullptr || c.gate_stride == 0 || c.rows == 1));
+}
 // V: values that every access of a row can take at once.  blocks: on return how
 // many rows of partial sums there are.
 #define MT_DECLARE_BLOCK_NORM(dt)                                            \

@@ -1,0 +1,53 @@
+"""Edges of the operators around a decoder's cache without a GPU: what their C
+calls allow and few callers use."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from test_step_host import A, BACK, changed
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+RULES = r"""
+#include "mt_decoder_internal.h"
+extern "C" int plain(const mt_block_norm_back_t *c) {
+    return mt::gate_plain(*c);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    """The rules that the host goes by, built with the host compiler."""
+    d = tmp_path_factory.mktemp("rules")
+    (d / "rules.cpp").write_text(RULES)
+    cuda = next(p for p in (os.environ.get("CUDA_HOME"), "/usr/local/cuda")
+                if p and os.path.exists(os.path.join(p, "include")))
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "row_reduction_gb300", "csrc"), "-I",
+                    os.path.join(cuda, "include"), str(d / "rules.cpp"), "-o",
+                    str(d / "rules.so")], check=True)
+    return ctypes.CDLL(str(d / "rules.so"))
+
+
+# ---- norms around a block ----------------------------------------------------
+@pytest.mark.parametrize("change,plain", [
+    # x is there, or no gate is
+    (dict(), True), (dict(dgate_sum=None), True),
+    (dict(gate=None, dgate_sum=None), True),
+    (dict(gate=None, dgate_sum=None, x=None), True),
+    (dict(gate_stride=64, dgate=13 * A, dgate_sum=None), True),
+    (dict(gate_stride=64, dgate_sum=None, rows=1), True),
+    # a gate matrix without its gradient
+    (dict(gate_stride=64, dgate_sum=None), False),
+    # a gate, of which nothing is asked that would need x, and no x: the
+    # kernels that bring rows ahead would read it
+    (dict(dgate_sum=None, x=None), False),
+    (dict(dgate_sum=None, x=None, rows=1), False),
+    (dict(dgate_sum=None, x=None, gate_stride=64), False),
+    (dict(dgate_sum=None, x=None, gate_stride=64, rows=1), False)], ids=str)
+def test_a_gate_without_x_goes_the_general_way(rules, change, plain):
+    c = changed(BACK, norms=2, weight=None, dweight=None, **change)
+    assert bool(rules.plain(ctypes.byref(c))) == plain
