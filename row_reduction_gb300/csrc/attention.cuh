@@ -59,7 +59,8 @@ __device__ __forceinline__ int sequence_of(const int32_t *offsets, int n,
     return lo;
 }
 
-// The keys that a row at position p sees, of `held` keys: lo..hi.
+// The keys that a row at position p sees, of `held` keys: lo..hi (none before
+// position 0, whatever its bounds say).
 __device__ __forceinline__ void row_sees(const mt_attention_call_t &c,
                                          int64_t row, int64_t p, int64_t held,
                                          int64_t &lo, int64_t &hi) {
@@ -67,7 +68,7 @@ __device__ __forceinline__ void row_sees(const mt_attention_call_t &c,
     hi = c.last ? (int64_t)c.last[row] : p;
     if (c.window) lo = max(lo, p - c.window + 1);
     lo = max(lo, (int64_t)0);
-    hi = c.slots > 0
+    hi = c.slots > 0 && p >= 0
              ? min(hi, min(held, (int64_t)c.pages * c.page_size) - 1) : -1;
 }
 

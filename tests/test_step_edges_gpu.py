@@ -5,12 +5,47 @@ import torch
 
 import row_reduction_gb300 as mt
 from decoder_util import DTYPES, check, half_step
-from step_util import block_norm_back_ref
-from test_step_gpu import gen, randn
+from step_util import attention_ref, block_norm_back_ref
+from test_step_gpu import attention_inputs, gen, i32, randn
 
 pytestmark = pytest.mark.gpu
 
 CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+# ---- attention over the cache ------------------------------------------------
+@pytest.mark.parametrize("dt,dim,group", [
+    ("bf16", 128, 128), ("bf16", 128, 64), ("f16", 64, 64), ("f32", 96, 96),
+    ("bf16", 40, 40)])
+@pytest.mark.parametrize("rows", [(3, 5), (100, 130), (400, 300)], ids=str)
+@pytest.mark.parametrize("kind", ["last", "both", "window"])
+def test_rows_before_position_zero_see_nothing(dt, dim, group, rows, kind):
+    """... with bounds of their own too, which would let them see keys."""
+    batch = [(rows[0], rows[0] - 2), (rows[1], rows[1] // 2), (4, 60)]
+    a = attention_inputs(dim, batch, 4, 1, dim, group, 16, "e4m3", DTYPES[dt])
+    n = sum(r for r, _ in batch)
+    p = torch.cat([torch.arange(k - r, k) for r, k in batch])
+    last = torch.where(p % 3 == 0, p + 40, 2)
+    kw = {}
+    if kind == "both":
+        kw["first"] = i32(torch.where(p % 5 == 0, p, -1).tolist())
+    if kind == "window":
+        kw["window"] = 50
+    out = torch.full(a["q"].shape, 7.0, dtype=a["q"].dtype, device="cuda")
+    got, lse = mt.cache_attention(
+        a["q"], a["k_cache"], a["v_cache"], a["table"], a["offsets"],
+        a["starts"], 16, out=out, return_lse=True, last=i32(last.tolist()),
+        **kw)
+    assert bool((got[p < 0] == 0).all())
+    assert bool((lse[p < 0] == -torch.inf).all())
+    # the same as with bounds that let those rows see nothing
+    ref, err, rlse, lerr, there = attention_ref(
+        a["q"], a["k_cache"], a["v_cache"], a["table"], a["offsets"],
+        a["starts"], 16, last=i32(torch.where(p < 0, -1, last).tolist()), **kw)
+    assert bool(there.all()) and len(there) == n
+    check(got, ref, err + half_step(ref, got.dtype), "out")
+    check(lse, rlse, lerr + torch.nan_to_num(rlse, neginf=0.0).abs() * 2e-7,
+          "lse")
 
 
 # ---- norms around a block ----------------------------------------------------
