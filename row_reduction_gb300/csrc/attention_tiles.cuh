@@ -110,8 +110,10 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// The 32 columns from `at` on of the thread's own lane.
+// The 32 columns from `at` on of the thread's own lane.  Loads and stores are
+// the warp's: its lanes, which may have gone different ways, come together here.
 __device__ __forceinline__ void tensor_load(unsigned (&r)[32], unsigned at) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -130,6 +132,7 @@ __device__ __forceinline__ void tensor_load(unsigned (&r)[32], unsigned at) {
 }
 __device__ __forceinline__ void tensor_store(unsigned at,
                                              const unsigned (&r)[32]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
         "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
@@ -696,22 +699,24 @@ struct TileRun {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0;
             if (any) tensor_load(o, sums_at + d);  // the same for the CTA
-            if (!at.used) continue;
+            if (at.used) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[x] = __uint_as_float(o[e + x]) * by;
-                if (whole) {
+                for (int e = 0; e < 32; e += 4) {
+                    float v[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        v[x] = ref != ref ? NAN : none ? 0.f : v[x] / l;
-                    store4(DT_BF16, (cut.whole & 2) != 0, c.out, to + d + e, v);
-                } else {
-                    *reinterpret_cast<float4 *>(sums + 2 * kTileColumns +
-                                                col * DIM + d + e) =
-                        make_float4(v[0], v[1], v[2], v[3]);
+                        v[x] = __uint_as_float(o[e + x]) * by;
+                    if (whole) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            v[x] = ref != ref ? NAN : none ? 0.f : v[x] / l;
+                        store4(DT_BF16, (cut.whole & 2) != 0, c.out,
+                               to + d + e, v);
+                    } else {
+                        *reinterpret_cast<float4 *>(sums + 2 * kTileColumns +
+                                                    col * DIM + d + e) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                    }
                 }
             }
         }

@@ -2,6 +2,7 @@
 calls allow and few callers use."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -51,3 +52,22 @@ def rules(tmp_path_factory):
 def test_a_gate_without_x_goes_the_general_way(rules, change, plain):
     c = changed(BACK, norms=2, weight=None, dweight=None, **change)
     assert bool(rules.plain(ctypes.byref(c))) == plain
+
+
+# ---- attention over the cache ------------------------------------------------
+def test_a_warp_comes_together_before_tensor_memory():
+    """Loads from tensor memory and stores to it are the whole warp's, and come
+    behind code in which its lanes go different ways: each stands right behind
+    a __syncwarp().  (Whether lanes were apart cannot be seen from outside.)"""
+    csrc = os.path.join(ROOT, "row_reduction_gb300", "csrc")
+    found = 0
+    for name in sorted(os.listdir(csrc)):
+        if not name.endswith((".cu", ".cuh")):
+            continue
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for m in re.finditer(r"tcgen05\.(ld|st)\.sync", text):
+            before = text[:text.rindex("asm volatile", 0, m.start())]
+            assert before.rstrip().endswith("__syncwarp();"), (name, m.group())
+            found += 1
+    assert found == 2
