@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kAnyThreads)
     const T *q = static_cast<const T *>(c.q) + row * c.q_row +
                  (int64_t)head * c.q_head;
     const float slope = c.slopes ? c.slopes[head] : 0.f;
-    const float inv_cap = c.cap > 0.f ? 1.f / c.cap : 0.f;
+    const Cap cap(c.cap, 1.f);
     const bool int8 = c.format == MT_CACHE_INT8;
     float qv[kPerLane], o[kPerLane];
     bool bad = false;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kAnyThreads)
         for (int off = 16; off > 0; off >>= 1)
             z += __shfl_xor_sync(kFull, z, off);
         z *= c.scale;
-        if (c.cap > 0.f) z = capped(z, c.cap, inv_cap);
+        if (c.cap > 0.f) z = cap.any(make_float2(z, z), 0.f).x;
         if (c.slopes) z -= slope * fabsf((float)(p - j));
         const float next = nanmax(top, z);
         const float keep = top == -INFINITY ? 0.f

@@ -331,8 +331,7 @@ struct Shared {
     uint2 q[kWarps][NT][PARTS][H::STEPS][32];  // fragments, of each key head
     Column column[8 * NT];
     // Of each key head's columns: what the product takes to be a score in units
-    // of log 2 (with cap, to be 2 score / cap in them), the scale and the
-    // query's power of two; the slope in those units.
+    // of log 2, the scale and the query's power of two; the slope in those units.
     float f[kWarps][8 * NT], slope[kWarps][8 * NT];
     int32_t lo_any, hi_any, lo_all, hi_all;
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
@@ -507,14 +506,9 @@ struct Warp {
                     for (int i = 0; i < 2; ++i) z[n][t][2 * i + h] *= f;
             }
         if (c.cap > 0.f) {
-            const float cap2 = c.cap * kLog2e;
+            const Cap cap(c.cap, kLog2e);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[n][t][e] = capped2(z[n][t][e], cap2);
+            for (int n = 0; n < NT; ++n) cap_scores(cap, z[n]);
         }
         if (c.slopes == nullptr && whole) return false;
 #pragma unroll
@@ -972,8 +966,7 @@ struct Queries {
             if (lane == 0)
                 sh.f[hs][col] =
                     bad ? NAN
-                        : (c.cap > 0.f ? c.scale / c.cap * 2.f : c.scale) *
-                              kLog2e * __uint_as_float((e - 14u) << 23);
+                        : c.scale * kLog2e * __uint_as_float((e - 14u) << 23);
         }
     }
 };

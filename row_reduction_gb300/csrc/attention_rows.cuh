@@ -180,8 +180,7 @@ struct RowWarp {
                     }
                 }
             f[i] = bad ? NAN
-                       : (c.cap > 0.f ? c.scale / c.cap * 2.f : c.scale) *
-                             kLog2e * __uint_as_float((e - 14u) << 23);
+                       : c.scale * kLog2e * __uint_as_float((e - 14u) << 23);
             slope[i] = 0.f;
             lo[i] = INT32_MIN;
             hi[i] = INT32_MAX;
@@ -264,11 +263,8 @@ struct RowWarp {
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[n][e] *= f[e >> 1];
         if (c.cap > 0.f) {
-            const float cap2 = c.cap * kLog2e;
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[n][e] = capped2(z[n][e], cap2);
+            const Cap cap(c.cap, kLog2e);
+            cap_scores(cap, z);
         }
         if (c.slopes == nullptr && whole) return false;
 #pragma unroll
