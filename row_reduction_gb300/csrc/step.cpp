@@ -152,11 +152,12 @@ struct Widest {
     int values() const { return widest(bits, 16 / es); }
 };
 
+// A row of partial sums for each CTA, of which there are no more than rows.
 size_t norm_workspace(const mt_block_norm_back_t &c) {
-    return c.dgate_sum || c.dweight || c.dnext_weight
-               ? (size_t)norm_back_blocks(c.cols) * 3 * (size_t)c.cols *
-                     sizeof(float)
-               : 0;
+    if (!c.dgate_sum && !c.dweight && !c.dnext_weight) return 0;
+    const int64_t most = norm_back_blocks(c.cols);
+    return (size_t)(c.rows < most ? c.rows : most) * 3 * (size_t)c.cols *
+           sizeof(float);
 }
 
 // Whether no output of the call is one of its inputs or another output (those

@@ -159,6 +159,42 @@ def back_call(c, dtype):
                               n, torch.cuda.current_stream().cuda_stream)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 2, 5, 200, 700])
+@pytest.mark.parametrize("cols", [8, 7, 256, 1024, 1235, 2048, 4096, 8190,
+                                  16384, 40001])
+def test_backward_keeps_to_its_workspace(dt, rows, cols):
+    """Every way that rows go, with as many bytes as the call asks for."""
+    if rows * cols > 4_000_000:
+        rows = 4_000_000 // cols
+    dtype, g = DTYPES[dt], gen(rows + cols)
+    dy, x, h = (randn(g, rows, cols, dtype=dtype) for _ in range(3))
+    gate, w, w2 = (randn(g, cols, dtype=dtype) for _ in range(3))
+    dx, dres = torch.empty_like(dy), torch.empty_like(dy)
+    sums = torch.empty(3, cols, device="cuda")
+    c = mt.MtBlockNormBack(
+        dy=dy.data_ptr(), x=x.data_ptr(), h=h.data_ptr(), gate=gate.data_ptr(),
+        weight=w.data_ptr(), next_weight=w2.data_ptr(), dx=dx.data_ptr(),
+        dresidual=dres.data_ptr(), dgate_sum=sums[0].data_ptr(),
+        dweight=sums[1].data_ptr(), dnext_weight=sums[2].data_ptr(),
+        dy_stride=cols, x_stride=cols, h_stride=cols, dx_stride=cols,
+        dresidual_stride=cols, rows=rows, cols=cols, norms=3, eps=1e-5,
+        residual_scale=1.0)
+    n = mt.mt_block_norm_backward_workspace(CODES[dtype], c)
+    assert n <= rows * 12 * cols
+    # what lies behind belongs to the buffer, as much as the largest call needs
+    room = torch.full((n + 608 * 12 * cols,), 171, dtype=torch.uint8,
+                      device="cuda")
+    mt.mt_block_norm_backward(CODES[dtype], c, room.data_ptr(), n,
+                              torch.cuda.current_stream().cuda_stream)
+    assert bool((room[n:] == 171).all())
+    want = block_norm_back_ref(dy, None, x, h, w, gate, w2, "both", 1.0, 1e-5)
+    for name, got, (ref, err) in zip(
+            ("dx", "dresidual", "dgate", "dweight", "dnext_weight"),
+            (dx, dres, *sums), want):
+        check(got, ref, err + half_step(ref, got.dtype), name)
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,cols", [(7, 1024), (1, 4096), (9, 1235),
                                        (1, 8190), (4, 24), (5, 7), (3, 20000),

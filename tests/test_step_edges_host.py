@@ -7,7 +7,8 @@ import subprocess
 
 import pytest
 
-from test_step_host import A, BACK, changed
+import row_reduction_gb300 as mt
+from test_step_host import A, BACK, built, changed  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -52,6 +53,22 @@ def rules(tmp_path_factory):
 def test_a_gate_without_x_goes_the_general_way(rules, change, plain):
     c = changed(BACK, norms=2, weight=None, dweight=None, **change)
     assert bool(rules.plain(ctypes.byref(c))) == plain
+
+
+def test_backward_workspace_goes_by_the_rows():
+    """A row of partial sums for each CTA at most, and for each row at most: a
+    call of few wide rows asks for little."""
+    def need(**kw):
+        return mt.mt_block_norm_backward_workspace(
+            0, changed(BACK, **{**dict(dy_stride=1 << 20, dh_stride=1 << 20,
+                                       x_stride=1 << 20, h_stride=1 << 20,
+                                       dx_stride=1 << 20,
+                                       dresidual_stride=1 << 20), **kw}))
+    for cols, most in ((64, 608), (2048, 608), (2049, 304), (16384, 304),
+                       (1 << 20, 304)):
+        row = 3 * cols * 4
+        for rows in (0, 1, 2, 8, 303, 304, 305, 607, 608, 609, 10 ** 6):
+            assert need(rows=rows, cols=cols) == min(rows, most) * row
 
 
 # ---- attention over the cache ------------------------------------------------
