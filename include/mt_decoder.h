@@ -348,7 +348,8 @@ typedef struct mt_attention_call {
                                   nothing */
     const int32_t *first, *last; /* rows each, or NULL */
     const float *slopes;       /* q_heads, or NULL */
-    int64_t rows;              /* 0..2^31 - 1 */
+    int64_t rows;              /* 0..2^31 - 1; rows x q_heads to 2^33 - 4 for
+                                  heads that no matrix kernel takes */
     int64_t slots;
     int32_t sequences, pages, page_size;
     int32_t q_heads;           /* a multiple of k_heads, at most 65536 */

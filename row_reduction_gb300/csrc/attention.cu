@@ -6,7 +6,7 @@ namespace mt {
 
 namespace {
 
-constexpr int kAnyThreads = 128;
+constexpr int kAnyThreads = 32 * kAttentionAnyWarps;
 constexpr int kPerLane = kAttentionMaxDim / 32;
 
 __device__ __forceinline__ float code_value(uint8_t code, bool int8) {
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kAnyThreads)
 
 cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
                                  cudaStream_t s) {
-    constexpr int kWarps = kAnyThreads / 32;
-    const int64_t grid = (c.rows * c.q_heads + kWarps - 1) / kWarps;
+    const int64_t grid =
+        (c.rows * c.q_heads + kAttentionAnyWarps - 1) / kAttentionAnyWarps;
     switch (dtype) {
         case DT_F32:
             return launch_dependent(attention_any_kernel<float>, grid,

@@ -113,6 +113,7 @@ cudaError_t launch_cache_extend(const mt_cache_extend_call_t &c,
 
 // ---- attention over the cache --------------------------------------------------
 constexpr int kAttentionMaxDim = 512;
+constexpr int kAttentionAnyWarps = 4;  // of a CTA, each with a row's query head
 cudaError_t launch_attention_any(int dtype, const mt_attention_call_t &c,
                                  cudaStream_t s);
 // A call on the matrix kernels: how its rows and query heads are cut into

@@ -74,7 +74,9 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
               c.slots <= INT32_MAX &&
               !misaligned(c.k_codes, 32) && !misaligned(c.v_codes, 32) &&
               !misaligned(c.k_scales, 16) && !misaligned(c.v_scales, 16);
-    if (!*matrix) return MT_OK;
+    if (!*matrix)
+        return c.rows * c.q_heads <= (int64_t)INT32_MAX * kAttentionAnyWarps
+                   ? MT_OK : MT_ERR_UNSUPPORTED;
     int sms = 0;
     if (cudaError_t e = current_sm_count(&sms)) return status_from_cuda(e);
     p->times = c.q_heads / c.k_heads;

@@ -8,7 +8,8 @@ import subprocess
 import pytest
 
 import row_reduction_gb300 as mt
-from test_step_host import A, BACK, built, changed  # noqa: F401
+from test_step_choices_host import fake  # noqa: F401
+from test_step_host import A, ATTENTION, BACK, built, changed  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -72,6 +73,30 @@ def test_backward_workspace_goes_by_the_rows():
 
 
 # ---- attention over the cache ------------------------------------------------
+def test_more_rows_than_a_launch_takes(fake):  # noqa: F811
+    """A warp per row and query head, four to a CTA, 2^31 - 1 CTAs at most."""
+    most = 4 * (2 ** 31 - 1)
+
+    def call(dim, rows, heads):
+        return changed(ATTENTION, dim=dim, group=dim, q_heads=heads, k_heads=1,
+                       rows=rows, q_row=heads * dim, q_head=dim,
+                       out_row=heads * dim, out_head=dim)
+
+    def status(c):
+        n = ctypes.c_size_t()
+        got = fake.mt_cache_attention_workspace(2, ctypes.byref(c),
+                                                ctypes.byref(n))
+        assert got == fake.mt_cache_attention(
+            2, ctypes.byref(c), ctypes.c_void_p(A), ctypes.c_size_t(1 << 50),
+            None)
+        return got
+    assert status(call(8, most // 4, 4)) == 0
+    assert status(call(8, most // 1024, 1024)) == 0
+    assert status(call(8, most // 1024 + 1, 1024)) == mt.MT_ERR_UNSUPPORTED
+    assert status(call(8, 2 ** 31 - 1, 65536)) == mt.MT_ERR_UNSUPPORTED
+    assert status(call(64, 2 ** 31 - 1, 65536)) == 0    # matrix kernels
+
+
 def test_a_warp_comes_together_before_tensor_memory():
     """Loads from tensor memory and stores to it are the whole warp's, and come
     behind code in which its lanes go different ways: each stands right behind
