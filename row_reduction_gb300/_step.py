@@ -298,7 +298,9 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
     """Attention of the queries q [rows, q_heads, dim] over the keys and values
     that k_cache and v_cache hold, each (codes, scales) as from
     :func:`cache_alloc`.  q_heads is a multiple of the cache's heads; q may be
-    a strided view.
+    a strided view.  Heads of 64 (one or two groups), 80, 96 (one), 128 (one, two
+    or four) and 256 (one, two or eight) in a cache whose codes begin at 32 bytes
+    and scales at 16 go to matrix instructions; other heads take far longer.
 
     Rows offsets[s] .. offsets[s+1]-1 belong to sequence s and stand at
     positions starts[s], starts[s]+1, ... of it; its page p is table[s, p]
@@ -313,7 +315,9 @@ def cache_attention(q, k_cache, v_cache, table, offsets, starts, page_size,
     slopes[head] times the distance in positions.  Returns [rows, q_heads,
     dim], zeros for a row that sees nothing, and with return_lse also the
     logarithm of the sum of the exponentials of its scores (float32 [rows,
-    q_heads], then -inf).  out: where to write, not q; rows outside the batch
+    q_heads], then -inf).  What a row does not see has no effect on it, but that
+    codes which are NaN themselves (cache_write stores none) must not stand in
+    slots that a row of its sequence sees.  out: where to write, not q; rows outside the batch
     (offsets[0] .. offsets[-1]) are left as they were (in new outputs:
     zeros)."""
     dt, index = _first(q, "q")

@@ -1,5 +1,12 @@
 // attention.cu -- attention over the quantised cache for any head and group: a
-// warp per row and query head.
+// warp per row and query head, a key at a time.
+//
+// For what the matrix kernels do not take (attention_head in step.cpp).  Bound by
+// instructions and the sum over the warp, five exchanges a key; every query head
+// reads its key head's keys for itself.  64 sequences to 16384 keys: heads of 32
+// 36 ms, of 96 in three groups 53, of 192 84; prompts of 2 x 512 rows at 4096 keys
+// 59, 91 and 78.  That is 3 to 5 times the time of plain torch operations for
+// the former, 22 to 37 times for the latter.
 #include "attention.cuh"
 
 namespace mt {

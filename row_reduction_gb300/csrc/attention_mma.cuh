@@ -24,8 +24,12 @@
 // times FP16 with the head's largest value at 2^14..2^15, BF16 and FP16 values
 // exactly (down to 2^-28 of the largest), FP32 in two parts (2^-22).  Weights
 // times the values' scales are held likewise, their largest so far at
-// 2^11..2^12 or above: one part for BF16 output (2^-11, a quarter of its own
-// rounding), two for FP16 and FP32.  Sums are FP32: for BF16 output the
+// 2^11..2^12 or above: one part for BF16 output (half a step 2^-11 of a weight,
+// an eighth of the output's own), two for FP16 and FP32.  Against 64 bits outputs
+// are off by 1.7e-3 rms with one part and with two, which is the rounding to
+// BF16; two would bring them within 1e-4 of FP32 sums rounded once for 9e-4, at 210
+// us in place of 205 (64 sequences to 16384 keys), 128 of 121 (heads of 64) and
+// 90 of 83 (one of 131072, capped).  Sums are FP32: for BF16 output the
 // instruction's own all along, else its sums of a chunk, added up to nearest.
 //
 // References.  A column's weights are exponentials about a reference that
@@ -43,11 +47,13 @@
 // runs is left as partial sums, which a second kernel joins in order.
 //
 // Bound.  Long contexts by memory: 64 sequences to 16384 keys, 8 key heads of
-// 128, BF16 200 us, 6.2 TB/s, 93% of the measured copy bandwidth (heads of 64 122
-// us, 79%: more chunks to the byte).  Short ones by a chain of waits: plan,
+// 128, BF16 200-205 us, 6.2 TB/s, 93-91% of the measured copy bandwidth (heads of
+// 64 121 us, 79%: more chunks to the byte).  Short ones by a chain of waits: plan,
 // queries, first keys, two or three chunks of some 2000 cycles a warp, sums, and
-// the second kernel: eight sequences to 2048 keys 22 us.  One sequence of 131072
-// keys 81 us, 53%: each CTA has 27 chunks a warp.
+// the second kernel: eight sequences to 2048 keys 21 us.  One sequence of 131072
+// keys, two groups a head, capped, 83 us, 51% (uncapped 77): each CTA has 27
+// chunks a warp.  Half of the variants spill some words, 92 bytes at most (two
+// parts, tiles of 16 columns).
 //
 // Two CTAs per SM of heads of 128 (three: 250 us for 242 before key heads shared
 // a CTA): registers for a chunk's fragments count for more than warps.

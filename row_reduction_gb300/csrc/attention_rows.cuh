@@ -17,8 +17,11 @@
 //
 // Bound: shared memory (73% of its throughput: every warp reads all of a chunk
 // for its 16 columns) and the instructions around the products; those have 34%
-// of the tensor pipe.  Two sequences of up to 512 rows at 4096 keys, 32 + 8 heads
-// of 128, FP16, causal: 380 us (BF16 capped 308 here, 372 on tiles of 16).
+// of the tensor pipe (with two parts, FP16, 58% and 51%).  Two
+// sequences of up to 512 rows at 4096 keys, 32 + 8 heads of 128, causal: FP16 383
+// us (capped 416), FP32 387; BF16 with two groups a head 318, four 392 (184 bytes
+// spilled, FP32 312; one group 180); heads of 96 230.  BF16 with one group took
+// 308 here, capped, and 372 on tiles of 16.
 #pragma once
 
 #include "attention_mma.cuh"

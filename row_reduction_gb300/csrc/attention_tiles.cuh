@@ -16,13 +16,14 @@
 // and their joining are the same as there.
 //
 // Bound.  Two sequences of up to 512 rows at 4096 keys, 32 + 8 heads of 128,
-// capped: 175 us, 340 TFLOP/s, 308 on tiles of 64 columns with mma.sync (uncapped
-// and causal 164 for 283); 2 x 2048 rows at 8192 keys 816 us, 440 TFLOP/s.  A
-// chunk's weights take 4000 cycles of a warp for 650 instructions, of which a
-// quarter wait for scales from shared memory (53% of that pipe's throughput:
-// operands, codes and scales share it), a quarter for the two exponentials and
-// the reciprocal of a capped score; issue slots are 44% busy.  All eight warps on
-// weights, halves of a column each, took 239 us, all four on everything 214.
+// capped: 178 us, 322 TFLOP/s, 308 on tiles of 64 columns with mma.sync (uncapped
+// and causal 155 for 283); 2 x 2048 rows at 8192 keys 830 us, 425 TFLOP/s.  What
+// is done for a score sets it, not the products (16% of the tensor pipe; heads of
+// 64, half the products, 148 us): issue slots are 45% busy at 16 warps per SM, and
+// weights wait for scales from shared memory, 52% of whose throughput operands,
+// codes and scales share, and for each other's results.  Some 220 bytes of a
+// thread's 128 registers spill.  All eight warps on weights, halves of a column
+// each, took 239 us, all four on everything 214 (175 at the time).
 //
 // Waits have a limit; a CTA whose wait ran out gives NaN.  No barrier gets two
 // phases ahead of who waits for it: weights of a chunk arrive only after the sums

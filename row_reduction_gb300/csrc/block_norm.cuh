@@ -11,8 +11,12 @@
 // shared memory where it has 16 columns or more; a second kernel adds up the
 // CTAs' in order.
 //
-// Bound: memory.  BF16 16384 x 4096, both norms and a gate of one row, 92 us, 87%
-// of the measured copy bandwidth; backward 8192 x 4096 68 us, 89%.
+// Bound: memory.  BF16 16384 x 4096, both norms and a gate of one row, 93 us, 87%
+// of the measured copy bandwidth; backward 8192 x 4096 68 us, 89%.  Rows of 16384
+// leave one CTA on an SM, which has nothing on its way while it adds up: 4096 of
+// them 125 us, 64%; of 200 columns, 25 lanes of a warp have one pack each: 65536
+// rows 24 us, 65%.  Backward, rows of 16384 are past both the kernel with rows
+// ahead and the registers (300 bytes spill): 2048 of them 281 us, 22%.
 //
 // Packs are as wide as every row's address allows.  Rows that 16-byte packs do
 // not divide, from 512 columns on, are copied into shared memory with what lies

@@ -11,8 +11,11 @@
 // another.  More sequences take two kernels: one CTA goes through them in order
 // and gives out the pages, then a thread per row.
 //
-// Bound: latency.  256 sequences of a token each 4.5 us, 1024 with 107 thousand
-// rows 10 (two kernels: 8.0 and 12.9).
+// Bound: latency.  256 sequences of a token each 4.3 us, 1024 6.5 (sums that every
+// CTA makes for itself, 64-bit divisions by the page size among them), 1024 with
+// 107 thousand rows 10 (two kernels: 8.0 and 12.9): a row is a thread's one search,
+// two divisions and a page.  4096 with a token each 17 us; by two kernels 4097 24,
+// 65536 232, where one CTA goes through the sequences.
 #include "mt_decoder.cuh"
 
 namespace mt {

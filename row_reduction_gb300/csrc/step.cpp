@@ -54,7 +54,10 @@ mt_status attention_setup(int dtype, const mt_attention_call_t *c,
     return MT_OK;
 }
 
-// The sizes that the matrix kernels take (on any device).
+// The sizes that the matrix kernels take (on any device): those they are built
+// for, each of which is a kernel of its own for either format and both numbers of
+// parts.  Other sizes are right and slow (128 in one group, 64 sequences to 16384
+// keys, 0.2 ms; 112 on the general kernel 60).
 bool attention_head(const mt_attention_call_t &c) {
     const int groups = c.dim / c.group;
     switch (c.dim) {
@@ -84,7 +87,11 @@ mt_status attention_plan(int dtype, const mt_attention_call_t &c, bool *matrix,
     // 256 on: tiles of 128 on tensor memory (at 304 columns 61 us for 71, at 482
     // 75 for 97, at 1930 175 for 308; at 190 56 for 49).  From 48 on the kernel for many rows,
     // which fills tiles of 64 (34 us for 41 at 132 columns, 73 for 66 at 34);
-    // else tiles of 16 where there are more than 8.
+    // else tiles of 16 where there are more than 8.  An average over all rows that
+    // q has, since the host does not know the batch: a batch of unlike sequences
+    // goes by the middle (a prompt of 2048 rows 221 us, 63 tokens 60, both 398),
+    // and rows of q outside the batch count too (8 tokens 20 us, in a q of 256
+    // rows 27, of 512 and more 35).
     const int64_t columns_all = (int64_t)p->times * c.rows;
     const bool many = c.dim <= 128 && c.dim % 32 == 0 &&
                       columns_all >= kManyColumns * (int64_t)c.sequences;
